@@ -76,6 +76,15 @@ enum swin_wattn_kernel {
   SWIN_WATTN_KERNEL_TCGEN05 = 2    /* tensor-memory kernels: M = 7 or 12 with bf16 */
 };
 
+/* Activations of the MLP's products (swin_wattn_linear, swin_wattn_linear_bwd_data). */
+enum swin_wattn_activation {
+  SWIN_WATTN_ACT_NONE = 0,
+  SWIN_WATTN_ACT_RELU = 1,      /* max(z, 0); derivative 0 at z = 0 */
+  SWIN_WATTN_ACT_GELU = 2,      /* z Phi(z), Phi the normal distribution function */
+  SWIN_WATTN_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  SWIN_WATTN_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+};
+
 /*
  * Create a plan for one layer shape and run the preprocessing on `stream`:
  * the dense bias [nH, M^2, M^2] is expanded from `bias_table` (the lookup done once, as
@@ -271,6 +280,104 @@ int swin_wattn_qkv_proj_prepared_fp8(const void* x, const void* prepared, void* 
  */
 int swin_wattn_proj_residual(const void* o, const void* w_proj, const float* b_proj, const void* residual,
                              void* y, int tokens, int C, int* status, struct CUstream_st* stream);
+
+/*
+ * A product with bias, activation and residual in its epilogue, the two halves of a block's
+ * MLP (NVIDIA Swin talk, section 1: a block's FFN; section 3: bias, activation and residual
+ * fused into the products around them) and any other dense layer:
+ *   z = x W^T + b,   y = residual + act(z)
+ * Arguments (device pointers of the current device, contiguous, 16-byte aligned unless
+ * stated):
+ *   x        bf16 [tokens, K];
+ *   w        bf16 [N, K] (row n = output channel n);
+ *   b        fp32 [N], 4-byte aligned, or NULL for no bias;
+ *   residual bf16 [tokens, N], or NULL for none;
+ *   y        bf16 [tokens, N], written. y may be the residual buffer itself (each element is
+ *            read before it is written) but must not overlap x, w, or pre;
+ *   pre      bf16 [tokens, N], or NULL: z is also written there, rounded to bf16, for
+ *            swin_wattn_linear_bwd_data. act is applied to the unrounded z;
+ *   tokens   >= 0 (0: nothing is done); K, N: multiples of 8 in [8, 32768];
+ *   act      SWIN_WATTN_ACT_*;
+ *   status   optional device int (may be NULL): bit 0 is OR-ed in if a bounded device wait
+ *            ran out (then the results are not valid).
+ * The product is accumulated in fp32 on the bf16 operands; bias, activation and residual are
+ * applied in fp32 and each result is rounded once. One kernel launch on `stream`; nothing is
+ * allocated. Deterministic. Errors: INVALID_ARG for negative tokens, an unknown act, overlapping
+ * buffers, or a pointer that is not memory of the current device; MISALIGNED for a pointer
+ * off its alignment; UNSUPPORTED for K or N.
+ */
+int swin_wattn_linear(const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
+                      int tokens, int K, int N, int act, int* status, struct CUstream_st* stream);
+
+/*
+ * The gradient of a product's input, taken through the activation that made that input:
+ *   dx = (dy W) * act'(pre)
+ *   dy   bf16 [tokens, N];   w  bf16 [N, K] (the forward's weight);
+ *   pre  bf16 [tokens, K], the pre-activation kept by the forward that made x; NULL (and not
+ *        read) when act is SWIN_WATTN_ACT_NONE;
+ *   dx   bf16 [tokens, K], written. dx may be the pre buffer itself but must not overlap dy
+ *        or w.
+ * With act NONE, dx = dy W is the gradient of x; with an activation, of the pre-activation
+ * that x = act(pre) came from. Sizes, status, arithmetic and errors as for swin_wattn_linear.
+ * One launch.
+ */
+int swin_wattn_linear_bwd_data(const void* dy, const void* w, const void* pre, void* dx, int tokens, int K, int N,
+                               int act, int* status, struct CUstream_st* stream);
+
+/*
+ * The gradients of a product's weight and bias:
+ *   dw = [dw +] dy^T x,   db = [db +] sum of dy over the tokens
+ *   dy   bf16 [tokens, N];   x  bf16 [tokens, K];
+ *   dw   [N, K], fp32 or bf16 by `dtype` (SWIN_WATTN_FP32 or SWIN_WATTN_BF16), written;
+ *   db   fp32 [N], 4-byte aligned, or NULL;
+ *   accumulate  nonzero: the gradients are added to what dw and db hold (in fp32, rounded
+ *        once), for several micro-batches; zero: they are overwritten. With no tokens the sum
+ *        is empty: dw and db are zeroed, or left as they are when accumulating;
+ *   workspace   caller-owned device memory of at least
+ *        swin_wattn_linear_bwd_weight_workspace_bytes(tokens, K, N) bytes, 256-byte aligned,
+ *        overwritten (partial results of groups of tokens); one call at a time per workspace,
+ *        and none of the other buffers.
+ * Summed in fp32, in an order that depends on the sizes alone: deterministic. One or two
+ * launches; nothing is allocated. dw, db and workspace must not overlap the inputs or one
+ * another. Sizes, status and errors as for swin_wattn_linear (INVALID_ARG also for a small
+ * workspace or an unknown dtype). The size query returns 0 for unsupported arguments.
+ */
+size_t swin_wattn_linear_bwd_weight_workspace_bytes(int tokens, int K, int N);
+int swin_wattn_linear_bwd_weight(const void* dy, const void* x, void* dw, float* db, int tokens, int K, int N,
+                                 int dtype, int accumulate, void* workspace, size_t workspace_bytes, int* status,
+                                 struct CUstream_st* stream);
+
+/*
+ * A stack of weight updates made near orthogonal by Newton-Schulz products, for an optimiser
+ * that steps along U V^T of its momentum G = U S V^T instead of along G. Per matrix:
+ *   X = G / (|G|_F + eps), then `steps` times X <- a X + (b A + c A^2) X, A = X X^T,
+ *   (a, b, c) = (3.4445, -4.7750, 2.0315);   out = scale * X
+ * (on the side of the smaller dimension, which gives the same). Every singular value is
+ * taken towards [0.7, 1.2]; U and V are kept.
+ *   g      [count, rows, cols], fp32 or bf16 by `dtype` (SWIN_WATTN_FP32 or
+ *          SWIN_WATTN_BF16), contiguous, 4- or 2-byte aligned;
+ *   out    bf16 [count, rows, cols], 2-byte aligned, written (16-byte aligned with cols a
+ *          multiple of 8 is the fast case); must not overlap g;
+ *   count  in [0, 65535] (0: nothing is done); rows, cols in [1, 16384];
+ *   steps  in [1, 20]; eps finite and > 0; scale finite;
+ *   workspace  caller-owned device memory of at least
+ *          swin_wattn_orthogonalize_workspace_bytes(count, rows, cols) bytes, 256-byte
+ *          aligned, overwritten; one call at a time per workspace.
+ * Operands of the products are held in fp16 (scaled; the values are bounded), products are
+ * accumulated in fp32; the result is within about 1.5e-3 (relative 2-norm, before its
+ * rounding to bf16) of the exact iteration for matrices whose singular values span a
+ * factor of about a hundred, and loses accuracy in the directions of smaller ones. The norm
+ * is summed in fp32, with large values scaled so that it does not overflow. A matrix with a
+ * NaN or an infinity gives NaN and leaves the others of the stack alone; a zero matrix gives zeros.
+ * 2 + 3 * steps launches; nothing is allocated. Deterministic. Errors: INVALID_ARG for the
+ * scalars, overlaps, a small workspace or a pointer that is not memory of the current
+ * device; MISALIGNED; UNSUPPORTED for sizes out of range. The size query returns 0 for
+ * unsupported arguments.
+ */
+size_t swin_wattn_orthogonalize_workspace_bytes(int count, int rows, int cols);
+int swin_wattn_orthogonalize(const void* g, void* out, int count, int rows, int cols, int dtype, int steps, float eps,
+                             float scale, void* workspace, size_t workspace_bytes, int* status,
+                             struct CUstream_st* stream);
 
 /*
  * Forward on 8-bit operands (7x7 windows, a SWIN_WATTN_BF16 plan): the attention of

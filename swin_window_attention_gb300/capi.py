@@ -27,6 +27,13 @@ KERNEL_AUTO = 0
 KERNEL_MMA_SYNC = 1
 KERNEL_TCGEN05 = 2
 
+ACT_NONE = 0
+ACT_RELU = 1
+ACT_GELU = 2
+ACT_GELU_TANH = 3
+ACT_SILU = 4
+ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
+
 # Every symbol include/swin_wattn.h declares, with (argtypes, restype).
 _vp, _i, _cp = ctypes.c_void_p, ctypes.c_int, ctypes.c_char_p
 SIGNATURES = {
@@ -46,6 +53,12 @@ SIGNATURES = {
     "swin_wattn_qkv_proj_prepared_fp8": ([_vp] * 3 + [_i, _i] + [ctypes.c_float] * 4 +
                                          [_vp, _vp, ctypes.c_size_t, _vp, _vp], _i),
     "swin_wattn_proj_residual": ([_vp] * 5 + [_i, _i, _vp, _vp], _i),
+    "swin_wattn_linear": ([_vp] * 6 + [_i] * 4 + [_vp, _vp], _i),
+    "swin_wattn_linear_bwd_data": ([_vp] * 4 + [_i] * 4 + [_vp, _vp], _i),
+    "swin_wattn_linear_bwd_weight_workspace_bytes": ([_i] * 3, ctypes.c_size_t),
+    "swin_wattn_linear_bwd_weight": ([_vp] * 4 + [_i] * 5 + [_vp, ctypes.c_size_t, _vp, _vp], _i),
+    "swin_wattn_orthogonalize_workspace_bytes": ([_i] * 3, ctypes.c_size_t),
+    "swin_wattn_orthogonalize": ([_vp, _vp] + [_i] * 5 + [ctypes.c_float] * 2 + [_vp, ctypes.c_size_t, _vp, _vp], _i),
     "swin_wattn_fwd_fp8": ([_vp, _vp, ctypes.c_float, ctypes.c_float, ctypes.c_float, _vp, _vp], _i),
     "swin_wattn_set_fwd_kernel": ([_vp, _i], _i),
     "swin_wattn_fwd_kernel": ([_vp], _i),
@@ -279,6 +292,199 @@ def proj_residual(o, wp, bp, residual, y=None, status=None, stream=None):
     if rc != OK:
         raise SwinWAttnError("swin_wattn_proj_residual", rc)
     return y
+
+
+def swin_wattn_linear(x_ptr, w_ptr, b_ptr, residual_ptr, y_ptr, pre_ptr, tokens, K, N, act, status_ptr, stream):
+    return load().swin_wattn_linear(x_ptr, w_ptr, b_ptr, residual_ptr, y_ptr, pre_ptr, tokens, K, N, act, status_ptr,
+                                    stream)
+
+
+def swin_wattn_linear_bwd_data(dy_ptr, w_ptr, pre_ptr, dx_ptr, tokens, K, N, act, status_ptr, stream):
+    return load().swin_wattn_linear_bwd_data(dy_ptr, w_ptr, pre_ptr, dx_ptr, tokens, K, N, act, status_ptr, stream)
+
+
+def swin_wattn_linear_bwd_weight_workspace_bytes(tokens, K, N):
+    return int(load().swin_wattn_linear_bwd_weight_workspace_bytes(tokens, K, N))
+
+
+def swin_wattn_linear_bwd_weight(dy_ptr, x_ptr, dw_ptr, db_ptr, tokens, K, N, dtype, accumulate, workspace_ptr,
+                                 workspace_bytes, status_ptr, stream):
+    return load().swin_wattn_linear_bwd_weight(dy_ptr, x_ptr, dw_ptr, db_ptr, tokens, K, N, dtype, accumulate,
+                                               workspace_ptr, workspace_bytes, status_ptr, stream)
+
+
+def swin_wattn_orthogonalize_workspace_bytes(count, rows, cols):
+    return int(load().swin_wattn_orthogonalize_workspace_bytes(count, rows, cols))
+
+
+def swin_wattn_orthogonalize(g_ptr, out_ptr, count, rows, cols, dtype, steps, eps, scale, workspace_ptr,
+                             workspace_bytes, status_ptr, stream):
+    return load().swin_wattn_orthogonalize(g_ptr, out_ptr, count, rows, cols, dtype, steps, eps, scale, workspace_ptr,
+                                           workspace_bytes, status_ptr, stream)
+
+
+def _tensor(name, t, shape, dtypes, device):
+    """Check one operand of the MLP's products and the weight update: a contiguous CUDA
+    tensor of the given shape, one of the given dtypes, on `device`."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+def _device_of(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} is not a CUDA tensor")
+    return t.device
+
+
+def _call_on(device, where, fn, stream, status):
+    """fn(stream handle, status pointer) with `device` current, on `stream` or that device's
+    current stream; raises on an error status."""
+    import torch
+    if status is not None:
+        _tensor("status", status, (1,), (torch.int32,), device)
+    with torch.cuda.device(device):
+        s = stream if stream is not None else torch.cuda.current_stream(device)
+        rc = fn(s.cuda_stream, _ptr(status))
+    if rc != OK:
+        raise SwinWAttnError(where, rc)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _empty(shape, dtype, device, stream):
+    """A tensor of `stream`'s own memory pool (of the device's current stream without one),
+    so that it may be used and freed in that stream's order."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _act_code(act):
+    code = ACTIVATIONS.get(act, act) if isinstance(act, str) else act
+    if code not in ACTIVATIONS.values():
+        raise ValueError(f"unknown activation {act!r}: one of {sorted(ACTIVATIONS)} or an ACT_ code")
+    return int(code)
+
+
+def linear(x, w, b=None, act=ACT_NONE, residual=None, y=None, pre=None, status=None, stream=None):
+    """residual + act(x W^T + b) over the last axis of the bf16 CUDA tensor x [..., K] with
+    W [N, K] bf16 and b [N] fp32 (or None), into a bf16 [..., N] tensor (allocated here when
+    not given; it may be the residual itself). act: "none", "relu", "gelu", "gelu_tanh",
+    "silu" or an ACT_ code. pre, a bf16 [..., N] tensor, receives x W^T + b for the backward."""
+    import torch
+    dev, bf16 = _device_of("x", x), (torch.bfloat16,)
+    code = _act_code(act)
+    if w.dim() != 2:
+        raise ValueError(f"w has {w.dim()} dimensions, not 2")
+    N, K = w.shape
+    lead = x.shape[:-1]
+    _tensor("x", x, lead + (K,), bf16, dev)
+    _tensor("w", w, (N, K), bf16, dev)
+    if b is not None:
+        _tensor("b", b, (N,), (torch.float32,), dev)
+    if y is None:
+        y = _empty(lead + (N,), torch.bfloat16, dev, stream)
+    for name, t in (("residual", residual), ("y", y), ("pre", pre)):
+        if t is not None:
+            _tensor(name, t, lead + (N,), bf16, dev)
+    _call_on(dev, "swin_wattn_linear",
+             lambda s, st: swin_wattn_linear(x.data_ptr(), w.data_ptr(), _ptr(b), _ptr(residual), y.data_ptr(),
+                                             _ptr(pre), lead.numel(), K, N, code, st, s), stream, status)
+    return y
+
+
+def linear_bwd_data(dy, w, pre=None, act=ACT_NONE, dx=None, status=None, stream=None):
+    """(dy W) * act'(pre) for dy [..., N] and W [N, K], into a bf16 [..., K] tensor (allocated
+    here when not given; it may be pre itself): with act "none" the gradient of the product's
+    input, else of the pre-activation [..., K] whose activation that input was."""
+    import torch
+    dev, bf16 = _device_of("dy", dy), (torch.bfloat16,)
+    code = _act_code(act)
+    if w.dim() != 2:
+        raise ValueError(f"w has {w.dim()} dimensions, not 2")
+    N, K = w.shape
+    lead = dy.shape[:-1]
+    _tensor("dy", dy, lead + (N,), bf16, dev)
+    _tensor("w", w, (N, K), bf16, dev)
+    if code != ACT_NONE and pre is None:
+        raise ValueError("an activation needs its pre-activation: pre is None")
+    if dx is None:
+        dx = _empty(lead + (K,), torch.bfloat16, dev, stream)
+    for name, t in (("pre", pre), ("dx", dx)):
+        if t is not None:
+            _tensor(name, t, lead + (K,), bf16, dev)
+    _call_on(dev, "swin_wattn_linear_bwd_data",
+             lambda s, st: swin_wattn_linear_bwd_data(dy.data_ptr(), w.data_ptr(), _ptr(pre), dx.data_ptr(),
+                                                      lead.numel(), K, N, code, st, s), stream, status)
+    return dx
+
+
+def linear_bwd_weight(dy, x, dw=None, db=None, accumulate=False, workspace=None, status=None, stream=None):
+    """dW = dy^T x [N, K] and db = the sum of dy over the tokens, for dy [..., N] and
+    x [..., K]. dw (fp32 or bf16) and db (fp32) are the tensors to write, or with accumulate
+    to add to; without dw both are allocated here, in fp32; with dw alone there is no db.
+    workspace: a uint8 tensor of swin_wattn_linear_bwd_weight_workspace_bytes (allocated here
+    when not given). Returns (dw, db)."""
+    import torch
+    dev, bf16 = _device_of("dy", dy), (torch.bfloat16,)
+    lead, N, K = dy.shape[:-1], dy.shape[-1], x.shape[-1]
+    _tensor("dy", dy, lead + (N,), bf16, dev)
+    _tensor("x", x, lead + (K,), bf16, dev)
+    if dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs the dw to add to")
+        dw = _empty((N, K), torch.float32, dev, stream)
+        db = _empty((N,), torch.float32, dev, stream) if db is None else db
+    _tensor("dw", dw, (N, K), (torch.float32, torch.bfloat16), dev)
+    if db is not None:
+        _tensor("db", db, (N,), (torch.float32,), dev)
+    tokens = lead.numel()
+    if workspace is None:
+        workspace = _empty((max(swin_wattn_linear_bwd_weight_workspace_bytes(tokens, K, N), 1),), torch.uint8, dev,
+                           stream)
+    _tensor("workspace", workspace, (workspace.numel(),), (torch.uint8,), dev)
+    code = FP32 if dw.dtype == torch.float32 else BF16
+    _call_on(dev, "swin_wattn_linear_bwd_weight",
+             lambda s, st: swin_wattn_linear_bwd_weight(dy.data_ptr(), x.data_ptr(), dw.data_ptr(), _ptr(db), tokens,
+                                                        K, N, code, int(bool(accumulate)), workspace.data_ptr(),
+                                                        workspace.numel(), st, s), stream, status)
+    return dw, db
+
+
+def orthogonalize(g, steps=5, eps=1e-7, scale=1.0, out=None, workspace=None, status=None, stream=None):
+    """scale * X after `steps` Newton-Schulz steps from X = G / (|G| + eps) for each matrix of
+    the fp32 or bf16 CUDA tensor g [rows, cols] or [count, rows, cols], into a bf16 tensor of
+    its shape (allocated here when not given). workspace: a uint8 tensor of
+    swin_wattn_orthogonalize_workspace_bytes (allocated here when not given)."""
+    import torch
+    dev = _device_of("g", g)
+    if g.dim() not in (2, 3):
+        raise ValueError(f"g has {g.dim()} dimensions, not 2 or 3")
+    _tensor("g", g, g.shape, (torch.float32, torch.bfloat16), dev)
+    count, (rows, cols) = (1 if g.dim() == 2 else g.shape[0]), g.shape[-2:]
+    if out is None:
+        out = _empty(g.shape, torch.bfloat16, dev, stream)
+    _tensor("out", out, g.shape, (torch.bfloat16,), dev)
+    if workspace is None:
+        workspace = _empty((max(swin_wattn_orthogonalize_workspace_bytes(count, rows, cols), 1),), torch.uint8, dev,
+                           stream)
+    _tensor("workspace", workspace, (workspace.numel(),), (torch.uint8,), dev)
+    code = FP32 if g.dtype == torch.float32 else BF16
+    _call_on(dev, "swin_wattn_orthogonalize",
+             lambda s, st: swin_wattn_orthogonalize(g.data_ptr(), out.data_ptr(), count, rows, cols, code, int(steps),
+                                                    float(eps), float(scale), workspace.data_ptr(),
+                                                    workspace.numel(), st, s), stream, status)
+    return out
 
 
 def swin_wattn_fwd_fp8(plan, qkv8_ptr, scale_q, scale_k, scale_v, out_ptr, stream):

@@ -47,6 +47,18 @@ cudaError_t proj_residual_launch(const void* o, const void* wp, const float* bp,
                                  int T, int C, int* status, cudaStream_t st);
 cudaError_t bwd_launch(const Plan& pl, const BwdLaunch& L, const void* qkv, const void* dout,
                        void* dqkv, float* dtable, cudaStream_t st);
+cudaError_t linear_launch(const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
+                          int T, int K, int N, int act, int* status, cudaStream_t st);
+cudaError_t linear_bwd_data_launch(const void* dy, const void* w, const void* pre, void* dx, int T, int K, int N,
+                                   int act, int* status, cudaStream_t st);
+size_t linear_bwd_weight_workspace_bytes(int64_t T, int K, int N);
+int linear_bwd_weight_launches(int64_t T, int K, int N);
+cudaError_t linear_bwd_weight_launch(const void* dy, const void* x, void* dw, float* db, int T, int K, int N,
+                                     int dtype, int accumulate, void* workspace, int* status, cudaStream_t st);
+size_t orthogonalize_workspace_bytes(int count, int rows, int cols);
+int orthogonalize_launches(int steps);
+cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, int cols, int dtype, int steps,
+                                 float eps, float scale, void* workspace, int* status, cudaStream_t st);
 }  // namespace swin
 
 // Streams and events of the host-buffer forward's copy/compute pipeline, created on
@@ -92,6 +104,55 @@ int check_device_ptr(const void* ptr, size_t align) {
   if (a.type == cudaMemoryTypeHost && a.devicePointer == ptr) return SWIN_WATTN_OK;
   return SWIN_WATTN_ERR_INVALID_ARG;
 }
+
+// A device pointer, as above, of memory that lies on the current device (or is mapped).
+int check_here(const void* ptr, size_t align) {
+  int rc = check_device_ptr(ptr, align);
+  if (rc != SWIN_WATTN_OK) return rc;
+  cudaPointerAttributes a;
+  int dev = 0;
+  if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  }
+  return a.type == cudaMemoryTypeDevice && a.device != dev ? SWIN_WATTN_ERR_INVALID_ARG : SWIN_WATTN_OK;
+}
+
+// A buffer of a call: its pointer, size and alignment.
+struct Buffer {
+  const void* ptr;
+  uint64_t bytes;
+  size_t align;
+  bool written;
+};
+
+bool overlaps(const Buffer& a, const Buffer& b) {
+  const uint64_t pa = reinterpret_cast<uintptr_t>(a.ptr), pb = reinterpret_cast<uintptr_t>(b.ptr);
+  return pa < pb + b.bytes && pb < pa + a.bytes;
+}
+
+// Every buffer that is given is memory of the current device, and none that is written
+// overlaps another, except buffer `same_a` that is buffer `same_b` itself.
+int check_buffers(const char* where, const Buffer* bufs, int n, int same_a = -1, int same_b = -1) {
+  for (int i = 0; i < n; ++i) {
+    if (bufs[i].ptr == nullptr) continue;
+    const int rc = check_here(bufs[i].ptr, bufs[i].align);
+    if (rc != SWIN_WATTN_OK) return rc;
+  }
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j) {
+      if (bufs[i].ptr == nullptr || bufs[j].ptr == nullptr || !(bufs[i].written || bufs[j].written)) continue;
+      if (i == same_a && j == same_b && bufs[i].ptr == bufs[j].ptr) continue;
+      if (overlaps(bufs[i], bufs[j])) {
+        std::snprintf(g_last_error, sizeof(g_last_error), "%s: overlapping buffers", where);
+        return SWIN_WATTN_ERR_INVALID_ARG;
+      }
+    }
+  return SWIN_WATTN_OK;
+}
+
+bool linear_width(int n) { return n >= 8 && n <= 32768 && n % 8 == 0; }
+bool known_act(int act) { return act >= SWIN_WATTN_ACT_NONE && act <= SWIN_WATTN_ACT_SILU; }
 
 // Live plans. A handle is checked against this set before it is dereferenced, so a
 // destroyed or foreign handle is reported instead of read.
@@ -569,6 +630,111 @@ int swin_wattn_proj_residual(const void* o, const void* w_proj, const float* b_p
                                              reinterpret_cast<cudaStream_t>(stream));
   ++g_launches;
   return e == cudaSuccess ? SWIN_WATTN_OK : cuda_fail(e, "swin_wattn_proj_residual");
+}
+
+int swin_wattn_linear(const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
+                      int tokens, int K, int N, int act, int* status, struct CUstream_st* stream) {
+  if (tokens < 0 || !known_act(act)) return SWIN_WATTN_ERR_INVALID_ARG;
+  if (!linear_width(K) || !linear_width(N)) return SWIN_WATTN_ERR_UNSUPPORTED;
+  if (tokens == 0) return SWIN_WATTN_OK;
+  if (x == nullptr || w == nullptr || y == nullptr) return SWIN_WATTN_ERR_INVALID_ARG;
+  const uint64_t T = (uint64_t)tokens;
+  const Buffer bufs[] = {{x, T * K * 2, 16, false}, {w, (uint64_t)N * K * 2, 16, false}, {b, (uint64_t)N * 4, 4, false},
+                         {residual, T * N * 2, 16, false}, {y, T * N * 2, 16, true}, {pre, T * N * 2, 16, true},
+                         {status, 4, 4, true}};
+  int rc = check_buffers("swin_wattn_linear", bufs, 7, 3, 4);
+  if (rc != SWIN_WATTN_OK) return rc;
+  cudaError_t e = swin::linear_launch(x, w, b, residual, y, pre, tokens, K, N, act, status,
+                                      reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_linear");
+  ++g_launches;
+  return SWIN_WATTN_OK;
+}
+
+int swin_wattn_linear_bwd_data(const void* dy, const void* w, const void* pre, void* dx, int tokens, int K, int N,
+                               int act, int* status, struct CUstream_st* stream) {
+  if (tokens < 0 || !known_act(act)) return SWIN_WATTN_ERR_INVALID_ARG;
+  if (!linear_width(K) || !linear_width(N)) return SWIN_WATTN_ERR_UNSUPPORTED;
+  if (tokens == 0) return SWIN_WATTN_OK;
+  if (act == SWIN_WATTN_ACT_NONE) pre = nullptr;
+  if (dy == nullptr || w == nullptr || dx == nullptr || (act != SWIN_WATTN_ACT_NONE && pre == nullptr))
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  const uint64_t T = (uint64_t)tokens;
+  const Buffer bufs[] = {{dy, T * N * 2, 16, false}, {w, (uint64_t)N * K * 2, 16, false}, {pre, T * K * 2, 16, false},
+                         {dx, T * K * 2, 16, true}, {status, 4, 4, true}};
+  int rc = check_buffers("swin_wattn_linear_bwd_data", bufs, 5, 2, 3);
+  if (rc != SWIN_WATTN_OK) return rc;
+  cudaError_t e = swin::linear_bwd_data_launch(dy, w, pre, dx, tokens, K, N, act, status,
+                                               reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_linear_bwd_data");
+  ++g_launches;
+  return SWIN_WATTN_OK;
+}
+
+size_t swin_wattn_linear_bwd_weight_workspace_bytes(int tokens, int K, int N) {
+  if (tokens < 0 || !linear_width(K) || !linear_width(N)) return 0;
+  return swin::linear_bwd_weight_workspace_bytes(tokens, K, N);
+}
+
+int swin_wattn_linear_bwd_weight(const void* dy, const void* x, void* dw, float* db, int tokens, int K, int N,
+                                 int dtype, int accumulate, void* workspace, size_t workspace_bytes, int* status,
+                                 struct CUstream_st* stream) {
+  if (tokens < 0 || (dtype != SWIN_WATTN_FP32 && dtype != SWIN_WATTN_BF16)) return SWIN_WATTN_ERR_INVALID_ARG;
+  if (!linear_width(K) || !linear_width(N)) return SWIN_WATTN_ERR_UNSUPPORTED;
+  if (dw == nullptr || (tokens > 0 && (dy == nullptr || x == nullptr || workspace == nullptr)))
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  if (tokens > 0 && workspace_bytes < swin::linear_bwd_weight_workspace_bytes(tokens, K, N)) {
+    swin::set_last_error("swin_wattn_linear_bwd_weight: workspace smaller than "
+                         "swin_wattn_linear_bwd_weight_workspace_bytes(tokens, K, N)");
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  }
+  const uint64_t T = (uint64_t)tokens;
+  const Buffer bufs[] = {{T ? dy : nullptr, T * N * 2, 16, false}, {T ? x : nullptr, T * K * 2, 16, false},
+                         {dw, (uint64_t)N * K * (dtype == SWIN_WATTN_FP32 ? 4 : 2), 16, true},
+                         {db, (uint64_t)N * 4, 4, true}, {T ? workspace : nullptr, workspace_bytes, 256, true},
+                         {status, 4, 4, true}};
+  int rc = check_buffers("swin_wattn_linear_bwd_weight", bufs, 6);
+  if (rc != SWIN_WATTN_OK) return rc;
+  cudaError_t e = swin::linear_bwd_weight_launch(dy, x, dw, db, tokens, K, N, dtype, accumulate, workspace, status,
+                                                 reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_linear_bwd_weight");
+  g_launches += swin::linear_bwd_weight_launches(tokens, K, N);
+  return SWIN_WATTN_OK;
+}
+
+static bool orthogonalize_sizes(int count, int rows, int cols) {
+  return count >= 0 && count <= 65535 && rows >= 1 && rows <= 16384 && cols >= 1 && cols <= 16384;
+}
+
+size_t swin_wattn_orthogonalize_workspace_bytes(int count, int rows, int cols) {
+  return orthogonalize_sizes(count, rows, cols) ? swin::orthogonalize_workspace_bytes(count, rows, cols) : 0;
+}
+
+int swin_wattn_orthogonalize(const void* g, void* out, int count, int rows, int cols, int dtype, int steps, float eps,
+                             float scale, void* workspace, size_t workspace_bytes, int* status,
+                             struct CUstream_st* stream) {
+  if (count < 0 || (dtype != SWIN_WATTN_FP32 && dtype != SWIN_WATTN_BF16)) return SWIN_WATTN_ERR_INVALID_ARG;
+  if (!(eps > 0.0f) || !std::isfinite(eps) || !std::isfinite(scale) || steps < 1 || steps > 20)
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  if (!orthogonalize_sizes(count, rows, cols)) return SWIN_WATTN_ERR_UNSUPPORTED;
+  if (count == 0) return SWIN_WATTN_OK;
+  if (g == nullptr || out == nullptr || workspace == nullptr) return SWIN_WATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < swin::orthogonalize_workspace_bytes(count, rows, cols)) {
+    swin::set_last_error("swin_wattn_orthogonalize: workspace smaller than "
+                         "swin_wattn_orthogonalize_workspace_bytes(count, rows, cols)");
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  }
+  const uint64_t elements = (uint64_t)count * rows * cols;
+  const size_t elem = dtype == SWIN_WATTN_FP32 ? 4 : 2;
+  const Buffer bufs[] = {{g, elements * elem, elem, false}, {out, elements * 2, 2, true},
+                         {workspace, workspace_bytes, 256, true}, {status, 4, 4, true}};
+  int rc = check_buffers("swin_wattn_orthogonalize", bufs, 4);
+  if (rc != SWIN_WATTN_OK) return rc;
+  cudaError_t e = swin::orthogonalize_launch(g, out, count, rows, cols, dtype, steps, eps, scale, workspace, status,
+                                             reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_orthogonalize");
+  g_launches += swin::orthogonalize_launches(steps);
+  return SWIN_WATTN_OK;
 }
 
 int swin_wattn_set_fwd_kernel(swin_wattn_plan_t plan, int kernel) {

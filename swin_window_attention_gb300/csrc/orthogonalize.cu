@@ -1,0 +1,210 @@
+// A stack of weight updates brought near orthogonal by Newton-Schulz products. Per matrix
+// G (rows x cols):
+//   X = G / (|G|_F + eps);   `steps` times:  A = X X^T,  X <- (a I + b A + c A^2) X;
+//   out = scale X                  (A = X^T X and X <- X (a I + b A + c A^2) when rows > cols)
+// with (a, b, c) = (3.4445, -4.7750, 2.0315): each step applies the odd quintic
+// a s + b s^3 + c s^5 to every singular value s, which takes (0, 1] towards [0.7, 1.2] and
+// stays below 1.21, so U V^T of G = U S V^T is approached with every singular value within
+// that band, without a decomposition.
+//
+// All products run on the engine of product.cuh. Nothing is transposed: for wide matrices
+// the Gram product reads X K-major twice and the update reads X MN-major; for tall ones the
+// Gram product reads X MN-major twice and the update reads it K-major; A and the
+// polynomial B = a I + b A + c A^2 are symmetric.
+//
+// Operands are fp16, not bf16: the entries of X, A and B are bounded (|X| <= 1.21,
+// |A| <= 1.45, |B| < 16), so the exponent range of bf16 is not needed and its 8 significant
+// bits cost eight times the error: on random matrices the result is 1.0e-3 to 1.5e-3
+// (relative 2-norm) from the 64-bit one with fp16 and 0.8e-2 to 1.1e-2 with bf16, where the
+// final rounding to bf16 alone is 1.7e-3. Everything is kept times 2^8, so an entry of X a
+// hundredth of the smallest typical one (1 / sqrt(rows cols) = 3e-4 at 1536 x 6144) is
+// still a normal number, and the largest B stays a tenth of the largest fp16. Products are
+// accumulated in fp32. Singular values far below the largest come out with the error of
+// rounding the large ones' entries (the same is true, eight times worse, in bf16).
+#include "product.cuh"
+
+namespace swin {
+
+namespace {
+
+using prod::Matrix;
+using prod::Params;
+using prod::Tiling;
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kScale = 256.0f;  // of every fp16 matrix held
+constexpr CUtensorMapDataType kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+
+constexpr int kNormThreads = 256;
+constexpr int kNormBlocks = 64;  // partial sums per matrix at most
+
+// Blocks that sum one matrix: 4096 elements each at least.
+int norm_blocks(int64_t elements) { return (int)std::max<int64_t>(1, std::min<int64_t>(kNormBlocks, elements / 4096)); }
+
+__device__ __forceinline__ float load_f32(const float* p) { return *p; }
+__device__ __forceinline__ float load_f32(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// Sum of squares of a block's share of one matrix as two sums, of the values below 2^48
+// and, times 2^-64, of the others, so that neither overflows where the norm does not.
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads) norm_partial_kernel(const T* __restrict__ g, int64_t elements,
+                                                                    float2* __restrict__ partial) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const T* x = g + (int64_t)blockIdx.y * elements;
+  float lo = 0.0f, hi = 0.0f;
+  for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < elements; i += (int64_t)gridDim.x * kNormThreads) {
+    const float v = load_f32(x + i);
+    if (fabsf(v) < 281474976710656.0f) {
+      lo = fmaf(v, v, lo);
+    } else {  // NaN and infinity too
+      const float s = v * 5.421010862427522e-20f;
+      hi = fmaf(s, s, hi);
+    }
+  }
+  __shared__ float2 part[kNormThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo += __shfl_xor_sync(0xffffffffu, lo, o);
+    hi += __shfl_xor_sync(0xffffffffu, hi, o);
+  }
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(lo, hi);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kNormThreads / 32; ++w) {
+      lo += part[w].x;
+      hi += part[w].y;
+    }
+    partial[blockIdx.y * gridDim.x + blockIdx.x] = make_float2(lo, hi);
+  }
+}
+
+// X = G / (|G| + eps), times 2^8, in fp16 rows of ld elements.
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads) normalize_kernel(const T* __restrict__ g, int rows, int cols, int ld,
+                                                                 const float2* __restrict__ partial, int n_partial,
+                                                                 float eps, __half* __restrict__ x) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ float s_inv;
+  if (threadIdx.x < 32) {
+    float lo = 0.0f, hi = 0.0f;
+    for (int i = threadIdx.x; i < n_partial; i += 32) {
+      const float2 v = partial[blockIdx.y * n_partial + i];
+      lo += v.x;
+      hi += v.y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      lo += __shfl_xor_sync(0xffffffffu, lo, o);
+      hi += __shfl_xor_sync(0xffffffffu, hi, o);
+    }
+    if (threadIdx.x == 0) {
+      // |G| of both sums; where the second is not empty the first is added in its scale
+      const float norm = hi == 0.0f ? sqrtf(lo) : sqrtf(hi + lo * 5.421010862427522e-20f * 5.421010862427522e-20f) * 18446744073709551616.0f;
+      s_inv = norm + eps;
+    }
+  }
+  __syncthreads();
+  const float inv = kScale / s_inv;
+  const int64_t elements = (int64_t)rows * cols;
+  const T* gm = g + (int64_t)blockIdx.y * elements;
+  __half* xm = x + (int64_t)blockIdx.y * rows * ld;
+  for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < elements; i += (int64_t)gridDim.x * kNormThreads) {
+    const int r = (int)(i / cols), c = (int)(i - (int64_t)r * cols);
+    xm[(int64_t)r * ld + c] = __float2half_rn(load_f32(gm + i) * inv);
+  }
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+int round8(int n) { return (n + 7) & ~7; }
+
+// Workspace: two copies of X, A, B, the partial sums of squares.
+struct Layout {
+  int m, ldx, lda;
+  size_t x_bytes, a_bytes, total;
+};
+Layout layout(int count, int rows, int cols) {
+  Layout l;
+  l.m = std::min(rows, cols);
+  l.ldx = round8(cols);
+  l.lda = round8(l.m);
+  l.x_bytes = align256((size_t)count * rows * l.ldx * 2);
+  l.a_bytes = align256((size_t)count * l.m * l.lda * 2);
+  l.total = 2 * l.x_bytes + 2 * l.a_bytes + align256((size_t)count * kNormBlocks * sizeof(float2));
+  return l;
+}
+
+template <typename T>
+cudaError_t normalize(const T* g, int count, int rows, int cols, float eps, float2* partial, __half* x, int ld,
+                      cudaStream_t st) {
+  const int64_t elements = (int64_t)rows * cols;
+  const int nb = norm_blocks(elements);
+  cudaError_t e = launch_pdl(norm_partial_kernel<T>, dim3(nb, count), dim3(kNormThreads), 0, st, g, elements, partial);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(normalize_kernel<T>, dim3(nb, count), dim3(kNormThreads), 0, st, g, rows, cols, ld,
+                    (const float2*)partial, nb, eps, x);
+}
+
+}  // namespace
+
+size_t orthogonalize_workspace_bytes(int count, int rows, int cols) { return layout(count, rows, cols).total; }
+int orthogonalize_launches(int steps) { return 2 + 3 * steps; }
+
+cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, int cols, int dtype, int steps,
+                                 float eps, float scale, void* workspace, int* status, cudaStream_t st) {
+  const Layout l = layout(count, rows, cols);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  __half* x[2] = {reinterpret_cast<__half*>(ws), reinterpret_cast<__half*>(ws + l.x_bytes)};
+  __half* gram = reinterpret_cast<__half*>(ws + 2 * l.x_bytes);
+  __half* poly = reinterpret_cast<__half*>(ws + 2 * l.x_bytes + l.a_bytes);
+  float2* partial = reinterpret_cast<float2*>(ws + 2 * l.x_bytes + 2 * l.a_bytes);
+  cudaError_t e = dtype == SWIN_WATTN_FP32
+                      ? normalize(static_cast<const float*>(g), count, rows, cols, eps, partial, x[0], l.ldx, st)
+                      : normalize(static_cast<const __nv_bfloat16*>(g), count, rows, cols, eps, partial, x[0], l.ldx, st);
+  const bool tall = rows > cols;
+  const int m = l.m, n = std::max(rows, cols);
+  const Tiling t_gram = prod::choose_tiling(m, m, n, count, tall, 1, 1);
+  const Tiling t_poly = prod::choose_tiling(m, m, m, count, false, 1, 1);
+  const Tiling t_step = prod::choose_tiling(rows, cols, m, count, !tall, 1, 1);
+  const Matrix A{gram, m, m, l.lda, (int64_t)m * l.lda}, B{poly, m, m, l.lda, (int64_t)m * l.lda};
+  const bool direct = cols % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+  for (int s = 0; s < steps && e == cudaSuccess; ++s) {
+    const Matrix X{x[s & 1], rows, cols, l.ldx, (int64_t)rows * l.ldx};
+    Matrix Y{x[(s + 1) & 1], rows, cols, l.ldx, (int64_t)rows * l.ldx};
+    Params p{};
+    p.status = status;
+    p.M = p.N = m;
+    p.alpha = 1.0f / kScale;  // (2^8 X)(2^8 X)^T = 2^16 A -> 2^8 A
+    prod::Extra none;
+    e = tall ? prod::launch_product<true, true, prod::kEpiStep>(t_gram, p, X, X, A, count, kF16, kF16, none, st)
+             : prod::launch_product<false, false, prod::kEpiStep>(t_gram, p, X, X, A, count, kF16, kF16, none, st);
+    if (e != cudaSuccess) return e;
+    p.alpha = kC / kScale;
+    p.beta = kB;
+    p.diag = kA * kScale;
+    prod::Extra with_a;
+    with_a.aux = &A;
+    e = prod::launch_product<false, false, prod::kEpiStep>(t_poly, p, A, A, B, count, kF16, kF16, with_a, st);
+    if (e != cudaSuccess) return e;
+    Params q{};
+    q.status = status;
+    q.M = rows;
+    q.N = cols;
+    q.alpha = 1.0f / kScale;
+    CUtensorMapDataType out_type = kF16;
+    if (s == steps - 1) {
+      q.alpha = scale / (kScale * kScale);
+      q.to_bf16 = true;
+      out_type = kBf16;
+      Y = Matrix{out, rows, cols, cols, (int64_t)rows * cols};
+      if (!direct) q.raw_out = static_cast<__nv_bfloat16*>(out);
+    }
+    e = tall ? prod::launch_product<false, false, prod::kEpiStep>(t_step, q, X, B, Y, count, kF16, out_type, none, st)
+             : prod::launch_product<false, true, prod::kEpiStep>(t_step, q, B, X, Y, count, kF16, out_type, none, st);
+  }
+  return e;
+}
+
+}  // namespace swin

@@ -1,0 +1,867 @@
+// Batched matrix products on the fifth-generation tensor cores, with the epilogues of a
+// block's MLP, of its gradients and of the weight update:
+//   D[b] (M x N) = A[b] (M x K) B[b]^T (N x K),   A, B 16-bit, fp32 accumulation.
+// Each operand may be stored K-major (rows of K contiguous elements) or MN-major (K rows
+// of M or N contiguous elements): the copy engine brings either into 128-byte-swizzled
+// shared memory as it lies, and the matrix descriptor tells the tensor core which it is,
+// so no operand is ever transposed in memory.
+//
+// One persistent CTA per SM (CG = 1) or one pair of CTAs on two SMs (CG = 2) walks output
+// tiles of CG * 128 rows by NT <= 256 columns:
+// * copy warp: per chunk of 64 along K, the CTA's 128 rows of A and NT / CG rows of B into a
+//   ring of stages;
+// * MMA warp, one thread (of the pair's first CTA): four K16 MMAs a chunk into one of two
+//   tensor-memory accumulators;
+// * eight epilogue warps, two per tensor-memory lane quadrant, taking alternate 32-column
+//   slices: the epilogue's arithmetic in fp32 on a thread's 32 columns of one row, one
+//   rounding, a swizzled staging tile per warp, a TMA store; while the next tile
+//   accumulates. A second operand of the epilogue (residual, pre-activation, ...) arrives
+//   by TMA one slice ahead in the staging tile that the result is written over.
+// A pair (CG = 2) reads each row of B once for 256 rows of A instead of 128: per chunk a CTA
+// brings 128 + NT / 2 rows instead of 128 + NT, which is what the tensor cores need to run
+// at full rate at NT = 256 (shared memory is both filled and read by the chunk).
+// Every wait is bounded (1 s); a wait that runs out sets the caller's status word (when one
+// is given) and the CTA leaves after its copies have landed and its tensor memory is freed.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+#include "tc.cuh"
+
+namespace swin {
+namespace prod {
+
+constexpr int kBM = 128;   // rows of A per CTA
+constexpr int kKC = 64;    // K per chunk: one 128-byte row
+constexpr int kSC = 32;    // columns per epilogue slice
+constexpr int kMaxNT = 256;
+constexpr int kMaxStages = 8;
+constexpr int kEpiWarps = 8, kMMA = 8, kCOPY = 9, kThreads = 320;
+constexpr int kABytes = kBM * 128;
+constexpr uint32_t kSW128 = 2;  // descriptor layout: 128-byte swizzle
+constexpr int kTmemCols = 512;  // two accumulators of up to 256 columns
+
+// Barriers: full and empty per stage, full and free per accumulator, aux loads (three per
+// epilogue warp), the last commit.
+constexpr int kDFull = 2 * kMaxStages, kDFree = kDFull + 2, kAux = kDFree + 2, kDrain = kAux + 3 * kEpiWarps;
+constexpr int kNBar = kDrain + 1;
+
+enum Epi {
+  kEpiAct = 0,     // bf16: aux + act(acc + bias), optionally acc + bias into a second result
+  kEpiSlope = 1,   // bf16: acc * act'(aux)
+  kEpiGrad32 = 2,  // fp32: [old +] acc, optionally the column sums of A^T (sum over K of A)
+  kEpiGrad16 = 3,  // bf16: [aux +] acc, optionally the same sums
+  kEpiStep = 4     // fp16 or bf16: alpha * acc + beta * aux + diag on the diagonal
+};
+
+struct Params {
+  int M, N, NT;
+  int n_mt, n_nt, n_items;  // items: batch * splits * n_mt * n_nt, n fastest
+  int chunks, chunks_per_split, splits;
+  int stages, stage_bytes;
+  int off_out, warp_bytes, off_ones, off_bar;
+  uint32_t idesc, idesc_ones;
+  int act;
+  bool has_aux, has_pre;
+  bool to_bf16;           // kEpiStep: bf16 instead of fp16
+  const float* bias;      // kEpiAct: [N] or null
+  const float* old;       // kEpiGrad32: [M, N] added to the product, or null
+  float* k_sums;          // kEpiGrad*: [splits, M], or null
+  bool add_k_sums;        // the sums are added to what k_sums holds
+  float alpha, beta, diag;
+  __nv_bfloat16* raw_out;  // kEpiStep: plain stores (a row length the copy engine cannot address), or null
+  int* status;
+  uint64_t wait_ns;
+  int fault;
+};
+
+// ---- pairs of CTAs ------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// The address, in the cluster's shared memory, of this CTA's address `addr` in CTA `rank`.
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t mbar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(mbar) : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t mbar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(mbar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(mbar)
+        : "memory");
+}
+__device__ __forceinline__ void store_3d(const CUtensorMap* map, int c0, int c1, int c2, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(map),
+               "r"(c0), "r"(c1), "r"(c2), "r"(src)
+               : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+  else
+    tc::mma_ss(d, a, b, idesc, accumulate);
+}
+// Arrive on the mbarrier (of both CTAs of a pair) when every MMA issued so far has completed.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t mbar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+            mbar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    tc::commit(mbar);
+}
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t dst) {
+  if constexpr (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(dst), "n"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+  } else {
+    tc::tmem_alloc<kTmemCols>(dst);
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc(uint32_t base) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(base), "n"(kTmemCols) : "memory");
+  else
+    tc::tmem_dealloc<kTmemCols>(base);
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t mbar, uint32_t parity, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, tc::mbar_wait(mbar, parity, limit_ns)) != 0;
+}
+
+// ---- activations --------------------------------------------------------------------
+//
+// Every smooth activation here is z * s(z) with s(-z) = 1 - s(z), so with t = |z| and
+// h(t) = s(-t):   act(z) = max(z, 0) - t h(t),   s(z) = z > 0 ? 1 - h : h.
+// This form keeps the relative accuracy of the small tail h and needs no sign handling.
+// * GELU: h(t) = Phi(-t), the normal distribution function. log2 Phi(-t) is close to a
+//   parabola, so h = 2^Q(t) with Q of degree 6, fitted (minimax, iteratively reweighted
+//   least squares) on [0, 6]: |h / Phi(-t) - 1| < 5e-5 there, |t h - t Phi(-t)| < 7e-6
+//   everywhere, a fortieth of a bf16 rounding; six multiply-adds and one exponential where
+//   erff takes some twenty instructions. Q falls monotonically up to t = 12, where
+//   t is cut (t h < 1e-30), which also keeps infinities out of the polynomial.
+// * tanh-GELU: 0.5 (1 + tanh u) = 1 / (1 + exp(-2u)), so h = 1 / (1 + exp(2 u(t))).
+// * SiLU: h = 1 / (1 + exp(t)).
+// t is cut at 100 there: exp overflows to infinity and h is 0 long before.
+// The maximum propagates NaN, so a NaN input gives NaN.
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// z > 0 ? 1 : 0, subnormal z included (an ordinary comparison here is built to flush them).
+__device__ __forceinline__ float step01(float z) {
+  float r;
+  asm("set.gt.f32.f32 %0, %1, 0f00000000;\n" : "=f"(r) : "f"(z));
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+
+constexpr float kGeluCut = 12.0f, kSigmoidCut = 100.0f;
+constexpr float kTanhA = 0.7978845608028654f, kTanhB = 0.044715f;  // u(z) = A (z + B z^3)
+
+// t = min(|z|, cut) and h(t), for two values.
+template <int ACT>
+__device__ __forceinline__ void act_tail(float2 z, float2& t, float2& h) {
+  if constexpr (ACT == SWIN_WATTN_ACT_GELU) {
+    t = make_float2(fminf(fabsf(z.x), kGeluCut), fminf(fabsf(z.y), kGeluCut));
+    float2 q = splat(2.29900633712532e-05f);
+    q = __ffma2_rn(q, t, splat(-0.0006111000548116863f));
+    q = __ffma2_rn(q, t, splat(0.007195565849542618f));
+    q = __ffma2_rn(q, t, splat(-0.05118533596396446f));
+    q = __ffma2_rn(q, t, splat(-0.46127191185951233f));
+    q = __ffma2_rn(q, t, splat(-1.1501742601394653f));
+    q = __ffma2_rn(q, t, splat(-1.000064730644226f));
+    h = make_float2(fast_exp2(q.x), fast_exp2(q.y));
+  } else {
+    t = make_float2(fminf(fabsf(z.x), kSigmoidCut), fminf(fabsf(z.y), kSigmoidCut));
+    float2 e;  // the exponent, in powers of two
+    if constexpr (ACT == SWIN_WATTN_ACT_GELU_TANH) {
+      constexpr float kA2 = 2.0f * kTanhA * kLog2e;
+      e = __fmul2_rn(t, __ffma2_rn(__fmul2_rn(t, t), splat(kA2 * kTanhB), splat(kA2)));
+    } else {
+      e = __fmul2_rn(t, splat(kLog2e));
+    }
+    h = make_float2(fast_rcp(1.0f + fast_exp2(e.x)), fast_rcp(1.0f + fast_exp2(e.y)));
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 act_value(float2 z) {
+  if constexpr (ACT == SWIN_WATTN_ACT_NONE) return z;
+  const float2 p = make_float2(max_nan(z.x, 0.0f), max_nan(z.y, 0.0f));
+  if constexpr (ACT == SWIN_WATTN_ACT_RELU) return p;
+  float2 t, h;
+  act_tail<ACT>(z, t, h);
+  return __ffma2_rn(make_float2(-t.x, -t.y), h, p);
+}
+
+// act'(z) = s + z s'(z):  GELU: z phi(z), phi the normal density; the others:
+// s' = s (1 - s) (2 u)', and s (1 - s) = h (1 - h).
+template <int ACT>
+__device__ __forceinline__ float2 act_slope(float2 z) {
+  if constexpr (ACT == SWIN_WATTN_ACT_RELU) return make_float2(step01(z.x), step01(z.y));
+  float2 t, h;
+  act_tail<ACT>(z, t, h);
+  float2 g;  // |z| s'(z)
+  if constexpr (ACT == SWIN_WATTN_ACT_GELU) {
+    // phi(t) = 2^(-t^2 log2(e) / 2 - log2 sqrt(2 pi))
+    const float2 e = __ffma2_rn(__fmul2_rn(t, t), splat(-0.5f * kLog2e), splat(-1.3257480647361595f));
+    g = __fmul2_rn(t, make_float2(fast_exp2(e.x), fast_exp2(e.y)));
+  } else {
+    g = __fmul2_rn(t, __fmul2_rn(h, fsub2(splat(1.0f), h)));
+    if constexpr (ACT == SWIN_WATTN_ACT_GELU_TANH)
+      g = __fmul2_rn(g, __ffma2_rn(__fmul2_rn(t, t), splat(6.0f * kTanhA * kTanhB), splat(2.0f * kTanhA)));
+  }
+  // z > 0: 1 - h + g; z < 0: h - g; a NaN stays one
+  return make_float2(z.x > 0.0f ? 1.0f - (h.x - g.x) : (z.x <= 0.0f ? h.x - g.x : z.x),
+                     z.y > 0.0f ? 1.0f - (h.y - g.y) : (z.y <= 0.0f ? h.y - g.y : z.y));
+}
+
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Bytes of one staging tile (32 rows x 32 columns) of an epilogue.
+__host__ __device__ constexpr int tile_bytes(int epi) { return epi == kEpiGrad32 ? 4096 : 2048; }
+// Staging tiles a warp rotates through: three 16-bit ones (with a second operand the next
+// slice's load, this slice and the last store's read are in flight together), two fp32 ones.
+__host__ __device__ constexpr int out_tiles(int epi) { return epi == kEpiGrad32 ? 2 : 3; }
+
+template <int CG, bool AMN, bool BMN, int EPI>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
+                   const __grid_constant__ CUtensorMap out_map, const __grid_constant__ CUtensorMap aux_map,
+                   const __grid_constant__ CUtensorMap pre_map, const Params p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  pdl_launch_dependents();
+  const uint32_t smem0 = smem_u32(smem);
+  const uint32_t bar0 = smem0 + p.off_bar;
+  auto full_bar = [&](int st) { return bar0 + 8 * st; };
+  auto empty_bar = [&](int st) { return bar0 + 8 * (kMaxStages + st); };
+  auto dfull_bar = [&](int b) { return bar0 + 8 * (kDFull + b); };
+  auto dfree_bar = [&](int b) { return bar0 + 8 * (kDFree + b); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + p.off_bar + 8 * kNBar);
+  const int stages = p.stages;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = CG == 2 ? (int)cluster_rank() : 0;
+  const int group = blockIdx.x / CG, n_groups = gridDim.x / CG;
+
+  // Work item -> first row and column of this CTA's part, first and last chunk, batch or split.
+  struct Item {
+    int m0, n0, c0, c1, nt, b, split;
+  };
+  auto decode = [&](int it) {
+    Item w;
+    w.nt = it % p.n_nt;
+    int r = it / p.n_nt;
+    const int mt = r % p.n_mt;
+    r /= p.n_mt;
+    w.split = r % p.splits;
+    w.b = r / p.splits;
+    w.m0 = (mt * CG + rank) * kBM;
+    w.n0 = w.nt * p.NT;
+    w.c0 = w.split * p.chunks_per_split;
+    w.c1 = min(w.c0 + p.chunks_per_split, p.chunks);
+    return w;
+  };
+
+  if (warp == kMMA) tmem_alloc<CG>(smem_u32(tmem_slot));
+  if (tid == 0) {
+    for (int st = 0; st < stages; ++st) {
+      tc::mbar_init(full_bar(st), 1);
+      tc::mbar_init(empty_bar(st), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(dfull_bar(b), 1);
+      tc::mbar_init(dfree_bar(b), kEpiWarps * CG);
+    }
+    for (int b = 0; b < 3 * kEpiWarps; ++b) tc::mbar_init(bar0 + 8 * (kAux + b), 1);
+    tc::mbar_init(bar0 + 8 * kDrain, 1);
+    tc::mbar_init_fence();
+  }
+  if constexpr (EPI == kEpiGrad32 || EPI == kEpiGrad16) {
+    // 16 rows x 16 of K, all ones (any layout): the B operand that sums A over K
+    if (tid < 128) reinterpret_cast<uint32_t*>(smem + p.off_ones)[tid] = 0x3F803F80u;
+    tc::fence_proxy_async();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  // The prologue above touches only this CTA's shared and tensor memory, so it may overlap
+  // the previous kernel on the stream; every global access comes after this wait.
+  pdl_wait();
+  int bad = 0;
+
+  if (warp == kCOPY) {
+    if (lane == 0) {
+      int st = 0;
+      uint32_t ph = 0, first = 1;
+      for (int it = group; it < p.n_items && !bad; it += n_groups) {
+        const Item w = decode(it);
+        const int nb0 = w.n0 + rank * (p.NT / CG);
+        for (int c = w.c0; c < w.c1; ++c) {
+          if (!first && !tc::mbar_wait(empty_bar(st), ph ^ 1, p.wait_ns)) {
+            bad = 1;
+            break;
+          }
+          const uint32_t base = smem0 + st * p.stage_bytes;
+          // a pair's loads all complete on the first CTA's barrier
+          const uint32_t fb = CG == 2 ? map_to_rank(full_bar(st), 0) : full_bar(st);
+          if (rank == 0) tc::mbar_expect_tx(full_bar(st), CG * p.stage_bytes);
+          if constexpr (AMN) {
+#pragma unroll
+            for (int j = 0; j < kBM / 64; ++j)
+              load_3d<CG>(base + j * 8192, &a_map, w.m0 + 64 * j, c * kKC, w.b, fb);
+          } else {
+            load_3d<CG>(base, &a_map, c * kKC, w.m0, w.b, fb);
+          }
+          if constexpr (BMN) {
+            for (int j = 0; j < p.NT / (64 * CG); ++j)
+              load_3d<CG>(base + kABytes + j * 8192, &b_map, nb0 + 64 * j, c * kKC, w.b, fb);
+          } else {
+            load_3d<CG>(base + kABytes, &b_map, c * kKC, nb0, w.b, fb);
+          }
+          if (++st == stages) {
+            st = 0;
+            ph ^= 1;
+            first = 0;
+          }
+        }
+      }
+      // every load issued has landed before the CTA leaves (the second CTA of a pair is held
+      // by the cluster barrier below until the first has seen its bytes too)
+      if (rank == 0)
+        for (int s2 = 0; s2 < (first ? st : stages); ++s2)
+          tc::mbar_wait(full_bar(s2), s2 < st ? ph : ph ^ 1, p.wait_ns);
+    }
+    __syncwarp();
+  } else if (warp == kMMA) {
+    if (rank == 0) {
+      int st = 0, g = 0;
+      uint32_t ph = 0;
+      bool prev_ones = false;
+      for (int it = group; it < p.n_items && !bad; it += n_groups, ++g) {
+        const Item w = decode(it);
+        const int buf = g & 1;
+        const bool ones = (EPI == kEpiGrad32 || EPI == kEpiGrad16) && p.k_sums != nullptr && w.nt == 0;
+        if (g >= 2 && !warp_wait(dfree_bar(buf), ((g >> 1) - 1) & 1, p.wait_ns)) {
+          bad = 1;
+          break;
+        }
+        // the sums of a first-column tile lie in the other accumulator's first columns: that
+        // one's epilogue has to be over before, and this tile's before the next begins
+        if (g >= 1 && (ones || prev_ones) && !warp_wait(dfree_bar(buf ^ 1), ((g - 1) >> 1) & 1, p.wait_ns)) {
+          bad = 1;
+          break;
+        }
+        prev_ones = ones;
+        for (int c = w.c0; c < w.c1; ++c) {
+          if (!warp_wait(full_bar(st), ph, p.wait_ns)) {
+            bad = 1;
+            break;
+          }
+          if (lane == 0) {
+            tc::fence_after_sync();
+            const uint32_t a = smem0 + st * p.stage_bytes, b = a + kABytes;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              // K-major: 32 bytes further in the 128-byte row; MN-major: 16 rows further,
+              // blocks of 64 of M or N 8192 bytes apart
+              const uint64_t ad = AMN ? tc::sdesc(a + kk * 2048, 8192, 1024, kSW128) : tc::sdesc(a + kk * 32, 16, 1024, kSW128);
+              const uint64_t bd = BMN ? tc::sdesc(b + kk * 2048, 8192, 1024, kSW128) : tc::sdesc(b + kk * 32, 16, 1024, kSW128);
+              mma<CG>(tmem + buf * kMaxNT, ad, bd, p.idesc, c > w.c0 || kk > 0);
+              if (ones)
+                mma<CG>(tmem + (buf ^ 1) * kMaxNT, ad, tc::sdesc(smem0 + p.off_ones, 128, 256), p.idesc_ones,
+                        c > w.c0 || kk > 0);
+            }
+            commit<CG>(empty_bar(st));
+#ifdef SWIN_WATTN_FAULT_INJECTION
+            if (!(p.fault == kFaultGemm && g == 0))
+#endif
+              if (c == w.c1 - 1) commit<CG>(dfull_bar(buf));
+          }
+          __syncwarp();
+          if (++st == stages) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      // every MMA issued has completed before the tensor memory is released
+      if (lane == 0) commit<CG>(bar0 + 8 * kDrain);
+      __syncwarp();
+      if (!warp_wait(bar0 + 8 * kDrain, 0, p.wait_ns)) bad = 1;
+    }
+  } else {
+    // ==== epilogue warps ================================================================
+    constexpr int kTile = tile_bytes(EPI), NB = out_tiles(EPI);
+    const int quad = warp & 3, parity = warp >> 2;
+    const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
+    unsigned char* wstage = smem + p.off_out + warp * p.warp_bytes;
+    unsigned char* wpre = wstage + NB * kTile;                        // kEpiAct: two more tiles, if kept
+    float* wbias = reinterpret_cast<float*>(wstage + p.warp_bytes - 512);  // kEpiAct: 4 slices x 32
+    const uint32_t aux0 = bar0 + 8 * (kAux + 3 * warp);
+    constexpr bool kHasAux = EPI != kEpiGrad32;
+    // the next slice whose second operand is to be requested
+    int nx_it = group, nx_c0 = parity * kSC, issued = 0;
+    auto request_next = [&]() {
+      while (nx_it < p.n_items) {
+        const Item w = decode(nx_it);
+        const int row0 = w.m0 + quad * 32;
+        if (row0 < p.M && nx_c0 < p.NT && w.n0 + nx_c0 < p.N) {
+          if (lane == 0) {
+            const uint32_t rb = aux0 + 8 * (issued % 3);
+            tc::mbar_expect_tx(rb, kTile);
+            load_3d<1>(smem_u32(wstage + (issued % 3) * kTile), &aux_map, w.n0 + nx_c0, row0, w.b, rb);
+          }
+          ++issued;
+          nx_c0 += 2 * kSC;
+          return;
+        }
+        nx_it += n_groups;
+        nx_c0 = parity * kSC;
+      }
+    };
+    if constexpr (kHasAux)
+      if (p.has_aux) request_next();
+    int g = 0, m = 0;  // tiles, slices of this warp
+    for (int it = group; it < p.n_items && !bad; it += n_groups, ++g) {
+      const Item w = decode(it);
+      const int buf = g & 1;
+      const int row0 = w.m0 + quad * 32, row = row0 + lane;
+      if constexpr (EPI == kEpiAct) {
+        // the bias of the warp's slices, kept in its corner of shared memory for broadcasts
+        float bt[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = w.n0 + parity * kSC + 2 * kSC * i + lane;
+          bt[i] = p.bias != nullptr && c < p.N ? __ldg(p.bias + c) : 0.0f;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wbias[32 * i + lane] = bt[i];
+        __syncwarp();
+      }
+      if (!warp_wait(dfull_bar(buf), (g >> 1) & 1, p.wait_ns)) {
+        bad = 1;
+        break;
+      }
+      tc::fence_after_sync();
+      if constexpr (EPI == kEpiGrad32 || EPI == kEpiGrad16) {
+        if (p.k_sums != nullptr && w.nt == 0 && parity == 0 && row0 < p.M) {
+          uint32_t s;
+          tc::ld1_nowait(trow + (buf ^ 1) * kMaxNT, s);
+          tc::wait_ld_then();
+          tc::dep1(s);
+          if (row < p.M) {
+            float* d = p.k_sums + (int64_t)w.split * p.M + row;
+            *d = p.add_k_sums ? *d + __uint_as_float(s) : __uint_as_float(s);
+          }
+        }
+      }
+      int si = 0;
+      for (int c0 = parity * kSC; row0 < p.M && c0 < p.NT && w.n0 + c0 < p.N; c0 += 2 * kSC, ++m, ++si) {
+        unsigned char* so = wstage + (m % NB) * kTile;
+        // the tiles written next (this slice's, its second result's, the next slice's load)
+        // have been read by the stores that held them
+        if ((kHasAux && p.has_aux) || (EPI == kEpiAct && p.has_pre)) {
+          if (m >= 2) {
+            if (lane == 0) tc::bulk_wait_read<1>();
+            __syncwarp();
+          }
+          if (kHasAux && p.has_aux) request_next();
+        } else if (m >= NB) {
+          if (lane == 0) tc::bulk_wait_read<NB - 1>();
+          __syncwarp();
+        }
+        uint32_t a[32];
+        tc::ld32_wait(trow + buf * kMaxNT + c0, a);
+        if (kHasAux && p.has_aux) {
+          if (!warp_wait(aux0 + 8 * (m % 3), (m / 3) & 1, p.wait_ns)) {
+            bad = 1;
+            break;
+          }
+        }
+        if constexpr (EPI == kEpiGrad32) {
+          const float* old = p.old != nullptr && row < p.M ? p.old + (int64_t)row * p.N + w.n0 + c0 : nullptr;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float4 v = make_float4(__uint_as_float(a[4 * c]), __uint_as_float(a[4 * c + 1]),
+                                   __uint_as_float(a[4 * c + 2]), __uint_as_float(a[4 * c + 3]));
+            if (old != nullptr && w.n0 + c0 + 4 * c < p.N) {
+              const float4 o = *reinterpret_cast<const float4*>(old + 4 * c);
+              v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+            }
+            *reinterpret_cast<float4*>(so + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
+          }
+        } else {
+          unsigned char* sr = so + lane * 64;
+          const int sw = (lane >> 1) & 3;
+          auto at = [&](unsigned char* base, int c) { return reinterpret_cast<uint4*>(base + ((c ^ sw) << 4)); };
+          auto pair = [&](int e) { return make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])); };
+          if constexpr (EPI == kEpiAct) {
+            unsigned char* sp = wpre + (m & 1) * kTile + lane * 64;
+            auto run = [&](auto act) {
+              constexpr int ACT = decltype(act)::value;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float4 b0 = reinterpret_cast<const float4*>(wbias + 32 * si)[2 * c];
+                const float4 b1 = reinterpret_cast<const float4*>(wbias + 32 * si)[2 * c + 1];
+                const float2 bb[4] = {make_float2(b0.x, b0.y), make_float2(b0.z, b0.w), make_float2(b1.x, b1.y),
+                                      make_float2(b1.z, b1.w)};
+                uint4 r = make_uint4(0, 0, 0, 0);
+                if (p.has_aux) r = *at(sr, c);
+                const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
+                uint32_t o[4], z16[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const float2 z = __fadd2_rn(pair(8 * c + 2 * q), bb[q]);
+                  z16[q] = pack_bf16(z.x, z.y);
+                  float2 y = act_value<ACT>(z);
+                  if (p.has_aux) y = __fadd2_rn(y, unpack_bf16(rr[q]));
+                  o[q] = pack_bf16(y.x, y.y);
+                }
+                *at(sr, c) = make_uint4(o[0], o[1], o[2], o[3]);
+                if (p.has_pre) *at(sp, c) = make_uint4(z16[0], z16[1], z16[2], z16[3]);
+              }
+            };
+            switch (p.act) {
+              case SWIN_WATTN_ACT_RELU: run(std::integral_constant<int, SWIN_WATTN_ACT_RELU>()); break;
+              case SWIN_WATTN_ACT_GELU: run(std::integral_constant<int, SWIN_WATTN_ACT_GELU>()); break;
+              case SWIN_WATTN_ACT_GELU_TANH: run(std::integral_constant<int, SWIN_WATTN_ACT_GELU_TANH>()); break;
+              case SWIN_WATTN_ACT_SILU: run(std::integral_constant<int, SWIN_WATTN_ACT_SILU>()); break;
+              default: run(std::integral_constant<int, SWIN_WATTN_ACT_NONE>()); break;
+            }
+          } else if constexpr (EPI == kEpiSlope) {
+            auto run = [&](auto act) {
+              constexpr int ACT = decltype(act)::value;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t o[4];
+                if constexpr (ACT == SWIN_WATTN_ACT_NONE) {
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) o[q] = pack_bf16(pair(8 * c + 2 * q).x, pair(8 * c + 2 * q).y);
+                } else {
+                  const uint4 r = *at(sr, c);
+                  const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {
+                    const float2 y = __fmul2_rn(pair(8 * c + 2 * q), act_slope<ACT>(unpack_bf16(rr[q])));
+                    o[q] = pack_bf16(y.x, y.y);
+                  }
+                }
+                *at(sr, c) = make_uint4(o[0], o[1], o[2], o[3]);
+              }
+            };
+            switch (p.act) {
+              case SWIN_WATTN_ACT_RELU: run(std::integral_constant<int, SWIN_WATTN_ACT_RELU>()); break;
+              case SWIN_WATTN_ACT_GELU: run(std::integral_constant<int, SWIN_WATTN_ACT_GELU>()); break;
+              case SWIN_WATTN_ACT_GELU_TANH: run(std::integral_constant<int, SWIN_WATTN_ACT_GELU_TANH>()); break;
+              case SWIN_WATTN_ACT_SILU: run(std::integral_constant<int, SWIN_WATTN_ACT_SILU>()); break;
+              default: run(std::integral_constant<int, SWIN_WATTN_ACT_NONE>()); break;
+            }
+          } else if constexpr (EPI == kEpiGrad16) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint4 r = make_uint4(0, 0, 0, 0);
+              if (p.has_aux) r = *at(sr, c);
+              const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
+              uint32_t o[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float2 y = __fadd2_rn(pair(8 * c + 2 * q), unpack_bf16(rr[q]));
+                o[q] = pack_bf16(y.x, y.y);
+              }
+              *at(sr, c) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          } else {
+            const bool on_diag = w.n0 + c0 == row0;  // both are multiples of 32
+            const float dg = on_diag ? p.diag : 0.0f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint4 r = make_uint4(0, 0, 0, 0);
+              if (p.has_aux) r = *at(sr, c);
+              const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
+              uint32_t o[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int e = 8 * c + 2 * q;
+                const float2 d2 = make_float2(lane == e ? dg : 0.0f, lane == e + 1 ? dg : 0.0f);
+                const float2 y = __ffma2_rn(pair(e), splat(p.alpha), __ffma2_rn(unpack_f16(rr[q]), splat(p.beta), d2));
+                o[q] = p.to_bf16 ? pack_bf16(y.x, y.y) : pack_f16(y.x, y.y);
+              }
+              *at(sr, c) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+        }
+        if (EPI == kEpiStep && p.raw_out != nullptr) {
+          __syncwarp();
+          const int col = w.n0 + c0 + lane;
+          if (col < p.N)
+            for (int r = 0; r < 32 && row0 + r < p.M; ++r)
+              p.raw_out[((int64_t)w.b * p.M + row0 + r) * p.N + col] = *reinterpret_cast<const __nv_bfloat16*>(
+                  so + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+          __syncwarp();
+          continue;
+        }
+        tc::fence_proxy_async();  // the staging tile to the copy engine
+        __syncwarp();
+        if (lane == 0) {
+          store_3d(&out_map, w.n0 + c0, row0, EPI == kEpiGrad32 ? w.split : w.b, smem_u32(so));
+          if (EPI == kEpiAct && p.has_pre)
+            store_3d(&pre_map, w.n0 + c0, row0, w.b, smem_u32(wpre + (m & 1) * kTile));
+          tc::bulk_commit();
+        }
+      }
+      if (bad) break;
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2)
+          arrive_cluster(map_to_rank(dfree_bar(buf), 0));
+        else
+          tc::mbar_arrive(dfree_bar(buf));
+      }
+    }
+    if constexpr (kHasAux) {
+      // after a timeout: the loads still in flight land before the CTA leaves
+      for (int q = m; q < issued; ++q) warp_wait(aux0 + 8 * (q % 3), (q / 3) & 1, p.wait_ns);
+    }
+    if (lane == 0) tc::bulk_wait_all();
+  }
+  if (bad && p.status != nullptr) atomicOr(p.status, 1);
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();
+  if (warp == kMMA) tmem_dealloc<CG>(tmem);
+}
+
+// ---- host side ------------------------------------------------------------------------
+
+// One GB300: 152 SMs, 76 pairs. The tile choice is made for that and does not ask the
+// device, so that workspace sizes depend on the shape alone.
+constexpr int kSms = 152;
+
+// A matrix stack [batch, rows, cols], row-major, `ld` elements from row to row.
+struct Matrix {
+  const void* ptr;
+  int64_t rows, cols, ld, batch_stride;
+};
+
+inline cudaError_t encode_3d(CUtensorMap* map, const Matrix& x, int batch, CUtensorMapDataType type, int elem,
+                             int box_cols, int box_rows, CUtensorMapSwizzle swz, CUtensorMapL2promotion l2) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder_fn();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows, (cuuint64_t)batch};
+  const cuuint64_t strides[2] = {(cuuint64_t)x.ld * elem, (cuuint64_t)(batch > 1 ? x.batch_stride : x.ld) * elem};
+  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return encode(map, type, 3, const_cast<void*>(x.ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, l2,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+struct Tiling {
+  int cg, NT, splits, chunks, chunks_per_split, n_mt, n_nt;
+};
+
+// Estimated time, in SM clocks, of a tiling: rounds of tiles over the SMs (or pairs), each
+// the longer of its chunks and its epilogue, plus one epilogue that nothing overlaps and,
+// where K is split, the sum of the partial results.
+// A chunk of CG * 128 x NT x 64 takes 2 NT clocks of the tensor cores, and the 128 + NT / CG
+// rows of 128 bytes a CTA brings for it arrive at about 64 bytes a clock.
+inline double tiling_cost(const Tiling& t, int64_t M, int64_t N, int batch) {
+  const int64_t items = (int64_t)t.n_mt * t.n_nt * t.splits * batch;
+  const int64_t groups = kSms / t.cg;
+  const double rounds = (double)((items + groups - 1) / groups);
+  const double chunk = std::max(2.0 * t.NT, 2.0 * (kBM + t.NT / t.cg));
+  const double epi = 600.0 + 16.0 * t.NT;
+  double cost = rounds * std::max(t.chunks_per_split * chunk, epi) + epi + 2000.0;
+  if (t.splits > 1) cost += 4000.0 + (double)(t.splits + 1) * M * N * 4.0 / 3000.0;
+  return cost;
+}
+
+// The cheapest tiling. `max_splits` > 1 allows K to be split into partial results.
+inline Tiling choose_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn, int max_splits, int max_cg) {
+  Tiling best{};
+  double best_cost = -1.0;
+  const int chunks = (int)((K + kKC - 1) / kKC);
+  for (int cg = 1; cg <= max_cg; ++cg) {
+    for (int nt = kMaxNT; nt >= 32; nt -= 32) {
+      if (bmn ? nt % (64 * cg) != 0 : nt % (16 * cg) != 0) continue;
+      Tiling t{};
+      t.cg = cg;
+      t.NT = nt;
+      t.chunks = chunks;
+      t.n_mt = (int)((M + cg * kBM - 1) / (cg * kBM));
+      t.n_nt = (int)((N + nt - 1) / nt);
+      for (int s = 1; s <= max_splits; ++s) {
+        const int per = (chunks + s - 1) / s;
+        if (s > 1 && per < 4) break;
+        if ((chunks + per - 1) / per != s) continue;  // every split has chunks
+        t.splits = s;
+        t.chunks_per_split = per;
+        const double c = tiling_cost(t, M, N, batch);
+        if (best_cost < 0.0 || c < best_cost) {
+          best_cost = c;
+          best = t;
+        }
+      }
+    }
+  }
+  return best;
+}
+
+struct Extra {
+  const Matrix* aux = nullptr;
+  const Matrix* pre = nullptr;
+};
+
+template <int CG, bool AMN, bool BMN, int EPI>
+cudaError_t launch_tiles(const Tiling& t, Params p, const Matrix& a, const Matrix& b, const Matrix& out, int batch,
+                         CUtensorMapDataType in_type, CUtensorMapDataType out_type, const Extra& ex, cudaStream_t st) {
+  constexpr int kTile = tile_bytes(EPI);
+  constexpr CUtensorMapSwizzle kOutSwz = EPI == kEpiGrad32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  constexpr CUtensorMapL2promotion kL2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+  CUtensorMap a_map, b_map, out_map, aux_map, pre_map;
+  cudaError_t e = encode_3d(&a_map, a, batch, in_type, 2, kKC, AMN ? 64 : kBM, CU_TENSOR_MAP_SWIZZLE_128B, kL2);
+  if (e == cudaSuccess)
+    e = encode_3d(&b_map, b, batch, in_type, 2, kKC, BMN ? 64 : t.NT / CG, CU_TENSOR_MAP_SWIZZLE_128B, kL2);
+  if (e != cudaSuccess) return e;
+  if (p.raw_out == nullptr) {
+    e = encode_3d(&out_map, out, EPI == kEpiGrad32 ? t.splits : batch, out_type, EPI == kEpiGrad32 ? 4 : 2, kSC, 32,
+                  kOutSwz, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+    if (e != cudaSuccess) return e;
+  } else {
+    out_map = a_map;  // not used
+  }
+  aux_map = pre_map = a_map;
+  p.has_aux = ex.aux != nullptr;
+  p.has_pre = ex.pre != nullptr;
+  if (p.has_aux) {
+    const CUtensorMapDataType aux_type = EPI == kEpiStep ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    e = encode_3d(&aux_map, *ex.aux, batch, aux_type, 2, kSC, 32, kOutSwz, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.has_pre) {
+    e = encode_3d(&pre_map, *ex.pre, batch, out_type, 2, kSC, 32, kOutSwz, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+    if (e != cudaSuccess) return e;
+  }
+  p.NT = t.NT;
+  p.n_mt = t.n_mt;
+  p.n_nt = t.n_nt;
+  p.splits = t.splits;
+  p.chunks = t.chunks;
+  p.chunks_per_split = t.chunks_per_split;
+  const int64_t items = (int64_t)t.n_mt * t.n_nt * t.splits * batch;
+  if (items > 0x7fffffff) return cudaErrorInvalidValue;
+  p.n_items = (int)items;
+  p.wait_ns = wait_limit_ns();
+  p.fault = fault_site();
+  // kind::f16: fp32 accumulator, A and B bf16 (format 1) or fp16 (format 0)
+  const uint32_t fmt = in_type == CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 ? 0u : (1u << 7) | (1u << 10);
+  p.idesc = tc::idesc_bf16(CG * kBM, t.NT, BMN, AMN) ^ fmt;
+  p.idesc_ones = tc::idesc_bf16(CG * kBM, 16 * CG, false, AMN) ^ fmt;
+  p.stage_bytes = kABytes + t.NT / CG * 128;
+  const bool small_corner = EPI == kEpiAct;
+  p.warp_bytes = out_tiles(EPI) * kTile + (p.has_pre ? 2 * kTile : 0) + (small_corner ? 512 : 0);
+  // the staging tiles' swizzle wants 1024-byte (fp32) or 512-byte alignment
+  const int fixed = kEpiWarps * p.warp_bytes + 512 + 8 * kNBar + 16 + 1024;
+  int dev = 0, smem_max = 0, sms = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  p.stages = std::min(kMaxStages, (smem_max - fixed) / p.stage_bytes);
+  if (p.stages < 2) return cudaErrorInvalidConfiguration;
+  p.off_out = p.stages * p.stage_bytes;
+  p.off_ones = p.off_out + kEpiWarps * p.warp_bytes;
+  p.off_bar = p.off_ones + 512;
+  // more than half of an SM's shared memory: one CTA per SM, so the tensor memory is free
+  const int smem = std::max(120 * 1024, p.off_out + fixed);
+  auto kern = product_kernel<CG, AMN, BMN, EPI>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, sms / CG)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, a_map, b_map, out_map, aux_map, pre_map, p);
+}
+
+template <bool AMN, bool BMN, int EPI>
+cudaError_t launch_product(const Tiling& t, const Params& p, const Matrix& a, const Matrix& b, const Matrix& out,
+                           int batch, CUtensorMapDataType in_type, CUtensorMapDataType out_type, const Extra& ex,
+                           cudaStream_t st) {
+  return t.cg == 2 ? launch_tiles<2, AMN, BMN, EPI>(t, p, a, b, out, batch, in_type, out_type, ex, st)
+                   : launch_tiles<1, AMN, BMN, EPI>(t, p, a, b, out, batch, in_type, out_type, ex, st);
+}
+
+}  // namespace prod
+}  // namespace swin

@@ -1,0 +1,161 @@
+"""Orthogonalised weight updates on the GPU against the Newton-Schulz iteration in fp64: the
+error may be a quarter above that of the same iteration in fp64 with the held matrices
+rounded to fp16 and the result to bf16 (what the kernels' fp32 accumulation adds to those
+roundings is a thousandth of them; a quarter leaves room for roundings that fall the other
+way), and the properties of the result that do not need the iteration."""
+import pytest
+import torch
+
+from swin_window_attention_gb300 import capi
+from tests.linear_util import orthogonalize64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from swin_window_attention_gb300 import build
+    build.build()
+    capi.load()
+
+
+def _g(seed, *shape, dtype=torch.float32, strong=0.5):
+    gen = torch.Generator().manual_seed(seed)
+    n, r, c = shape
+    k = min(4, r, c)
+    low = torch.randn(n, r, k, generator=gen) @ torch.randn(n, k, c, generator=gen)
+    return ((strong * low + torch.randn(n, r, c, generator=gen)) * 1e-3).to(dtype)
+
+
+def _run(g, **kw):
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = capi.orthogonalize(g.to(DEV), status=st, **kw)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert out.dtype == torch.bfloat16 and out.shape == g.shape
+    return out.cpu().double()
+
+
+def _check(out, g, steps=5, scale=1.0):
+    for o, m in zip(out, g):
+        exact = orthogonalize64(m, steps, scale=scale)
+        held = orthogonalize64(m, steps, scale=scale, half=True)
+        err, allow = float((o - exact).norm()), float((held - exact).norm())
+        assert err <= 1.25 * allow + 1e-4 * float(exact.norm()), (err, allow, float(exact.norm()))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,r,c", [(1, 96, 384), (1, 384, 96), (3, 64, 64), (2, 200, 136), (2, 136, 200), (5, 33, 77),
+                                   (4, 77, 33), (1, 129, 513), (1, 512, 300), (7, 24, 1000), (2, 700, 40),
+                                   (40, 130, 264), (1, 1024, 640)])
+def test_against_fp64(n, r, c, dtype):
+    g = _g(n + r + c, n, r, c, dtype=dtype)
+    _check(_run(g), g)
+
+
+@pytest.mark.parametrize("steps,scale", [(1, 1.0), (2, 0.25), (3, -2.0), (8, 1.7)])
+def test_steps_and_scale(steps, scale):
+    g = _g(steps, 2, 96, 160)
+    _check(_run(g, steps=steps, scale=scale), g, steps, scale)
+
+
+@pytest.mark.parametrize("r,c", [(1, 1), (1, 7), (9, 1), (1, 1000), (8, 8), (2, 3)])
+def test_smallest_sizes(r, c):
+    g = _g(r + c, 3, r, c)
+    _check(_run(g), g)
+
+
+def test_two_dimensions_and_singular_values():
+    g = _g(5, 1, 192, 768)[0]
+    o = _run(g)
+    s = torch.linalg.svdvals(o)
+    assert 0.6 < float(s.min()) and float(s.max()) < 1.25
+    # U and V are kept: O G^T is near symmetric and positive
+    p = o @ g.double().T
+    assert float((p - p.T).norm() / p.norm()) < 2e-2 and float(torch.linalg.eigvalsh(p + p.T).min()) > 0
+
+
+def test_scale_of_the_input_does_not_matter():
+    """eps is 4e-7 of the unscaled norm: below the roundings, so the result for G holds for f G."""
+    g = _g(6, 1, 100, 136)
+    for f in (2.0 ** 40, 2.0 ** 80, 2.0 ** 100):  # squares that overflow fp32 beyond 2^64
+        _check(_run(g * f), g)
+
+
+def test_zero_and_non_finite_matrices_leave_the_others_alone():
+    g = _g(7, 4, 72, 96)
+    ref = _run(g)
+    g[1] = 0.0
+    g[2, 3, 5] = float("nan")
+    out = _run(g)
+    assert torch.equal(out[0], ref[0]) and torch.equal(out[3], ref[3])
+    assert torch.all(out[1] == 0) and torch.isnan(out[2]).all()
+    g[2, 3, 5] = float("inf")
+    assert torch.isnan(_run(g)[2]).any()
+
+
+def test_unaligned_rows_write_only_the_result():
+    n, r, c = 2, 50, 37
+    g = _g(8, n, r, c)
+    buf = torch.full((n * r * c + 41,), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[21:21 + n * r * c].view(n, r, c)
+    capi.orthogonalize(g.to(DEV), out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu().double(), _run(g))
+    assert torch.all(buf[:21] == 7.0) and torch.all(buf[21 + n * r * c:] == 7.0)
+    # an aligned shape at an address that is not
+    g = _g(9, 1, 40, 64)
+    out = buf[1:1 + 40 * 64].view(1, 40, 64)
+    capi.orthogonalize(g.to(DEV), out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu().double(), _run(g))
+
+
+def test_streams_graph_and_empty_stack():
+    g = [_g(s, 3, 96, 128).to(DEV) for s in (1, 2)]
+    want = [capi.orthogonalize(a) for a in g]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [capi.orthogonalize(a, stream=s) for a, s in zip(g, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    x = g[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = capi.orthogonalize(x)
+    x.copy_(g[1])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[1])
+    assert capi.orthogonalize(torch.empty(0, 8, 8, device=DEV)).shape == (0, 8, 8)
+
+
+def test_error_paths():
+    g = torch.zeros(2, 16, 24, device=DEV)
+    out = torch.full((2, 16, 24), 3.0, dtype=torch.bfloat16, device=DEV)
+    need = capi.swin_wattn_orthogonalize_workspace_bytes(2, 16, 24)
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    s = torch.cuda.current_stream().cuda_stream
+
+    def f(gp=g.data_ptr(), op=out.data_ptr(), n=2, r=16, c=24, dt=capi.FP32, steps=5, eps=1e-7, scale=1.0,
+          wp=ws.data_ptr(), nb=need):
+        return capi.swin_wattn_orthogonalize(gp, op, n, r, c, dt, steps, eps, scale, wp, nb, None, s)
+
+    bad = capi.ERR_INVALID_ARG
+    assert f(n=0) == capi.OK and f(n=-1) == bad and f(n=65536) == capi.ERR_UNSUPPORTED
+    assert f(r=0) == capi.ERR_UNSUPPORTED and f(c=16385) == capi.ERR_UNSUPPORTED
+    assert f(steps=0) == bad and f(steps=21) == bad and f(eps=0.0) == bad and f(eps=float("nan")) == bad
+    assert f(scale=float("inf")) == bad and f(dt=4) == bad and f(nb=need - 1) == bad
+    assert f(gp=None) == bad and f(op=g.data_ptr()) == bad and f(op=ws.data_ptr()) == bad
+    assert f(gp=g.data_ptr() + 2) == capi.ERR_MISALIGNED and f(wp=ws.data_ptr() + 8) == capi.ERR_MISALIGNED
+    torch.cuda.synchronize()
+    assert torch.all(out == 3.0)
+    with pytest.raises(ValueError):
+        capi.orthogonalize(g.half())
+    with pytest.raises(ValueError):
+        capi.orthogonalize(g.transpose(1, 2))
+    with pytest.raises(ValueError):
+        capi.orthogonalize(g, out=torch.empty(2, 16, 24, device=DEV))
