@@ -326,14 +326,15 @@ def swin_wattn_orthogonalize(g_ptr, out_ptr, count, rows, cols, dtype, steps, ep
 def _tensor(name, t, shape, dtypes, device):
     """Check one operand of the MLP's products and the weight update: a contiguous CUDA
     tensor of the given shape, one of the given dtypes, on `device`."""
+    if t.device == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
+    raise ValueError(f"{name} is not contiguous")
 
 
 def _device_of(name, t):
@@ -342,15 +343,20 @@ def _device_of(name, t):
     return t.device
 
 
-def _call_on(device, where, fn, stream, status):
-    """fn(stream handle, status pointer) with `device` current, on `stream` or that device's
-    current stream; raises on an error status."""
+def _call(where, fn, device, stream, status, *args):
+    """fn(*args, status, stream) with `device` current, on `stream` or that device's current
+    stream; raises on an error status."""
     import torch
+    st = None
     if status is not None:
         _tensor("status", status, (1,), (torch.int32,), device)
-    with torch.cuda.device(device):
-        s = stream if stream is not None else torch.cuda.current_stream(device)
-        rc = fn(s.cuda_stream, _ptr(status))
+        st = status.data_ptr()
+    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, st, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, st, handle)
     if rc != OK:
         raise SwinWAttnError(where, rc)
 
@@ -370,10 +376,10 @@ def _empty(shape, dtype, device, stream):
 
 
 def _act_code(act):
-    code = ACTIVATIONS.get(act, act) if isinstance(act, str) else act
-    if code not in ACTIVATIONS.values():
+    code = ACTIVATIONS.get(act) if isinstance(act, str) else act
+    if code is None or not ACT_NONE <= code <= ACT_SILU:
         raise ValueError(f"unknown activation {act!r}: one of {sorted(ACTIVATIONS)} or an ACT_ code")
-    return int(code)
+    return code
 
 
 def linear(x, w, b=None, act=ACT_NONE, residual=None, y=None, pre=None, status=None, stream=None):
@@ -397,9 +403,8 @@ def linear(x, w, b=None, act=ACT_NONE, residual=None, y=None, pre=None, status=N
     for name, t in (("residual", residual), ("y", y), ("pre", pre)):
         if t is not None:
             _tensor(name, t, lead + (N,), bf16, dev)
-    _call_on(dev, "swin_wattn_linear",
-             lambda s, st: swin_wattn_linear(x.data_ptr(), w.data_ptr(), _ptr(b), _ptr(residual), y.data_ptr(),
-                                             _ptr(pre), lead.numel(), K, N, code, st, s), stream, status)
+    _call("swin_wattn_linear", load().swin_wattn_linear, dev, stream, status, x.data_ptr(), w.data_ptr(), _ptr(b),
+          _ptr(residual), y.data_ptr(), _ptr(pre), lead.numel(), K, N, code)
     return y
 
 
@@ -423,9 +428,8 @@ def linear_bwd_data(dy, w, pre=None, act=ACT_NONE, dx=None, status=None, stream=
     for name, t in (("pre", pre), ("dx", dx)):
         if t is not None:
             _tensor(name, t, lead + (K,), bf16, dev)
-    _call_on(dev, "swin_wattn_linear_bwd_data",
-             lambda s, st: swin_wattn_linear_bwd_data(dy.data_ptr(), w.data_ptr(), _ptr(pre), dx.data_ptr(),
-                                                      lead.numel(), K, N, code, st, s), stream, status)
+    _call("swin_wattn_linear_bwd_data", load().swin_wattn_linear_bwd_data, dev, stream, status, dy.data_ptr(),
+          w.data_ptr(), _ptr(pre), dx.data_ptr(), lead.numel(), K, N, code)
     return dx
 
 
@@ -454,10 +458,9 @@ def linear_bwd_weight(dy, x, dw=None, db=None, accumulate=False, workspace=None,
                            stream)
     _tensor("workspace", workspace, (workspace.numel(),), (torch.uint8,), dev)
     code = FP32 if dw.dtype == torch.float32 else BF16
-    _call_on(dev, "swin_wattn_linear_bwd_weight",
-             lambda s, st: swin_wattn_linear_bwd_weight(dy.data_ptr(), x.data_ptr(), dw.data_ptr(), _ptr(db), tokens,
-                                                        K, N, code, int(bool(accumulate)), workspace.data_ptr(),
-                                                        workspace.numel(), st, s), stream, status)
+    _call("swin_wattn_linear_bwd_weight", load().swin_wattn_linear_bwd_weight, dev, stream, status, dy.data_ptr(),
+          x.data_ptr(), dw.data_ptr(), _ptr(db), tokens, K, N, code, 1 if accumulate else 0, workspace.data_ptr(),
+          workspace.numel())
     return dw, db
 
 
@@ -480,10 +483,9 @@ def orthogonalize(g, steps=5, eps=1e-7, scale=1.0, out=None, workspace=None, sta
                            stream)
     _tensor("workspace", workspace, (workspace.numel(),), (torch.uint8,), dev)
     code = FP32 if g.dtype == torch.float32 else BF16
-    _call_on(dev, "swin_wattn_orthogonalize",
-             lambda s, st: swin_wattn_orthogonalize(g.data_ptr(), out.data_ptr(), count, rows, cols, code, int(steps),
-                                                    float(eps), float(scale), workspace.data_ptr(),
-                                                    workspace.numel(), st, s), stream, status)
+    _call("swin_wattn_orthogonalize", load().swin_wattn_orthogonalize, dev, stream, status, g.data_ptr(),
+          out.data_ptr(), count, rows, cols, code, int(steps), float(eps), float(scale), workspace.data_ptr(),
+          workspace.numel())
     return out
 
 

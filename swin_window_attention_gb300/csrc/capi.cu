@@ -105,17 +105,17 @@ int check_device_ptr(const void* ptr, size_t align) {
   return SWIN_WATTN_ERR_INVALID_ARG;
 }
 
-// A device pointer, as above, of memory that lies on the current device (or is mapped).
-int check_here(const void* ptr, size_t align) {
-  int rc = check_device_ptr(ptr, align);
-  if (rc != SWIN_WATTN_OK) return rc;
+// A device pointer, as above, of memory that lies on device `dev` (or is mapped).
+int check_on_device(const void* ptr, size_t align, int dev) {
+  if (reinterpret_cast<uintptr_t>(ptr) % align != 0) return SWIN_WATTN_ERR_MISALIGNED;
   cudaPointerAttributes a;
-  int dev = 0;
-  if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+  if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess) {
     cudaGetLastError();
     return SWIN_WATTN_ERR_INVALID_ARG;
   }
-  return a.type == cudaMemoryTypeDevice && a.device != dev ? SWIN_WATTN_ERR_INVALID_ARG : SWIN_WATTN_OK;
+  if (a.type == cudaMemoryTypeDevice) return a.device == dev ? SWIN_WATTN_OK : SWIN_WATTN_ERR_INVALID_ARG;
+  if (a.type == cudaMemoryTypeManaged) return SWIN_WATTN_OK;
+  return a.type == cudaMemoryTypeHost && a.devicePointer == ptr ? SWIN_WATTN_OK : SWIN_WATTN_ERR_INVALID_ARG;
 }
 
 // A buffer of a call: its pointer, size and alignment.
@@ -134,9 +134,14 @@ bool overlaps(const Buffer& a, const Buffer& b) {
 // Every buffer that is given is memory of the current device, and none that is written
 // overlaps another, except buffer `same_a` that is buffer `same_b` itself.
 int check_buffers(const char* where, const Buffer* bufs, int n, int same_a = -1, int same_b = -1) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  }
   for (int i = 0; i < n; ++i) {
     if (bufs[i].ptr == nullptr) continue;
-    const int rc = check_here(bufs[i].ptr, bufs[i].align);
+    const int rc = check_on_device(bufs[i].ptr, bufs[i].align, dev);
     if (rc != SWIN_WATTN_OK) return rc;
   }
   for (int i = 0; i < n; ++i)

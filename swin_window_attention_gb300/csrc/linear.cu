@@ -66,13 +66,13 @@ __global__ void __launch_bounds__(256) sum_splits_kernel(const float* __restrict
 
 constexpr int kMaxSplits = 64;
 
-Tiling weight_tiling(int64_t T, int K, int N) { return prod::choose_tiling(N, K, T, 1, true, kMaxSplits, 1); }
+Tiling weight_tiling(int64_t T, int K, int N) { return prod::choose_tiling(N, K, T, 1, true, kMaxSplits, 2); }
 
 }  // namespace
 
 cudaError_t linear_launch(const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
                           int T, int K, int N, int act, int* status, cudaStream_t st) {
-  const Tiling t = prod::choose_tiling(T, N, K, 1, false, 1, 1);
+  const Tiling t = prod::choose_tiling(T, N, K, 1, false, 1, 2);
   Params p{};
   p.M = T;
   p.N = N;
@@ -89,7 +89,7 @@ cudaError_t linear_launch(const void* x, const void* w, const float* b, const vo
 
 cudaError_t linear_bwd_data_launch(const void* dy, const void* w, const void* pre, void* dx, int T, int K, int N,
                                    int act, int* status, cudaStream_t st) {
-  const Tiling t = prod::choose_tiling(T, K, N, 1, true, 1, 1);
+  const Tiling t = prod::choose_tiling(T, K, N, 1, true, 1, 2);
   Params p{};
   p.M = T;
   p.N = K;

@@ -12,11 +12,12 @@
 //   ring of stages;
 // * MMA warp, one thread (of the pair's first CTA): four K16 MMAs a chunk into one of two
 //   tensor-memory accumulators;
-// * eight epilogue warps, two per tensor-memory lane quadrant, taking alternate 32-column
-//   slices: the epilogue's arithmetic in fp32 on a thread's 32 columns of one row, one
+// * sixteen epilogue warps, four per tensor-memory lane quadrant, taking 32-column slices in
+//   turn: the epilogue's arithmetic in fp32 on a thread's 32 columns of one row, one
 //   rounding, a swizzled staging tile per warp, a TMA store; while the next tile
 //   accumulates. A second operand of the epilogue (residual, pre-activation, ...) arrives
-//   by TMA one slice ahead in the staging tile that the result is written over.
+//   by TMA ahead of its slice in the staging tile that the result is written over. (Eight
+//   warps left the issue slots 42 % busy on the GELU epilogues: XXX us instead of YYY.)
 // A pair (CG = 2) reads each row of B once for 256 rows of A instead of 128: per chunk a CTA
 // brings 128 + NT / 2 rows instead of 128 + NT, which is what the tensor cores need to run
 // at full rate at NT = 256 (shared memory is both filled and read by the chunk).
@@ -28,6 +29,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -41,15 +43,20 @@ constexpr int kKC = 64;    // K per chunk: one 128-byte row
 constexpr int kSC = 32;    // columns per epilogue slice
 constexpr int kMaxNT = 256;
 constexpr int kMaxStages = 8;
-constexpr int kEpiWarps = 8, kMMA = 8, kCOPY = 9, kThreads = 320;
 constexpr int kABytes = kBM * 128;
 constexpr uint32_t kSW128 = 2;  // descriptor layout: 128-byte swizzle
 constexpr int kTmemCols = 512;  // two accumulators of up to 256 columns
+// An fp32 result keeps its accuracy over a long K by accumulating at most this many chunks
+// (32 MMAs) in tensor memory, whose additions truncate; the epilogue warps add such segments
+// up in registers, rounding to nearest. On 50176 tokens the error against 64 bits is XXX
+// (relative 2-norm), where one accumulation per tile of 33 chunks left 2.1e-6.
+constexpr int kSegChunks = 8;
 
-// Barriers: full and empty per stage, full and free per accumulator, aux loads (three per
-// epilogue warp), the last commit.
-constexpr int kDFull = 2 * kMaxStages, kDFree = kDFull + 2, kAux = kDFree + 2, kDrain = kAux + 3 * kEpiWarps;
-constexpr int kNBar = kDrain + 1;
+// Barriers: full and empty per stage, full and free per accumulator, the last commit, aux
+// loads (up to four per epilogue warp).
+constexpr int kMaxAuxTiles = 4;
+constexpr int kDFull = 2 * kMaxStages, kDFree = kDFull + 2, kDrain = kDFree + 2, kAux = kDrain + 1;
+constexpr int kNBar = kAux + kMaxAuxTiles * 16;
 
 enum Epi {
   kEpiAct = 0,     // bf16: aux + act(acc + bias), optionally acc + bias into a second result
@@ -59,12 +66,19 @@ enum Epi {
   kEpiStep = 4     // fp16 or bf16: alpha * acc + beta * aux + diag on the diagonal
 };
 
+// Warps: the epilogue's, MMA, copy. The fp32 gradient has eight epilogue warps, which hold 128
+// running sums a thread, more than an even share of the registers: two idle warps complete a
+// third warpgroup, which gives registers up (2 x 216 + 64 of the 3 x 168 that 384 threads are
+// launched with).
+__host__ __device__ constexpr int epi_warps(int epi) { return epi == kEpiGrad32 ? 8 : 16; }
+__host__ __device__ constexpr int n_threads(int epi) { return epi == kEpiGrad32 ? 384 : 576; }
+
 struct Params {
   int M, N, NT;
   int n_mt, n_nt, n_items;  // items: batch * splits * n_mt * n_nt, n fastest
   int chunks, chunks_per_split, splits;
   int stages, stage_bytes;
-  int off_out, warp_bytes, off_ones, off_bar;
+  int off_out, warp_bytes, tiles, off_small, off_bar;  // tiles: a warp's staging tiles before that of pre
   uint32_t idesc, idesc_ones;
   int act;
   bool has_aux, has_pre;
@@ -121,17 +135,28 @@ __device__ __forceinline__ void store_3d(const CUtensorMap* map, int c0, int c1,
                : "memory");
 }
 
+// D[tmem] (+)= A B^T; a and b are the low words of the operands' descriptors, *_hi the high
+// ones. (One thread issues every MMA: building whole descriptors there, some twenty
+// instructions each, took it longer than the tensor core takes for a chunk.)
 template <int CG>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc,
+                                    bool accumulate) {
   if constexpr (CG == 2)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.u32 p, %6, 0;\n mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
   else
-    tc::mma_ss(d, a, b, idesc, accumulate);
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.u32 p, %6, 0;\n mov.b64 da, {%1, %2};\n mov.b64 db, {%3, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
 }
+// The words of a descriptor (tc::sdesc): low, address and lbo; high, sbo, version and layout.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | (lbo >> 4) << 16; }
+__device__ __forceinline__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t layout) { return (sbo >> 4) | 1u << 14 | layout << 29; }
 // Arrive on the mbarrier (of both CTAs of a pair) when every MMA issued so far has completed.
 template <int CG>
 __device__ __forceinline__ void commit(uint32_t mbar) {
@@ -162,8 +187,19 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t base) {
     tc::tmem_dealloc<kTmemCols>(base);
 }
 
+// Wait for a phase, as tc::mbar_wait; its clock is read only where the first try, which
+// suspends the thread itself, has run out.
+__device__ __forceinline__ bool wait(uint32_t mbar, uint32_t parity, uint64_t limit_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred q;\n mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(ok)
+      : "r"(mbar), "r"(parity)
+      : "memory");
+  return ok ? true : tc::mbar_wait(mbar, parity, limit_ns);
+}
 __device__ __forceinline__ bool warp_wait(uint32_t mbar, uint32_t parity, uint64_t limit_ns) {
-  return __all_sync(0xffffffffu, tc::mbar_wait(mbar, parity, limit_ns)) != 0;
+  return __all_sync(0xffffffffu, wait(mbar, parity, limit_ns)) != 0;
 }
 
 // ---- activations --------------------------------------------------------------------
@@ -180,8 +216,13 @@ __device__ __forceinline__ bool warp_wait(uint32_t mbar, uint32_t parity, uint64
 // * tanh-GELU: 0.5 (1 + tanh u) = 1 / (1 + exp(-2u)), so h = 1 / (1 + exp(2 u(t))).
 // * SiLU: h = 1 / (1 + exp(t)).
 // t is cut at 100 there: exp overflows to infinity and h is 0 long before.
-// The maximum propagates NaN, so a NaN input gives NaN.
+// The minimum that cuts t propagates NaN, so a NaN input gives NaN.
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
@@ -203,11 +244,11 @@ __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 constexpr float kGeluCut = 12.0f, kSigmoidCut = 100.0f;
 constexpr float kTanhA = 0.7978845608028654f, kTanhB = 0.044715f;  // u(z) = A (z + B z^3)
 
-// t = min(|z|, cut) and h(t), for two values.
+// t = min(|z|, cut), NaN kept, and h(t), for two values.
 template <int ACT>
 __device__ __forceinline__ void act_tail(float2 z, float2& t, float2& h) {
   if constexpr (ACT == SWIN_WATTN_ACT_GELU) {
-    t = make_float2(fminf(fabsf(z.x), kGeluCut), fminf(fabsf(z.y), kGeluCut));
+    t = make_float2(min_nan(fabsf(z.x), kGeluCut), min_nan(fabsf(z.y), kGeluCut));
     float2 q = splat(2.29900633712532e-05f);
     q = __ffma2_rn(q, t, splat(-0.0006111000548116863f));
     q = __ffma2_rn(q, t, splat(0.007195565849542618f));
@@ -217,7 +258,7 @@ __device__ __forceinline__ void act_tail(float2 z, float2& t, float2& h) {
     q = __ffma2_rn(q, t, splat(-1.000064730644226f));
     h = make_float2(fast_exp2(q.x), fast_exp2(q.y));
   } else {
-    t = make_float2(fminf(fabsf(z.x), kSigmoidCut), fminf(fabsf(z.y), kSigmoidCut));
+    t = make_float2(min_nan(fabsf(z.x), kSigmoidCut), min_nan(fabsf(z.y), kSigmoidCut));
     float2 e;  // the exponent, in powers of two
     if constexpr (ACT == SWIN_WATTN_ACT_GELU_TANH) {
       constexpr float kA2 = 2.0f * kTanhA * kLog2e;
@@ -232,33 +273,31 @@ __device__ __forceinline__ void act_tail(float2 z, float2& t, float2& h) {
 template <int ACT>
 __device__ __forceinline__ float2 act_value(float2 z) {
   if constexpr (ACT == SWIN_WATTN_ACT_NONE) return z;
-  const float2 p = make_float2(max_nan(z.x, 0.0f), max_nan(z.y, 0.0f));
-  if constexpr (ACT == SWIN_WATTN_ACT_RELU) return p;
+  if constexpr (ACT == SWIN_WATTN_ACT_RELU) return make_float2(max_nan(z.x, 0.0f), max_nan(z.y, 0.0f));
   float2 t, h;
   act_tail<ACT>(z, t, h);
-  return __ffma2_rn(make_float2(-t.x, -t.y), h, p);
+  return __ffma2_rn(make_float2(-t.x, -t.y), h, make_float2(fmaxf(z.x, 0.0f), fmaxf(z.y, 0.0f)));
 }
 
-// act'(z) = s + z s'(z):  GELU: z phi(z), phi the normal density; the others:
+// act'(z) = s + z s'(z). With n = h - t s'(t) it is 1 - n for z > 0 and n for z < 0, that is
+// 1/2 + copysign(1/2 - n, z). GELU: s' = phi, the normal density; the others:
 // s' = s (1 - s) (2 u)', and s (1 - s) = h (1 - h).
 template <int ACT>
 __device__ __forceinline__ float2 act_slope(float2 z) {
   if constexpr (ACT == SWIN_WATTN_ACT_RELU) return make_float2(step01(z.x), step01(z.y));
-  float2 t, h;
+  float2 t, h, s;
   act_tail<ACT>(z, t, h);
-  float2 g;  // |z| s'(z)
   if constexpr (ACT == SWIN_WATTN_ACT_GELU) {
     // phi(t) = 2^(-t^2 log2(e) / 2 - log2 sqrt(2 pi))
     const float2 e = __ffma2_rn(__fmul2_rn(t, t), splat(-0.5f * kLog2e), splat(-1.3257480647361595f));
-    g = __fmul2_rn(t, make_float2(fast_exp2(e.x), fast_exp2(e.y)));
+    s = make_float2(fast_exp2(e.x), fast_exp2(e.y));
   } else {
-    g = __fmul2_rn(t, __fmul2_rn(h, fsub2(splat(1.0f), h)));
+    s = __fmul2_rn(h, fsub2(splat(1.0f), h));
     if constexpr (ACT == SWIN_WATTN_ACT_GELU_TANH)
-      g = __fmul2_rn(g, __ffma2_rn(__fmul2_rn(t, t), splat(6.0f * kTanhA * kTanhB), splat(2.0f * kTanhA)));
+      s = __fmul2_rn(s, __ffma2_rn(__fmul2_rn(t, t), splat(6.0f * kTanhA * kTanhB), splat(2.0f * kTanhA)));
   }
-  // z > 0: 1 - h + g; z < 0: h - g; a NaN stays one
-  return make_float2(z.x > 0.0f ? 1.0f - (h.x - g.x) : (z.x <= 0.0f ? h.x - g.x : z.x),
-                     z.y > 0.0f ? 1.0f - (h.y - g.y) : (z.y <= 0.0f ? h.y - g.y : z.y));
+  const float2 d = __ffma2_rn(t, s, __ffma2_rn(h, splat(-1.0f), splat(0.5f)));  // 1/2 - n
+  return __fadd2_rn(splat(0.5f), make_float2(copysignf(d.x, z.x), copysignf(d.y, z.y)));
 }
 
 __device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
@@ -275,19 +314,24 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t w) {
 
 // Bytes of one staging tile (32 rows x 32 columns) of an epilogue.
 __host__ __device__ constexpr int tile_bytes(int epi) { return epi == kEpiGrad32 ? 4096 : 2048; }
-// Staging tiles a warp rotates through: three 16-bit ones (with a second operand the next
-// slice's load, this slice and the last store's read are in flight together), two fp32 ones.
-__host__ __device__ constexpr int out_tiles(int epi) { return epi == kEpiGrad32 ? 2 : 3; }
+// Staging tiles of an epilogue warp: with a second operand (aux) up to four, for the store of
+// the last slice, this slice, and two loads ahead, or two where K is long; else two, or one
+// where K is long; and one more for a second result (pre). Where K is long a tile's product
+// takes longer than its epilogue, and shared memory is worth more in the ring: at 8192^3 a
+// pair runs at 1580 TFLOP/s with four stages, 1750 with five.
 
 template <int CG, bool AMN, bool BMN, int EPI>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(n_threads(EPI), 1)
     product_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
                    const __grid_constant__ CUtensorMap out_map, const __grid_constant__ CUtensorMap aux_map,
                    const __grid_constant__ CUtensorMap pre_map, const Params p) {
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) unsigned char smem[];
   pdl_launch_dependents();
   const uint32_t smem0 = smem_u32(smem);
+  if ((smem0 & 1023u) != 0) {  // the swizzled tiles need the declared alignment
+    if (threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, 1);
+    return;
+  }
   const uint32_t bar0 = smem0 + p.off_bar;
   auto full_bar = [&](int st) { return bar0 + 8 * st; };
   auto empty_bar = [&](int st) { return bar0 + 8 * (kMaxStages + st); };
@@ -295,6 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto dfree_bar = [&](int b) { return bar0 + 8 * (kDFree + b); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + p.off_bar + 8 * kNBar);
   const int stages = p.stages;
+  constexpr int kEW = epi_warps(EPI), kMMA = kEW, kCOPY = kEW + 1;
+  constexpr int kPerQuad = kEW / 4, kSlices = kMaxNT / kSC / kPerQuad;  // warps per quadrant, slices per warp
+  constexpr bool kSums = EPI == kEpiGrad32 || EPI == kEpiGrad16;
+  constexpr int kSeg = EPI == kEpiGrad32 ? kSegChunks : 1 << 30;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = CG == 2 ? (int)cluster_rank() : 0;
   const int group = blockIdx.x / CG, n_groups = gridDim.x / CG;
@@ -326,15 +374,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(dfull_bar(b), 1);
-      tc::mbar_init(dfree_bar(b), kEpiWarps * CG);
+      tc::mbar_init(dfree_bar(b), kEW * CG);
     }
-    for (int b = 0; b < 3 * kEpiWarps; ++b) tc::mbar_init(bar0 + 8 * (kAux + b), 1);
+    for (int b = 0; b < kMaxAuxTiles * kEW; ++b) tc::mbar_init(bar0 + 8 * (kAux + b), 1);
     tc::mbar_init(bar0 + 8 * kDrain, 1);
     tc::mbar_init_fence();
   }
-  if constexpr (EPI == kEpiGrad32 || EPI == kEpiGrad16) {
+  if constexpr (kSums) {
     // 16 rows x 16 of K, all ones (any layout): the B operand that sums A over K
-    if (tid < 128) reinterpret_cast<uint32_t*>(smem + p.off_ones)[tid] = 0x3F803F80u;
+    if (tid < 128) reinterpret_cast<uint32_t*>(smem + p.off_small)[tid] = 0x3F803F80u;
     tc::fence_proxy_async();
   }
   tc::fence_before_sync();
@@ -346,203 +394,273 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the previous kernel on the stream; every global access comes after this wait.
   pdl_wait();
   int bad = 0;
-
-  if (warp == kCOPY) {
-    if (lane == 0) {
-      int st = 0;
-      uint32_t ph = 0, first = 1;
-      for (int it = group; it < p.n_items && !bad; it += n_groups) {
-        const Item w = decode(it);
-        const int nb0 = w.n0 + rank * (p.NT / CG);
-        for (int c = w.c0; c < w.c1; ++c) {
-          if (!first && !tc::mbar_wait(empty_bar(st), ph ^ 1, p.wait_ns)) {
-            bad = 1;
-            break;
-          }
-          const uint32_t base = smem0 + st * p.stage_bytes;
-          // a pair's loads all complete on the first CTA's barrier
-          const uint32_t fb = CG == 2 ? map_to_rank(full_bar(st), 0) : full_bar(st);
-          if (rank == 0) tc::mbar_expect_tx(full_bar(st), CG * p.stage_bytes);
-          if constexpr (AMN) {
-#pragma unroll
-            for (int j = 0; j < kBM / 64; ++j)
-              load_3d<CG>(base + j * 8192, &a_map, w.m0 + 64 * j, c * kKC, w.b, fb);
-          } else {
-            load_3d<CG>(base, &a_map, c * kKC, w.m0, w.b, fb);
-          }
-          if constexpr (BMN) {
-            for (int j = 0; j < p.NT / (64 * CG); ++j)
-              load_3d<CG>(base + kABytes + j * 8192, &b_map, nb0 + 64 * j, c * kKC, w.b, fb);
-          } else {
-            load_3d<CG>(base + kABytes, &b_map, c * kKC, nb0, w.b, fb);
-          }
-          if (++st == stages) {
-            st = 0;
-            ph ^= 1;
-            first = 0;
-          }
-        }
-      }
-      // every load issued has landed before the CTA leaves (the second CTA of a pair is held
-      // by the cluster barrier below until the first has seen its bytes too)
-      if (rank == 0)
-        for (int s2 = 0; s2 < (first ? st : stages); ++s2)
-          tc::mbar_wait(full_bar(s2), s2 < st ? ph : ph ^ 1, p.wait_ns);
-    }
-    __syncwarp();
-  } else if (warp == kMMA) {
-    if (rank == 0) {
-      int st = 0, g = 0;
-      uint32_t ph = 0;
-      bool prev_ones = false;
-      for (int it = group; it < p.n_items && !bad; it += n_groups, ++g) {
-        const Item w = decode(it);
-        const int buf = g & 1;
-        const bool ones = (EPI == kEpiGrad32 || EPI == kEpiGrad16) && p.k_sums != nullptr && w.nt == 0;
-        if (g >= 2 && !warp_wait(dfree_bar(buf), ((g >> 1) - 1) & 1, p.wait_ns)) {
-          bad = 1;
-          break;
-        }
-        // the sums of a first-column tile lie in the other accumulator's first columns: that
-        // one's epilogue has to be over before, and this tile's before the next begins
-        if (g >= 1 && (ones || prev_ones) && !warp_wait(dfree_bar(buf ^ 1), ((g - 1) >> 1) & 1, p.wait_ns)) {
-          bad = 1;
-          break;
-        }
-        prev_ones = ones;
-        for (int c = w.c0; c < w.c1; ++c) {
-          if (!warp_wait(full_bar(st), ph, p.wait_ns)) {
-            bad = 1;
-            break;
-          }
-          if (lane == 0) {
-            tc::fence_after_sync();
-            const uint32_t a = smem0 + st * p.stage_bytes, b = a + kABytes;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              // K-major: 32 bytes further in the 128-byte row; MN-major: 16 rows further,
-              // blocks of 64 of M or N 8192 bytes apart
-              const uint64_t ad = AMN ? tc::sdesc(a + kk * 2048, 8192, 1024, kSW128) : tc::sdesc(a + kk * 32, 16, 1024, kSW128);
-              const uint64_t bd = BMN ? tc::sdesc(b + kk * 2048, 8192, 1024, kSW128) : tc::sdesc(b + kk * 32, 16, 1024, kSW128);
-              mma<CG>(tmem + buf * kMaxNT, ad, bd, p.idesc, c > w.c0 || kk > 0);
-              if (ones)
-                mma<CG>(tmem + (buf ^ 1) * kMaxNT, ad, tc::sdesc(smem0 + p.off_ones, 128, 256), p.idesc_ones,
-                        c > w.c0 || kk > 0);
+  if (warp >= kEW) {
+    if constexpr (EPI == kEpiGrad32) tc::setmaxnreg_dec<64>();
+    if (warp == kCOPY) {
+      if (lane == 0) {
+        int st = 0;
+        uint32_t ph = 0, first = 1;
+        // a pair's loads all complete on the first CTA's barriers
+        const uint32_t full0 = CG == 2 ? map_to_rank(full_bar(0), 0) : full_bar(0);
+        for (int it = group; it < p.n_items && !bad; it += n_groups) {
+          const Item w = decode(it);
+          const int nb0 = w.n0 + rank * (p.NT / CG);
+          for (int c = w.c0; c < w.c1; ++c) {
+            if (!first && !wait(empty_bar(st), ph ^ 1, p.wait_ns)) {
+              bad = 1;
+              break;
             }
-            commit<CG>(empty_bar(st));
-#ifdef SWIN_WATTN_FAULT_INJECTION
-            if (!(p.fault == kFaultGemm && g == 0))
-#endif
-              if (c == w.c1 - 1) commit<CG>(dfull_bar(buf));
-          }
-          __syncwarp();
-          if (++st == stages) {
-            st = 0;
-            ph ^= 1;
+            const uint32_t base = smem0 + st * p.stage_bytes;
+            const uint32_t fb = full0 + 8 * st;
+            if (rank == 0) tc::mbar_expect_tx(full_bar(st), CG * p.stage_bytes);
+            if constexpr (AMN) {
+#pragma unroll
+              for (int j = 0; j < kBM / 64; ++j)
+                load_3d<CG>(base + j * 8192, &a_map, w.m0 + 64 * j, c * kKC, w.b, fb);
+            } else {
+              load_3d<CG>(base, &a_map, c * kKC, w.m0, w.b, fb);
+            }
+            if constexpr (BMN) {
+              for (int j = 0; j < p.NT / (64 * CG); ++j)
+                load_3d<CG>(base + kABytes + j * 8192, &b_map, nb0 + 64 * j, c * kKC, w.b, fb);
+            } else {
+              load_3d<CG>(base + kABytes, &b_map, c * kKC, nb0, w.b, fb);
+            }
+            if (++st == stages) {
+              st = 0;
+              ph ^= 1;
+              first = 0;
+            }
           }
         }
+        // every load issued has landed before the CTA leaves (the second CTA of a pair is held
+        // by the cluster barrier below until the first has seen its bytes too)
+        if (rank == 0)
+          for (int s2 = 0; s2 < (first ? st : stages); ++s2)
+            tc::mbar_wait(full_bar(s2), s2 < st ? ph : ph ^ 1, p.wait_ns);
       }
-      // every MMA issued has completed before the tensor memory is released
-      if (lane == 0) commit<CG>(bar0 + 8 * kDrain);
       __syncwarp();
-      if (!warp_wait(bar0 + 8 * kDrain, 0, p.wait_ns)) bad = 1;
+    } else if (warp == kMMA) {
+      if (rank == 0 && lane == 0) {
+        constexpr uint32_t kHi = desc_hi(1024, kSW128), kOnesHi = desc_hi(256, 0);
+        // along K by 16: K-major, 32 bytes further in the 128-byte row; MN-major, 16 rows
+        // further, blocks of 64 of M or N 8192 bytes apart
+        constexpr uint32_t kAStep = (AMN ? 2048 : 32) >> 4, kBStep = (BMN ? 2048 : 32) >> 4;
+        const uint32_t a0 = desc_lo(smem0, AMN ? 8192 : 16), b0 = desc_lo(smem0 + kABytes, BMN ? 8192 : 16);
+        const uint32_t ones_lo = desc_lo(smem0 + p.off_small, 128);
+        int st = 0, g = 0;  // ring stage; accumulations begun
+        uint32_t ph = 0;
+        bool prev_ones = false;
+        for (int it = group; it < p.n_items && !bad; it += n_groups) {
+          const Item w = decode(it);
+          const bool ones = kSums && p.k_sums != nullptr && w.nt == 0;
+          // the sums of a first-column tile: behind the tile's columns where there is room, else
+          // in the other accumulator's first columns
+          const bool ones_aside = ones && p.NT + 16 * CG > kMaxNT;
+          for (int s0 = w.c0; s0 < w.c1 && !bad; s0 += kSeg, ++g) {
+            const int s1 = min(s0 + kSeg, w.c1), buf = g & 1;
+            const uint32_t acc = tmem + buf * kMaxNT;
+            const uint32_t sums = ones_aside ? tmem + (buf ^ 1) * kMaxNT : acc + p.NT;
+            if (g >= 2 && !wait(dfree_bar(buf), ((g >> 1) - 1) & 1, p.wait_ns)) {
+              bad = 1;
+              break;
+            }
+            // where the other accumulator holds sums, its own epilogue has to be over before,
+            // and this one's before the next begins
+            if (g >= 1 && (ones_aside || prev_ones) && !wait(dfree_bar(buf ^ 1), ((g - 1) >> 1) & 1, p.wait_ns)) {
+              bad = 1;
+              break;
+            }
+            prev_ones = ones_aside;
+            for (int c = s0; c < s1; ++c) {
+              if (!wait(full_bar(st), ph, p.wait_ns)) {
+                bad = 1;
+                break;
+              }
+              tc::fence_after_sync();
+              const uint32_t step = st * (p.stage_bytes >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                mma<CG>(acc, a0 + step + kk * kAStep, kHi, b0 + step + kk * kBStep, kHi, p.idesc, c > s0 || kk > 0);
+                if (kSums && ones)
+                  mma<CG>(sums, a0 + step + kk * kAStep, kHi, ones_lo, kOnesHi, p.idesc_ones, c > s0 || kk > 0);
+              }
+              commit<CG>(empty_bar(st));
+#ifdef SWIN_WATTN_FAULT_INJECTION
+              if (!(p.fault == kFaultGemm && g == 0))
+#endif
+                if (c == s1 - 1) commit<CG>(dfull_bar(buf));
+              if (++st == stages) {
+                st = 0;
+                ph ^= 1;
+              }
+            }
+          }
+        }
+        // every MMA issued has completed before the tensor memory is released
+        commit<CG>(bar0 + 8 * kDrain);
+        if (!wait(bar0 + 8 * kDrain, 0, p.wait_ns)) bad = 1;
+      }
+      __syncwarp();
     }
   } else {
+    if constexpr (EPI == kEpiGrad32) tc::setmaxnreg_inc<216>();
     // ==== epilogue warps ================================================================
-    constexpr int kTile = tile_bytes(EPI), NB = out_tiles(EPI);
-    const int quad = warp & 3, parity = warp >> 2;
+    constexpr int kTile = tile_bytes(EPI);
+    const int quad = warp & 3, part = warp >> 2;
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
     unsigned char* wstage = smem + p.off_out + warp * p.warp_bytes;
-    unsigned char* wpre = wstage + NB * kTile;                        // kEpiAct: two more tiles, if kept
-    float* wbias = reinterpret_cast<float*>(wstage + p.warp_bytes - 512);  // kEpiAct: 4 slices x 32
-    const uint32_t aux0 = bar0 + 8 * (kAux + 3 * warp);
     constexpr bool kHasAux = EPI != kEpiGrad32;
-    // the next slice whose second operand is to be requested
-    int nx_it = group, nx_c0 = parity * kSC, issued = 0;
+    const bool aux = kHasAux && p.has_aux, pre = EPI == kEpiAct && p.has_pre;
+    const int NB = p.tiles;
+    const uint32_t aux0 = bar0 + 8 * (kAux + kMaxAuxTiles * warp);
+    // the next slice whose second operand is to be requested, and its staging tile
+    int nx_it = group, nx_c0 = part * kSC, nx_tile = 0, issued = 0;
     auto request_next = [&]() {
       while (nx_it < p.n_items) {
         const Item w = decode(nx_it);
         const int row0 = w.m0 + quad * 32;
         if (row0 < p.M && nx_c0 < p.NT && w.n0 + nx_c0 < p.N) {
           if (lane == 0) {
-            const uint32_t rb = aux0 + 8 * (issued % 3);
+            const uint32_t rb = aux0 + 8 * nx_tile;
             tc::mbar_expect_tx(rb, kTile);
-            load_3d<1>(smem_u32(wstage + (issued % 3) * kTile), &aux_map, w.n0 + nx_c0, row0, w.b, rb);
+            load_3d<1>(smem_u32(wstage + nx_tile * kTile), &aux_map, w.n0 + nx_c0, row0, w.b, rb);
           }
           ++issued;
-          nx_c0 += 2 * kSC;
+          if (++nx_tile == NB) nx_tile = 0;
+          nx_c0 += kPerQuad * kSC;
           return;
         }
         nx_it += n_groups;
-        nx_c0 = parity * kSC;
+        nx_c0 = part * kSC;
       }
     };
-    if constexpr (kHasAux)
-      if (p.has_aux) request_next();
-    int g = 0, m = 0;  // tiles, slices of this warp
-    for (int it = group; it < p.n_items && !bad; it += n_groups, ++g) {
+    if (aux)
+      for (int i = 0; i < max(NB - 2, 1); ++i) request_next();
+    int g = 0, m = 0;                   // accumulations, slices of this warp
+    int tile = 0;                       // the slice's staging tile
+    uint32_t aux_phase = 0;             // of that tile's barrier
+    for (int it = group; it < p.n_items && !bad; it += n_groups) {
       const Item w = decode(it);
-      const int buf = g & 1;
       const int row0 = w.m0 + quad * 32, row = row0 + lane;
+      // kEpiAct: the bias of the tile's columns in shared memory, for broadcast reads. Every
+      // warp of a part writes the same values; two buffers, and the write waits for this
+      // tile's accumulator, which is given out when every warp has left the tile before last.
+      float* sbias = reinterpret_cast<float*>(smem + p.off_small) + (g & 1) * kMaxNT + part * kSC;
+      float bt[kSlices];
       if constexpr (EPI == kEpiAct) {
-        // the bias of the warp's slices, kept in its corner of shared memory for broadcasts
-        float bt[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = w.n0 + parity * kSC + 2 * kSC * i + lane;
+        for (int i = 0; i < kSlices; ++i) {
+          const int c = w.n0 + (part + kPerQuad * i) * kSC + lane;
           bt[i] = p.bias != nullptr && c < p.N ? __ldg(p.bias + c) : 0.0f;
         }
-        __syncwarp();
+      }
+      float seg_sum[EPI == kEpiGrad32 ? kSlices : 1][32];  // kEpiGrad32: the segments' sum, a slice each
+      if constexpr (EPI == kEpiGrad32) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wbias[32 * i + lane] = bt[i];
+        for (int i = 0; i < kSlices; ++i)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) seg_sum[i][e] = 0.0f;
+      }
+      float ones_sum = 0.0f;
+      const bool ones = kSums && p.k_sums != nullptr && w.nt == 0 && part == 0 && row0 < p.M;
+      int buf = g & 1;
+      auto release = [&]() {
+        tc::fence_before_sync();
         __syncwarp();
-      }
-      if (!warp_wait(dfull_bar(buf), (g >> 1) & 1, p.wait_ns)) {
-        bad = 1;
-        break;
-      }
-      tc::fence_after_sync();
-      if constexpr (EPI == kEpiGrad32 || EPI == kEpiGrad16) {
-        if (p.k_sums != nullptr && w.nt == 0 && parity == 0 && row0 < p.M) {
-          uint32_t s;
-          tc::ld1_nowait(trow + (buf ^ 1) * kMaxNT, s);
-          tc::wait_ld_then();
-          tc::dep1(s);
-          if (row < p.M) {
-            float* d = p.k_sums + (int64_t)w.split * p.M + row;
-            *d = p.add_k_sums ? *d + __uint_as_float(s) : __uint_as_float(s);
-          }
+        if (lane == 0) {
+          if constexpr (CG == 2)
+            arrive_cluster(map_to_rank(dfree_bar(buf), 0));
+          else
+            tc::mbar_arrive(dfree_bar(buf));
         }
-      }
-      int si = 0;
-      for (int c0 = parity * kSC; row0 < p.M && c0 < p.NT && w.n0 + c0 < p.N; c0 += 2 * kSC, ++m, ++si) {
-        unsigned char* so = wstage + (m % NB) * kTile;
-        // the tiles written next (this slice's, its second result's, the next slice's load)
-        // have been read by the stores that held them
-        if ((kHasAux && p.has_aux) || (EPI == kEpiAct && p.has_pre)) {
-          if (m >= 2) {
-            if (lane == 0) tc::bulk_wait_read<1>();
-            __syncwarp();
-          }
-          if (kHasAux && p.has_aux) request_next();
-        } else if (m >= NB) {
-          if (lane == 0) tc::bulk_wait_read<NB - 1>();
+        ++g;
+      };
+      for (int s0 = w.c0; s0 < w.c1; s0 += kSeg) {
+        buf = g & 1;
+        if (!warp_wait(dfull_bar(buf), (g >> 1) & 1, p.wait_ns)) {
+          bad = 1;
+          break;
+        }
+        tc::fence_after_sync();
+        if constexpr (EPI == kEpiAct) {
+#pragma unroll
+          for (int i = 0; i < kSlices; ++i) sbias[kPerQuad * kSC * i + lane] = bt[i];
           __syncwarp();
         }
-        uint32_t a[32];
-        tc::ld32_wait(trow + buf * kMaxNT + c0, a);
-        if (kHasAux && p.has_aux) {
-          if (!warp_wait(aux0 + 8 * (m % 3), (m / 3) & 1, p.wait_ns)) {
-            bad = 1;
-            break;
-          }
+        if (ones) {
+          uint32_t s;
+          tc::ld1_nowait(trow + (p.NT + 16 * CG > kMaxNT ? (buf ^ 1) * kMaxNT : buf * kMaxNT + p.NT), s);
+          tc::wait_ld_then();
+          tc::dep1(s);
+          ones_sum += __uint_as_float(s);
         }
         if constexpr (EPI == kEpiGrad32) {
+#pragma unroll
+          for (int i = 0; i < kSlices; ++i) {
+            const int c0 = (part + kPerQuad * i) * kSC;
+            if (row0 < p.M && c0 < p.NT && w.n0 + c0 < p.N) {
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {
+                uint32_t a[16];
+                tc::ld16_wait(trow + buf * kMaxNT + c0 + h, a);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) seg_sum[i][h + e] += __uint_as_float(a[e]);
+              }
+            }
+          }
+          release();
+        } else if (s0 + kSeg >= w.c1) {
+          break;
+        }
+      }
+      if (bad) break;
+      if (ones && row < p.M) {
+        float* d = p.k_sums + (int64_t)w.split * p.M + row;
+        *d = p.add_k_sums ? *d + ones_sum : ones_sum;
+      }
+#pragma unroll(EPI == kEpiGrad32 ? kSlices : 1)
+      for (int si = 0; si < kSlices; ++si) {
+        const int c0 = (part + kPerQuad * si) * kSC;
+        if (!(row0 < p.M && c0 < p.NT && w.n0 + c0 < p.N)) continue;
+        unsigned char* so = wstage + tile * kTile;
+        unsigned char* sz = wstage + NB * kTile;
+        if (aux) {
+          // all stores but the last slice's (of two tiles, all) have read their tiles: load
+          // ahead into the oldest
+          if (lane == 0) {
+            if (NB == 2)
+              tc::bulk_wait_read<0>();
+            else
+              tc::bulk_wait_read<1>();
+          }
+          __syncwarp();
+          request_next();
+        }
+        uint32_t a[32];
+        if constexpr (EPI != kEpiGrad32) tc::ld32_wait(trow + buf * kMaxNT + c0, a);
+        if (aux && !warp_wait(aux0 + 8 * tile, aux_phase, p.wait_ns)) {
+          bad = 1;
+          break;
+        }
+        // Before a tile without a second operand is written: the store that held it has read it.
+        auto tile_free = [&]() {
+          if (aux) return;
+          if (lane == 0) {
+            if (NB == 1)
+              tc::bulk_wait_read<0>();
+            else
+              tc::bulk_wait_read<1>();
+          }
+          __syncwarp();
+        };
+        if constexpr (EPI == kEpiGrad32) {
+          tile_free();
           const float* old = p.old != nullptr && row < p.M ? p.old + (int64_t)row * p.N + w.n0 + c0 : nullptr;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            float4 v = make_float4(__uint_as_float(a[4 * c]), __uint_as_float(a[4 * c + 1]),
-                                   __uint_as_float(a[4 * c + 2]), __uint_as_float(a[4 * c + 3]));
+            float4 v = make_float4(seg_sum[si][4 * c], seg_sum[si][4 * c + 1], seg_sum[si][4 * c + 2],
+                                   seg_sum[si][4 * c + 3]);
             if (old != nullptr && w.n0 + c0 + 4 * c < p.N) {
               const float4 o = *reinterpret_cast<const float4*>(old + 4 * c);
               v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
@@ -554,99 +672,72 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int sw = (lane >> 1) & 3;
           auto at = [&](unsigned char* base, int c) { return reinterpret_cast<uint4*>(base + ((c ^ sw) << 4)); };
           auto pair = [&](int e) { return make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])); };
-          if constexpr (EPI == kEpiAct) {
-            unsigned char* sp = wpre + (m & 1) * kTile + lane * 64;
-            auto run = [&](auto act) {
-              constexpr int ACT = decltype(act)::value;
+          uint32_t o[16];  // the result, packed; a[0..15] receives the second one
+          auto activate = [&](auto act) {
+            constexpr int ACT = decltype(act)::value;
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float4 b0 = reinterpret_cast<const float4*>(wbias + 32 * si)[2 * c];
-                const float4 b1 = reinterpret_cast<const float4*>(wbias + 32 * si)[2 * c + 1];
+            for (int c = 0; c < 4; ++c) {
+              uint4 r = make_uint4(0, 0, 0, 0);
+              if (aux) r = *at(sr, c);
+              const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
+              if constexpr (EPI == kEpiAct) {
+                const float4 b0 = reinterpret_cast<const float4*>(sbias + kPerQuad * kSC * si)[2 * c];
+                const float4 b1 = reinterpret_cast<const float4*>(sbias + kPerQuad * kSC * si)[2 * c + 1];
                 const float2 bb[4] = {make_float2(b0.x, b0.y), make_float2(b0.z, b0.w), make_float2(b1.x, b1.y),
                                       make_float2(b1.z, b1.w)};
-                uint4 r = make_uint4(0, 0, 0, 0);
-                if (p.has_aux) r = *at(sr, c);
-                const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
-                uint32_t o[4], z16[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                   const float2 z = __fadd2_rn(pair(8 * c + 2 * q), bb[q]);
-                  z16[q] = pack_bf16(z.x, z.y);
+                  a[4 * c + q] = pack_bf16(z.x, z.y);
                   float2 y = act_value<ACT>(z);
-                  if (p.has_aux) y = __fadd2_rn(y, unpack_bf16(rr[q]));
-                  o[q] = pack_bf16(y.x, y.y);
+                  if (aux) y = __fadd2_rn(y, unpack_bf16(rr[q]));
+                  o[4 * c + q] = pack_bf16(y.x, y.y);
                 }
-                *at(sr, c) = make_uint4(o[0], o[1], o[2], o[3]);
-                if (p.has_pre) *at(sp, c) = make_uint4(z16[0], z16[1], z16[2], z16[3]);
-              }
-            };
-            switch (p.act) {
-              case SWIN_WATTN_ACT_RELU: run(std::integral_constant<int, SWIN_WATTN_ACT_RELU>()); break;
-              case SWIN_WATTN_ACT_GELU: run(std::integral_constant<int, SWIN_WATTN_ACT_GELU>()); break;
-              case SWIN_WATTN_ACT_GELU_TANH: run(std::integral_constant<int, SWIN_WATTN_ACT_GELU_TANH>()); break;
-              case SWIN_WATTN_ACT_SILU: run(std::integral_constant<int, SWIN_WATTN_ACT_SILU>()); break;
-              default: run(std::integral_constant<int, SWIN_WATTN_ACT_NONE>()); break;
-            }
-          } else if constexpr (EPI == kEpiSlope) {
-            auto run = [&](auto act) {
-              constexpr int ACT = decltype(act)::value;
+              } else {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                uint32_t o[4];
-                if constexpr (ACT == SWIN_WATTN_ACT_NONE) {
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) o[q] = pack_bf16(pair(8 * c + 2 * q).x, pair(8 * c + 2 * q).y);
-                } else {
-                  const uint4 r = *at(sr, c);
-                  const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    const float2 y = __fmul2_rn(pair(8 * c + 2 * q), act_slope<ACT>(unpack_bf16(rr[q])));
-                    o[q] = pack_bf16(y.x, y.y);
-                  }
+                for (int q = 0; q < 4; ++q) {
+                  float2 y = pair(8 * c + 2 * q);
+                  if constexpr (ACT != SWIN_WATTN_ACT_NONE) y = __fmul2_rn(y, act_slope<ACT>(unpack_bf16(rr[q])));
+                  o[4 * c + q] = pack_bf16(y.x, y.y);
                 }
-                *at(sr, c) = make_uint4(o[0], o[1], o[2], o[3]);
               }
-            };
-            switch (p.act) {
-              case SWIN_WATTN_ACT_RELU: run(std::integral_constant<int, SWIN_WATTN_ACT_RELU>()); break;
-              case SWIN_WATTN_ACT_GELU: run(std::integral_constant<int, SWIN_WATTN_ACT_GELU>()); break;
-              case SWIN_WATTN_ACT_GELU_TANH: run(std::integral_constant<int, SWIN_WATTN_ACT_GELU_TANH>()); break;
-              case SWIN_WATTN_ACT_SILU: run(std::integral_constant<int, SWIN_WATTN_ACT_SILU>()); break;
-              default: run(std::integral_constant<int, SWIN_WATTN_ACT_NONE>()); break;
             }
-          } else if constexpr (EPI == kEpiGrad16) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint4 r = make_uint4(0, 0, 0, 0);
-              if (p.has_aux) r = *at(sr, c);
-              const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
-              uint32_t o[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float2 y = __fadd2_rn(pair(8 * c + 2 * q), unpack_bf16(rr[q]));
-                o[q] = pack_bf16(y.x, y.y);
-              }
-              *at(sr, c) = make_uint4(o[0], o[1], o[2], o[3]);
+          };
+          if constexpr (EPI == kEpiAct || EPI == kEpiSlope) {
+            switch (p.act) {
+              case SWIN_WATTN_ACT_RELU: activate(std::integral_constant<int, SWIN_WATTN_ACT_RELU>()); break;
+              case SWIN_WATTN_ACT_GELU: activate(std::integral_constant<int, SWIN_WATTN_ACT_GELU>()); break;
+              case SWIN_WATTN_ACT_GELU_TANH: activate(std::integral_constant<int, SWIN_WATTN_ACT_GELU_TANH>()); break;
+              case SWIN_WATTN_ACT_SILU: activate(std::integral_constant<int, SWIN_WATTN_ACT_SILU>()); break;
+              default: activate(std::integral_constant<int, SWIN_WATTN_ACT_NONE>()); break;
             }
           } else {
-            const bool on_diag = w.n0 + c0 == row0;  // both are multiples of 32
-            const float dg = on_diag ? p.diag : 0.0f;
+            const float dg = w.n0 + c0 == row0 ? p.diag : 0.0f;  // both are multiples of 32
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint4 r = make_uint4(0, 0, 0, 0);
-              if (p.has_aux) r = *at(sr, c);
+              if (aux) r = *at(sr, c);
               const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
-              uint32_t o[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const int e = 8 * c + 2 * q;
-                const float2 d2 = make_float2(lane == e ? dg : 0.0f, lane == e + 1 ? dg : 0.0f);
-                const float2 y = __ffma2_rn(pair(e), splat(p.alpha), __ffma2_rn(unpack_f16(rr[q]), splat(p.beta), d2));
-                o[q] = p.to_bf16 ? pack_bf16(y.x, y.y) : pack_f16(y.x, y.y);
+                if constexpr (EPI == kEpiGrad16) {
+                  const float2 y = __fadd2_rn(pair(e), unpack_bf16(rr[q]));
+                  o[4 * c + q] = pack_bf16(y.x, y.y);
+                } else {
+                  const float2 d2 = make_float2(lane == e ? dg : 0.0f, lane == e + 1 ? dg : 0.0f);
+                  const float2 y = __ffma2_rn(pair(e), splat(p.alpha), __ffma2_rn(unpack_f16(rr[q]), splat(p.beta), d2));
+                  o[4 * c + q] = p.to_bf16 ? pack_bf16(y.x, y.y) : pack_f16(y.x, y.y);
+                }
               }
-              *at(sr, c) = make_uint4(o[0], o[1], o[2], o[3]);
             }
+          }
+          tile_free();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            *at(sr, c) = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            if (EPI == kEpiAct && pre)
+              *at(sz + lane * 64, c) = make_uint4(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
           }
         }
         if (EPI == kEpiStep && p.raw_out != nullptr) {
@@ -657,30 +748,33 @@ __global__ void __launch_bounds__(kThreads, 1)
               p.raw_out[((int64_t)w.b * p.M + row0 + r) * p.N + col] = *reinterpret_cast<const __nv_bfloat16*>(
                   so + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
           __syncwarp();
-          continue;
+        } else {
+          tc::fence_proxy_async();  // the staging tile to the copy engine
+          __syncwarp();
+          if (lane == 0) {
+            store_3d(&out_map, w.n0 + c0, row0, EPI == kEpiGrad32 ? w.split : w.b, smem_u32(so));
+            if (EPI == kEpiAct && pre) store_3d(&pre_map, w.n0 + c0, row0, w.b, smem_u32(sz));
+            tc::bulk_commit();
+          }
         }
-        tc::fence_proxy_async();  // the staging tile to the copy engine
-        __syncwarp();
-        if (lane == 0) {
-          store_3d(&out_map, w.n0 + c0, row0, EPI == kEpiGrad32 ? w.split : w.b, smem_u32(so));
-          if (EPI == kEpiAct && p.has_pre)
-            store_3d(&pre_map, w.n0 + c0, row0, w.b, smem_u32(wpre + (m & 1) * kTile));
-          tc::bulk_commit();
+        ++m;
+        if (++tile == NB) {
+          tile = 0;
+          aux_phase ^= 1;
         }
       }
       if (bad) break;
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (CG == 2)
-          arrive_cluster(map_to_rank(dfree_bar(buf), 0));
-        else
-          tc::mbar_arrive(dfree_bar(buf));
-      }
+      if constexpr (EPI != kEpiGrad32) release();
     }
     if constexpr (kHasAux) {
       // after a timeout: the loads still in flight land before the CTA leaves
-      for (int q = m; q < issued; ++q) warp_wait(aux0 + 8 * (q % 3), (q / 3) & 1, p.wait_ns);
+      for (; m < issued; ++m) {
+        warp_wait(aux0 + 8 * tile, aux_phase, p.wait_ns);
+        if (++tile == NB) {
+          tile = 0;
+          aux_phase ^= 1;
+        }
+      }
     }
     if (lane == 0) tc::bulk_wait_all();
   }
@@ -697,6 +791,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 // One GB300: 152 SMs, 76 pairs. The tile choice is made for that and does not ask the
 // device, so that workspace sizes depend on the shape alone.
 constexpr int kSms = 152;
+
+// What a launch asks of the current device; read once per device.
+struct DeviceInfo {
+  int device, smem_max, sms;
+};
+inline cudaError_t device_info(DeviceInfo* d) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];  // 0, or SMs * 2^20 + shared memory per block
+  cudaError_t e = cudaGetDevice(&d->device);
+  if (e != cudaSuccess) return e;
+  const int slot = d->device < kDevices ? d->device : -1;
+  const int k = slot >= 0 ? known[slot].load(std::memory_order_relaxed) : 0;
+  if (k != 0) {
+    d->smem_max = k & 0xfffff;
+    d->sms = k >> 20;
+    return cudaSuccess;
+  }
+  e = cudaDeviceGetAttribute(&d->smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, d->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->device);
+  if (e == cudaSuccess && slot >= 0 && d->sms < 2048 && d->smem_max < (1 << 20))
+    known[slot].store(d->sms << 20 | d->smem_max, std::memory_order_relaxed);
+  return e;
+}
+// Raise a kernel's dynamic shared memory limit, once per device (64 of them remembered).
+inline cudaError_t allow_smem(const void* kern, int bytes, int device, std::atomic<uint64_t>* allowed) {
+  const uint64_t bit = device < 64 ? 1ull << device : 0;
+  if (allowed->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) allowed->fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // A matrix stack [batch, rows, cols], row-major, `ld` elements from row to row.
 struct Matrix {
@@ -739,7 +864,7 @@ inline double tiling_cost(const Tiling& t, int64_t M, int64_t N, int batch) {
 }
 
 // The cheapest tiling. `max_splits` > 1 allows K to be split into partial results.
-inline Tiling choose_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn, int max_splits, int max_cg) {
+inline Tiling search_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn, int max_splits, int max_cg) {
   Tiling best{};
   double best_cost = -1.0;
   const int chunks = (int)((K + kKC - 1) / kKC);
@@ -768,6 +893,29 @@ inline Tiling choose_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn
   }
   return best;
 }
+
+// The same, with the calling thread's last choices remembered by their sizes (a search
+// compares some hundred tilings, which is more than a small launch takes).
+inline Tiling choose_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn, int max_splits, int max_cg) {
+  struct Entry {
+    int64_t key[7];
+    Tiling t;
+  };
+  constexpr int kEntries = 64;
+  thread_local Entry cache[kEntries] = {};
+  const int64_t key[7] = {M, N, K, batch, bmn, max_splits, max_cg};
+  uint64_t h = 0;
+  for (const int64_t k : key) h = (h ^ (uint64_t)k) * 0x9E3779B97F4A7C15ull;
+  Entry& c = cache[h >> 58];
+  if (!std::equal(key, key + 7, c.key)) {
+    c.t = search_tiling(M, N, K, batch, bmn, max_splits, max_cg);
+    std::copy(key, key + 7, c.key);
+  }
+  return c.t;
+}
+
+// Chunks of K from which K is long.
+constexpr int kLongK = 20;
 
 struct Extra {
   const Matrix* aux = nullptr;
@@ -820,28 +968,35 @@ cudaError_t launch_tiles(const Tiling& t, Params p, const Matrix& a, const Matri
   p.idesc = tc::idesc_bf16(CG * kBM, t.NT, BMN, AMN) ^ fmt;
   p.idesc_ones = tc::idesc_bf16(CG * kBM, 16 * CG, false, AMN) ^ fmt;
   p.stage_bytes = kABytes + t.NT / CG * 128;
-  const bool small_corner = EPI == kEpiAct;
-  p.warp_bytes = out_tiles(EPI) * kTile + (p.has_pre ? 2 * kTile : 0) + (small_corner ? 512 : 0);
-  // the staging tiles' swizzle wants 1024-byte (fp32) or 512-byte alignment
-  const int fixed = kEpiWarps * p.warp_bytes + 512 + 8 * kNBar + 16 + 1024;
-  int dev = 0, smem_max = 0, sms = 0;
-  e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  DeviceInfo di;
+  e = device_info(&di);
   if (e != cudaSuccess) return e;
-  p.stages = std::min(kMaxStages, (smem_max - fixed) / p.stage_bytes);
+  const int smem_max = di.smem_max, sms = di.sms;
+  constexpr int kEW = epi_warps(EPI);
+  // the bias of two tiles, or the ones that sum A over K
+  constexpr int kSmall = EPI == kEpiAct ? 2 * kMaxNT * 4 : EPI == kEpiGrad32 || EPI == kEpiGrad16 ? 512 : 0;
+  const bool long_k = t.chunks_per_split >= kLongK;
+  int fixed = 0;
+  p.tiles = p.has_aux ? (p.has_pre || long_k ? 2 : kMaxAuxTiles) : (p.has_pre || long_k ? 1 : 2);
+  for (;; --p.tiles) {  // fewer aux tiles where the ring would not have three stages
+    p.warp_bytes = (p.tiles + (p.has_pre ? 1 : 0)) * kTile;
+    fixed = kEW * p.warp_bytes + kSmall + 8 * kNBar + 16;
+    p.stages = std::min(kMaxStages, (smem_max - fixed) / p.stage_bytes);
+    if (p.stages >= 3 || p.tiles <= 2) break;
+  }
   if (p.stages < 2) return cudaErrorInvalidConfiguration;
   p.off_out = p.stages * p.stage_bytes;
-  p.off_ones = p.off_out + kEpiWarps * p.warp_bytes;
-  p.off_bar = p.off_ones + 512;
+  p.off_small = p.off_out + kEW * p.warp_bytes;
+  p.off_bar = p.off_small + kSmall;
   // more than half of an SM's shared memory: one CTA per SM, so the tensor memory is free
   const int smem = std::max(120 * 1024, p.off_out + fixed);
   auto kern = product_kernel<CG, AMN, BMN, EPI>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};  // devices whose limit has been raised
+  e = allow_smem(reinterpret_cast<const void*>(kern), smem_max, di.device, &allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, sms / CG)));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(n_threads(EPI));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
