@@ -11,6 +11,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libswin_wattn.so")
 
@@ -323,11 +325,22 @@ def swin_wattn_orthogonalize(g_ptr, out_ptr, count, rows, cols, dtype, steps, ep
                                            workspace_bytes, status_ptr, stream)
 
 
+# The wrappers of the MLP's products and the weight update check their tensors: a small product
+# is over in a few microseconds, so the checks compare attributes first and look for the
+# reason only when one differs.
+
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_F32_BF16 = (torch.float32, torch.bfloat16)
+_U8 = (torch.uint8,)
+_I32 = (torch.int32,)
+
+
 def _tensor(name, t, shape, dtypes, device):
-    """Check one operand of the MLP's products and the weight update: a contiguous CUDA
-    tensor of the given shape, one of the given dtypes, on `device`."""
+    """Check one operand: a contiguous CUDA tensor of the given shape, one of the given dtypes,
+    on `device`. Returns its address."""
     if t.device == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
-        return
+        return t.data_ptr()
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if t.dtype not in dtypes:
@@ -343,32 +356,23 @@ def _device_of(name, t):
     return t.device
 
 
-def _call(where, fn, device, stream, status, *args):
-    """fn(*args, status, stream) with `device` current, on `stream` or that device's current
-    stream; raises on an error status."""
-    import torch
-    st = None
-    if status is not None:
-        _tensor("status", status, (1,), (torch.int32,), device)
-        st = status.data_ptr()
-    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+def _call(fn, device, stream, status, *args):
+    """The C function fn(*args, status, stream) with `device` current, on `stream` or that
+    device's current stream; raises on an error status."""
+    st = None if status is None else _tensor("status", status, (1,), _I32, device)
+    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
     if device.index == torch.cuda.current_device():
         rc = fn(*args, st, handle)
     else:
         with torch.cuda.device(device):
             rc = fn(*args, st, handle)
     if rc != OK:
-        raise SwinWAttnError(where, rc)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+        raise SwinWAttnError(fn.__name__, rc)
 
 
 def _empty(shape, dtype, device, stream):
     """A tensor of `stream`'s own memory pool (of the device's current stream without one),
     so that it may be used and freed in that stream's order."""
-    import torch
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
@@ -382,29 +386,37 @@ def _act_code(act):
     return code
 
 
+def _weight(w, device):
+    if w.dim() != 2:
+        raise ValueError(f"w has {w.dim()} dimensions, not 2")
+    N, K = w.shape
+    return N, K, _tensor("w", w, (N, K), _BF16, device)
+
+
+def _rows(name, t, width, device):
+    """Check a bf16 [..., width] tensor; returns its leading axes and its address."""
+    lead = t.shape[:-1]
+    return lead, _tensor(name, t, (*lead, width), _BF16, device)
+
+
 def linear(x, w, b=None, act=ACT_NONE, residual=None, y=None, pre=None, status=None, stream=None):
     """residual + act(x W^T + b) over the last axis of the bf16 CUDA tensor x [..., K] with
     W [N, K] bf16 and b [N] fp32 (or None), into a bf16 [..., N] tensor (allocated here when
     not given; it may be the residual itself). act: "none", "relu", "gelu", "gelu_tanh",
     "silu" or an ACT_ code. pre, a bf16 [..., N] tensor, receives x W^T + b for the backward."""
-    import torch
-    dev, bf16 = _device_of("x", x), (torch.bfloat16,)
+    dev = _device_of("x", x)
     code = _act_code(act)
-    if w.dim() != 2:
-        raise ValueError(f"w has {w.dim()} dimensions, not 2")
-    N, K = w.shape
-    lead = x.shape[:-1]
-    _tensor("x", x, lead + (K,), bf16, dev)
-    _tensor("w", w, (N, K), bf16, dev)
-    if b is not None:
-        _tensor("b", b, (N,), (torch.float32,), dev)
+    N, K, w_ptr = _weight(w, dev)
+    lead, x_ptr = _rows("x", x, K, dev)
+    shape = (*lead, N)
+    b_ptr = None if b is None else _tensor("b", b, (N,), _F32, dev)
+    r_ptr = None if residual is None else _tensor("residual", residual, shape, _BF16, dev)
+    p_ptr = None if pre is None else _tensor("pre", pre, shape, _BF16, dev)
     if y is None:
-        y = _empty(lead + (N,), torch.bfloat16, dev, stream)
-    for name, t in (("residual", residual), ("y", y), ("pre", pre)):
-        if t is not None:
-            _tensor(name, t, lead + (N,), bf16, dev)
-    _call("swin_wattn_linear", load().swin_wattn_linear, dev, stream, status, x.data_ptr(), w.data_ptr(), _ptr(b),
-          _ptr(residual), y.data_ptr(), _ptr(pre), lead.numel(), K, N, code)
+        y = _empty(shape, torch.bfloat16, dev, stream)
+    y_ptr = _tensor("y", y, shape, _BF16, dev)
+    _call(load().swin_wattn_linear, dev, stream, status, x_ptr, w_ptr, b_ptr, r_ptr, y_ptr, p_ptr, lead.numel(), K, N,
+          code)
     return y
 
 
@@ -412,24 +424,19 @@ def linear_bwd_data(dy, w, pre=None, act=ACT_NONE, dx=None, status=None, stream=
     """(dy W) * act'(pre) for dy [..., N] and W [N, K], into a bf16 [..., K] tensor (allocated
     here when not given; it may be pre itself): with act "none" the gradient of the product's
     input, else of the pre-activation [..., K] whose activation that input was."""
-    import torch
-    dev, bf16 = _device_of("dy", dy), (torch.bfloat16,)
+    dev = _device_of("dy", dy)
     code = _act_code(act)
-    if w.dim() != 2:
-        raise ValueError(f"w has {w.dim()} dimensions, not 2")
-    N, K = w.shape
-    lead = dy.shape[:-1]
-    _tensor("dy", dy, lead + (N,), bf16, dev)
-    _tensor("w", w, (N, K), bf16, dev)
+    N, K, w_ptr = _weight(w, dev)
+    lead, dy_ptr = _rows("dy", dy, N, dev)
+    shape = (*lead, K)
     if code != ACT_NONE and pre is None:
         raise ValueError("an activation needs its pre-activation: pre is None")
+    p_ptr = None if pre is None else _tensor("pre", pre, shape, _BF16, dev)
     if dx is None:
-        dx = _empty(lead + (K,), torch.bfloat16, dev, stream)
-    for name, t in (("pre", pre), ("dx", dx)):
-        if t is not None:
-            _tensor(name, t, lead + (K,), bf16, dev)
-    _call("swin_wattn_linear_bwd_data", load().swin_wattn_linear_bwd_data, dev, stream, status, dy.data_ptr(),
-          w.data_ptr(), _ptr(pre), dx.data_ptr(), lead.numel(), K, N, code)
+        dx = _empty(shape, torch.bfloat16, dev, stream)
+    dx_ptr = _tensor("dx", dx, shape, _BF16, dev)
+    _call(load().swin_wattn_linear_bwd_data, dev, stream, status, dy_ptr, w_ptr, p_ptr, dx_ptr, lead.numel(), K, N,
+          code)
     return dx
 
 
@@ -439,28 +446,25 @@ def linear_bwd_weight(dy, x, dw=None, db=None, accumulate=False, workspace=None,
     to add to; without dw both are allocated here, in fp32; with dw alone there is no db.
     workspace: a uint8 tensor of swin_wattn_linear_bwd_weight_workspace_bytes (allocated here
     when not given). Returns (dw, db)."""
-    import torch
-    dev, bf16 = _device_of("dy", dy), (torch.bfloat16,)
-    lead, N, K = dy.shape[:-1], dy.shape[-1], x.shape[-1]
-    _tensor("dy", dy, lead + (N,), bf16, dev)
-    _tensor("x", x, lead + (K,), bf16, dev)
+    dev = _device_of("dy", dy)
+    N, K = dy.shape[-1], x.shape[-1]
+    lead, dy_ptr = _rows("dy", dy, N, dev)
+    x_ptr = _tensor("x", x, (*lead, K), _BF16, dev)
     if dw is None:
         if accumulate:
             raise ValueError("accumulate needs the dw to add to")
         dw = _empty((N, K), torch.float32, dev, stream)
         db = _empty((N,), torch.float32, dev, stream) if db is None else db
-    _tensor("dw", dw, (N, K), (torch.float32, torch.bfloat16), dev)
-    if db is not None:
-        _tensor("db", db, (N,), (torch.float32,), dev)
+    dw_ptr = _tensor("dw", dw, (N, K), _F32_BF16, dev)
+    db_ptr = None if db is None else _tensor("db", db, (N,), _F32, dev)
     tokens = lead.numel()
     if workspace is None:
         workspace = _empty((max(swin_wattn_linear_bwd_weight_workspace_bytes(tokens, K, N), 1),), torch.uint8, dev,
                            stream)
-    _tensor("workspace", workspace, (workspace.numel(),), (torch.uint8,), dev)
-    code = FP32 if dw.dtype == torch.float32 else BF16
-    _call("swin_wattn_linear_bwd_weight", load().swin_wattn_linear_bwd_weight, dev, stream, status, dy.data_ptr(),
-          x.data_ptr(), dw.data_ptr(), _ptr(db), tokens, K, N, code, 1 if accumulate else 0, workspace.data_ptr(),
-          workspace.numel())
+    nbytes = workspace.numel()
+    ws_ptr = _tensor("workspace", workspace, (nbytes,), _U8, dev)
+    _call(load().swin_wattn_linear_bwd_weight, dev, stream, status, dy_ptr, x_ptr, dw_ptr, db_ptr, tokens, K, N,
+          FP32 if dw.dtype == torch.float32 else BF16, 1 if accumulate else 0, ws_ptr, nbytes)
     return dw, db
 
 
@@ -469,23 +473,21 @@ def orthogonalize(g, steps=5, eps=1e-7, scale=1.0, out=None, workspace=None, sta
     the fp32 or bf16 CUDA tensor g [rows, cols] or [count, rows, cols], into a bf16 tensor of
     its shape (allocated here when not given). workspace: a uint8 tensor of
     swin_wattn_orthogonalize_workspace_bytes (allocated here when not given)."""
-    import torch
     dev = _device_of("g", g)
     if g.dim() not in (2, 3):
         raise ValueError(f"g has {g.dim()} dimensions, not 2 or 3")
-    _tensor("g", g, g.shape, (torch.float32, torch.bfloat16), dev)
+    g_ptr = _tensor("g", g, g.shape, _F32_BF16, dev)
     count, (rows, cols) = (1 if g.dim() == 2 else g.shape[0]), g.shape[-2:]
     if out is None:
         out = _empty(g.shape, torch.bfloat16, dev, stream)
-    _tensor("out", out, g.shape, (torch.bfloat16,), dev)
+    out_ptr = _tensor("out", out, g.shape, _BF16, dev)
     if workspace is None:
         workspace = _empty((max(swin_wattn_orthogonalize_workspace_bytes(count, rows, cols), 1),), torch.uint8, dev,
                            stream)
-    _tensor("workspace", workspace, (workspace.numel(),), (torch.uint8,), dev)
-    code = FP32 if g.dtype == torch.float32 else BF16
-    _call("swin_wattn_orthogonalize", load().swin_wattn_orthogonalize, dev, stream, status, g.data_ptr(),
-          out.data_ptr(), count, rows, cols, code, int(steps), float(eps), float(scale), workspace.data_ptr(),
-          workspace.numel())
+    nbytes = workspace.numel()
+    ws_ptr = _tensor("workspace", workspace, (nbytes,), _U8, dev)
+    _call(load().swin_wattn_orthogonalize, dev, stream, status, g_ptr, out_ptr, count, rows, cols,
+          FP32 if g.dtype == torch.float32 else BF16, int(steps), float(eps), float(scale), ws_ptr, nbytes)
     return out
 
 

@@ -37,32 +37,43 @@ constexpr CUtensorMapDataType kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 
 constexpr int kNormThreads = 256;
-constexpr int kNormBlocks = 64;  // partial sums per matrix at most
+constexpr int kNormBlocks = 256;  // partial sums per matrix at most
 
-// Blocks that sum one matrix: 4096 elements each at least.
-int norm_blocks(int64_t elements) { return (int)std::max<int64_t>(1, std::min<int64_t>(kNormBlocks, elements / 4096)); }
+// Blocks per matrix: four per SM over the stack, of 2048 elements each at least.
+int norm_blocks(int64_t elements, int count) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>({kNormBlocks, (elements + 2047) / 2048, (4 * prod::kSms + count - 1) / count}));
+}
 
 __device__ __forceinline__ float load_f32(const float* p) { return *p; }
 __device__ __forceinline__ float load_f32(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-
-// Sum of squares of a block's share of one matrix as two sums, of the values below 2^48
-// and, times 2^-64, of the others, so that neither overflows where the norm does not.
-template <typename T>
-__global__ void __launch_bounds__(kNormThreads) norm_partial_kernel(const T* __restrict__ g, int64_t elements,
-                                                                    float2* __restrict__ partial) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const T* x = g + (int64_t)blockIdx.y * elements;
-  float lo = 0.0f, hi = 0.0f;
-  for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < elements; i += (int64_t)gridDim.x * kNormThreads) {
-    const float v = load_f32(x + i);
-    if (fabsf(v) < 281474976710656.0f) {
-      lo = fmaf(v, v, lo);
-    } else {  // NaN and infinity too
-      const float s = v * 5.421010862427522e-20f;
-      hi = fmaf(s, s, hi);
-    }
+// Eight consecutive values, 16-byte aligned.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = prod::unpack_bf16(in[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
   }
+}
+
+// Squares are summed apart for values below 2^48 (lo) and, times 2^-64, for the others (hi:
+// NaN and infinity too), so that neither sum overflows where the norm does not.
+__device__ __forceinline__ void add_square(float v, float& lo, float& hi) {
+  if (fabsf(v) < 281474976710656.0f) {
+    lo = fmaf(v, v, lo);
+  } else {
+    const float s = v * 5.421010862427522e-20f;
+    hi = fmaf(s, s, hi);
+  }
+}
+// Sum over the block of both; the result in every thread of the first warp.
+__device__ __forceinline__ float2 block_sum(float lo, float hi) {
   __shared__ float2 part[kNormThreads / 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -71,49 +82,81 @@ __global__ void __launch_bounds__(kNormThreads) norm_partial_kernel(const T* __r
   }
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(lo, hi);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kNormThreads / 32; ++w) {
-      lo += part[w].x;
-      hi += part[w].y;
-    }
-    partial[blockIdx.y * gridDim.x + blockIdx.x] = make_float2(lo, hi);
+  lo = hi = 0.0f;
+  for (int w = 0; w < kNormThreads / 32; ++w) {
+    lo += part[w].x;
+    hi += part[w].y;
   }
+  return make_float2(lo, hi);
+}
+
+// Sum of squares of a block's share of one matrix. `vec`: every matrix starts on a 16-byte
+// boundary and holds a multiple of eight elements, which are then read eight at a time, four
+// such reads in flight.
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads) norm_partial_kernel(const T* __restrict__ g, int64_t elements, bool vec,
+                                                                    float2* __restrict__ partial) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const T* x = g + (int64_t)blockIdx.y * elements;
+  const int64_t first = (int64_t)blockIdx.x * kNormThreads + threadIdx.x, stride = (int64_t)gridDim.x * kNormThreads;
+  float lo = 0.0f, hi = 0.0f;
+  if (vec) {
+    const int64_t n8 = elements / 8;
+    int64_t i = first;
+    for (; i + 3 * stride < n8; i += 4 * stride) {
+      float v[4][8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) load8(x + (i + u * stride) * 8, v[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) add_square(v[u][e], lo, hi);
+    }
+    for (; i < n8; i += stride) {
+      float v[8];
+      load8(x + i * 8, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) add_square(v[e], lo, hi);
+    }
+  } else {
+    for (int64_t i = first; i < elements; i += stride) add_square(load_f32(x + i), lo, hi);
+  }
+  const float2 s = block_sum(lo, hi);
+  if (threadIdx.x == 0) partial[blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
 // X = G / (|G| + eps), times 2^8, in fp16 rows of ld elements.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) normalize_kernel(const T* __restrict__ g, int rows, int cols, int ld,
-                                                                 const float2* __restrict__ partial, int n_partial,
-                                                                 float eps, __half* __restrict__ x) {
+                                                                 bool vec, const float2* __restrict__ partial,
+                                                                 int n_partial, float eps, __half* __restrict__ x) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ float s_inv;
-  if (threadIdx.x < 32) {
-    float lo = 0.0f, hi = 0.0f;
-    for (int i = threadIdx.x; i < n_partial; i += 32) {
-      const float2 v = partial[blockIdx.y * n_partial + i];
-      lo += v.x;
-      hi += v.y;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      lo += __shfl_xor_sync(0xffffffffu, lo, o);
-      hi += __shfl_xor_sync(0xffffffffu, hi, o);
-    }
-    if (threadIdx.x == 0) {
-      // |G| of both sums; where the second is not empty the first is added in its scale
-      const float norm = hi == 0.0f ? sqrtf(lo) : sqrtf(hi + lo * 5.421010862427522e-20f * 5.421010862427522e-20f) * 18446744073709551616.0f;
-      s_inv = norm + eps;
-    }
-  }
-  __syncthreads();
-  const float inv = kScale / s_inv;
+  const float2 p = (int)threadIdx.x < n_partial ? partial[blockIdx.y * n_partial + threadIdx.x] : make_float2(0.0f, 0.0f);
+  const float2 s = block_sum(p.x, p.y);
+  // |G| of both sums; where the second is not empty the first is added in its scale
+  const float norm = s.y == 0.0f ? sqrtf(s.x)
+                                 : sqrtf(s.y + s.x * 5.421010862427522e-20f * 5.421010862427522e-20f) * 18446744073709551616.0f;
+  const float inv = kScale / (norm + eps);
   const int64_t elements = (int64_t)rows * cols;
   const T* gm = g + (int64_t)blockIdx.y * elements;
   __half* xm = x + (int64_t)blockIdx.y * rows * ld;
-  for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < elements; i += (int64_t)gridDim.x * kNormThreads) {
-    const int r = (int)(i / cols), c = (int)(i - (int64_t)r * cols);
-    xm[(int64_t)r * ld + c] = __float2half_rn(load_f32(gm + i) * inv);
+  if (vec && ld == cols) {
+    const int64_t n8 = elements / 8, stride = (int64_t)gridDim.x * kNormThreads;
+#pragma unroll 4
+    for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < n8; i += stride) {
+      float v[8];
+      load8(gm + i * 8, v);
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = prod::pack_f16(v[2 * e] * inv, v[2 * e + 1] * inv);
+      reinterpret_cast<uint4*>(xm)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  } else {
+    const int wpb = kNormThreads / 32, lane = threadIdx.x & 31;
+    for (int r = blockIdx.x * wpb + (threadIdx.x >> 5); r < rows; r += gridDim.x * wpb)
+      for (int c = lane; c < cols; c += 32) xm[(int64_t)r * ld + c] = __float2half_rn(load_f32(gm + (int64_t)r * cols + c) * inv);
   }
 }
 
@@ -140,10 +183,11 @@ template <typename T>
 cudaError_t normalize(const T* g, int count, int rows, int cols, float eps, float2* partial, __half* x, int ld,
                       cudaStream_t st) {
   const int64_t elements = (int64_t)rows * cols;
-  const int nb = norm_blocks(elements);
-  cudaError_t e = launch_pdl(norm_partial_kernel<T>, dim3(nb, count), dim3(kNormThreads), 0, st, g, elements, partial);
+  const int nb = norm_blocks(elements, count);
+  const bool vec = elements % 8 == 0 && reinterpret_cast<uintptr_t>(g) % 16 == 0;
+  cudaError_t e = launch_pdl(norm_partial_kernel<T>, dim3(nb, count), dim3(kNormThreads), 0, st, g, elements, vec, partial);
   if (e != cudaSuccess) return e;
-  return launch_pdl(normalize_kernel<T>, dim3(nb, count), dim3(kNormThreads), 0, st, g, rows, cols, ld,
+  return launch_pdl(normalize_kernel<T>, dim3(nb, count), dim3(kNormThreads), 0, st, g, rows, cols, ld, vec,
                     (const float2*)partial, nb, eps, x);
 }
 
