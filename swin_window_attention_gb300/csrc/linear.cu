@@ -14,7 +14,16 @@
 
 namespace swin {
 
+cudaError_t linear_few_launch(const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
+                              int T, int K, int N, int act, int* status, cudaStream_t st);
+cudaError_t linear_bwd_data_few_launch(const void* dy, const void* w, const void* pre, void* dx, int T, int K, int N,
+                                       int act, int* status, cudaStream_t st);
+
 namespace {
+
+// Up to this many tokens the weight is read by linear_few.cu's clusters, above it the tokens
+// fill the tiles of product.cuh.
+constexpr int kFewTokens = 128;
 
 using prod::Matrix;
 using prod::Params;
@@ -72,6 +81,7 @@ Tiling weight_tiling(int64_t T, int K, int N) { return prod::choose_tiling(N, K,
 
 cudaError_t linear_launch(const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
                           int T, int K, int N, int act, int* status, cudaStream_t st) {
+  if (T <= kFewTokens) return linear_few_launch(x, w, b, residual, y, pre, T, K, N, act, status, st);
   const Tiling t = prod::choose_tiling(T, N, K, 1, false, 1, 2);
   Params p{};
   p.M = T;
@@ -89,6 +99,7 @@ cudaError_t linear_launch(const void* x, const void* w, const float* b, const vo
 
 cudaError_t linear_bwd_data_launch(const void* dy, const void* w, const void* pre, void* dx, int T, int K, int N,
                                    int act, int* status, cudaStream_t st) {
+  if (T <= kFewTokens) return linear_bwd_data_few_launch(dy, w, pre, dx, T, K, N, act, status, st);
   const Tiling t = prod::choose_tiling(T, K, N, 1, true, 1, 2);
   Params p{};
   p.M = T;

@@ -102,6 +102,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 __device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 // The address, in the cluster's shared memory, of this CTA's address `addr` in CTA `rank`.
@@ -137,7 +138,7 @@ __device__ __forceinline__ void store_3d(const CUtensorMap* map, int c0, int c1,
 
 // D[tmem] (+)= A B^T; a and b are the low words of the operands' descriptors, *_hi the high
 // ones. (One thread issues every MMA: building whole descriptors there, some twenty
-// instructions each, took it longer than the tensor core takes for a chunk.)
+// instructions each, took 700 clocks a chunk where the tensor core takes 512 at N = 256.)
 template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc,
                                     bool accumulate) {
@@ -153,6 +154,14 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t a_hi, uint3
         " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d),
         "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
+}
+// True in one lane of a converged warp. The MMA loop runs in the whole warp, with only the
+// issue in this lane: the compiler then knows the operands uniform and keeps them in uniform
+// registers (a chunk of four MMAs issues in 180 clocks; in a one-thread loop, in 260).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(r));
+  return r != 0;
 }
 // The words of a descriptor (tc::sdesc): low, address and lbo; high, sbo, version and layout.
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3FFFu) | (lbo >> 4) << 16; }
@@ -343,7 +352,7 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
   constexpr int kPerQuad = kEW / 4, kSlices = kMaxNT / kSC / kPerQuad;  // warps per quadrant, slices per warp
   constexpr bool kSums = EPI == kEpiGrad32 || EPI == kEpiGrad16;
   constexpr int kSeg = EPI == kEpiGrad32 ? kSegChunks : 1 << 30;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rank = CG == 2 ? (int)cluster_rank() : 0;
   const int group = blockIdx.x / CG, n_groups = gridDim.x / CG;
 
@@ -389,7 +398,7 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
   __syncthreads();
   if constexpr (CG == 2) cluster_sync_all();
   tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   // The prologue above touches only this CTA's shared and tensor memory, so it may overlap
   // the previous kernel on the stream; every global access comes after this wait.
   pdl_wait();
@@ -441,13 +450,15 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
       }
       __syncwarp();
     } else if (warp == kMMA) {
-      if (rank == 0 && lane == 0) {
+      if (rank == 0) {
         constexpr uint32_t kHi = desc_hi(1024, kSW128), kOnesHi = desc_hi(256, 0);
         // along K by 16: K-major, 32 bytes further in the 128-byte row; MN-major, 16 rows
         // further, blocks of 64 of M or N 8192 bytes apart
         constexpr uint32_t kAStep = (AMN ? 2048 : 32) >> 4, kBStep = (BMN ? 2048 : 32) >> 4;
         const uint32_t a0 = desc_lo(smem0, AMN ? 8192 : 16), b0 = desc_lo(smem0 + kABytes, BMN ? 8192 : 16);
         const uint32_t ones_lo = desc_lo(smem0 + p.off_small, 128);
+        const uint32_t stage_step = p.stage_bytes >> 4, idesc = p.idesc;
+        [[maybe_unused]] const uint32_t idesc_ones = p.idesc_ones;
         int st = 0, g = 0;  // ring stage; accumulations begun
         uint32_t ph = 0;
         bool prev_ones = false;
@@ -461,35 +472,38 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
             const int s1 = min(s0 + kSeg, w.c1), buf = g & 1;
             const uint32_t acc = tmem + buf * kMaxNT;
             const uint32_t sums = ones_aside ? tmem + (buf ^ 1) * kMaxNT : acc + p.NT;
-            if (g >= 2 && !wait(dfree_bar(buf), ((g >> 1) - 1) & 1, p.wait_ns)) {
+            if (g >= 2 && !warp_wait(dfree_bar(buf), ((g >> 1) - 1) & 1, p.wait_ns)) {
               bad = 1;
               break;
             }
             // where the other accumulator holds sums, its own epilogue has to be over before,
             // and this one's before the next begins
-            if (g >= 1 && (ones_aside || prev_ones) && !wait(dfree_bar(buf ^ 1), ((g - 1) >> 1) & 1, p.wait_ns)) {
+            if (g >= 1 && (ones_aside || prev_ones) && !warp_wait(dfree_bar(buf ^ 1), ((g - 1) >> 1) & 1, p.wait_ns)) {
               bad = 1;
               break;
             }
             prev_ones = ones_aside;
             for (int c = s0; c < s1; ++c) {
-              if (!wait(full_bar(st), ph, p.wait_ns)) {
+              if (!warp_wait(full_bar(st), ph, p.wait_ns)) {
                 bad = 1;
                 break;
               }
               tc::fence_after_sync();
-              const uint32_t step = st * (p.stage_bytes >> 4);
+              const uint32_t a = a0 + st * stage_step, b = b0 + st * stage_step;
+              if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                mma<CG>(acc, a0 + step + kk * kAStep, kHi, b0 + step + kk * kBStep, kHi, p.idesc, c > s0 || kk > 0);
-                if (kSums && ones)
-                  mma<CG>(sums, a0 + step + kk * kAStep, kHi, ones_lo, kOnesHi, p.idesc_ones, c > s0 || kk > 0);
-              }
-              commit<CG>(empty_bar(st));
+                for (int kk = 0; kk < 4; ++kk) {
+                  mma<CG>(acc, a + kk * kAStep, kHi, b + kk * kBStep, kHi, idesc, c > s0 || kk > 0);
+                  if (kSums && ones)
+                    mma<CG>(sums, a + kk * kAStep, kHi, ones_lo, kOnesHi, idesc_ones, c > s0 || kk > 0);
+                }
+                commit<CG>(empty_bar(st));
 #ifdef SWIN_WATTN_FAULT_INJECTION
-              if (!(p.fault == kFaultGemm && g == 0))
+                if (!(p.fault == kFaultGemm && g == 0))
 #endif
-                if (c == s1 - 1) commit<CG>(dfull_bar(buf));
+                  if (c == s1 - 1) commit<CG>(dfull_bar(buf));
+              }
+              __syncwarp();
               if (++st == stages) {
                 st = 0;
                 ph ^= 1;
@@ -498,8 +512,9 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
           }
         }
         // every MMA issued has completed before the tensor memory is released
-        commit<CG>(bar0 + 8 * kDrain);
-        if (!wait(bar0 + 8 * kDrain, 0, p.wait_ns)) bad = 1;
+        if (elect_one()) commit<CG>(bar0 + 8 * kDrain);
+        __syncwarp();
+        if (!warp_wait(bar0 + 8 * kDrain, 0, p.wait_ns)) bad = 1;
       }
       __syncwarp();
     }
