@@ -208,7 +208,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
           if (s < S) {
             float v[kBatch];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) v[u] = load_cluster(peer[s] + min(t0 + u * step, p.TN - 1) * (kBM * 4));
+            for (int u = 0; u < kBatch; ++u) {
+              v[u] = 0.0f;
+              if (t0 + u * step < tokens) v[u] = load_cluster(peer[s] + (t0 + u * step) * (kBM * 4));
+            }
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) acc[u] += v[u];
           }

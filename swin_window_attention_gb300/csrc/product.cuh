@@ -73,10 +73,24 @@ enum Epi {
 __host__ __device__ constexpr int epi_warps(int epi) { return epi == kEpiGrad32 ? 8 : 16; }
 __host__ __device__ constexpr int n_threads(int epi) { return epi == kEpiGrad32 ? 384 : 576; }
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1: n / d = (umulhi(n, mul) + n) >> shift. (The
+// plain divisions of an item's number cost every epilogue warp a hundred instructions a tile,
+// as many as a slice's own work.)
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t divisor) : d(divisor), shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 struct Params {
   int M, N, NT;
-  int n_mt, n_nt, n_items;  // items: batch * splits * n_mt * n_nt, n fastest
-  int chunks, chunks_per_split, splits;
+  FastDiv n_mt, n_nt, n_splits;
+  int n_items;  // batch * splits * n_mt * n_nt, n fastest
+  int chunks, chunks_per_split;
   int stages, stage_bytes;
   int off_out, warp_bytes, tiles, off_small, off_bar;  // tiles: a warp's staging tiles before that of pre
   uint32_t idesc, idesc_ones;
@@ -112,7 +126,7 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   return r;
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t mbar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(mbar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(mbar) : "memory");
 }
 
 template <int CG>
@@ -362,12 +376,11 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
   };
   auto decode = [&](int it) {
     Item w;
-    w.nt = it % p.n_nt;
-    int r = it / p.n_nt;
-    const int mt = r % p.n_mt;
-    r /= p.n_mt;
-    w.split = r % p.splits;
-    w.b = r / p.splits;
+    const uint32_t r1 = p.n_nt.quotient(it), r2 = p.n_mt.quotient(r1);
+    w.nt = it - r1 * p.n_nt.d;
+    const int mt = r1 - r2 * p.n_mt.d;
+    w.b = p.n_splits.quotient(r2);
+    w.split = r2 - w.b * p.n_splits.d;
     w.m0 = (mt * CG + rank) * kBM;
     w.n0 = w.nt * p.NT;
     w.c0 = w.split * p.chunks_per_split;
@@ -865,15 +878,16 @@ struct Tiling {
 // Estimated time, in SM clocks, of a tiling: rounds of tiles over the SMs (or pairs), each
 // the longer of its chunks and its epilogue, plus one epilogue that nothing overlaps and,
 // where K is split, the sum of the partial results.
-// A chunk of CG * 128 x NT x 64 takes 2 NT clocks of the tensor cores, and the 128 + NT / CG
-// rows of 128 bytes a CTA brings for it arrive at about 64 bytes a clock.
+// A chunk of CG * 128 x NT x 64 takes 2 NT clocks of the tensor cores, 200 to issue, and the
+// 128 + NT / CG rows of 128 bytes a CTA brings for it arrive at some 53 bytes a clock
+// (measured: 24.2 us for 96 chunks of 160 rows, 599 us for 1792 of 256).
+inline double chunk_clocks(int NT, int cg) { return std::max({2.0 * NT, 200.0, 2.4 * (kBM + NT / cg)}); }
 inline double tiling_cost(const Tiling& t, int64_t M, int64_t N, int batch) {
   const int64_t items = (int64_t)t.n_mt * t.n_nt * t.splits * batch;
   const int64_t groups = kSms / t.cg;
   const double rounds = (double)((items + groups - 1) / groups);
-  const double chunk = std::max(2.0 * t.NT, 2.0 * (kBM + t.NT / t.cg));
-  const double epi = 600.0 + 16.0 * t.NT;
-  double cost = rounds * std::max(t.chunks_per_split * chunk, epi) + epi + 2000.0;
+  const double epi = 500.0 + 14.0 * t.NT;
+  double cost = 5000.0 + rounds * std::max(t.chunks_per_split * chunk_clocks(t.NT, t.cg), epi) + epi;
   if (t.splits > 1) cost += 4000.0 + (double)(t.splits + 1) * M * N * 4.0 / 3000.0;
   return cost;
 }
@@ -968,9 +982,9 @@ cudaError_t launch_tiles(const Tiling& t, Params p, const Matrix& a, const Matri
     if (e != cudaSuccess) return e;
   }
   p.NT = t.NT;
-  p.n_mt = t.n_mt;
-  p.n_nt = t.n_nt;
-  p.splits = t.splits;
+  p.n_mt = FastDiv(t.n_mt);
+  p.n_nt = FastDiv(t.n_nt);
+  p.n_splits = FastDiv(t.splits);
   p.chunks = t.chunks;
   p.chunks_per_split = t.chunks_per_split;
   const int64_t items = (int64_t)t.n_mt * t.n_nt * t.splits * batch;
