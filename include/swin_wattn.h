@@ -369,7 +369,8 @@ int swin_wattn_linear_bwd_weight(const void* dy, const void* x, void* dw, float*
  * factor of about a hundred, and loses accuracy in the directions of smaller ones. The norm
  * is summed in fp32, with large values scaled so that it does not overflow. A matrix with a
  * NaN or an infinity gives NaN and leaves the others of the stack alone; a zero matrix gives zeros.
- * 2 + 3 * steps launches; nothing is allocated. Deterministic. Errors: INVALID_ARG for the
+ * One launch where the smaller side is at most 128 and the larger at most 4096, else
+ * 2 + 3 * steps; nothing is allocated. Deterministic. Errors: INVALID_ARG for the
  * scalars, overlaps, a small workspace or a pointer that is not memory of the current
  * device; MISALIGNED; UNSUPPORTED for sizes out of range. The size query returns 0 for
  * unsupported arguments.

@@ -21,9 +21,14 @@
 // still a normal number, and the largest B stays a tenth of the largest fp16. Products are
 // accumulated in fp32. Singular values far below the largest come out with the error of
 // rounding the large ones' entries (the same is true, eight times worse, in bf16).
+#include "orthogonalize.cuh"
 #include "product.cuh"
 
 namespace swin {
+
+bool orthogonalize_small_applies(int rows, int cols);
+cudaError_t orthogonalize_small_launch(const void* g, void* out, int count, int rows, int cols, int dtype, int steps,
+                                       float eps, float scale, int* status, cudaStream_t st);
 
 namespace {
 
@@ -31,8 +36,6 @@ using prod::Matrix;
 using prod::Params;
 using prod::Tiling;
 
-constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
-constexpr float kScale = 256.0f;  // of every fp16 matrix held
 constexpr CUtensorMapDataType kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 
@@ -44,34 +47,6 @@ int norm_blocks(int64_t elements, int count) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({kNormBlocks, (elements + 2047) / 2048, (4 * prod::kSms + count - 1) / count}));
 }
 
-__device__ __forceinline__ float load_f32(const float* p) { return *p; }
-__device__ __forceinline__ float load_f32(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-// Eight consecutive values, 16-byte aligned.
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = prod::unpack_bf16(in[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
-
-// Squares are summed apart for values below 2^48 (lo) and, times 2^-64, for the others (hi:
-// NaN and infinity too), so that neither sum overflows where the norm does not.
-__device__ __forceinline__ void add_square(float v, float& lo, float& hi) {
-  if (fabsf(v) < 281474976710656.0f) {
-    lo = fmaf(v, v, lo);
-  } else {
-    const float s = v * 5.421010862427522e-20f;
-    hi = fmaf(s, s, hi);
-  }
-}
 // Sum over the block of both; the result in every thread of the first warp.
 __device__ __forceinline__ float2 block_sum(float lo, float hi) {
   __shared__ float2 part[kNormThreads / 32];
@@ -135,10 +110,7 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(const T* __rest
   pdl_wait();
   const float2 p = (int)threadIdx.x < n_partial ? partial[blockIdx.y * n_partial + threadIdx.x] : make_float2(0.0f, 0.0f);
   const float2 s = block_sum(p.x, p.y);
-  // |G| of both sums; where the second is not empty the first is added in its scale
-  const float norm = s.y == 0.0f ? sqrtf(s.x)
-                                 : sqrtf(s.y + s.x * 5.421010862427522e-20f * 5.421010862427522e-20f) * 18446744073709551616.0f;
-  const float inv = kScale / (norm + eps);
+  const float inv = kScale / (norm_of(s.x, s.y) + eps);
   const int64_t elements = (int64_t)rows * cols;
   const T* gm = g + (int64_t)blockIdx.y * elements;
   __half* xm = x + (int64_t)blockIdx.y * rows * ld;
@@ -193,11 +165,15 @@ cudaError_t normalize(const T* g, int count, int rows, int cols, float eps, floa
 
 }  // namespace
 
-size_t orthogonalize_workspace_bytes(int count, int rows, int cols) { return layout(count, rows, cols).total; }
-int orthogonalize_launches(int steps) { return 2 + 3 * steps; }
+size_t orthogonalize_workspace_bytes(int count, int rows, int cols) {
+  return orthogonalize_small_applies(rows, cols) ? 256 : layout(count, rows, cols).total;
+}
+int orthogonalize_launches(int rows, int cols, int steps) { return orthogonalize_small_applies(rows, cols) ? 1 : 2 + 3 * steps; }
 
 cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, int cols, int dtype, int steps,
                                  float eps, float scale, void* workspace, int* status, cudaStream_t st) {
+  if (orthogonalize_small_applies(rows, cols))
+    return orthogonalize_small_launch(g, out, count, rows, cols, dtype, steps, eps, scale, status, st);
   const Layout l = layout(count, rows, cols);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   __half* x[2] = {reinterpret_cast<__half*>(ws), reinterpret_cast<__half*>(ws + l.x_bytes)};
@@ -225,9 +201,9 @@ cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, 
     e = tall ? prod::launch_product<true, true, prod::kEpiStep>(t_gram, p, X, X, A, count, kF16, kF16, none, st)
              : prod::launch_product<false, false, prod::kEpiStep>(t_gram, p, X, X, A, count, kF16, kF16, none, st);
     if (e != cudaSuccess) return e;
-    p.alpha = kC / kScale;
-    p.beta = kB;
-    p.diag = kA * kScale;
+    p.alpha = kNsC / kScale;
+    p.beta = kNsB;
+    p.diag = kNsA * kScale;
     prod::Extra with_a;
     with_a.aux = &A;
     e = prod::launch_product<false, false, prod::kEpiStep>(t_poly, p, A, A, B, count, kF16, kF16, with_a, st);

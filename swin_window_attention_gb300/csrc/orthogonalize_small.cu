@@ -1,0 +1,409 @@
+// The Newton-Schulz update (orthogonalize.cu) of matrices whose smaller side is at most 128, in
+// one launch. A cluster of CTAs keeps a matrix in shared memory for all its steps: each CTA a
+// slab of up to 512 of the longer side (fp16, times 2^8), and all of A and B = a I + b A + c A^2.
+// Per step
+//   1. A's part from the slab on the tensor cores; the cluster's parts are summed in order
+//      through distributed shared memory, each CTA adding up its share of the rows and handing
+//      the rounded rows to the others;
+//   2. A^2, and B from it;
+//   3. the slab times B, written over the slab.
+// Nothing but the matrix itself crosses memory, once in (twice, from L2, for its norm) and once
+// out. What bounds it is latency: the steps' products depend on each other, and take a few
+// hundred to two thousand clocks each. As separate launches of product.cuh's tiles the same
+// products take about 3.5 us each (96 x 384, five steps: 52 us; here XXX us).
+//
+// The slab lies in blocks of 64 columns of 128-byte rows, 128-byte swizzled, so that one
+// placement serves both products: for wide matrices (slab: all rows, a range of columns) the
+// Gram product reads it K-major and the update MN-major, for tall ones (a range of rows, all
+// columns) the other way round.
+#include "product.cuh"
+#include "orthogonalize.cuh"
+
+namespace swin {
+
+namespace {
+
+using namespace prod;
+
+constexpr int kSmThreads = 512, kSmWarps = kSmThreads / 32;
+constexpr int kSide = 128;        // the smaller side at most
+constexpr int kSlab = 512;        // of the longer side, per CTA
+constexpr int kSmCluster = 8;
+constexpr int kMatBytes = kSide * kSide * 2;
+constexpr uint32_t kF16Format = (1u << 7) | (1u << 10);  // bits that make an operand bf16
+
+struct SmallParams {
+  const void* g;
+  __nv_bfloat16* out;
+  int rows, cols, steps, cluster, slab;  // slab: of the longer side, per CTA
+  int slab_rows, slab_bytes;
+  float eps, scale;
+  int* status;
+  uint64_t wait_ns;
+  int fault;
+};
+
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint4 v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <bool TALL, typename T>
+__global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(const SmallParams p) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ uint32_t s_tmem;
+  __shared__ __align__(8) uint64_t s_bar;
+  __shared__ float2 s_part[kSmWarps], s_norm;
+  pdl_launch_dependents();
+  const uint32_t smem0 = smem_u32(smem), bar = smem_u32(&s_bar);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int S = p.cluster, rank = blockIdx.x % S, mat = blockIdx.x / S;
+  const int m = TALL ? p.cols : p.rows, n = TALL ? p.rows : p.cols;
+  const int first = rank * p.slab, len = min(p.slab, n - first);  // this CTA's part of the longer side
+  const int mp = (m + 15) & ~15;
+  int bad = (smem0 & 1023u) != 0;
+
+  // slab at 0; A and B behind it
+  unsigned char* sA = smem + p.slab_bytes;
+  unsigned char* sB = sA + kMatBytes;
+  const uint32_t slab0 = smem0, a0 = smem0 + p.slab_bytes, b0 = a0 + kMatBytes;
+  const int block = p.slab_rows * 128;  // bytes of 64 columns of the slab
+  // element (r, c) of the slab; of A or B (blocks of 128 rows)
+  auto at = [&](int r, int c) { return (c >> 6) * block + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) + (c & 7) * 2; };
+  auto mat_at = [](int r, int c) { return (c >> 6) * (kSide * 128) + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) + (c & 7) * 2; };
+
+  if (warp == 0) tc::tmem_alloc<512>(smem_u32(&s_tmem));
+  if (tid == 0) {
+    tc::mbar_init(bar, 1);
+    tc::mbar_init_fence();
+  }
+  for (int i = tid; i < p.slab_bytes / 16; i += kSmThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+  pdl_wait();
+
+  // ---- the slab of G: its share of the norm, then X = G / (|G| + eps) --------------------
+  const int srows = TALL ? len : m, scols = TALL ? m : len;  // of the slab that hold G
+  const int64_t origin = (int64_t)mat * p.rows * p.cols + (TALL ? (int64_t)first * p.cols : first);
+  const T* g = static_cast<const T*>(p.g) + origin;
+  // eight columns at a time where every row starts on a 16-byte boundary
+  const bool vec = p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(p.g) % 16 == 0;
+  const int c8 = scols / 8, n8 = srows * c8;  // vec: scols is a multiple of 8
+  {
+    float lo = 0.0f, hi = 0.0f;
+    if (vec) {
+#pragma unroll 2
+      for (int i = tid; i < n8; i += kSmThreads) {
+        float v[8];
+        load8(g + (int64_t)(i / c8) * p.cols + i % c8 * 8, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) add_square(v[e], lo, hi);
+      }
+    } else {
+      for (int r = warp; r < srows; r += kSmWarps)
+        for (int c = lane; c < scols; c += 32) add_square(load_f32(g + (int64_t)r * p.cols + c), lo, hi);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      lo += __shfl_xor_sync(0xffffffffu, lo, o);
+      hi += __shfl_xor_sync(0xffffffffu, hi, o);
+    }
+    if (lane == 0) s_part[warp] = make_float2(lo, hi);
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 1; w < kSmWarps; ++w) {
+        lo += s_part[w].x;
+        hi += s_part[w].y;
+      }
+      s_norm = make_float2(lo, hi);
+    }
+  }
+  if (S > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  float lo = 0.0f, hi = 0.0f;
+  for (int s = 0; s < S; ++s) {
+    const uint32_t peer = map_to_rank(smem_u32(&s_norm), s);
+    float a, b;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(a), "=f"(b) : "r"(peer) : "memory");
+    lo += a;
+    hi += b;
+  }
+  const float inv = kScale / (norm_of(lo, hi) + p.eps);
+  if (vec) {
+#pragma unroll 2
+    for (int i = tid; i < n8; i += kSmThreads) {
+      const int r = i / c8, c = i % c8 * 8;
+      float v[8];
+      load8(g + (int64_t)r * p.cols + c, v);
+      *reinterpret_cast<uint4*>(smem + at(r, c)) =
+          make_uint4(pack_f16(v[0] * inv, v[1] * inv), pack_f16(v[2] * inv, v[3] * inv), pack_f16(v[4] * inv, v[5] * inv),
+                     pack_f16(v[6] * inv, v[7] * inv));
+    }
+  } else {
+    for (int r = warp; r < srows; r += kSmWarps)
+      for (int c = lane; c < scols; c += 32)
+        *reinterpret_cast<__half*>(smem + at(r, c)) = __float2half_rn(load_f32(g + (int64_t)r * p.cols + c) * inv);
+  }
+  tc::fence_proxy_async();
+  __syncthreads();
+
+  // ---- the steps ------------------------------------------------------------------------
+  constexpr uint32_t kHi = desc_hi(1024, kSW128);
+  const uint32_t id_gram = (tc::idesc_bf16(kSide, 16, TALL, TALL) ^ kF16Format) + ((uint32_t)(mp - 16) >> 3 << 17);
+  const uint32_t id_mat = (tc::idesc_bf16(kSide, 16, false, false) ^ kF16Format) + ((uint32_t)(mp - 16) >> 3 << 17);
+  uint32_t phase = 0;
+  // warp 0 issues; every thread waits for the products to complete
+  auto products = [&](auto issue) {
+    if (warp == 0 && !bad) {
+      tc::fence_after_sync();
+      if (elect_one()) {
+        issue();
+#ifdef SWIN_WATTN_FAULT_INJECTION
+        if (p.fault != kFaultGemm)
+#endif
+          tc::commit(bar);
+      }
+      __syncwarp();
+    }
+    if (!bad && !warp_wait(bar, phase, p.wait_ns)) bad = 1;
+    phase ^= 1;
+    tc::fence_after_sync();
+  };
+  const int quad = warp & 3, part = warp >> 2;  // tensor-memory lanes; columns
+  const int row = quad * 32 + lane;
+  const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
+  const int k_steps = (len + 15) / 16;  // of the Gram product
+  const int m_steps = mp / 16;
+
+  for (int step = 0; step < p.steps; ++step) {
+    const bool last = step == p.steps - 1;
+    // A's part: columns [0, mp) of the accumulator
+    products([&]() {
+      for (int t = 0; t < k_steps; ++t) {
+        const uint32_t x = TALL ? desc_lo(slab0 + t * 2048, block) : desc_lo(slab0 + (t >> 2) * block + (t & 3) * 32, 16);
+        mma<1>(tmem, x, kHi, x, kHi, id_gram, t > 0);
+      }
+    });
+    const int c0 = part * 32;
+    if (S == 1) {
+      if (c0 < mp) {
+        uint32_t a[32];
+        tc::ld32_wait(trow + c0, a);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            o[q] = pack_f16(__uint_as_float(a[8 * c + 2 * q]) * (1.0f / kScale), __uint_as_float(a[8 * c + 2 * q + 1]) * (1.0f / kScale));
+          *reinterpret_cast<uint4*>(sA + mat_at(row, c0 + 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    } else {
+      // fp32 parts [128][128] over A and B, of which nothing is needed any more; 16-byte pieces
+      // of a row swizzled against bank conflicts
+      float* fp = reinterpret_cast<float*>(sA);
+      auto f_at = [](int r, int c4) { return r * kSide + ((c4 ^ (r & 7)) << 2); };  // c4: piece of four columns
+      if (c0 < mp) {
+        uint32_t a[32];
+        tc::ld32_wait(trow + c0, a);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(fp + f_at(row, c0 / 4 + c)) = make_uint4(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
+      }
+      tc::fence_before_sync();
+      cluster_sync_all();
+      // rows rank, rank + S, ... : a thread sums eight columns of a row over the cluster
+      constexpr int kMine = kSide / 2 * (kSide / 8) / kSmThreads;  // at S = 2, pieces per thread
+      uint4 mine[kMine];
+      const int my_rows = (mp - rank + S - 1) / S, pieces = mp / 8;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int e = tid + i * kSmThreads, r = rank + e / pieces * S, c = e % pieces;
+        if (e < my_rows * pieces) {
+          float4 u = make_float4(0, 0, 0, 0), v = u;
+          for (int s = 0; s < S; ++s) {
+            const uint32_t base = map_to_rank(a0, s);
+            const float4 x = load_cluster4(base + f_at(r, 2 * c) * 4), y = load_cluster4(base + f_at(r, 2 * c + 1) * 4);
+            u = make_float4(u.x + x.x, u.y + x.y, u.z + x.z, u.w + x.w);
+            v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
+          }
+          constexpr float k = 1.0f / kScale;
+          mine[i] = make_uint4(pack_f16(u.x * k, u.y * k), pack_f16(u.z * k, u.w * k), pack_f16(v.x * k, v.y * k),
+                               pack_f16(v.z * k, v.w * k));
+        }
+      }
+      cluster_sync_all();  // every part has been read
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int e = tid + i * kSmThreads, r = rank + e / pieces * S, c = e % pieces;
+        if (e < my_rows * pieces)
+          for (int s = 0; s < S; ++s) store_cluster(map_to_rank(a0 + mat_at(r, 8 * c), s), mine[i]);
+      }
+      tc::fence_proxy_async();
+      cluster_sync_all();  // A is complete in every CTA
+    }
+    tc::fence_proxy_async();
+    tc::fence_before_sync();
+    __syncthreads();
+
+    // A^2 behind the Gram accumulator, then B
+    products([&]() {
+      for (int t = 0; t < m_steps; ++t) {
+        const uint32_t x = desc_lo(a0 + (t >> 2) * (kSide * 128) + (t & 3) * 32, 16);
+        mma<1>(tmem + kSide, x, kHi, x, kHi, id_mat, t > 0);
+      }
+    });
+    if (c0 < mp) {
+      uint32_t a[32];
+      tc::ld32_wait(trow + kSide + c0, a);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 w = *reinterpret_cast<const uint4*>(sA + mat_at(row, c0 + 8 * c));
+        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int e = 8 * c + 2 * q;
+          const float2 x = unpack_f16(in[q]);
+          const float d0 = row == c0 + e ? kNsA * kScale : 0.0f, d1 = row == c0 + e + 1 ? kNsA * kScale : 0.0f;
+          o[q] = pack_f16(fmaf(__uint_as_float(a[e]), kNsC / kScale, fmaf(x.x, kNsB, d0)),
+                          fmaf(__uint_as_float(a[e + 1]), kNsC / kScale, fmaf(x.y, kNsB, d1)));
+        }
+        *reinterpret_cast<uint4*>(sB + mat_at(row, c0 + 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    tc::fence_proxy_async();
+    tc::fence_before_sync();
+    __syncthreads();
+
+    // the slab times B: wide, 128 rows by up to 512 columns in one accumulator of 512 columns;
+    // tall, up to four tiles of 128 rows by mp columns
+    products([&]() {
+      if constexpr (TALL) {
+        for (int tile = 0; tile < p.slab_rows / kSide; ++tile)
+          for (int t = 0; t < m_steps; ++t)
+            mma<1>(tmem + tile * kSide, desc_lo(slab0 + tile * (kSide * 128) + (t >> 2) * block + (t & 3) * 32, 16), kHi,
+                   desc_lo(b0 + (t >> 2) * (kSide * 128) + (t & 3) * 32, 16), kHi, id_mat, t > 0);
+      } else {
+        for (int c = 0; c < len; c += 256) {
+          const int nn = min(256, (len - c + 15) & ~15);
+          const uint32_t id = (tc::idesc_bf16(kSide, 16, true, false) ^ kF16Format) + ((uint32_t)(nn - 16) >> 3 << 17);
+          for (int t = 0; t < m_steps; ++t)
+            mma<1>(tmem + c, desc_lo(b0 + (t >> 2) * (kSide * 128) + (t & 3) * 32, 16), kHi,
+                   desc_lo(slab0 + (c >> 6) * block + t * 2048, block), kHi, id, t > 0);
+        }
+      }
+    });
+    const float alpha = last ? p.scale / (kScale * kScale) : 1.0f / kScale;
+    // the accumulator's 32-column pieces, four quadrants' rows each: wide, piece = columns; tall,
+    // tile of 128 rows and columns
+    const int n_pieces = TALL ? p.slab_rows / kSide * ((mp + 31) / 32) : (len + 31) / 32;
+    for (int i = part; i < n_pieces; i += 4) {
+      const int tiles32 = (mp + 31) / 32;
+      const int r = TALL ? i / tiles32 * kSide + row : row, c = (TALL ? i % tiles32 : i) * 32;
+      const uint32_t col = TALL ? (uint32_t)(i / tiles32 * kSide + c) : (uint32_t)c;
+      uint32_t a[32];
+      tc::ld32_wait(trow + col, a);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float x = __uint_as_float(a[8 * k + 2 * q]) * alpha, y = __uint_as_float(a[8 * k + 2 * q + 1]) * alpha;
+          o[q] = last ? pack_bf16(x, y) : pack_f16(x, y);
+        }
+        *reinterpret_cast<uint4*>(smem + at(r, c + 8 * k)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    tc::fence_proxy_async();
+    tc::fence_before_sync();
+    __syncthreads();
+  }
+
+  // ---- the result, from the slab in bf16 -------------------------------------------------
+  __nv_bfloat16* out = p.out + origin;
+  if (p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0) {
+    for (int i = tid; i < n8; i += kSmThreads) {
+      const int r = i / c8, c = i % c8 * 8;
+      *reinterpret_cast<uint4*>(out + (int64_t)r * p.cols + c) = *reinterpret_cast<const uint4*>(smem + at(r, c));
+    }
+  } else {
+    for (int r = warp; r < srows; r += kSmWarps)
+      for (int c = lane; c < scols; c += 32)
+        out[(int64_t)r * p.cols + c] = *reinterpret_cast<const __nv_bfloat16*>(smem + at(r, c));
+  }
+  if (bad && p.status != nullptr) atomicOr(p.status, 1);
+  // no CTA leaves while another may still read its parts
+  if (S > 1) cluster_sync_all();
+  __syncthreads();
+  if (warp == 0) tc::tmem_dealloc<512>(tmem);
+}
+
+template <bool TALL, typename T>
+cudaError_t launch_small(SmallParams p, int count, cudaStream_t st) {
+  const int n = TALL ? p.rows : p.cols;
+  p.cluster = (n + kSlab - 1) / kSlab;
+  p.slab = ((n + p.cluster - 1) / p.cluster + 63) / 64 * 64;
+  p.slab_rows = TALL ? (p.slab + kSide - 1) / kSide * kSide : kSide;
+  p.slab_bytes = TALL ? 2 * p.slab_rows * 128 : p.slab / 64 * (kSide * 128);
+  p.wait_ns = wait_limit_ns();
+  p.fault = fault_site();
+  DeviceInfo di;
+  cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  const int smem = std::max(120 * 1024, p.slab_bytes + 2 * kMatBytes);
+  auto kern = orthogonalize_small_kernel<TALL, T>;
+  static std::atomic<uint64_t> allowed{0};
+  e = allow_smem(reinterpret_cast<const void*>(kern), di.smem_max - 1024, di.device, &allowed);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(count * p.cluster));
+  cfg.blockDim = dim3(kSmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace
+
+bool orthogonalize_small_applies(int rows, int cols) {
+  return std::min(rows, cols) <= kSide && std::max(rows, cols) <= kSlab * kSmCluster;
+}
+
+cudaError_t orthogonalize_small_launch(const void* g, void* out, int count, int rows, int cols, int dtype, int steps,
+                                       float eps, float scale, int* status, cudaStream_t st) {
+  SmallParams p{};
+  p.g = g;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.rows = rows;
+  p.cols = cols;
+  p.steps = steps;
+  p.eps = eps;
+  p.scale = scale;
+  p.status = status;
+  const bool f32 = dtype == SWIN_WATTN_FP32;
+  if (rows > cols) return f32 ? launch_small<true, float>(p, count, st) : launch_small<true, __nv_bfloat16>(p, count, st);
+  return f32 ? launch_small<false, float>(p, count, st) : launch_small<false, __nv_bfloat16>(p, count, st);
+}
+
+}  // namespace swin

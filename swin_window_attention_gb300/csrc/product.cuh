@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
           const int sw = (lane >> 1) & 3;
           auto at = [&](unsigned char* base, int c) { return reinterpret_cast<uint4*>(base + ((c ^ sw) << 4)); };
           auto pair = [&](int e) { return make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])); };
-          uint32_t o[16];  // the result, packed; a[0..15] receives the second one
+          uint32_t o[16];  // the result, packed
           auto activate = [&](auto act) {
             constexpr int ACT = decltype(act)::value;
 #pragma unroll
@@ -716,7 +716,8 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                   const float2 z = __fadd2_rn(pair(8 * c + 2 * q), bb[q]);
-                  a[4 * c + q] = pack_bf16(z.x, z.y);
+                  a[8 * c + 2 * q] = __float_as_uint(z.x);  // kept for the second result
+                  a[8 * c + 2 * q + 1] = __float_as_uint(z.y);
                   float2 y = act_value<ACT>(z);
                   if (aux) y = __fadd2_rn(y, unpack_bf16(rr[q]));
                   o[4 * c + q] = pack_bf16(y.x, y.y);
@@ -764,8 +765,12 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             *at(sr, c) = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-            if (EPI == kEpiAct && pre)
-              *at(sz + lane * 64, c) = make_uint4(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
+            if (EPI == kEpiAct && pre) {
+              uint32_t z16[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) z16[q] = pack_bf16(pair(8 * c + 2 * q).x, pair(8 * c + 2 * q).y);
+              *at(sz + lane * 64, c) = make_uint4(z16[0], z16[1], z16[2], z16[3]);
+            }
           }
         }
         if (EPI == kEpiStep && p.raw_out != nullptr) {
