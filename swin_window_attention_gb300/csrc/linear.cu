@@ -34,55 +34,70 @@ constexpr CUtensorMapDataType kF32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
 
 Matrix rows_of(const void* p, int64_t rows, int64_t cols) { return Matrix{p, rows, cols, cols, rows * cols}; }
 
-// out[i] = [old +] sum over the splits of part[s][i], four values per thread; the last
-// blocks do the same for the bias gradient. Bound by the reads of the partial results,
-// which the product has just left in L2.
+// out[i] = [old +] sum over the splits of part[s][i], i in fours; the last blocks do the same for
+// the bias gradient. A block of 64 fours by kSumGroups threads each: a thread has all its splits'
+// reads in flight and the groups are added in order. Bound by those reads' latency: the product
+// has just left the partial results in L2.
+constexpr int kSumGroups = 4, kSumWidth = 64;
 template <typename T>
-__global__ void __launch_bounds__(256) sum_splits_kernel(const float* __restrict__ part, int64_t n, int splits,
-                                                         T* __restrict__ out, bool add,
-                                                         const float* __restrict__ bpart, int nb,
-                                                         float* __restrict__ bout) {
+__global__ void __launch_bounds__(kSumGroups * kSumWidth)
+    sum_splits_kernel(const float* __restrict__ part, int64_t n, int splits, T* __restrict__ out, bool add,
+                      const float* __restrict__ bpart, int nb, float* __restrict__ bout) {
+  __shared__ float4 group_sum[kSumGroups][kSumWidth];
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
-  if (i < n) {
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int lane = threadIdx.x % kSumWidth, grp = threadIdx.x / kSumWidth;
+  const int64_t four = (int64_t)blockIdx.x * kSumWidth + lane, n4 = (n + 3) / 4;
+  // the splits of this group
+  const int s0 = splits * grp / kSumGroups, s1 = splits * (grp + 1) / kSumGroups;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int64_t j = four - n4;  // the bias gradient's element
+  if (four < n4) {
 #pragma unroll 8
-    for (int s = 0; s < splits; ++s) {
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(part + (int64_t)s * n + i));
+    for (int s = s0; s < s1; ++s) {
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(part + (int64_t)s * n) + four);
       v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
     }
+  } else if (bpart != nullptr && j < nb) {
+#pragma unroll 8
+    for (int s = s0; s < s1; ++s) v.x += __ldcg(bpart + (int64_t)s * nb + j);
+  }
+  group_sum[grp][lane] = v;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int k = 1; k < kSumGroups; ++k) {
+    const float4 a = group_sum[k][lane];
+    v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
+  }
+  if (four < n4) {
     if constexpr (sizeof(T) == 4) {
-      float4* o = reinterpret_cast<float4*>(out + i);
+      float4* o = reinterpret_cast<float4*>(out) + four;
       if (add) v = make_float4(v.x + o->x, v.y + o->y, v.z + o->z, v.w + o->w);
       *o = v;
     } else {
-      uint2* o = reinterpret_cast<uint2*>(out + i);
+      uint2* o = reinterpret_cast<uint2*>(out) + four;
       if (add) {
         const float2 a = prod::unpack_bf16(o->x), b = prod::unpack_bf16(o->y);
         v = make_float4(v.x + a.x, v.y + a.y, v.z + b.x, v.w + b.y);
       }
       *o = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
     }
-  }
-  const int64_t j = i / 4 - (n + 3) / 4;
-  if (bpart != nullptr && j >= 0 && j < nb) {
-    float v = 0.0f;
-    for (int s = 0; s < splits; ++s) v += __ldcg(bpart + (int64_t)s * nb + j);
-    bout[j] = add ? bout[j] + v : v;
+  } else if (bpart != nullptr && j < nb) {
+    bout[j] = add ? bout[j] + v.x : v.x;
   }
 }
 
 constexpr int kMaxSplits = 64;
 
-Tiling weight_tiling(int64_t T, int K, int N) { return prod::choose_tiling(N, K, T, 1, true, kMaxSplits, 2); }
+Tiling weight_tiling(int64_t T, int K, int N) { return prod::choose_tiling(N, K, T, 1, true, kMaxSplits, true); }
 
 }  // namespace
 
 cudaError_t linear_launch(const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
                           int T, int K, int N, int act, int* status, cudaStream_t st) {
   if (T <= kFewTokens) return linear_few_launch(x, w, b, residual, y, pre, T, K, N, act, status, st);
-  const Tiling t = prod::choose_tiling(T, N, K, 1, false, 1, 2);
+  const Tiling t = prod::choose_tiling(T, N, K, 1, false, 1, false);
   Params p{};
   p.M = T;
   p.N = N;
@@ -100,7 +115,7 @@ cudaError_t linear_launch(const void* x, const void* w, const float* b, const vo
 cudaError_t linear_bwd_data_launch(const void* dy, const void* w, const void* pre, void* dx, int T, int K, int N,
                                    int act, int* status, cudaStream_t st) {
   if (T <= kFewTokens) return linear_bwd_data_few_launch(dy, w, pre, dx, T, K, N, act, status, st);
-  const Tiling t = prod::choose_tiling(T, K, N, 1, true, 1, 2);
+  const Tiling t = prod::choose_tiling(T, K, N, 1, true, 1, false);
   Params p{};
   p.M = T;
   p.N = K;
@@ -155,12 +170,12 @@ cudaError_t linear_bwd_weight_launch(const void* dy, const void* x, void* dw, fl
   cudaError_t e = prod::launch_product<true, true, prod::kEpiGrad32>(t, p, a, b, rows_of(part, N, K), 1, kBf16, kF32,
                                                                      ex, st);
   if (e != cudaSuccess) return e;
-  const int64_t n = (int64_t)N * K, threads = (n + 3) / 4 + (db != nullptr ? N : 0);
-  const dim3 grid((unsigned)((threads + 255) / 256));
+  const int64_t n = (int64_t)N * K, fours = (n + 3) / 4 + (db != nullptr ? N : 0);
+  const dim3 grid((unsigned)((fours + kSumWidth - 1) / kSumWidth)), block(kSumGroups * kSumWidth);
   if (f32)
-    return launch_pdl(sum_splits_kernel<float>, grid, dim3(256), 0, st, (const float*)part, n, t.splits,
+    return launch_pdl(sum_splits_kernel<float>, grid, block, 0, st, (const float*)part, n, t.splits,
                       static_cast<float*>(dw), accumulate != 0, (const float*)(db != nullptr ? bpart : nullptr), N, db);
-  return launch_pdl(sum_splits_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, (const float*)part, n, t.splits,
+  return launch_pdl(sum_splits_kernel<__nv_bfloat16>, grid, block, 0, st, (const float*)part, n, t.splits,
                     static_cast<__nv_bfloat16*>(dw), accumulate != 0, (const float*)(db != nullptr ? bpart : nullptr),
                     N, db);
 }

@@ -185,9 +185,9 @@ cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, 
                       : normalize(static_cast<const __nv_bfloat16*>(g), count, rows, cols, eps, partial, x[0], l.ldx, st);
   const bool tall = rows > cols;
   const int m = l.m, n = std::max(rows, cols);
-  const Tiling t_gram = prod::choose_tiling(m, m, n, count, tall, 1, 2);
-  const Tiling t_poly = prod::choose_tiling(m, m, m, count, false, 1, 2);
-  const Tiling t_step = prod::choose_tiling(rows, cols, m, count, !tall, 1, 2);
+  const Tiling t_gram = prod::choose_tiling(m, m, n, count, tall, 1, false);
+  const Tiling t_poly = prod::choose_tiling(m, m, m, count, false, 1, false);
+  const Tiling t_step = prod::choose_tiling(rows, cols, m, count, !tall, 1, false);
   const Matrix A{gram, m, m, l.lda, (int64_t)m * l.lda}, B{poly, m, m, l.lda, (int64_t)m * l.lda};
   const bool direct = cols % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
   for (int s = 0; s < steps && e == cudaSuccess; ++s) {

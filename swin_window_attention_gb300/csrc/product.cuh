@@ -887,22 +887,25 @@ struct Tiling {
 // 128 + NT / CG rows of 128 bytes a CTA brings for it arrive at some 53 bytes a clock
 // (measured: 24.2 us for 96 chunks of 160 rows, 599 us for 1792 of 256).
 inline double chunk_clocks(int NT, int cg) { return std::max({2.0 * NT, 200.0, 2.4 * (kBM + NT / cg)}); }
-inline double tiling_cost(const Tiling& t, int64_t M, int64_t N, int batch) {
+// `extra` columns beside a tile's hold the sums over K; where they lie in the other accumulator
+// every segment of an fp32 result waits for the last one's epilogue, some 2000 clocks.
+inline double tiling_cost(const Tiling& t, int64_t M, int64_t N, int batch, bool sums) {
   const int64_t items = (int64_t)t.n_mt * t.n_nt * t.splits * batch;
   const int64_t groups = kSms / t.cg;
   const double rounds = (double)((items + groups - 1) / groups);
   const double epi = 500.0 + 14.0 * t.NT;
   double cost = 5000.0 + rounds * std::max(t.chunks_per_split * chunk_clocks(t.NT, t.cg), epi) + epi;
+  if (sums && t.n_nt == 1 && t.NT + 16 * t.cg > kMaxNT) cost += rounds * 2000.0 * (t.chunks_per_split / kSegChunks);
   if (t.splits > 1) cost += 4000.0 + (double)(t.splits + 1) * M * N * 4.0 / 3000.0;
   return cost;
 }
 
 // The cheapest tiling. `max_splits` > 1 allows K to be split into partial results.
-inline Tiling search_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn, int max_splits, int max_cg) {
+inline Tiling search_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn, int max_splits, bool sums) {
   Tiling best{};
   double best_cost = -1.0;
   const int chunks = (int)((K + kKC - 1) / kKC);
-  for (int cg = 1; cg <= max_cg; ++cg) {
+  for (int cg = 1; cg <= 2; ++cg) {
     for (int nt = kMaxNT; nt >= 32; nt -= 32) {
       if (bmn ? nt % (64 * cg) != 0 : nt % (16 * cg) != 0) continue;
       Tiling t{};
@@ -917,7 +920,7 @@ inline Tiling search_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn
         if ((chunks + per - 1) / per != s) continue;  // every split has chunks
         t.splits = s;
         t.chunks_per_split = per;
-        const double c = tiling_cost(t, M, N, batch);
+        const double c = tiling_cost(t, M, N, batch, sums);
         if (best_cost < 0.0 || c < best_cost) {
           best_cost = c;
           best = t;
@@ -930,19 +933,19 @@ inline Tiling search_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn
 
 // The same, with the calling thread's last choices remembered by their sizes (a search
 // compares some hundred tilings, which is more than a small launch takes).
-inline Tiling choose_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn, int max_splits, int max_cg) {
+inline Tiling choose_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn, int max_splits, bool sums) {
   struct Entry {
     int64_t key[7];
     Tiling t;
   };
   constexpr int kEntries = 64;
   thread_local Entry cache[kEntries] = {};
-  const int64_t key[7] = {M, N, K, batch, bmn, max_splits, max_cg};
+  const int64_t key[7] = {M, N, K, batch, bmn, max_splits, sums};
   uint64_t h = 0;
   for (const int64_t k : key) h = (h ^ (uint64_t)k) * 0x9E3779B97F4A7C15ull;
   Entry& c = cache[h >> 58];
   if (!std::equal(key, key + 7, c.key)) {
-    c.t = search_tiling(M, N, K, batch, bmn, max_splits, max_cg);
+    c.t = search_tiling(M, N, K, batch, bmn, max_splits, sums);
     std::copy(key, key + 7, c.key);
   }
   return c.t;
