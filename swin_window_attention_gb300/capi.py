@@ -336,13 +336,13 @@ _U8 = (torch.uint8,)
 _I32 = (torch.int32,)
 
 
-def _tensor(name, t, shape, dtypes, device):
+def _tensor(name, t, shape, dtypes, dev):
     """Check one operand: a contiguous CUDA tensor of the given shape, one of the given dtypes,
-    on `device`. Returns its address."""
-    if t.device == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+    on CUDA device number `dev`. Returns its address."""
+    if t.get_device() == dev and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
     if t.shape != shape:
@@ -351,52 +351,53 @@ def _tensor(name, t, shape, dtypes, device):
 
 
 def _device_of(name, t):
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} is not a CUDA tensor")
-    return t.device
+    return dev
 
 
-def _call(fn, device, stream, status, *args):
-    """The C function fn(*args, status, stream) with `device` current, on `stream` or that
-    device's current stream; raises on an error status."""
-    st = None if status is None else _tensor("status", status, (1,), _I32, device)
-    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    if device.index == torch.cuda.current_device():
+def _call(fn, dev, stream, status, *args):
+    """The C function fn(*args, status, stream) with device number `dev` current, on `stream`
+    or that device's current stream; raises on an error status."""
+    st = None if status is None else _tensor("status", status, (1,), _I32, dev)
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
         rc = fn(*args, st, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             rc = fn(*args, st, handle)
     if rc != OK:
         raise SwinWAttnError(fn.__name__, rc)
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, dtype, dev, stream):
     """A tensor of `stream`'s own memory pool (of the device's current stream without one),
     so that it may be used and freed in that stream's order."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _act_code(act):
-    code = ACTIVATIONS.get(act) if isinstance(act, str) else act
+    code = ACTIVATIONS.get(act) if type(act) is str else act
     if code is None or not ACT_NONE <= code <= ACT_SILU:
         raise ValueError(f"unknown activation {act!r}: one of {sorted(ACTIVATIONS)} or an ACT_ code")
     return code
 
 
-def _weight(w, device):
+def _weight(w, dev):
     if w.dim() != 2:
         raise ValueError(f"w has {w.dim()} dimensions, not 2")
-    N, K = w.shape
-    return N, K, _tensor("w", w, (N, K), _BF16, device)
+    shape = w.shape
+    return (*shape, _tensor("w", w, shape, _BF16, dev))
 
 
-def _rows(name, t, width, device):
+def _rows(name, t, width, dev):
     """Check a bf16 [..., width] tensor; returns its leading axes and its address."""
     lead = t.shape[:-1]
-    return lead, _tensor(name, t, (*lead, width), _BF16, device)
+    return lead, _tensor(name, t, (*lead, width), _BF16, dev)
 
 
 def linear(x, w, b=None, act=ACT_NONE, residual=None, y=None, pre=None, status=None, stream=None):
