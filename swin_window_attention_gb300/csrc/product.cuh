@@ -820,6 +820,11 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
 }
 
 // ---- host side ------------------------------------------------------------------------
+//
+// In an unnamed namespace: the variables that remember what a device has been asked or told
+// belong to one library. (With external linkage they are unique in a process, and the
+// fault-injection build, loaded beside the library, would find its kernels' attributes set.)
+namespace {
 
 // One GB300: 152 SMs, 76 pairs. The tile choice is made for that and does not ask the
 // device, so that workspace sizes depend on the shape alone.
@@ -1055,5 +1060,6 @@ cudaError_t launch_product(const Tiling& t, const Params& p, const Matrix& a, co
                    : launch_tiles<1, AMN, BMN, EPI>(t, p, a, b, out, batch, in_type, out_type, ex, st);
 }
 
+}  // namespace
 }  // namespace prod
 }  // namespace swin

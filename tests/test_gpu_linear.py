@@ -423,3 +423,85 @@ def test_launches_are_counted():
     capi.orthogonalize(w)
     assert capi.swin_wattn_launch_count(reset=True) >= 1
     torch.cuda.synchronize()
+
+
+def test_results_beyond_32_bit_offsets():
+    """More than 2^32 bytes of result and of second operand; sampled rows, the last ones among
+    them, against fp64."""
+    T, K, N = 300_001, 64, 8192
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(T, K, generator=g, device=DEV).to(torch.bfloat16)
+    w, b = _rand(2, N, K, std=0.1), _rand(3, N, dtype=torch.float32)
+    wd, bd = _dev(w, b)
+    y = torch.empty(T, N, dtype=torch.bfloat16, device=DEV)
+    pre = torch.empty_like(y)
+    st = _status()
+    capi.linear(x, wd, bd, act="silu", y=y, pre=pre, status=st)
+    _ok(st)
+    rows = torch.cat([torch.arange(0, 40), torch.randint(0, T, (200,), generator=torch.Generator().manual_seed(5)),
+                      torch.arange(262_100, 262_200), torch.arange(T - 40, T)])
+    xr = x[rows.to(DEV)].cpu()
+    ry, rz, ty, tz = linear64(xr, w, b, "silu", None)
+    assert_within("y", y[rows.to(DEV)], ry, ty)
+    assert_within("pre", pre[rows.to(DEV)], rz, tz)
+    # the gradient through it: dy is y, the result is written over x's shape
+    dx = capi.linear_bwd_data(y, wd, status=st)
+    dw, db = capi.linear_bwd_weight(y, x, status=st)
+    _ok(st)
+    dr, dt = bwd_data64(y[rows.to(DEV)].cpu(), w, None, "none")
+    assert_within("dx", dx[rows.to(DEV)], dr, dt)
+    cols = torch.tensor([0, 1, 4095, 8191])
+    yc = y[:, cols.to(DEV)].double()
+    ref = (yc.T @ x.double()).cpu()
+    mag = (yc.abs().T @ x.double().abs()).cpu()
+    assert_within("dw", dw[cols.to(DEV)], ref, 2000 * 2.0 ** -23 * mag)
+    assert_within("db", db[cols.to(DEV)], yc.sum(0).cpu(), 2000 * 2.0 ** -23 * yc.abs().sum(0).cpu())
+
+
+def test_first_calls_of_a_process_captured():
+    """No call before the capture: nothing that the first call of a kernel does may be illegal
+    while a stream is captured."""
+    import subprocess
+    import sys
+    code = (
+        "import torch\n"
+        "from swin_window_attention_gb300 import capi\n"
+        "r = lambda *s: torch.ones(*s, dtype=torch.bfloat16, device='cuda')\n"
+        "x, xs, w, dy = r(3000, 64), r(5, 64), r(96, 64), r(3000, 96)\n"
+        "g = torch.ones(2, 160, 200, device='cuda')\n"
+        "torch.cuda.synchronize()\n"
+        "graph = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(graph):\n"
+        "    o = [capi.linear(x, w), capi.linear(xs, w), capi.linear_bwd_data(dy, w), *capi.linear_bwd_weight(dy, x),\n"
+        "         capi.orthogonalize(g), capi.orthogonalize(g[:, :64].contiguous())]\n"
+        "graph.replay()\n"
+        "torch.cuda.synchronize()\n"
+        "assert bool((o[0] == 64).all() and (o[1] == 64).all() and (o[2] == 96).all() and (o[3] == 3000).all())\n"
+        "assert bool((o[4] == 3000).all() and torch.isfinite(o[5].float()).all() and torch.isfinite(o[6].float()).all())\n"
+        "print('captured')\n")
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and "captured" in out.stdout, out.stderr[-2000:]
+
+
+def test_calls_from_several_threads():
+    import threading
+    x, w, dy = _rand(1, 2500, 64).to(DEV), _rand(2, 96, 64).to(DEV), _rand(3, 2500, 96).to(DEV)
+    want = (capi.linear(x, w, act="gelu"), *capi.linear_bwd_weight(dy, x), capi.orthogonalize(w.float()))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                got = (capi.linear(x, w, act="gelu"), *capi.linear_bwd_weight(dy, x), capi.orthogonalize(w.float()))
+                s.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                    bad.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not bad
