@@ -10,20 +10,12 @@
 // its fp32 result in the workspace, and sum_splits_kernel adds them in order (the same
 // result on every run). db is one more column of the product: dy^T times a column of ones,
 // an MMA of 16 columns beside the tile's, so dy is read once for both.
+#include "linear_few.cuh"
 #include "product.cuh"
 
 namespace swin {
 
-cudaError_t linear_few_launch(const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
-                              int T, int K, int N, int act, int* status, cudaStream_t st);
-cudaError_t linear_bwd_data_few_launch(const void* dy, const void* w, const void* pre, void* dx, int T, int K, int N,
-                                       int act, int* status, cudaStream_t st);
-
 namespace {
-
-// Up to this many tokens the weight is read by linear_few.cu's clusters, above it the tokens
-// fill the tiles of product.cuh.
-constexpr int kFewTokens = 128;
 
 using prod::Matrix;
 using prod::Params;
@@ -88,6 +80,20 @@ __global__ void __launch_bounds__(kSumGroups * kSumWidth)
   }
 }
 
+// Few tokens, or few tiles of a long K, run as clusters (linear_few.cu), the rest as tiles: the
+// one whose estimated time is shorter. A tile of fewer than 128 tokens brings its missing
+// rows as zeros, more slowly than rows in memory (one token: 790 clocks a chunk; 128: 410).
+// Measured, clusters against tiles: 1 token 6144x1536 8.4 and 40 us, 64 tokens 1536x6144 8.5 and
+// 9.7 us, 100 tokens 192x768 8.4 and 4.5 us, 300 tokens 6144x1536 12.9 and 23.8 us, 500 tokens
+// 1536x384 10.0 and 9.0 us.
+constexpr int kFewTokens = 1024;
+bool runs_as_clusters(const Tiling& t, const FewTiling& few, int64_t T, int64_t N) {
+  if (T > kFewTokens) return false;
+  double cost = prod::tiling_cost(t, T, N, 1, false);
+  if (T < prod::kBM) cost += 0.9 * (1.0 - (double)T / prod::kBM) * t.chunks * prod::chunk_clocks(t.NT, t.cg);
+  return few.cost < cost;
+}
+
 constexpr int kMaxSplits = 64;
 
 Tiling weight_tiling(int64_t T, int K, int N) { return prod::choose_tiling(N, K, T, 1, true, kMaxSplits, true); }
@@ -96,8 +102,10 @@ Tiling weight_tiling(int64_t T, int K, int N) { return prod::choose_tiling(N, K,
 
 cudaError_t linear_launch(const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
                           int T, int K, int N, int act, int* status, cudaStream_t st) {
-  if (T <= kFewTokens) return linear_few_launch(x, w, b, residual, y, pre, T, K, N, act, status, st);
   const Tiling t = prod::choose_tiling(T, N, K, 1, false, 1, false);
+  const FewTiling few = few_tiling(T, N, K);
+  if (runs_as_clusters(t, few, T, N))
+    return linear_few_launch(few, x, w, b, residual, y, pre, T, K, N, act, status, st);
   Params p{};
   p.M = T;
   p.N = N;
@@ -114,8 +122,10 @@ cudaError_t linear_launch(const void* x, const void* w, const float* b, const vo
 
 cudaError_t linear_bwd_data_launch(const void* dy, const void* w, const void* pre, void* dx, int T, int K, int N,
                                    int act, int* status, cudaStream_t st) {
-  if (T <= kFewTokens) return linear_bwd_data_few_launch(dy, w, pre, dx, T, K, N, act, status, st);
   const Tiling t = prod::choose_tiling(T, K, N, 1, true, 1, false);
+  const FewTiling few = few_tiling(T, K, N);
+  if (runs_as_clusters(t, few, T, K))
+    return linear_bwd_data_few_launch(few, dy, w, pre, dx, T, K, N, act, status, st);
   Params p{};
   p.M = T;
   p.N = K;

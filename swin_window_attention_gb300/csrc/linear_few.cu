@@ -1,11 +1,12 @@
-// linear and linear_bwd_data for few tokens (one to kFewTokens): the product is then bound by
-// reading the weight once, and by latency. Against the tiles of product.cuh:
+// linear and linear_bwd_data for few tokens, or few tiles of a long K: the product is then bound by
+// reading the weight, and by latency. Against the tiles of product.cuh:
 // * the weight's rows are the MMA's 128 rows and the tokens its N (16 to 128), so no row of
 //   a tile is padding: the result arrives transposed, a thread holding one output channel of
 //   every token, and is stored 64 bytes per warp and token;
 // * a cluster of up to eight CTAs shares a tile, each over its part of K, so that some 150
 //   CTAs read the weight whatever its shape. Their partial results are summed in order
 //   through distributed shared memory, each CTA finishing its share of the tokens.
+#include "linear_few.cuh"
 #include "product.cuh"
 
 namespace swin {
@@ -17,6 +18,10 @@ using namespace prod;
 constexpr int kFewTmem = 128;  // columns: the accumulator
 constexpr int kFewEpi = 16, kFewMMA = kFewEpi, kFewCOPY = kFewEpi + 1, kFewWarps = kFewEpi + 2;
 constexpr int kMaxCluster = 8, kMaxTN = 128;
+// Clusters of each size that are resident at once on one GB300 (as cudaOccupancyMaxActiveClusters
+// reports them at one CTA per SM: a cluster stays within a group of SMs, and the groups are
+// not multiples of every size).
+constexpr int kResident[kMaxCluster + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
 constexpr int kFullBar = 0, kEmptyBar = kMaxStages, kDoneBar = 2 * kMaxStages, kFewBars = kDoneBar + 1;
 
 struct FewParams {
@@ -239,35 +244,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
   if (warp == kFewMMA) tc::tmem_dealloc<kFewTmem>(tmem);
 }
 
-// Clusters of each size that are resident at once on one GB300 (as cudaOccupancyMaxActiveClusters
-// reports them at one CTA per SM: a cluster stays within a group of SMs, and the groups are
-// not multiples of every size).
-constexpr int kResident[kMaxCluster + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
-
-struct FewTiling {
-  int TN, n_tiles, t_tiles, chunks, cluster;
-};
-
-// The largest cluster with which every tile is resident at once, of two chunks per CTA at
-// least. (One more CTA per tile than fits costs a second round: 48 tiles of 24 chunks took
-// 12.6 us in clusters of three, XXX in pairs.)
-FewTiling few_tiling(int64_t T, int N, int64_t K) {
-  FewTiling t;
-  t.t_tiles = (int)((T + kMaxTN - 1) / kMaxTN);
-  t.TN = (int)((T + t.t_tiles - 1) / t.t_tiles + 15) / 16 * 16;
-  t.n_tiles = (N + kBM - 1) / kBM;
-  t.chunks = (int)((K + kKC - 1) / kKC);
-  t.cluster = 1;
-  for (int s = 2; s <= kMaxCluster; ++s)
-    if ((int64_t)t.n_tiles * t.t_tiles <= kResident[s] && t.chunks >= 2 * s) t.cluster = s;
-  return t;
-}
-
 template <bool WMN, int EPI>
-cudaError_t launch_few(const Matrix& w, const Matrix& x, int64_t K, FewParams p, cudaStream_t st) {
+cudaError_t launch_few(const FewTiling& t, const Matrix& w, const Matrix& x, FewParams p, cudaStream_t st) {
   constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   constexpr CUtensorMapL2promotion kL2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-  const FewTiling t = few_tiling(p.T, p.N, K);
   p.TN = t.TN;
   p.n_tiles = t.n_tiles;
   p.chunks = t.chunks;
@@ -310,7 +290,23 @@ cudaError_t launch_few(const Matrix& w, const Matrix& x, int64_t K, FewParams p,
 
 }  // namespace
 
-cudaError_t linear_few_launch(const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
+FewTiling few_tiling(int64_t T, int N, int64_t K) {
+  FewTiling t;
+  t.t_tiles = (int)((T + kMaxTN - 1) / kMaxTN);
+  t.TN = (int)((T + t.t_tiles - 1) / t.t_tiles + 15) / 16 * 16;
+  t.n_tiles = (N + kBM - 1) / kBM;
+  t.chunks = (int)((K + kKC - 1) / kKC);
+  t.cluster = 1;
+  const int64_t tiles = (int64_t)t.n_tiles * t.t_tiles;
+  for (int s = 2; s <= kMaxCluster; ++s)
+    if (tiles <= kResident[s] && t.chunks >= 2 * s) t.cluster = s;
+  const double chunks = (t.chunks + t.cluster - 1) / t.cluster;
+  const double rounds = (double)((tiles + kResident[t.cluster] - 1) / kResident[t.cluster]);
+  t.cost = 7000.0 + rounds * (chunks * std::max(200.0, 2.4 * (kBM + t.TN)) + 500.0 * t.cluster + 40.0 * t.TN);
+  return t;
+}
+
+cudaError_t linear_few_launch(const FewTiling& t, const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
                               int T, int K, int N, int act, int* status, cudaStream_t st) {
   FewParams p{};
   p.T = T;
@@ -321,10 +317,10 @@ cudaError_t linear_few_launch(const void* x, const void* w, const float* b, cons
   p.out = static_cast<__nv_bfloat16*>(y);
   p.pre = static_cast<__nv_bfloat16*>(pre);
   p.status = status;
-  return launch_few<false, kEpiAct>(Matrix{w, N, K, K, 0}, Matrix{x, T, K, K, 0}, K, p, st);
+  return launch_few<false, kEpiAct>(t, Matrix{w, N, K, K, 0}, Matrix{x, T, K, K, 0}, p, st);
 }
 
-cudaError_t linear_bwd_data_few_launch(const void* dy, const void* w, const void* pre, void* dx, int T, int K, int N,
+cudaError_t linear_bwd_data_few_launch(const FewTiling& t, const void* dy, const void* w, const void* pre, void* dx, int T, int K, int N,
                                        int act, int* status, cudaStream_t st) {
   FewParams p{};
   p.T = T;
@@ -333,7 +329,7 @@ cudaError_t linear_bwd_data_few_launch(const void* dy, const void* w, const void
   p.aux = act == SWIN_WATTN_ACT_NONE ? nullptr : static_cast<const __nv_bfloat16*>(pre);
   p.out = static_cast<__nv_bfloat16*>(dx);
   p.status = status;
-  return launch_few<true, kEpiSlope>(Matrix{w, N, K, K, 0}, Matrix{dy, T, N, N, 0}, N, p, st);
+  return launch_few<true, kEpiSlope>(t, Matrix{w, N, K, K, 0}, Matrix{dy, T, N, N, 0}, p, st);
 }
 
 }  // namespace swin
