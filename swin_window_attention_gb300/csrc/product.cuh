@@ -119,6 +119,16 @@ __device__ __forceinline__ void cluster_sync_all() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
+// The two halves of the barrier, without memory ordering: for the end of a kernel, where a warp
+// arrives once it has no more to do with the other CTA and the CTA waits before it leaves.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
+}
 // The address, in the cluster's shared memory, of this CTA's address `addr` in CTA `rank`.
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -189,6 +199,15 @@ __device__ __forceinline__ void commit(uint32_t mbar) {
             mbar),
         "h"((uint16_t)3)
         : "memory");
+  else
+    tc::commit(mbar);
+}
+// The same, of the issuing CTA alone.
+template <int CG>
+__device__ __forceinline__ void commit_here(uint32_t mbar) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(mbar)
+                 : "memory");
   else
     tc::commit(mbar);
 }
@@ -525,7 +544,7 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
           }
         }
         // every MMA issued has completed before the tensor memory is released
-        if (elect_one()) commit<CG>(bar0 + 8 * kDrain);
+        if (elect_one()) commit_here<CG>(bar0 + 8 * kDrain);
         __syncwarp();
         if (!warp_wait(bar0 + 8 * kDrain, 0, p.wait_ns)) bad = 1;
       }
@@ -809,13 +828,16 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
         }
       }
     }
+    if constexpr (CG == 2) cluster_arrive();  // while the last stores are written
     if (lane == 0) tc::bulk_wait_all();
   }
+  if constexpr (CG == 2)
+    if (warp >= kEW) cluster_arrive();
   if (bad && p.status != nullptr) atomicOr(p.status, 1);
 
   tc::fence_before_sync();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync_all();
+  if constexpr (CG == 2) cluster_wait();
   if (warp == kMMA) tmem_dealloc<CG>(tmem);
 }
 
