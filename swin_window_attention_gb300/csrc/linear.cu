@@ -87,10 +87,10 @@ __global__ void __launch_bounds__(kSumGroups * kSumWidth)
 // 9.7 us, 100 tokens 192x768 8.4 and 4.5 us, 300 tokens 6144x1536 12.9 and 23.8 us, 500 tokens
 // 1536x384 10.0 and 9.0 us.
 constexpr int kFewTokens = 1024;
-bool runs_as_clusters(const Tiling& t, const FewTiling& few, int64_t T, int64_t N) {
+bool runs_as_clusters(const Tiling& t, const FewTiling& few, int64_t T, int64_t N, bool bmn) {
   if (T > kFewTokens) return false;
-  double cost = prod::tiling_cost(t, T, N, 1, false);
-  if (T < prod::kBM) cost += 0.9 * (1.0 - (double)T / prod::kBM) * t.chunks * prod::chunk_clocks(t.NT, t.cg);
+  double cost = prod::tiling_cost(t, T, N, 1, bmn, false);
+  if (T < prod::kBM) cost += 0.9 * (1.0 - (double)T / prod::kBM) * t.chunks * prod::chunk_clocks(t.NT, t.cg, bmn);
   return few.cost < cost;
 }
 
@@ -104,7 +104,7 @@ cudaError_t linear_launch(const void* x, const void* w, const float* b, const vo
                           int T, int K, int N, int act, int* status, cudaStream_t st) {
   const Tiling t = prod::choose_tiling(T, N, K, 1, false, 1, false);
   const FewTiling few = few_tiling(T, N, K);
-  if (runs_as_clusters(t, few, T, N))
+  if (runs_as_clusters(t, few, T, N, false))
     return linear_few_launch(few, x, w, b, residual, y, pre, T, K, N, act, status, st);
   Params p{};
   p.M = T;
@@ -124,7 +124,7 @@ cudaError_t linear_bwd_data_launch(const void* dy, const void* w, const void* pr
                                    int act, int* status, cudaStream_t st) {
   const Tiling t = prod::choose_tiling(T, K, N, 1, true, 1, false);
   const FewTiling few = few_tiling(T, K, N);
-  if (runs_as_clusters(t, few, T, K))
+  if (runs_as_clusters(t, few, T, K, true))
     return linear_bwd_data_few_launch(few, dy, w, pre, dx, T, K, N, act, status, st);
   Params p{};
   p.M = T;

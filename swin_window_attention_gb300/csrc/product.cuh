@@ -462,7 +462,8 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
               load_3d<CG>(base, &a_map, c * kKC, w.m0, w.b, fb);
             }
             if constexpr (BMN) {
-              for (int j = 0; j < p.NT / (64 * CG); ++j)
+              // whole boxes of 64 columns: the last one may bring some that belong to the next part
+              for (int j = 0; j * 64 < p.NT / CG; ++j)
                 load_3d<CG>(base + kABytes + j * 8192, &b_map, nb0 + 64 * j, c * kKC, w.b, fb);
             } else {
               load_3d<CG>(base + kABytes, &b_map, c * kKC, nb0, w.b, fb);
@@ -911,17 +912,21 @@ struct Tiling {
 // the longer of its chunks and its epilogue, plus one epilogue that nothing overlaps and,
 // where K is split, the sum of the partial results.
 // A chunk of CG * 128 x NT x 64 takes 2 NT clocks of the tensor cores, 200 to issue, and the
-// 128 + NT / CG rows of 128 bytes a CTA brings for it arrive at some 53 bytes a clock
+// 128 + NT / CG rows of 128 bytes a CTA brings for it (MN-major B comes in blocks of 64) arrive at
+// some 53 bytes a clock
 // (measured: 24.2 us for 96 chunks of 160 rows, 599 us for 1792 of 256).
-inline double chunk_clocks(int NT, int cg) { return std::max({2.0 * NT, 200.0, 2.4 * (kBM + NT / cg)}); }
+inline int b_rows(int NT, int cg, bool bmn) { return bmn ? (NT / cg + 63) / 64 * 64 : NT / cg; }
+inline double chunk_clocks(int NT, int cg, bool bmn) {
+  return std::max({2.0 * NT, 200.0, 2.4 * (kBM + b_rows(NT, cg, bmn))});
+}
 // `extra` columns beside a tile's hold the sums over K; where they lie in the other accumulator
 // every segment of an fp32 result waits for the last one's epilogue, some 2000 clocks.
-inline double tiling_cost(const Tiling& t, int64_t M, int64_t N, int batch, bool sums) {
+inline double tiling_cost(const Tiling& t, int64_t M, int64_t N, int batch, bool bmn, bool sums) {
   const int64_t items = (int64_t)t.n_mt * t.n_nt * t.splits * batch;
   const int64_t groups = kSms / t.cg;
   const double rounds = (double)((items + groups - 1) / groups);
   const double epi = 500.0 + 14.0 * t.NT;
-  double cost = 5000.0 + rounds * std::max(t.chunks_per_split * chunk_clocks(t.NT, t.cg), epi) + epi;
+  double cost = 5000.0 + rounds * std::max(t.chunks_per_split * chunk_clocks(t.NT, t.cg, bmn), epi) + epi;
   if (sums && t.n_nt == 1 && t.NT + 16 * t.cg > kMaxNT) cost += rounds * 2000.0 * (t.chunks_per_split / kSegChunks);
   if (t.splits > 1) cost += 4000.0 + (double)(t.splits + 1) * M * N * 4.0 / 3000.0;
   return cost;
@@ -934,7 +939,6 @@ inline Tiling search_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn
   const int chunks = (int)((K + kKC - 1) / kKC);
   for (int cg = 1; cg <= 2; ++cg) {
     for (int nt = kMaxNT; nt >= 32; nt -= 32) {
-      if (bmn ? nt % (64 * cg) != 0 : nt % (16 * cg) != 0) continue;
       Tiling t{};
       t.cg = cg;
       t.NT = nt;
@@ -947,7 +951,7 @@ inline Tiling search_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn
         if ((chunks + per - 1) / per != s) continue;  // every split has chunks
         t.splits = s;
         t.chunks_per_split = per;
-        const double c = tiling_cost(t, M, N, batch, sums);
+        const double c = tiling_cost(t, M, N, batch, bmn, sums);
         if (best_cost < 0.0 || c < best_cost) {
           best_cost = c;
           best = t;
@@ -1031,7 +1035,7 @@ cudaError_t launch_tiles(const Tiling& t, Params p, const Matrix& a, const Matri
   const uint32_t fmt = in_type == CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 ? 0u : (1u << 7) | (1u << 10);
   p.idesc = tc::idesc_bf16(CG * kBM, t.NT, BMN, AMN) ^ fmt;
   p.idesc_ones = tc::idesc_bf16(CG * kBM, 16 * CG, false, AMN) ^ fmt;
-  p.stage_bytes = kABytes + t.NT / CG * 128;
+  p.stage_bytes = kABytes + b_rows(t.NT, CG, BMN) * 128;
   DeviceInfo di;
   e = device_info(&di);
   if (e != cudaSuccess) return e;
