@@ -21,6 +21,11 @@
 // still a normal number, and the largest B stays a tenth of the largest fp16. Products are
 // accumulated in fp32. Singular values far below the largest come out with the error of
 // rounding the large ones' entries (the same is true, eight times worse, in bf16).
+//
+// Measured on one GB300: two 1536 x 6144 455 us (Gram 36, square 16, update 41 us a step: 83, 51
+// and 71 % of the tensor pipe; norm and scaling 33 us at 61 % of DRAM), eight 2048 x 512 154 us,
+// bound by the chain of fifteen dependent launches. A and A^2 are symmetric, and half of each would
+// do; the tiles on and above the diagonal (42 of 72 on 76 pairs) take one round all the same.
 #include "orthogonalize.cuh"
 #include "product.cuh"
 
