@@ -296,7 +296,7 @@ int swin_wattn_proj_residual(const void* o, const void* w_proj, const float* b_p
  *            read before it is written) but must not overlap x, w, or pre;
  *   pre      bf16 [tokens, N], or NULL: z is also written there, rounded to bf16, for
  *            swin_wattn_linear_bwd_data. act is applied to the unrounded z;
- *   tokens   >= 0 (0: nothing is done); K, N: multiples of 8 in [8, 32768];
+ *   tokens   in [0, 2147482624] (0: nothing is done); K, N: multiples of 8 in [8, 32768];
  *   act      SWIN_WATTN_ACT_*;
  *   status   optional device int (may be NULL): bit 0 is OR-ed in if a bounded device wait
  *            ran out (then the results are not valid).
@@ -304,7 +304,7 @@ int swin_wattn_proj_residual(const void* o, const void* w_proj, const float* b_p
  * applied in fp32 and each result is rounded once. One kernel launch on `stream`; nothing is
  * allocated. Deterministic. Errors: INVALID_ARG for negative tokens, an unknown act, overlapping
  * buffers, or a pointer that is not memory of the current device; MISALIGNED for a pointer
- * off its alignment; UNSUPPORTED for K or N.
+ * off its alignment; UNSUPPORTED for K, N or tokens out of range.
  */
 int swin_wattn_linear(const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
                       int tokens, int K, int N, int act, int* status, struct CUstream_st* stream);
@@ -367,7 +367,8 @@ int swin_wattn_linear_bwd_weight(const void* dy, const void* x, void* dw, float*
  * accumulated in fp32; the result is within about 1.5e-3 (relative 2-norm, before its
  * rounding to bf16) of the exact iteration for matrices whose singular values span a
  * factor of about a hundred, and loses accuracy in the directions of smaller ones. The norm
- * is summed in fp32, with large values scaled so that it does not overflow. A matrix with a
+ * is summed in fp32, with large values scaled so that their squares do not overflow; squares
+ * below the smallest fp32 count as zero (values below 1e-19 in size). A matrix with a
  * NaN or an infinity gives NaN and leaves the others of the stack alone; a zero matrix gives zeros.
  * One launch where the smaller side is at most 128 and the larger at most 4096, else
  * 2 + 3 * steps; nothing is allocated. Deterministic. Errors: INVALID_ARG for the

@@ -156,6 +156,8 @@ int check_buffers(const char* where, const Buffer* bufs, int n, int same_a = -1,
   return SWIN_WATTN_OK;
 }
 
+// Tile rows past the last token still have to fit an int.
+constexpr int kMaxLinearTokens = 0x7fffffff - 1023;
 bool linear_width(int n) { return n >= 8 && n <= 32768 && n % 8 == 0; }
 bool known_act(int act) { return act >= SWIN_WATTN_ACT_NONE && act <= SWIN_WATTN_ACT_SILU; }
 
@@ -640,7 +642,7 @@ int swin_wattn_proj_residual(const void* o, const void* w_proj, const float* b_p
 int swin_wattn_linear(const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
                       int tokens, int K, int N, int act, int* status, struct CUstream_st* stream) {
   if (tokens < 0 || !known_act(act)) return SWIN_WATTN_ERR_INVALID_ARG;
-  if (!linear_width(K) || !linear_width(N)) return SWIN_WATTN_ERR_UNSUPPORTED;
+  if (!linear_width(K) || !linear_width(N) || tokens > kMaxLinearTokens) return SWIN_WATTN_ERR_UNSUPPORTED;
   if (tokens == 0) return SWIN_WATTN_OK;
   if (x == nullptr || w == nullptr || y == nullptr) return SWIN_WATTN_ERR_INVALID_ARG;
   const uint64_t T = (uint64_t)tokens;
@@ -659,7 +661,7 @@ int swin_wattn_linear(const void* x, const void* w, const float* b, const void* 
 int swin_wattn_linear_bwd_data(const void* dy, const void* w, const void* pre, void* dx, int tokens, int K, int N,
                                int act, int* status, struct CUstream_st* stream) {
   if (tokens < 0 || !known_act(act)) return SWIN_WATTN_ERR_INVALID_ARG;
-  if (!linear_width(K) || !linear_width(N)) return SWIN_WATTN_ERR_UNSUPPORTED;
+  if (!linear_width(K) || !linear_width(N) || tokens > kMaxLinearTokens) return SWIN_WATTN_ERR_UNSUPPORTED;
   if (tokens == 0) return SWIN_WATTN_OK;
   if (act == SWIN_WATTN_ACT_NONE) pre = nullptr;
   if (dy == nullptr || w == nullptr || dx == nullptr || (act != SWIN_WATTN_ACT_NONE && pre == nullptr))
@@ -677,7 +679,7 @@ int swin_wattn_linear_bwd_data(const void* dy, const void* w, const void* pre, v
 }
 
 size_t swin_wattn_linear_bwd_weight_workspace_bytes(int tokens, int K, int N) {
-  if (tokens < 0 || !linear_width(K) || !linear_width(N)) return 0;
+  if (tokens < 0 || tokens > kMaxLinearTokens || !linear_width(K) || !linear_width(N)) return 0;
   return swin::linear_bwd_weight_workspace_bytes(tokens, K, N);
 }
 
@@ -685,7 +687,7 @@ int swin_wattn_linear_bwd_weight(const void* dy, const void* x, void* dw, float*
                                  int dtype, int accumulate, void* workspace, size_t workspace_bytes, int* status,
                                  struct CUstream_st* stream) {
   if (tokens < 0 || (dtype != SWIN_WATTN_FP32 && dtype != SWIN_WATTN_BF16)) return SWIN_WATTN_ERR_INVALID_ARG;
-  if (!linear_width(K) || !linear_width(N)) return SWIN_WATTN_ERR_UNSUPPORTED;
+  if (!linear_width(K) || !linear_width(N) || tokens > kMaxLinearTokens) return SWIN_WATTN_ERR_UNSUPPORTED;
   if (dw == nullptr || (tokens > 0 && (dy == nullptr || x == nullptr || workspace == nullptr)))
     return SWIN_WATTN_ERR_INVALID_ARG;
   if (tokens > 0 && workspace_bytes < swin::linear_bwd_weight_workspace_bytes(tokens, K, N)) {

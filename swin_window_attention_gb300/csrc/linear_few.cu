@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
     constexpr int kBatch = 8;
     const int n = n0 + (tid & (kBM - 1));
     if (warp < kFewEpi && n < p.N) {
-      const float bias = EPI == kEpiAct && p.bias != nullptr ? __ldg(p.bias + n) : 0.0f;
+      const float bias = EPI == kEpiAct && p.bias != nullptr ? p.bias[n] : 0.0f;
       const uint32_t mine = smem0 + (n - n0) * 4;
       uint32_t peer[kMaxCluster];
 #pragma unroll

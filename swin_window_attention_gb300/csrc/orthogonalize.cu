@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(const T* __rest
   pdl_wait();
   const float2 p = (int)threadIdx.x < n_partial ? partial[blockIdx.y * n_partial + threadIdx.x] : make_float2(0.0f, 0.0f);
   const float2 s = block_sum(p.x, p.y);
-  const float inv = kScale / (norm_of(s.x, s.y) + eps);
+  const float inv = __fdiv_rn(kScale, norm_of(s.x, s.y) + eps);
   const int64_t elements = (int64_t)rows * cols;
   const T* gm = g + (int64_t)blockIdx.y * elements;
   __half* xm = x + (int64_t)blockIdx.y * rows * ld;

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
     lo += a;
     hi += b;
   }
-  const float inv = kScale / (norm_of(lo, hi) + p.eps);
+  const float inv = __fdiv_rn(kScale, norm_of(lo, hi) + p.eps);
   if (vec) {
 #pragma unroll 2
     for (int i = tid; i < n8; i += kSmThreads) {

@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
 #pragma unroll
         for (int i = 0; i < kSlices; ++i) {
           const int c = w.n0 + (part + kPerQuad * i) * kSC + lane;
-          bt[i] = p.bias != nullptr && c < p.N ? __ldg(p.bias + c) : 0.0f;
+          bt[i] = p.bias != nullptr && c < p.N ? p.bias[c] : 0.0f;
         }
       }
       float seg_sum[EPI == kEpiGrad32 ? kSlices : 1][32];  // kEpiGrad32: the segments' sum, a slice each

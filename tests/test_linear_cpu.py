@@ -21,6 +21,7 @@ def test_products_reject_bad_arguments_before_touching_cuda(lib):
         assert f(4, 60, 64) == lib.ERR_UNSUPPORTED and f(4, 64, 4) == lib.ERR_UNSUPPORTED
         assert f(4, 0, 64) == lib.ERR_UNSUPPORTED and f(4, 64, 32776) == lib.ERR_UNSUPPORTED
         assert f(0, 64, 64) == lib.OK
+        assert f(2 ** 31 - 1, 8, 8) == lib.ERR_UNSUPPORTED
         assert f(4, 64, 64) == lib.ERR_INVALID_ARG  # null pointers
     wgt = lambda T, K, N, dt=1, nb=0: lib.swin_wattn_linear_bwd_weight(*([None] * 4), T, K, N, dt, 0, None, nb, None,
                                                                        None)
@@ -31,8 +32,8 @@ def test_products_reject_bad_arguments_before_touching_cuda(lib):
 
 def test_workspace_sizes(lib):
     f = lib.swin_wattn_linear_bwd_weight_workspace_bytes
-    assert f(-1, 64, 64) == 0 and f(4, 60, 64) == 0 and f(4, 64, 0) == 0
-    for T, K, N in [(0, 8, 8), (1, 8, 8), (50176, 192, 768), (2 ** 31 - 1, 8, 8), (12544, 1536, 6144), (1, 32768, 32768)]:
+    assert f(-1, 64, 64) == 0 and f(4, 60, 64) == 0 and f(4, 64, 0) == 0 and f(2 ** 31 - 1, 8, 8) == 0
+    for T, K, N in [(0, 8, 8), (1, 8, 8), (50176, 192, 768), (2 ** 31 - 1024, 8, 8), (12544, 1536, 6144), (1, 32768, 32768)]:
         n = f(T, K, N)
         assert n >= 256 and (n == 256 or n % ((N * K + N) * 4) == 0)
     g = lib.swin_wattn_orthogonalize_workspace_bytes
