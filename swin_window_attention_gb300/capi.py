@@ -329,22 +329,19 @@ def swin_wattn_orthogonalize(g_ptr, out_ptr, count, rows, cols, dtype, steps, ep
 # is over in a few microseconds, so the checks compare attributes first and look for the
 # reason only when one differs.
 
-_BF16 = (torch.bfloat16,)
-_F32 = (torch.float32,)
-_F32_BF16 = (torch.float32, torch.bfloat16)
-_U8 = (torch.uint8,)
-_I32 = (torch.int32,)
+_BF16 = torch.bfloat16
+_F32 = torch.float32
 
 
-def _tensor(name, t, shape, dtypes, dev):
-    """Check one operand: a contiguous CUDA tensor of the given shape, one of the given dtypes,
-    on CUDA device number `dev`. Returns its address."""
-    if t.get_device() == dev and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+def _address(name, t, shape, dtype, dev):
+    """The address of one operand, checked: a contiguous CUDA tensor of the given shape and
+    dtype on CUDA device number `dev`."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.shape == shape:
         return t.data_ptr()
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     raise ValueError(f"{name} is not contiguous")
@@ -357,10 +354,19 @@ def _device_of(name, t):
     return dev
 
 
+def _float_code(name, t):
+    """FP32 or BF16 for a tensor that may be either."""
+    if t.dtype is _F32:
+        return FP32
+    if t.dtype is _BF16:
+        return BF16
+    raise ValueError(f"{name} has dtype {t.dtype}, not {_F32} or {_BF16}")
+
+
 def _call(fn, dev, stream, status, *args):
     """The C function fn(*args, status, stream) with device number `dev` current, on `stream`
     or that device's current stream; raises on an error status."""
-    st = None if status is None else _tensor("status", status, (1,), _I32, dev)
+    st = None if status is None else _address("status", status, (1,), torch.int32, dev)
     handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if dev == torch._C._cuda_getDevice():
         rc = fn(*args, st, handle)
@@ -380,6 +386,14 @@ def _empty(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _workspace(workspace, need, dev, stream):
+    """The workspace given, or one of `need` bytes: the tensor, its address and its size."""
+    if workspace is None:
+        workspace = _empty((max(need(), 1),), torch.uint8, dev, stream)
+    nbytes = workspace.numel()
+    return workspace, _address("workspace", workspace, (nbytes,), torch.uint8, dev), nbytes
+
+
 def _act_code(act):
     code = ACTIVATIONS.get(act) if type(act) is str else act
     if code is None or not ACT_NONE <= code <= ACT_SILU:
@@ -388,16 +402,10 @@ def _act_code(act):
 
 
 def _weight(w, dev):
-    if w.dim() != 2:
-        raise ValueError(f"w has {w.dim()} dimensions, not 2")
     shape = w.shape
-    return (*shape, _tensor("w", w, shape, _BF16, dev))
-
-
-def _rows(name, t, width, dev):
-    """Check a bf16 [..., width] tensor; returns its leading axes and its address."""
-    lead = t.shape[:-1]
-    return lead, _tensor(name, t, (*lead, width), _BF16, dev)
+    if len(shape) != 2:
+        raise ValueError(f"w has {len(shape)} dimensions, not 2")
+    return (*shape, _address("w", w, shape, _BF16, dev))
 
 
 def linear(x, w, b=None, act=ACT_NONE, residual=None, y=None, pre=None, status=None, stream=None):
@@ -406,18 +414,16 @@ def linear(x, w, b=None, act=ACT_NONE, residual=None, y=None, pre=None, status=N
     not given; it may be the residual itself). act: "none", "relu", "gelu", "gelu_tanh",
     "silu" or an ACT_ code. pre, a bf16 [..., N] tensor, receives x W^T + b for the backward."""
     dev = _device_of("x", x)
-    code = _act_code(act)
     N, K, w_ptr = _weight(w, dev)
-    lead, x_ptr = _rows("x", x, K, dev)
+    lead = x.shape[:-1]
     shape = (*lead, N)
-    b_ptr = None if b is None else _tensor("b", b, (N,), _F32, dev)
-    r_ptr = None if residual is None else _tensor("residual", residual, shape, _BF16, dev)
-    p_ptr = None if pre is None else _tensor("pre", pre, shape, _BF16, dev)
     if y is None:
-        y = _empty(shape, torch.bfloat16, dev, stream)
-    y_ptr = _tensor("y", y, shape, _BF16, dev)
-    _call(load().swin_wattn_linear, dev, stream, status, x_ptr, w_ptr, b_ptr, r_ptr, y_ptr, p_ptr, lead.numel(), K, N,
-          code)
+        y = _empty(shape, _BF16, dev, stream)
+    _call(load().swin_wattn_linear, dev, stream, status, _address("x", x, (*lead, K), _BF16, dev), w_ptr,
+          None if b is None else _address("b", b, (N,), _F32, dev),
+          None if residual is None else _address("residual", residual, shape, _BF16, dev),
+          _address("y", y, shape, _BF16, dev), None if pre is None else _address("pre", pre, shape, _BF16, dev),
+          lead.numel(), K, N, _act_code(act))
     return y
 
 
@@ -428,16 +434,15 @@ def linear_bwd_data(dy, w, pre=None, act=ACT_NONE, dx=None, status=None, stream=
     dev = _device_of("dy", dy)
     code = _act_code(act)
     N, K, w_ptr = _weight(w, dev)
-    lead, dy_ptr = _rows("dy", dy, N, dev)
+    lead = dy.shape[:-1]
     shape = (*lead, K)
     if code != ACT_NONE and pre is None:
         raise ValueError("an activation needs its pre-activation: pre is None")
-    p_ptr = None if pre is None else _tensor("pre", pre, shape, _BF16, dev)
     if dx is None:
-        dx = _empty(shape, torch.bfloat16, dev, stream)
-    dx_ptr = _tensor("dx", dx, shape, _BF16, dev)
-    _call(load().swin_wattn_linear_bwd_data, dev, stream, status, dy_ptr, w_ptr, p_ptr, dx_ptr, lead.numel(), K, N,
-          code)
+        dx = _empty(shape, _BF16, dev, stream)
+    _call(load().swin_wattn_linear_bwd_data, dev, stream, status, _address("dy", dy, (*lead, N), _BF16, dev), w_ptr,
+          None if pre is None else _address("pre", pre, shape, _BF16, dev), _address("dx", dx, shape, _BF16, dev),
+          lead.numel(), K, N, code)
     return dx
 
 
@@ -448,24 +453,20 @@ def linear_bwd_weight(dy, x, dw=None, db=None, accumulate=False, workspace=None,
     workspace: a uint8 tensor of swin_wattn_linear_bwd_weight_workspace_bytes (allocated here
     when not given). Returns (dw, db)."""
     dev = _device_of("dy", dy)
-    N, K = dy.shape[-1], x.shape[-1]
-    lead, dy_ptr = _rows("dy", dy, N, dev)
-    x_ptr = _tensor("x", x, (*lead, K), _BF16, dev)
+    N, K, lead = dy.shape[-1], x.shape[-1], dy.shape[:-1]
+    tokens = lead.numel()
     if dw is None:
         if accumulate:
             raise ValueError("accumulate needs the dw to add to")
-        dw = _empty((N, K), torch.float32, dev, stream)
-        db = _empty((N,), torch.float32, dev, stream) if db is None else db
-    dw_ptr = _tensor("dw", dw, (N, K), _F32_BF16, dev)
-    db_ptr = None if db is None else _tensor("db", db, (N,), _F32, dev)
-    tokens = lead.numel()
-    if workspace is None:
-        workspace = _empty((max(swin_wattn_linear_bwd_weight_workspace_bytes(tokens, K, N), 1),), torch.uint8, dev,
-                           stream)
-    nbytes = workspace.numel()
-    ws_ptr = _tensor("workspace", workspace, (nbytes,), _U8, dev)
-    _call(load().swin_wattn_linear_bwd_weight, dev, stream, status, dy_ptr, x_ptr, dw_ptr, db_ptr, tokens, K, N,
-          FP32 if dw.dtype == torch.float32 else BF16, 1 if accumulate else 0, ws_ptr, nbytes)
+        dw = _empty((N, K), _F32, dev, stream)
+        db = _empty((N,), _F32, dev, stream) if db is None else db
+    code = _float_code("dw", dw)
+    workspace, ws_ptr, nbytes = _workspace(
+        workspace, lambda: swin_wattn_linear_bwd_weight_workspace_bytes(tokens, K, N), dev, stream)
+    _call(load().swin_wattn_linear_bwd_weight, dev, stream, status, _address("dy", dy, (*lead, N), _BF16, dev),
+          _address("x", x, (*lead, K), _BF16, dev), _address("dw", dw, (N, K), dw.dtype, dev),
+          None if db is None else _address("db", db, (N,), _F32, dev), tokens, K, N, code, 1 if accumulate else 0,
+          ws_ptr, nbytes)
     return dw, db
 
 
@@ -475,20 +476,17 @@ def orthogonalize(g, steps=5, eps=1e-7, scale=1.0, out=None, workspace=None, sta
     its shape (allocated here when not given). workspace: a uint8 tensor of
     swin_wattn_orthogonalize_workspace_bytes (allocated here when not given)."""
     dev = _device_of("g", g)
-    if g.dim() not in (2, 3):
-        raise ValueError(f"g has {g.dim()} dimensions, not 2 or 3")
-    g_ptr = _tensor("g", g, g.shape, _F32_BF16, dev)
-    count, (rows, cols) = (1 if g.dim() == 2 else g.shape[0]), g.shape[-2:]
+    shape, code = g.shape, _float_code("g", g)
+    if len(shape) not in (2, 3):
+        raise ValueError(f"g has {len(shape)} dimensions, not 2 or 3")
+    count, rows, cols = (1, *shape) if len(shape) == 2 else shape
     if out is None:
-        out = _empty(g.shape, torch.bfloat16, dev, stream)
-    out_ptr = _tensor("out", out, g.shape, _BF16, dev)
-    if workspace is None:
-        workspace = _empty((max(swin_wattn_orthogonalize_workspace_bytes(count, rows, cols), 1),), torch.uint8, dev,
-                           stream)
-    nbytes = workspace.numel()
-    ws_ptr = _tensor("workspace", workspace, (nbytes,), _U8, dev)
-    _call(load().swin_wattn_orthogonalize, dev, stream, status, g_ptr, out_ptr, count, rows, cols,
-          FP32 if g.dtype == torch.float32 else BF16, int(steps), float(eps), float(scale), ws_ptr, nbytes)
+        out = _empty(shape, _BF16, dev, stream)
+    workspace, ws_ptr, nbytes = _workspace(
+        workspace, lambda: swin_wattn_orthogonalize_workspace_bytes(count, rows, cols), dev, stream)
+    _call(load().swin_wattn_orthogonalize, dev, stream, status, _address("g", g, shape, g.dtype, dev),
+          _address("out", out, shape, _BF16, dev), count, rows, cols, code, int(steps), float(eps), float(scale),
+          ws_ptr, nbytes)
     return out
 
 
