@@ -60,10 +60,10 @@ template <bool TALL, typename T>
 __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(const SmallParams p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_tmem;
-  __shared__ __align__(8) uint64_t s_bar;
+  __shared__ __align__(8) uint64_t s_bar[3];
   __shared__ float2 s_part[kSmWarps], s_norm;
   pdl_launch_dependents();
-  const uint32_t smem0 = smem_u32(smem), bar = smem_u32(&s_bar);
+  const uint32_t smem0 = smem_u32(smem), bar = smem_u32(s_bar);  // A and A^2; the update's two halves
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int S = p.cluster, rank = blockIdx.x % S, mat = blockIdx.x / S;
   const int m = TALL ? p.cols : p.rows, n = TALL ? p.rows : p.cols;
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
 
   if (warp == 0) tc::tmem_alloc<512>(smem_u32(&s_tmem));
   if (tid == 0) {
-    tc::mbar_init(bar, 1);
+    for (int i = 0; i < 3; ++i) tc::mbar_init(bar + 8 * i, 1);
     tc::mbar_init_fence();
   }
   for (int i = tid; i < p.slab_bytes / 16; i += kSmThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
@@ -99,16 +99,46 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
   // eight columns at a time where every row starts on a 16-byte boundary
   const bool vec = p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(p.g) % 16 == 0;
   const int c8 = scols / 8, n8 = srows * c8;  // vec: scols is a multiple of 8
+  const int quad = warp & 3, part = warp >> 2;  // tensor-memory lanes; columns
+  const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
+  // vec: this thread's pieces are tid, tid + 512, ...; their rows and columns advance by these
+  const int r_first = vec ? tid / c8 : 0, c_first = tid - r_first * c8;
+  const int r_step = vec ? kSmThreads / c8 : 0, c_step = kSmThreads - r_step * c8;
+  constexpr int kPieces = kSide * kSlab / 8 / kSmThreads;  // per thread at most
   {
     float lo = 0.0f, hi = 0.0f;
     if (vec) {
-#pragma unroll 2
-      for (int i = tid; i < n8; i += kSmThreads) {
-        float v[8];
-        load8(g + (int64_t)(i / c8) * p.cols + i % c8 * 8, v);
+      // G is read once: it waits for its norm in tensor memory, which is idle until the steps
+      int r = r_first, c = c_first;
+#pragma unroll 1
+      for (int i = 0; i < kPieces && (tid & ~31) + i * kSmThreads < n8; i += 4) {
+        float v[4][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) add_square(v[e], lo, hi);
+        for (int u = 0; u < 4; ++u) {
+          if (tid + (i + u) * kSmThreads < n8) {
+            load8(g + (int64_t)r * p.cols + c * 8, v[u]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
+          }
+          r += r_step;
+          c += c_step;
+          if (c >= c8) {
+            c -= c8;
+            ++r;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) add_square(v[u][e], lo, hi);
+        uint32_t w[32];
+#pragma unroll
+        for (int u = 0; u < 32; ++u) w[u] = __float_as_uint(v[u >> 3][u & 7]);
+        __syncwarp();
+        tc::st_x32(trow + part * 128 + i * 8, w);
       }
+      tc::wait_st();
     } else {
       for (int r = warp; r < srows; r += kSmWarps)
         for (int c = lane; c < scols; c += 32) add_square(load_f32(g + (int64_t)r * p.cols + c), lo, hi);
@@ -142,14 +172,26 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
   }
   const float inv = __fdiv_rn(kScale, norm_of(lo, hi) + p.eps);
   if (vec) {
-#pragma unroll 2
-    for (int i = tid; i < n8; i += kSmThreads) {
-      const int r = i / c8, c = i % c8 * 8;
-      float v[8];
-      load8(g + (int64_t)r * p.cols + c, v);
-      *reinterpret_cast<uint4*>(smem + at(r, c)) =
-          make_uint4(pack_f16(v[0] * inv, v[1] * inv), pack_f16(v[2] * inv, v[3] * inv), pack_f16(v[4] * inv, v[5] * inv),
-                     pack_f16(v[6] * inv, v[7] * inv));
+    int r = r_first, c = c_first;
+#pragma unroll 1
+    for (int i = 0; i < kPieces && (tid & ~31) + i * kSmThreads < n8; i += 4) {
+      uint32_t w[32];
+      tc::ld32_wait(trow + part * 128 + i * 8, w);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e] = pack_f16(__uint_as_float(w[8 * u + 2 * e]) * inv, __uint_as_float(w[8 * u + 2 * e + 1]) * inv);
+        if (tid + (i + u) * kSmThreads < n8)
+          *reinterpret_cast<uint4*>(smem + at(r, 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+        r += r_step;
+        c += c_step;
+        if (c >= c8) {
+          c -= c8;
+          ++r;
+        }
+      }
     }
   } else {
     for (int r = warp; r < srows; r += kSmWarps)
@@ -157,45 +199,53 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
         *reinterpret_cast<__half*>(smem + at(r, c)) = __float2half_rn(load_f32(g + (int64_t)r * p.cols + c) * inv);
   }
   tc::fence_proxy_async();
+  tc::fence_before_sync();
   __syncthreads();
 
   // ---- the steps ------------------------------------------------------------------------
   constexpr uint32_t kHi = desc_hi(1024, kSW128);
   const uint32_t id_gram = (tc::idesc_bf16(kSide, 16, TALL, TALL) ^ kF16Format) + ((uint32_t)(mp - 16) >> 3 << 17);
   const uint32_t id_mat = (tc::idesc_bf16(kSide, 16, false, false) ^ kF16Format) + ((uint32_t)(mp - 16) >> 3 << 17);
-  uint32_t phase = 0;
-  // warp 0 issues; every thread waits for the products to complete
-  auto products = [&](auto issue) {
+  // Warp 0 issues; every thread waits for the products to complete.
+  auto issue = [&](auto mmas) {
     if (warp == 0 && !bad) {
       tc::fence_after_sync();
-      if (elect_one()) {
-        issue();
-#ifdef SWIN_WATTN_FAULT_INJECTION
-        if (p.fault != kFaultGemm)
-#endif
-          tc::commit(bar);
-      }
+      if (elect_one()) mmas();
       __syncwarp();
     }
-    if (!bad && !warp_wait(bar, phase, p.wait_ns)) bad = 1;
-    phase ^= 1;
+  };
+  auto commit_products = [&](int i) {
+#ifdef SWIN_WATTN_FAULT_INJECTION
+    if (p.fault != kFaultGemm)
+#endif
+      tc::commit(bar + 8 * i);
+  };
+  auto wait_products = [&](int i, uint32_t parity) {
+    if (!bad && !warp_wait(bar + 8 * i, parity, p.wait_ns)) bad = 1;
     tc::fence_after_sync();
   };
-  const int quad = warp & 3, part = warp >> 2;  // tensor-memory lanes; columns
   const int row = quad * 32 + lane;
-  const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
   const int k_steps = (len + 15) / 16;  // of the Gram product
   const int m_steps = mp / 16;
+  const uint32_t block_d = block >> 4;  // in a descriptor's units
+  // A's part, the K steps [t0, t1): columns [0, mp) of the accumulator
+  auto gram = [&](int t0, int t1) {
+    uint32_t x = TALL ? desc_lo(slab0, block) + t0 * 128 : desc_lo(slab0, 16) + (t0 >> 2) * block_d + (t0 & 3) * 2;
+    for (int t = t0; t < t1; ++t) {
+      mma<1>(tmem, x, kHi, x, kHi, id_gram, t > 0);
+      x += TALL ? 128 : (t & 3) == 3 ? block_d - 6 : 2;
+    }
+  };
+  uint32_t phase = 0;
+  issue([&]() {
+    gram(0, k_steps);
+    commit_products(0);
+  });
 
   for (int step = 0; step < p.steps; ++step) {
     const bool last = step == p.steps - 1;
-    // A's part: columns [0, mp) of the accumulator
-    products([&]() {
-      for (int t = 0; t < k_steps; ++t) {
-        const uint32_t x = TALL ? desc_lo(slab0 + t * 2048, block) : desc_lo(slab0 + (t >> 2) * block + (t & 3) * 32, 16);
-        mma<1>(tmem, x, kHi, x, kHi, id_gram, t > 0);
-      }
-    });
+    wait_products(0, phase);
+    phase ^= 1;
     const int c0 = part * 32;
     if (S == 1) {
       if (c0 < mp) {
@@ -259,12 +309,16 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
     __syncthreads();
 
     // A^2 behind the Gram accumulator, then B
-    products([&]() {
+    issue([&]() {
+      uint32_t x = desc_lo(a0, 16);
       for (int t = 0; t < m_steps; ++t) {
-        const uint32_t x = desc_lo(a0 + (t >> 2) * (kSide * 128) + (t & 3) * 32, 16);
         mma<1>(tmem + kSide, x, kHi, x, kHi, id_mat, t > 0);
+        x += (t & 3) == 3 ? (kSide * 128 >> 4) - 6 : 2;
       }
+      commit_products(0);
     });
+    wait_products(0, phase);
+    phase ^= 1;
     if (c0 < mp) {
       uint32_t a[32];
       tc::ld32_wait(trow + kSide + c0, a);
@@ -288,48 +342,75 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
     tc::fence_before_sync();
     __syncthreads();
 
-    // the slab times B: wide, 128 rows by up to 512 columns in one accumulator of 512 columns;
-    // tall, up to four tiles of 128 rows by mp columns
-    products([&]() {
-      if constexpr (TALL) {
-        for (int tile = 0; tile < p.slab_rows / kSide; ++tile)
-          for (int t = 0; t < m_steps; ++t)
-            mma<1>(tmem + tile * kSide, desc_lo(slab0 + tile * (kSide * 128) + (t >> 2) * block + (t & 3) * 32, 16), kHi,
-                   desc_lo(b0 + (t >> 2) * (kSide * 128) + (t & 3) * 32, 16), kHi, id_mat, t > 0);
-      } else {
-        for (int c = 0; c < len; c += 256) {
-          const int nn = min(256, (len - c + 15) & ~15);
+    // The slab times B, in two halves: wide, 128 rows by up to 256 columns each; tall, two tiles
+    // of 128 rows by mp columns each.
+    const int halves = TALL ? (p.slab_rows + 255) / 256 : (len + 255) / 256;
+    issue([&]() {
+      for (int h = 0; h < halves; ++h) {
+        if constexpr (TALL) {
+          for (int tile = 2 * h; tile < min(2 * h + 2, p.slab_rows / kSide); ++tile) {
+            uint32_t x = desc_lo(slab0 + tile * (kSide * 128), 16), y = desc_lo(b0, 16);
+            for (int t = 0; t < m_steps; ++t) {
+              mma<1>(tmem + tile * kSide, x, kHi, y, kHi, id_mat, t > 0);
+              x += (t & 3) == 3 ? block_d - 6 : 2;
+              y += (t & 3) == 3 ? (kSide * 128 >> 4) - 6 : 2;
+            }
+          }
+        } else {
+          const int c = 256 * h, nn = min(256, (len - c + 15) & ~15);
           const uint32_t id = (tc::idesc_bf16(kSide, 16, true, false) ^ kF16Format) + ((uint32_t)(nn - 16) >> 3 << 17);
-          for (int t = 0; t < m_steps; ++t)
-            mma<1>(tmem + c, desc_lo(b0 + (t >> 2) * (kSide * 128) + (t & 3) * 32, 16), kHi,
-                   desc_lo(slab0 + (c >> 6) * block + t * 2048, block), kHi, id, t > 0);
+          uint32_t x = desc_lo(b0, 16), y = desc_lo(slab0 + 4 * h * block, block);
+          for (int t = 0; t < m_steps; ++t) {
+            mma<1>(tmem + c, x, kHi, y, kHi, id, t > 0);
+            x += (t & 3) == 3 ? (kSide * 128 >> 4) - 6 : 2;
+            y += 128;
+          }
         }
+        commit_products(1 + h);
       }
     });
     const float alpha = last ? p.scale / (kScale * kScale) : 1.0f / kScale;
-    // the accumulator's 32-column pieces, four quadrants' rows each: wide, piece = columns; tall,
-    // tile of 128 rows and columns
-    const int n_pieces = TALL ? p.slab_rows / kSide * ((mp + 31) / 32) : (len + 31) / 32;
-    for (int i = part; i < n_pieces; i += 4) {
-      const int tiles32 = (mp + 31) / 32;
-      const int r = TALL ? i / tiles32 * kSide + row : row, c = (TALL ? i % tiles32 : i) * 32;
-      const uint32_t col = TALL ? (uint32_t)(i / tiles32 * kSide + c) : (uint32_t)c;
-      uint32_t a[32];
-      tc::ld32_wait(trow + col, a);
+    // The accumulator's 32-column pieces, four quadrants' rows each: wide, piece = columns; tall,
+    // tile of 128 rows and columns. After each round of four pieces the next step's Gram product
+    // takes the 128 columns (rows) that are complete; its accumulator is the first piece's place,
+    // which has been read by then.
+    const int tiles32 = (mp + 31) / 32;
+    const int n_pieces = TALL ? p.slab_rows / kSide * tiles32 : (len + 31) / 32;
+    int waited = 0, begun = 0;  // halves; K steps
+    for (int i0 = 0; i0 < n_pieces; i0 += 4) {
+      const int i = i0 + part, i_last = min(i0 + 3, n_pieces - 1);
+      // every thread waits for the halves that hold the round's pieces
+      const int need = (TALL ? i_last / tiles32 / 2 : i_last / 8) + 1;
+      for (; waited < need; ++waited) wait_products(1 + waited, step & 1);
+      if (i < n_pieces) {
+        const int r = TALL ? i / tiles32 * kSide + row : row, c = (TALL ? i % tiles32 : i) * 32;
+        const uint32_t col = TALL ? (uint32_t)(i / tiles32 * kSide + c) : (uint32_t)c;
+        uint32_t a[32];
+        tc::ld32_wait(trow + col, a);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t o[4];
+        for (int k = 0; k < 4; ++k) {
+          uint32_t o[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float x = __uint_as_float(a[8 * k + 2 * q]) * alpha, y = __uint_as_float(a[8 * k + 2 * q + 1]) * alpha;
-          o[q] = last ? pack_bf16(x, y) : pack_f16(x, y);
+          for (int q = 0; q < 4; ++q) {
+            const float x = __uint_as_float(a[8 * k + 2 * q]) * alpha, y = __uint_as_float(a[8 * k + 2 * q + 1]) * alpha;
+            o[q] = last ? pack_bf16(x, y) : pack_f16(x, y);
+          }
+          *reinterpret_cast<uint4*>(smem + at(r, c + 8 * k)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        *reinterpret_cast<uint4*>(smem + at(r, c + 8 * k)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      tc::fence_proxy_async();
+      tc::fence_before_sync();
+      __syncthreads();
+      if (!last) {
+        const bool end = i0 + 4 >= n_pieces;
+        const int complete = end ? k_steps : min(k_steps, 8 * (TALL ? (i0 + 4) / tiles32 : i0 / 4 + 1));
+        issue([&]() {
+          gram(begun, complete);
+          if (end) commit_products(0);
+        });
+        begun = complete;
       }
     }
-    tc::fence_proxy_async();
-    tc::fence_before_sync();
-    __syncthreads();
   }
 
   // ---- the result, from the slab in bf16 -------------------------------------------------
