@@ -18,10 +18,6 @@ using namespace prod;
 constexpr int kFewTmem = 128;  // columns: the accumulator
 constexpr int kFewEpi = 16, kFewMMA = kFewEpi, kFewCOPY = kFewEpi + 1, kFewWarps = kFewEpi + 2;
 constexpr int kMaxCluster = 8, kMaxTN = 128;
-// Clusters of each size that are resident at once on one GB300 (as cudaOccupancyMaxActiveClusters
-// reports them at one CTA per SM: a cluster stays within a group of SMs, and the groups are
-// not multiples of every size).
-constexpr int kResident[kMaxCluster + 1] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
 constexpr int kFullBar = 0, kEmptyBar = kMaxStages, kDoneBar = 2 * kMaxStages, kFewBars = kDoneBar + 1;
 
 struct FewParams {
@@ -299,9 +295,9 @@ FewTiling few_tiling(int64_t T, int N, int64_t K) {
   t.cluster = 1;
   const int64_t tiles = (int64_t)t.n_tiles * t.t_tiles;
   for (int s = 2; s <= kMaxCluster; ++s)
-    if (tiles <= kResident[s] && t.chunks >= 2 * s) t.cluster = s;
+    if (tiles <= kResidentClusters[s] && t.chunks >= 2 * s) t.cluster = s;
   const double chunks = (t.chunks + t.cluster - 1) / t.cluster;
-  const double rounds = (double)((tiles + kResident[t.cluster] - 1) / kResident[t.cluster]);
+  const double rounds = (double)((tiles + kResidentClusters[t.cluster] - 1) / kResidentClusters[t.cluster]);
   t.cost = 7000.0 + rounds * (chunks * std::max(200.0, 2.4 * (kBM + t.TN)) + 500.0 * t.cluster + 40.0 * t.TN);
   return t;
 }

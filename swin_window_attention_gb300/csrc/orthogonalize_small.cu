@@ -43,9 +43,30 @@ struct SmallParams {
   int fault;
 };
 
-__device__ __forceinline__ void store_cluster(uint32_t addr, uint4 v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint2 v) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};\n" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
+// One CTA has reached a point, with all its threads' accesses before it: an arrival on a barrier
+// of another CTA, and the wait for all of them.
+__device__ __forceinline__ void arrive_release_cluster(uint32_t mbar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(mbar) : "memory");
+}
+__device__ __forceinline__ bool wait_acquire_cluster(uint32_t mbar, uint32_t parity, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred q;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 q, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(ok)
+        : "r"(mbar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    uint64_t t1;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t1));
+    if (t0 == 0) t0 = t1;
+    if (t1 - t0 > limit_ns) return false;
+  }
 }
 __device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
   float4 v;
@@ -60,10 +81,10 @@ template <bool TALL, typename T>
 __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(const SmallParams p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_tmem;
-  __shared__ __align__(8) uint64_t s_bar[3];
+  __shared__ __align__(8) uint64_t s_bar[6];
   __shared__ float2 s_part[kSmWarps], s_norm;
   pdl_launch_dependents();
-  const uint32_t smem0 = smem_u32(smem), bar = smem_u32(s_bar);  // A and A^2; the update's two halves
+  const uint32_t smem0 = smem_u32(smem), bar = smem_u32(s_bar);  // A and A^2; the update's two halves; the cluster's exchanges
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int S = p.cluster, rank = blockIdx.x % S, mat = blockIdx.x / S;
   const int m = TALL ? p.cols : p.rows, n = TALL ? p.rows : p.cols;
@@ -82,7 +103,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
 
   if (warp == 0) tc::tmem_alloc<512>(smem_u32(&s_tmem));
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) tc::mbar_init(bar + 8 * i, 1);
+    for (int i = 0; i < 6; ++i) tc::mbar_init(bar + 8 * i, i < 3 ? 1 : S);
     tc::mbar_init_fence();
   }
   for (int i = tid; i < p.slab_bytes / 16; i += kSmThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
@@ -224,6 +245,14 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
     if (!bad && !warp_wait(bar + 8 * i, parity, p.wait_ns)) bad = 1;
     tc::fence_after_sync();
   };
+  // Every CTA of the cluster has reached exchange i of this step. (One thread a peer releases for
+  // its CTA: in a cluster barrier each of the 512 threads orders its own accesses, which took
+  // up to 4000 clocks.)
+  auto exchange = [&](int i, uint32_t parity) {
+    __syncthreads();
+    if (tid < S) arrive_release_cluster(map_to_rank(bar + 8 * (3 + i), tid));
+    if (!bad && !__all_sync(0xffffffffu, wait_acquire_cluster(bar + 8 * (3 + i), parity, p.wait_ns))) bad = 1;
+  };
   const int row = quad * 32 + lane;
   const int k_steps = (len + 15) / 16;  // of the Gram product
   const int m_steps = mp / 16;
@@ -273,36 +302,34 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
           *reinterpret_cast<uint4*>(fp + f_at(row, c0 / 4 + c)) = make_uint4(a[4 * c], a[4 * c + 1], a[4 * c + 2], a[4 * c + 3]);
       }
       tc::fence_before_sync();
-      cluster_sync_all();
-      // rows rank, rank + S, ... : a thread sums eight columns of a row over the cluster
-      constexpr int kMine = kSide / 2 * (kSide / 8) / kSmThreads;  // at S = 2, pieces per thread
-      uint4 mine[kMine];
-      const int my_rows = (mp - rank + S - 1) / S, pieces = mp / 8;
+      exchange(0, step & 1);
+      // Rows rank, rank + S, ...: a thread sums four columns of a row over the cluster, a warp
+      // whole rows, so that what it reads of another CTA at once is contiguous.
+      constexpr int kMine = kSide / 2 * (kSide / 4) / kSmThreads;  // at S = 2, pieces per thread
+      uint2 mine[kMine];
+      const int my_rows = (mp - rank + S - 1) / S, pieces = mp / 4;
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int e = tid + i * kSmThreads, r = rank + e / pieces * S, c = e % pieces;
         if (e < my_rows * pieces) {
-          float4 u = make_float4(0, 0, 0, 0), v = u;
+          float4 u = make_float4(0, 0, 0, 0);
           for (int s = 0; s < S; ++s) {
-            const uint32_t base = map_to_rank(a0, s);
-            const float4 x = load_cluster4(base + f_at(r, 2 * c) * 4), y = load_cluster4(base + f_at(r, 2 * c + 1) * 4);
+            const float4 x = load_cluster4(map_to_rank(a0, s) + f_at(r, c) * 4);
             u = make_float4(u.x + x.x, u.y + x.y, u.z + x.z, u.w + x.w);
-            v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
           }
           constexpr float k = 1.0f / kScale;
-          mine[i] = make_uint4(pack_f16(u.x * k, u.y * k), pack_f16(u.z * k, u.w * k), pack_f16(v.x * k, v.y * k),
-                               pack_f16(v.z * k, v.w * k));
+          mine[i] = make_uint2(pack_f16(u.x * k, u.y * k), pack_f16(u.z * k, u.w * k));
         }
       }
-      cluster_sync_all();  // every part has been read
+      exchange(1, step & 1);  // every part has been read
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int e = tid + i * kSmThreads, r = rank + e / pieces * S, c = e % pieces;
         if (e < my_rows * pieces)
-          for (int s = 0; s < S; ++s) store_cluster(map_to_rank(a0 + mat_at(r, 8 * c), s), mine[i]);
+          for (int s = 0; s < S; ++s) store_cluster(map_to_rank(a0 + mat_at(r, 4 * c), s), mine[i]);
       }
       tc::fence_proxy_async();
-      cluster_sync_all();  // A is complete in every CTA
+      exchange(2, step & 1);  // A is complete in every CTA
     }
     tc::fence_proxy_async();
     tc::fence_before_sync();
@@ -435,8 +462,16 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
 template <bool TALL, typename T>
 cudaError_t launch_small(SmallParams p, int count, cudaStream_t st) {
   const int n = TALL ? p.rows : p.cols;
+  // One CTA where the matrix fits it (no exchange: 128 x 512 32 us, in four CTAs 41 us); else the
+  // largest cluster that leaves every matrix of the stack resident at once (128 x 2048: in
+  // clusters of eight 48 us, of four 52 us; sixteen 100 x 1500: of six 54 us, of three 59 us,
+  // of eight in two rounds 97 us). Slabs are multiples of 64, none empty.
   p.cluster = (n + kSlab - 1) / kSlab;
+  if (p.cluster > 1)
+    for (int s = p.cluster + 1; s <= kSmCluster; ++s)
+      if (count <= kResidentClusters[s]) p.cluster = s;
   p.slab = ((n + p.cluster - 1) / p.cluster + 63) / 64 * 64;
+  p.cluster = (n + p.slab - 1) / p.slab;
   p.slab_rows = TALL ? (p.slab + kSide - 1) / kSide * kSide : kSide;
   p.slab_bytes = TALL ? 2 * p.slab_rows * 128 : p.slab / 64 * (kSide * 128);
   p.wait_ns = wait_limit_ns();

@@ -863,6 +863,10 @@ namespace {
 // One GB300: 152 SMs, 76 pairs. The tile choice is made for that and does not ask the
 // device, so that workspace sizes depend on the shape alone.
 constexpr int kSms = 152;
+// Clusters of each size that are resident at once on one GB300 (as cudaOccupancyMaxActiveClusters
+// reports them at one CTA per SM: a cluster stays within a group of SMs, and the groups are
+// not multiples of every size).
+constexpr int kResidentClusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
 
 // What a launch asks of the current device; read once per device.
 struct DeviceInfo {

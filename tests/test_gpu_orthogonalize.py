@@ -51,7 +51,8 @@ def _check(out, g, steps=5, scale=1.0):
 @pytest.mark.parametrize("n,r,c", [(1, 96, 384), (1, 384, 96), (3, 64, 64), (2, 200, 136), (2, 136, 200), (5, 33, 77),
                                    (4, 77, 33), (1, 129, 513), (1, 512, 300), (7, 24, 1000), (2, 700, 40),
                                    (40, 130, 264), (1, 1024, 640), (2, 128, 2049), (1, 4096, 128),
-                                   (1, 100, 4000), (3, 1500, 97), (20, 128, 512), (1, 128, 4104), (2, 129, 96)])
+                                   (1, 100, 4000), (3, 1500, 97), (20, 128, 512), (1, 128, 4104), (2, 129, 96),
+                                   (16, 50, 700), (30, 640, 33), (1, 20, 513), (80, 16, 600)])
 def test_against_fp64(n, r, c, dtype):
     g = _g(n + r + c, n, r, c, dtype=dtype)
     _check(_run(g), g)
