@@ -10,7 +10,7 @@
 // Nothing but the matrix itself crosses memory, once in (twice, from L2, for its norm) and once
 // out. What bounds it is latency: the steps' products depend on each other, and take a few
 // hundred to two thousand clocks each. As separate launches of product.cuh's tiles the same
-// products take about 3.5 us each (96 x 384, five steps: 52 us; here 25.5 us).
+// products take about 3.5 us each (96 x 384, five steps: 52 us; here 24.9 us).
 //
 // The slab lies in blocks of 64 columns of 128-byte rows, 128-byte swizzled, so that one
 // placement serves both products: for wide matrices (slab: all rows, a range of columns) the
@@ -245,9 +245,9 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
     if (!bad && !warp_wait(bar + 8 * i, parity, p.wait_ns)) bad = 1;
     tc::fence_after_sync();
   };
-  // Every CTA of the cluster has reached exchange i of this step. (One thread a peer releases for
-  // its CTA: in a cluster barrier each of the 512 threads orders its own accesses, which took
-  // up to 4000 clocks.)
+  // Every CTA of the cluster has reached exchange i of this step: one thread a peer releases for
+  // its CTA. (As fast as a cluster barrier, but a product that never completes in one CTA ends
+  // in this wait's limit, and the status says so.)
   auto exchange = [&](int i, uint32_t parity) {
     __syncthreads();
     if (tid < S) arrive_release_cluster(map_to_rank(bar + 8 * (3 + i), tid));
@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
       tc::fence_before_sync();
       exchange(0, step & 1);
       // Rows rank, rank + S, ...: a thread sums four columns of a row over the cluster, a warp
-      // whole rows, so that what it reads of another CTA at once is contiguous.
+      // whole rows, so that what it reads of another CTA at once is contiguous (2048 x 128, read
+      // by scattered pieces 67 us, by rows 51 us).
       constexpr int kMine = kSide / 2 * (kSide / 4) / kSmThreads;  // at S = 2, pieces per thread
       uint2 mine[kMine];
       const int my_rows = (mp - rank + S - 1) / S, pieces = mp / 4;
