@@ -363,6 +363,12 @@ def _float_code(name, t):
     raise ValueError(f"{name} has dtype {t.dtype}, not {_F32} or {_BF16}")
 
 
+def _check_sizes(*sizes):
+    """Sizes that the C functions take as ints (a larger one would arrive cut to 32 bits)."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"sizes {sizes}: none may be above 2^31 - 1")
+
+
 def _call(fn, dev, stream, status, *args):
     """The C function fn(*args, status, stream) with device number `dev` current, on `stream`
     or that device's current stream; raises on an error status."""
@@ -416,14 +422,15 @@ def linear(x, w, b=None, act=ACT_NONE, residual=None, y=None, pre=None, status=N
     dev = _device_of("x", x)
     N, K, w_ptr = _weight(w, dev)
     lead = x.shape[:-1]
-    shape = (*lead, N)
+    tokens, shape = lead.numel(), (*lead, N)
+    _check_sizes(tokens, K, N)
     if y is None:
         y = _empty(shape, _BF16, dev, stream)
     _call(load().swin_wattn_linear, dev, stream, status, _address("x", x, (*lead, K), _BF16, dev), w_ptr,
           None if b is None else _address("b", b, (N,), _F32, dev),
           None if residual is None else _address("residual", residual, shape, _BF16, dev),
           _address("y", y, shape, _BF16, dev), None if pre is None else _address("pre", pre, shape, _BF16, dev),
-          lead.numel(), K, N, _act_code(act))
+          tokens, K, N, _act_code(act))
     return y
 
 
@@ -435,14 +442,15 @@ def linear_bwd_data(dy, w, pre=None, act=ACT_NONE, dx=None, status=None, stream=
     code = _act_code(act)
     N, K, w_ptr = _weight(w, dev)
     lead = dy.shape[:-1]
-    shape = (*lead, K)
+    tokens, shape = lead.numel(), (*lead, K)
+    _check_sizes(tokens, K, N)
     if code != ACT_NONE and pre is None:
         raise ValueError("an activation needs its pre-activation: pre is None")
     if dx is None:
         dx = _empty(shape, _BF16, dev, stream)
     _call(load().swin_wattn_linear_bwd_data, dev, stream, status, _address("dy", dy, (*lead, N), _BF16, dev), w_ptr,
           None if pre is None else _address("pre", pre, shape, _BF16, dev), _address("dx", dx, shape, _BF16, dev),
-          lead.numel(), K, N, code)
+          tokens, K, N, code)
     return dx
 
 
@@ -455,6 +463,7 @@ def linear_bwd_weight(dy, x, dw=None, db=None, accumulate=False, workspace=None,
     dev = _device_of("dy", dy)
     N, K, lead = dy.shape[-1], x.shape[-1], dy.shape[:-1]
     tokens = lead.numel()
+    _check_sizes(tokens, K, N)
     if dw is None:
         if accumulate:
             raise ValueError("accumulate needs the dw to add to")
@@ -480,12 +489,14 @@ def orthogonalize(g, steps=5, eps=1e-7, scale=1.0, out=None, workspace=None, sta
     if len(shape) not in (2, 3):
         raise ValueError(f"g has {len(shape)} dimensions, not 2 or 3")
     count, rows, cols = (1, *shape) if len(shape) == 2 else shape
+    steps = int(steps)
+    _check_sizes(count, rows, cols, abs(steps))
     if out is None:
         out = _empty(shape, _BF16, dev, stream)
     workspace, ws_ptr, nbytes = _workspace(
         workspace, lambda: swin_wattn_orthogonalize_workspace_bytes(count, rows, cols), dev, stream)
     _call(load().swin_wattn_orthogonalize, dev, stream, status, _address("g", g, shape, g.dtype, dev),
-          _address("out", out, shape, _BF16, dev), count, rows, cols, code, int(steps), float(eps), float(scale),
+          _address("out", out, shape, _BF16, dev), count, rows, cols, code, steps, float(eps), float(scale),
           ws_ptr, nbytes)
     return out
 

@@ -53,11 +53,45 @@ def test_update_rejects_bad_scalars_before_touching_cuda(lib):
     assert f(n=0) == lib.OK and f() == bad
 
 
+def test_update_rejects_a_subnormal_eps(lib):
+    f = lambda eps: lib.swin_wattn_orthogonalize(None, None, 0, 8, 8, 1, 5, eps, 1.0, None, 0, None, None)
+    assert f(1e-40) == lib.ERR_INVALID_ARG and f(2.0 ** -149) == lib.ERR_INVALID_ARG and f(2.0 ** -126) == lib.OK
+
+
 def test_wrappers_refuse_host_tensors(lib):
     x, w = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(8, 8, dtype=torch.bfloat16)
     for call in (lambda: lib.linear(x, w), lambda: lib.linear_bwd_data(x, w), lambda: lib.linear_bwd_weight(x, x),
                  lambda: lib.orthogonalize(w)):
         with pytest.raises(ValueError):
+            call()
+
+
+class _Described:
+    """What the wrappers ask a tensor about, for sizes that no test allocates."""
+
+    def __init__(self, *shape, dtype=torch.bfloat16):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, "cuda:0"
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+def test_wrappers_refuse_sizes_that_no_int_holds(lib):
+    """2^32 + 8 of anything would arrive as 8."""
+    n = 2 ** 32 + 8
+    x, w = _Described(n, 8), _Described(8, 8)
+    for call in (lambda: lib.linear(x, w), lambda: lib.linear(_Described(n // 8, 8, 8), w),
+                 lambda: lib.linear(_Described(4, 8), _Described(n, 8)),
+                 lambda: lib.linear_bwd_data(x, w), lambda: lib.linear_bwd_data(_Described(4, 8), _Described(8, n)),
+                 lambda: lib.linear_bwd_weight(x, x), lambda: lib.orthogonalize(_Described(n, 1, 1)),
+                 lambda: lib.orthogonalize(_Described(8, 8), steps=n)):
+        with pytest.raises(ValueError, match="2\\^31"):
             call()
 
 
