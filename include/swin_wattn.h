@@ -359,16 +359,17 @@ int swin_wattn_linear_bwd_weight(const void* dy, const void* x, void* dw, float*
  *   out    bf16 [count, rows, cols], 2-byte aligned, written (16-byte aligned with cols a
  *          multiple of 8 is the fast case); must not overlap g;
  *   count  in [0, 65535] (0: nothing is done); rows, cols in [1, 16384];
- *   steps  in [1, 20]; eps finite and > 0; scale finite;
+ *   steps  in [1, 20]; eps finite and > 0, not subnormal; scale finite;
  *   workspace  caller-owned device memory of at least
  *          swin_wattn_orthogonalize_workspace_bytes(count, rows, cols) bytes, 256-byte
  *          aligned, overwritten; one call at a time per workspace.
  * Operands of the products are held in fp16 (scaled; the values are bounded), products are
  * accumulated in fp32; the result is within about 1.5e-3 (relative 2-norm, before its
  * rounding to bf16) of the exact iteration for matrices whose singular values span a
- * factor of about a hundred, and loses accuracy in the directions of smaller ones. The norm
- * is summed in fp32, with large values scaled so that their squares do not overflow; squares
- * below the smallest fp32 count as zero (values below 1e-19 in size). A matrix with a
+ * factor of about a hundred, and loses accuracy in the directions of smaller ones. Where |G|
+ * is far below eps, X is small from the start; its entries are held to 2^-33. The norm is summed
+ * in fp32, in three ranges of size so that no square overflows or is lost; subnormal values
+ * count as zero, and a norm beyond the largest fp32 gives zeros. A matrix with a
  * NaN or an infinity gives NaN and leaves the others of the stack alone; a zero matrix gives zeros.
  * One launch where the smaller side is at most 128 and the larger at most 4096, else
  * 2 + 3 * steps; nothing is allocated. Deterministic. Errors: INVALID_ARG for the

@@ -1,6 +1,7 @@
 // C ABI of the swin_wattn library: argument validation, plan ownership, launches and
 // error surfacing. No exception, abort or trap crosses this boundary.
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -721,7 +722,7 @@ int swin_wattn_orthogonalize(const void* g, void* out, int count, int rows, int 
                              float scale, void* workspace, size_t workspace_bytes, int* status,
                              struct CUstream_st* stream) {
   if (count < 0 || (dtype != SWIN_WATTN_FP32 && dtype != SWIN_WATTN_BF16)) return SWIN_WATTN_ERR_INVALID_ARG;
-  if (!(eps > 0.0f) || !std::isfinite(eps) || !std::isfinite(scale) || steps < 1 || steps > 20)
+  if (!(eps >= FLT_MIN) || !std::isfinite(eps) || !std::isfinite(scale) || steps < 1 || steps > 20)
     return SWIN_WATTN_ERR_INVALID_ARG;
   if (!orthogonalize_sizes(count, rows, cols)) return SWIN_WATTN_ERR_UNSUPPORTED;
   if (count == 0) return SWIN_WATTN_OK;

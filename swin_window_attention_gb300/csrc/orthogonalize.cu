@@ -52,22 +52,24 @@ int norm_blocks(int64_t elements, int count) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({kNormBlocks, (elements + 2047) / 2048, (4 * prod::kSms + count - 1) / count}));
 }
 
-// Sum over the block of both; the result in every thread of the first warp.
-__device__ __forceinline__ float2 block_sum(float lo, float hi) {
-  __shared__ float2 part[kNormThreads / 32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    lo += __shfl_xor_sync(0xffffffffu, lo, o);
-    hi += __shfl_xor_sync(0xffffffffu, hi, o);
-  }
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(lo, hi);
+// The sum over the block, in every thread.
+__device__ __forceinline__ Squares block_sum(const Squares& s) {
+  __shared__ Squares part[kNormThreads / 32];
+  const Squares w = warp_sum(s);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = w;
   __syncthreads();
-  lo = hi = 0.0f;
-  for (int w = 0; w < kNormThreads / 32; ++w) {
-    lo += part[w].x;
-    hi += part[w].y;
-  }
-  return make_float2(lo, hi);
+  Squares b = part[0];
+  for (int w = 1; w < kNormThreads / 32; ++w) add(b, part[w]);
+  return b;
+}
+__device__ __forceinline__ float block_sum(float s) {
+  __shared__ float part[kNormThreads / 32];
+  s = warp_sum(s);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = part[0];
+  for (int w = 1; w < kNormThreads / 32; ++w) s += part[w];
+  return s;
 }
 
 // Sum of squares of a block's share of one matrix. `vec`: every matrix starts on a 16-byte
@@ -75,12 +77,12 @@ __device__ __forceinline__ float2 block_sum(float lo, float hi) {
 // such reads in flight.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_partial_kernel(const T* __restrict__ g, int64_t elements, bool vec,
-                                                                    float2* __restrict__ partial) {
+                                                                    Squares* __restrict__ partial) {
   pdl_launch_dependents();
   pdl_wait();
   const T* x = g + (int64_t)blockIdx.y * elements;
   const int64_t first = (int64_t)blockIdx.x * kNormThreads + threadIdx.x, stride = (int64_t)gridDim.x * kNormThreads;
-  float lo = 0.0f, hi = 0.0f;
+  float2 plain = make_float2(0.0f, 0.0f);
   if (vec) {
     const int64_t n8 = elements / 8;
     int64_t i = first;
@@ -89,33 +91,41 @@ __global__ void __launch_bounds__(kNormThreads) norm_partial_kernel(const T* __r
 #pragma unroll
       for (int u = 0; u < 4; ++u) load8(x + (i + u * stride) * 8, v[u]);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) add_square(v[u][e], lo, hi);
+      for (int u = 0; u < 4; ++u) add_plain(v[u], plain);
     }
     for (; i < n8; i += stride) {
       float v[8];
       load8(x + i * 8, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) add_square(v[e], lo, hi);
+      add_plain(v, plain);
     }
   } else {
-    for (int64_t i = first; i < elements; i += stride) add_square(load_f32(x + i), lo, hi);
+    for (int64_t i = first; i < elements; i += stride) {
+      const float v = load_f32(x + i);
+      plain.x = fmaf(v, v, plain.x);
+    }
   }
-  const float2 s = block_sum(lo, hi);
-  if (threadIdx.x == 0) partial[blockIdx.y * gridDim.x + blockIdx.x] = s;
+  Squares sum{block_sum(plain.x + plain.y), 0.0f, 0.0f};
+  if (!plain_sum_holds(sum.mid)) {
+    // the same share, an element at a time
+    const int64_t per = vec ? 8 : 1;
+    sum.mid = 0.0f;
+    for (int64_t i = first; i < elements / per; i += stride)
+      for (int64_t e = 0; e < per; ++e) add_square(load_f32(x + i * per + e), sum);
+    sum = block_sum(sum);
+  }
+  if (threadIdx.x == 0) partial[blockIdx.y * gridDim.x + blockIdx.x] = sum;
 }
 
 // X = G / (|G| + eps), times 2^8, in fp16 rows of ld elements.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) normalize_kernel(const T* __restrict__ g, int rows, int cols, int ld,
-                                                                 bool vec, const float2* __restrict__ partial,
+                                                                 bool vec, const Squares* __restrict__ partial,
                                                                  int n_partial, float eps, __half* __restrict__ x) {
   pdl_launch_dependents();
   pdl_wait();
-  const float2 p = (int)threadIdx.x < n_partial ? partial[blockIdx.y * n_partial + threadIdx.x] : make_float2(0.0f, 0.0f);
-  const float2 s = block_sum(p.x, p.y);
-  const float inv = __fdiv_rn(kScale, norm_of(s.x, s.y) + eps);
+  Squares sum{};
+  if ((int)threadIdx.x < n_partial) sum = partial[blockIdx.y * n_partial + threadIdx.x];
+  const Inverse k = inverse_of(block_sum(sum), eps);
   const int64_t elements = (int64_t)rows * cols;
   const T* gm = g + (int64_t)blockIdx.y * elements;
   __half* xm = x + (int64_t)blockIdx.y * rows * ld;
@@ -127,13 +137,14 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(const T* __rest
       load8(gm + i * 8, v);
       uint32_t o[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = prod::pack_f16(v[2 * e] * inv, v[2 * e + 1] * inv);
+      for (int e = 0; e < 4; ++e) o[e] = prod::pack_f16(v[2 * e] * k.pre * k.inv, v[2 * e + 1] * k.pre * k.inv);
       reinterpret_cast<uint4*>(xm)[i] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   } else {
     const int wpb = kNormThreads / 32, lane = threadIdx.x & 31;
     for (int r = blockIdx.x * wpb + (threadIdx.x >> 5); r < rows; r += gridDim.x * wpb)
-      for (int c = lane; c < cols; c += 32) xm[(int64_t)r * ld + c] = __float2half_rn(load_f32(gm + (int64_t)r * cols + c) * inv);
+      for (int c = lane; c < cols; c += 32)
+        xm[(int64_t)r * ld + c] = __float2half_rn(load_f32(gm + (int64_t)r * cols + c) * k.pre * k.inv);
   }
 }
 
@@ -152,12 +163,12 @@ Layout layout(int count, int rows, int cols) {
   l.lda = round8(l.m);
   l.x_bytes = align256((size_t)count * rows * l.ldx * 2);
   l.a_bytes = align256((size_t)count * l.m * l.lda * 2);
-  l.total = 2 * l.x_bytes + 2 * l.a_bytes + align256((size_t)count * kNormBlocks * sizeof(float2));
+  l.total = 2 * l.x_bytes + 2 * l.a_bytes + align256((size_t)count * kNormBlocks * sizeof(Squares));
   return l;
 }
 
 template <typename T>
-cudaError_t normalize(const T* g, int count, int rows, int cols, float eps, float2* partial, __half* x, int ld,
+cudaError_t normalize(const T* g, int count, int rows, int cols, float eps, Squares* partial, __half* x, int ld,
                       cudaStream_t st) {
   const int64_t elements = (int64_t)rows * cols;
   const int nb = norm_blocks(elements, count);
@@ -165,7 +176,7 @@ cudaError_t normalize(const T* g, int count, int rows, int cols, float eps, floa
   cudaError_t e = launch_pdl(norm_partial_kernel<T>, dim3(nb, count), dim3(kNormThreads), 0, st, g, elements, vec, partial);
   if (e != cudaSuccess) return e;
   return launch_pdl(normalize_kernel<T>, dim3(nb, count), dim3(kNormThreads), 0, st, g, rows, cols, ld, vec,
-                    (const float2*)partial, nb, eps, x);
+                    (const Squares*)partial, nb, eps, x);
 }
 
 }  // namespace
@@ -184,7 +195,7 @@ cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, 
   __half* x[2] = {reinterpret_cast<__half*>(ws), reinterpret_cast<__half*>(ws + l.x_bytes)};
   __half* gram = reinterpret_cast<__half*>(ws + 2 * l.x_bytes);
   __half* poly = reinterpret_cast<__half*>(ws + 2 * l.x_bytes + l.a_bytes);
-  float2* partial = reinterpret_cast<float2*>(ws + 2 * l.x_bytes + 2 * l.a_bytes);
+  Squares* partial = reinterpret_cast<Squares*>(ws + 2 * l.x_bytes + 2 * l.a_bytes);
   cudaError_t e = dtype == SWIN_WATTN_FP32
                       ? normalize(static_cast<const float*>(g), count, rows, cols, eps, partial, x[0], l.ldx, st)
                       : normalize(static_cast<const __nv_bfloat16*>(g), count, rows, cols, eps, partial, x[0], l.ldx, st);

@@ -27,20 +27,62 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
   }
 }
 
-// Squares are summed apart for values below 2^48 (lo) and, times 2^-64, for the others (hi:
-// NaN and infinity too), so that neither sum overflows where the norm does not.
-__device__ __forceinline__ void add_square(float v, float& lo, float& hi) {
-  if (fabsf(v) < 281474976710656.0f) {
-    lo = fmaf(v, v, lo);
+// A plain fp32 sum of squares is the norm's if it comes out between these: then no square has
+// overflowed, and those below the smallest fp32 (2^28 of them at most) are nothing beside it. NaN
+// and infinities are outside too.
+__device__ __forceinline__ bool plain_sum_holds(float s) { return s >= 0x1p-60f && s <= 0x1p96f; }
+
+// Else squares are summed apart for values in [2^-48, 2^48), for larger ones times 2^-64 (NaN
+// and infinity too) and for smaller ones times 2^64, so that no square overflows or is lost
+// where the norm is a normal number. (Subnormal values count as zero. Summing every matrix
+// this way took 2.5 us of 27 for one 96 x 384.)
+struct Squares {
+  float mid, big, small;
+};
+constexpr float kTwo64 = 0x1p64f;
+__device__ __forceinline__ void add_square(float v, Squares& s) {
+  const float a = fabsf(v);
+  if (a < 0x1p-48f) {
+    const float x = v * kTwo64;
+    s.small = fmaf(x, x, s.small);
+  } else if (a < 0x1p48f) {
+    s.mid = fmaf(v, v, s.mid);
   } else {
-    const float s = v * 5.421010862427522e-20f;
-    hi = fmaf(s, s, hi);
+    const float x = v * (1.0f / kTwo64);
+    s.big = fmaf(x, x, s.big);
   }
 }
-// The norm of both sums; where the second is not empty the first is added in its scale.
-__device__ __forceinline__ float norm_of(float lo, float hi) {
-  return hi == 0.0f ? sqrtf(lo)
-                    : sqrtf(hi + lo * 5.421010862427522e-20f * 5.421010862427522e-20f) * 18446744073709551616.0f;
+// Eight squares to a plain sum's two halves.
+__device__ __forceinline__ void add_plain(const float (&v)[8], float2& s) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) s = __ffma2_rn(make_float2(v[e], v[e + 1]), make_float2(v[e], v[e + 1]), s);
+}
+__device__ __forceinline__ float warp_sum(float s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+__device__ __forceinline__ void add(Squares& s, const Squares& o) {
+  s.mid += o.mid;
+  s.big += o.big;
+  s.small += o.small;
+}
+__device__ __forceinline__ Squares warp_sum(const Squares& s) { return {warp_sum(s.mid), warp_sum(s.big), warp_sum(s.small)}; }
+// The norm: each sum joins the next larger one in that one's scale (what of it is lost
+// there is below that sum's rounding).
+__device__ __forceinline__ float norm_of(const Squares& s) {
+  constexpr float k = 1.0f / kTwo64;
+  if (s.big != 0.0f) return sqrtf(s.big + s.mid * k * k) * kTwo64;
+  if (s.mid != 0.0f) return sqrtf(s.mid + s.small * k * k);
+  return sqrtf(s.small) * k;
+}
+// X = kScale G / (|G| + eps) is G * pre * inv: 1 / (|G| + eps) itself can overflow.
+struct Inverse {
+  float pre, inv;
+};
+__device__ __forceinline__ Inverse inverse_of(const Squares& s, float eps) {
+  const float d = norm_of(s) + eps, pre = d < 1.0f / kTwo64 ? kTwo64 : 1.0f;
+  return {pre, __fdiv_rn(kScale, d * pre)};
 }
 
 }  // namespace swin

@@ -68,6 +68,11 @@ __device__ __forceinline__ bool wait_acquire_cluster(uint32_t mbar, uint32_t par
     if (t1 - t0 > limit_ns) return false;
   }
 }
+__device__ __forceinline__ float load_cluster1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
@@ -82,7 +87,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_tmem;
   __shared__ __align__(8) uint64_t s_bar[6];
-  __shared__ float2 s_part[kSmWarps], s_norm;
+  __shared__ float s_plain[kSmWarps];
+  __shared__ Squares s_part[kSmWarps], s_norm;
   pdl_launch_dependents();
   const uint32_t smem0 = smem_u32(smem), bar = smem_u32(s_bar);  // A and A^2; the update's two halves; the cluster's exchanges
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -126,8 +132,9 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
   const int r_first = vec ? tid / c8 : 0, c_first = tid - r_first * c8;
   const int r_step = vec ? kSmThreads / c8 : 0, c_step = kSmThreads - r_step * c8;
   constexpr int kPieces = kSide * kSlab / 8 / kSmThreads;  // per thread at most
+  Squares total;
   {
-    float lo = 0.0f, hi = 0.0f;
+    float2 plain = make_float2(0.0f, 0.0f);
     if (vec) {
       // G is read once: it waits for its norm in tensor memory, which is idle until the steps
       int r = r_first, c = c_first;
@@ -150,9 +157,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
           }
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) add_square(v[u][e], lo, hi);
+        for (int u = 0; u < 4; ++u) add_plain(v[u], plain);
         uint32_t w[32];
 #pragma unroll
         for (int u = 0; u < 32; ++u) w[u] = __float_as_uint(v[u >> 3][u & 7]);
@@ -162,36 +167,38 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
       tc::wait_st();
     } else {
       for (int r = warp; r < srows; r += kSmWarps)
-        for (int c = lane; c < scols; c += 32) add_square(load_f32(g + (int64_t)r * p.cols + c), lo, hi);
+        for (int c = lane; c < scols; c += 32) {
+          const float v = load_f32(g + (int64_t)r * p.cols + c);
+          plain.x = fmaf(v, v, plain.x);
+        }
     }
+    const float w = warp_sum(plain.x + plain.y);
+    if (lane == 0) s_plain[warp] = w;
+    __syncthreads();
+    total = {s_plain[0], 0.0f, 0.0f};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      lo += __shfl_xor_sync(0xffffffffu, lo, o);
-      hi += __shfl_xor_sync(0xffffffffu, hi, o);
-    }
-    if (lane == 0) s_part[warp] = make_float2(lo, hi);
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < kSmWarps; ++w) {
-        lo += s_part[w].x;
-        hi += s_part[w].y;
-      }
-      s_norm = make_float2(lo, hi);
+    for (int w = 1; w < kSmWarps; ++w) total.mid += s_plain[w];
+    if (!plain_sum_holds(total.mid)) {
+      Squares sum{};
+      for (int r = warp; r < srows; r += kSmWarps)
+        for (int c = lane; c < scols; c += 32) add_square(load_f32(g + (int64_t)r * p.cols + c), sum);
+      sum = warp_sum(sum);
+      if (lane == 0) s_part[warp] = sum;
+      __syncthreads();
+      total = s_part[0];
+      for (int w = 1; w < kSmWarps; ++w) add(total, s_part[w]);
     }
   }
-  if (S > 1)
+  if (S > 1) {
+    if (tid == 0) s_norm = total;
     cluster_sync_all();
-  else
-    __syncthreads();
-  float lo = 0.0f, hi = 0.0f;
-  for (int s = 0; s < S; ++s) {
-    const uint32_t peer = map_to_rank(smem_u32(&s_norm), s);
-    float a, b;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(a), "=f"(b) : "r"(peer) : "memory");
-    lo += a;
-    hi += b;
+    total = {};
+    for (int s = 0; s < S; ++s) {
+      const uint32_t peer = map_to_rank(smem_u32(&s_norm), s);
+      add(total, {load_cluster1(peer), load_cluster1(peer + 4), load_cluster1(peer + 8)});
+    }
   }
-  const float inv = __fdiv_rn(kScale, norm_of(lo, hi) + p.eps);
+  const Inverse k = inverse_of(total, p.eps);
   if (vec) {
     int r = r_first, c = c_first;
 #pragma unroll 1
@@ -203,7 +210,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
         uint32_t o[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          o[e] = pack_f16(__uint_as_float(w[8 * u + 2 * e]) * inv, __uint_as_float(w[8 * u + 2 * e + 1]) * inv);
+          o[e] = pack_f16(__uint_as_float(w[8 * u + 2 * e]) * k.pre * k.inv,
+                          __uint_as_float(w[8 * u + 2 * e + 1]) * k.pre * k.inv);
         if (tid + (i + u) * kSmThreads < n8)
           *reinterpret_cast<uint4*>(smem + at(r, 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
         r += r_step;
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
   } else {
     for (int r = warp; r < srows; r += kSmWarps)
       for (int c = lane; c < scols; c += 32)
-        *reinterpret_cast<__half*>(smem + at(r, c)) = __float2half_rn(load_f32(g + (int64_t)r * p.cols + c) * inv);
+        *reinterpret_cast<__half*>(smem + at(r, c)) = __float2half_rn(load_f32(g + (int64_t)r * p.cols + c) * k.pre * k.inv);
   }
   tc::fence_proxy_async();
   tc::fence_before_sync();

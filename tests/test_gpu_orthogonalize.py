@@ -87,6 +87,42 @@ def test_scale_of_the_input_does_not_matter():
         _check(_run(g * f), g)
 
 
+@pytest.mark.parametrize("r,c", [(100, 136), (1200, 30), (140, 200)])
+def test_small_values(r, c):
+    """Values whose squares are no fp32 numbers, with an eps as much smaller, and one scale at
+    which values lie on both sides of the bound between two ranges of the norm's sum. The exact
+    result is that of G and eps times the same power of two, here in 64 bits."""
+    for dtype in (torch.float32, torch.bfloat16):
+        g = _g(r, 2, r, c, dtype=dtype)
+        for f in (2.0 ** -38, 2.0 ** -60, 2.0 ** -80, 2.0 ** -100):
+            _check(_run(g * f, eps=1e-7 * f), g)
+    # |G| far below eps: X small from the start, where fp16 holds fewer bits
+    g = _g(r, 2, r, c) * 2.0 ** -40
+    _check(_run(g), g)
+
+
+@pytest.mark.parametrize("r,c", [(100, 136), (1200, 30), (140, 200)])
+def test_one_value_at_the_ends_of_the_range(r, c):
+    """A matrix of one entry keeps to the iteration on that number. Per step the roundings of A,
+    of the polynomial and of the result to fp16 (2^-11 of each) change it by less than 4 x 2^-11,
+    as |x| <= 1.2 and x A |b + 2 c A| < 1.7; the steps after it multiply that by their slopes."""
+    at = [(2.0 ** -126, 3, 5), (2.0 ** 127, 2, 1), (-(2.0 ** -64), 7, 7)]
+    g = torch.zeros(3, r, c)
+    for m, (v, i, j) in enumerate(at):
+        g[m, i, j] = v
+    out = _run(g, eps=2.0 ** -126)
+    for m, (v, i, j) in enumerate(at):
+        s, err = abs(v) / (abs(v) + 2.0 ** -126), 0.0
+        for _ in range(5):
+            slope = 3.4445 - 3 * 4.7750 * s ** 2 + 5 * 2.0315 * s ** 4
+            s, err = 3.4445 * s - 4.7750 * s ** 3 + 2.0315 * s ** 5, abs(slope) * err + 4 * 2.0 ** -11
+        got = float(out[m, i, j]) * (1 if v > 0 else -1)
+        assert abs(got - s) <= err + 2.0 ** -8 * (s + err), (m, got, s, err)
+        out[m, i, j] = 0.0
+    assert torch.all(out == 0)
+    assert torch.all(_run(torch.zeros(1, r, c), eps=2.0 ** -126) == 0)
+
+
 def test_zero_and_non_finite_matrices_leave_the_others_alone():
     g = _g(7, 4, 72, 96)
     ref = _run(g)
