@@ -82,6 +82,23 @@ __device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
   return v;
 }
 
+// The value at an address, or 0 without a read where `in` is false: a predicated load, so that
+// many are in flight (behind branches they came one after the other).
+__device__ __forceinline__ float load_if(const float* a, bool in) {
+  float v;
+  asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %2, 0;\n mov.f32 %0, 0f00000000;\n @q ld.global.f32 %0, [%1];\n}\n"
+               : "=f"(v)
+               : "l"(a), "r"((uint32_t)in));
+  return v;
+}
+__device__ __forceinline__ float load_if(const __nv_bfloat16* a, bool in) {
+  uint16_t v;
+  asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %2, 0;\n mov.u16 %0, 0;\n @q ld.global.u16 %0, [%1];\n}\n"
+               : "=h"(v)
+               : "l"(a), "r"((uint32_t)in));
+  return __uint_as_float((uint32_t)v << 16);
+}
+
 template <bool TALL, typename T>
 __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(const SmallParams p) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -128,50 +145,66 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
   const int c8 = scols / 8, n8 = srows * c8;  // vec: scols is a multiple of 8
   const int quad = warp & 3, part = warp >> 2;  // tensor-memory lanes; columns
   const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
-  // vec: this thread's pieces are tid, tid + 512, ...; their rows and columns advance by these
+  // G is read once: it waits for its norm in tensor memory, which is idle until the steps. 32
+  // values a thread at a time, `batch` to their columns of tensor memory:
+  // with vec, pieces of eight columns tid, tid + 512, ..., whose rows and columns advance by these;
   const int r_first = vec ? tid / c8 : 0, c_first = tid - r_first * c8;
   const int r_step = vec ? kSmThreads / c8 : 0, c_step = kSmThreads - r_step * c8;
-  constexpr int kPieces = kSide * kSlab / 8 / kSmThreads;  // per thread at most
+  auto advance = [&](int& r, int& c) {
+    r += r_step;
+    c += c_step;
+    if (c >= c8) {
+      c -= c8;
+      ++r;
+    }
+  };
+  // else kRows rows (16 apart) of kGroups groups of 32 columns, a lane each. (Element by element
+  // as the pieces, the addresses alone took 12 us of one 97 x 385.)
+  constexpr int kGroups = TALL ? kSide / 32 : kSlab / 32, kRows = 32 / kGroups;
+  constexpr int kBatches = kSide * kSlab / 32 / kSmThreads;
+  // place in the slab's row r of the lane's column of group j
+  auto at_group = [&](int r, int j) {
+    return (j >> 1) * block + r * 128 + (((lane >> 3) + 4 * (j & 1) ^ (r & 7)) << 4) + (lane & 7) * 2;
+  };
+  auto batch_begins = [&](int batch) {
+    return vec ? (tid & ~31) + 4 * batch * kSmThreads < n8 : warp + kSmWarps * kRows * batch < srows;
+  };
   Squares total;
   {
     float2 plain = make_float2(0.0f, 0.0f);
-    if (vec) {
-      // G is read once: it waits for its norm in tensor memory, which is idle until the steps
-      int r = r_first, c = c_first;
+    int r = r_first, c = c_first;
 #pragma unroll 1
-      for (int i = 0; i < kPieces && (tid & ~31) + i * kSmThreads < n8; i += 4) {
-        float v[4][8];
+    for (int batch = 0; batch < kBatches; ++batch) {
+      if (!batch_begins(batch)) break;
+      float v[4][8];
+      if (vec) {
+        const int i = 4 * batch * kSmThreads + tid;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          if (tid + (i + u) * kSmThreads < n8) {
+          if (i + u * kSmThreads < n8) {
             load8(g + (int64_t)r * p.cols + c * 8, v[u]);
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
           }
-          r += r_step;
-          c += c_step;
-          if (c >= c8) {
-            c -= c8;
-            ++r;
-          }
+          advance(r, c);
         }
+      } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) add_plain(v[u], plain);
-        uint32_t w[32];
-#pragma unroll
-        for (int u = 0; u < 32; ++u) w[u] = __float_as_uint(v[u >> 3][u & 7]);
-        __syncwarp();
-        tc::st_x32(trow + part * 128 + i * 8, w);
+        for (int u = 0; u < 32; ++u) {
+          const int row = warp + kSmWarps * (batch * kRows + u / kGroups), col = lane + u % kGroups * 32;
+          v[u >> 3][u & 7] = load_if(g + (int64_t)row * p.cols + col, row < srows && col < scols);
+        }
       }
-      tc::wait_st();
-    } else {
-      for (int r = warp; r < srows; r += kSmWarps)
-        for (int c = lane; c < scols; c += 32) {
-          const float v = load_f32(g + (int64_t)r * p.cols + c);
-          plain.x = fmaf(v, v, plain.x);
-        }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) add_plain(v[u], plain);
+      uint32_t w[32];
+#pragma unroll
+      for (int u = 0; u < 32; ++u) w[u] = __float_as_uint(v[u >> 3][u & 7]);
+      __syncwarp();
+      tc::st_x32(trow + part * 128 + batch * 32, w);
     }
+    tc::wait_st();
     const float w = warp_sum(plain.x + plain.y);
     if (lane == 0) s_plain[warp] = w;
     __syncthreads();
@@ -199,33 +232,35 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
     }
   }
   const Inverse k = inverse_of(total, p.eps);
-  if (vec) {
+  {
     int r = r_first, c = c_first;
 #pragma unroll 1
-    for (int i = 0; i < kPieces && (tid & ~31) + i * kSmThreads < n8; i += 4) {
+    for (int batch = 0; batch < kBatches; ++batch) {
+      if (!batch_begins(batch)) break;
       uint32_t w[32];
-      tc::ld32_wait(trow + part * 128 + i * 8, w);
+      tc::ld32_wait(trow + part * 128 + batch * 32, w);
+      float v[32];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        uint32_t o[4];
+      for (int u = 0; u < 32; ++u) v[u] = __uint_as_float(w[u]) * k.pre * k.inv;
+      if (vec) {
+        const int i = 4 * batch * kSmThreads + tid;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          o[e] = pack_f16(__uint_as_float(w[8 * u + 2 * e]) * k.pre * k.inv,
-                          __uint_as_float(w[8 * u + 2 * e + 1]) * k.pre * k.inv);
-        if (tid + (i + u) * kSmThreads < n8)
-          *reinterpret_cast<uint4*>(smem + at(r, 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
-        r += r_step;
-        c += c_step;
-        if (c >= c8) {
-          c -= c8;
-          ++r;
+        for (int u = 0; u < 4; ++u) {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = pack_f16(v[8 * u + 2 * e], v[8 * u + 2 * e + 1]);
+          if (i + u * kSmThreads < n8) *reinterpret_cast<uint4*>(smem + at(r, 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+          advance(r, c);
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+          const int row = warp + kSmWarps * (batch * kRows + u / kGroups), col = lane + u % kGroups * 32;
+          if (row < srows && col < scols)
+            *reinterpret_cast<__half*>(smem + at_group(row, u % kGroups)) = __float2half_rn(v[u]);
         }
       }
     }
-  } else {
-    for (int r = warp; r < srows; r += kSmWarps)
-      for (int c = lane; c < scols; c += 32)
-        *reinterpret_cast<__half*>(smem + at(r, c)) = __float2half_rn(load_f32(g + (int64_t)r * p.cols + c) * k.pre * k.inv);
   }
   tc::fence_proxy_async();
   tc::fence_before_sync();
@@ -457,9 +492,15 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
       *reinterpret_cast<uint4*>(out + (int64_t)r * p.cols + c) = *reinterpret_cast<const uint4*>(smem + at(r, c));
     }
   } else {
-    for (int r = warp; r < srows; r += kSmWarps)
-      for (int c = lane; c < scols; c += 32)
-        out[(int64_t)r * p.cols + c] = *reinterpret_cast<const __nv_bfloat16*>(smem + at(r, c));
+    for (int r = warp; r < srows; r += kSmWarps) {
+      __nv_bfloat16 v[kGroups];
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j)
+        if (lane + j * 32 < scols) v[j] = *reinterpret_cast<const __nv_bfloat16*>(smem + at_group(r, j));
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j)
+        if (lane + j * 32 < scols) out[(int64_t)r * p.cols + lane + j * 32] = v[j];
+    }
   }
   if (bad && p.status != nullptr) atomicOr(p.status, 1);
   // no CTA leaves while another may still read its parts
