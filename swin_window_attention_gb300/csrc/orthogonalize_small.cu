@@ -10,7 +10,7 @@
 // Nothing but the matrix itself crosses memory, once in (twice, from L2, for its norm) and once
 // out. What bounds it is latency: the steps' products depend on each other, and take a few
 // hundred to two thousand clocks each. As separate launches of product.cuh's tiles the same
-// products take about 3.5 us each (96 x 384, five steps: 52 us; here 24.9 us).
+// products take about 3.5 us each (96 x 384, five steps: 52 us; here 24.2 us).
 //
 // The slab lies in blocks of 64 columns of 128-byte rows, 128-byte swizzled, so that one
 // placement serves both products: for wide matrices (slab: all rows, a range of columns) the
@@ -99,7 +99,9 @@ __device__ __forceinline__ float load_if(const __nv_bfloat16* a, bool in) {
   return __uint_as_float((uint32_t)v << 16);
 }
 
-template <bool TALL, typename T>
+// VEC: every row of G starts on a 16-byte boundary and holds a multiple of eight values, which are
+// read eight at a time.
+template <bool TALL, bool VEC, typename T>
 __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(const SmallParams p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_tmem;
@@ -140,16 +142,14 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
   const int srows = TALL ? len : m, scols = TALL ? m : len;  // of the slab that hold G
   const int64_t origin = (int64_t)mat * p.rows * p.cols + (TALL ? (int64_t)first * p.cols : first);
   const T* g = static_cast<const T*>(p.g) + origin;
-  // eight columns at a time where every row starts on a 16-byte boundary
-  const bool vec = p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(p.g) % 16 == 0;
-  const int c8 = scols / 8, n8 = srows * c8;  // vec: scols is a multiple of 8
+  const int c8 = scols / 8, n8 = srows * c8;  // VEC: scols is a multiple of 8
   const int quad = warp & 3, part = warp >> 2;  // tensor-memory lanes; columns
   const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
   // G is read once: it waits for its norm in tensor memory, which is idle until the steps. 32
   // values a thread at a time, `batch` to their columns of tensor memory:
-  // with vec, pieces of eight columns tid, tid + 512, ..., whose rows and columns advance by these;
-  const int r_first = vec ? tid / c8 : 0, c_first = tid - r_first * c8;
-  const int r_step = vec ? kSmThreads / c8 : 0, c_step = kSmThreads - r_step * c8;
+  // with VEC, pieces of eight columns tid, tid + 512, ..., whose rows and columns advance by these;
+  const int r_first = VEC ? tid / c8 : 0, c_first = tid - r_first * c8;
+  const int r_step = VEC ? kSmThreads / c8 : 0, c_step = kSmThreads - r_step * c8;
   auto advance = [&](int& r, int& c) {
     r += r_step;
     c += c_step;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
     return (j >> 1) * block + r * 128 + (((lane >> 3) + 4 * (j & 1) ^ (r & 7)) << 4) + (lane & 7) * 2;
   };
   auto batch_begins = [&](int batch) {
-    return vec ? (tid & ~31) + 4 * batch * kSmThreads < n8 : warp + kSmWarps * kRows * batch < srows;
+    return VEC ? (tid & ~31) + 4 * batch * kSmThreads < n8 : warp + kSmWarps * kRows * batch < srows;
   };
   Squares total;
   {
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
     for (int batch = 0; batch < kBatches; ++batch) {
       if (!batch_begins(batch)) break;
       float v[4][8];
-      if (vec) {
+      if constexpr (VEC) {
         const int i = 4 * batch * kSmThreads + tid;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
       float v[32];
 #pragma unroll
       for (int u = 0; u < 32; ++u) v[u] = __uint_as_float(w[u]) * k.pre * k.inv;
-      if (vec) {
+      if constexpr (VEC) {
         const int i = 4 * batch * kSmThreads + tid;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -530,9 +530,10 @@ cudaError_t launch_small(SmallParams p, int count, cudaStream_t st) {
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
   const int smem = std::max(120 * 1024, p.slab_bytes + 2 * kMatBytes);
-  auto kern = orthogonalize_small_kernel<TALL, T>;
-  static std::atomic<uint64_t> allowed{0};
-  e = allow_smem(reinterpret_cast<const void*>(kern), di.smem_max - 1024, di.device, &allowed);
+  const bool vec = p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(p.g) % 16 == 0;
+  auto kern = vec ? orthogonalize_small_kernel<TALL, true, T> : orthogonalize_small_kernel<TALL, false, T>;
+  static std::atomic<uint64_t> allowed[2];
+  e = allow_smem(reinterpret_cast<const void*>(kern), di.smem_max - 1024, di.device, &allowed[vec]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(count * p.cluster));
