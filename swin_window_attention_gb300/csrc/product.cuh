@@ -573,17 +573,26 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
     const bool aux = kHasAux && p.has_aux, pre = EPI == kEpiAct && p.has_pre;
     const int NB = p.tiles;
     const uint32_t aux0 = bar0 + 8 * (kAux + kMaxAuxTiles * warp);
-    // the next slice whose second operand is to be requested, and its staging tile
-    int nx_it = group, nx_c0 = part * kSC, nx_tile = 0, issued = 0;
+    // the next slice whose second operand is to be requested: its item, decoded, and its columns,
+    // and its staging tile
+    int nx_it = group, nx_c0 = part * kSC, nx_end = 0, nx_row = 0, nx_n0 = 0, nx_b = 0, nx_tile = 0, issued = 0;
+    auto next_item = [&]() {
+      nx_end = 0;
+      if (nx_it < p.n_items) {
+        const Item w = decode(nx_it);
+        nx_row = w.m0 + quad * 32;
+        nx_n0 = w.n0;
+        nx_b = w.b;
+        nx_end = nx_row < p.M ? min(p.NT, p.N - w.n0) : 0;
+      }
+    };
     auto request_next = [&]() {
       while (nx_it < p.n_items) {
-        const Item w = decode(nx_it);
-        const int row0 = w.m0 + quad * 32;
-        if (row0 < p.M && nx_c0 < p.NT && w.n0 + nx_c0 < p.N) {
+        if (nx_c0 < nx_end) {
           if (lane == 0) {
             const uint32_t rb = aux0 + 8 * nx_tile;
             tc::mbar_expect_tx(rb, kTile);
-            load_3d<1>(smem_u32(wstage + nx_tile * kTile), &aux_map, w.n0 + nx_c0, row0, w.b, rb);
+            load_3d<1>(smem_u32(wstage + nx_tile * kTile), &aux_map, nx_n0 + nx_c0, nx_row, nx_b, rb);
           }
           ++issued;
           if (++nx_tile == NB) nx_tile = 0;
@@ -592,8 +601,10 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
         }
         nx_it += n_groups;
         nx_c0 = part * kSC;
+        next_item();
       }
     };
+    if (aux) next_item();
     if (aux)
       for (int i = 0; i < max(NB - 2, 1); ++i) request_next();
     int g = 0, m = 0;                   // accumulations, slices of this warp
