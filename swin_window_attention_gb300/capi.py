@@ -363,10 +363,21 @@ def _float_code(name, t):
     raise ValueError(f"{name} has dtype {t.dtype}, not {_F32} or {_BF16}")
 
 
-def _check_sizes(*sizes):
-    """Sizes that the C functions take as ints (a larger one would arrive cut to 32 bits)."""
-    if max(sizes) > 0x7fffffff:
-        raise ValueError(f"sizes {sizes}: none may be above 2^31 - 1")
+_INT_MAX = 0x7fffffff  # the C functions take sizes as ints: a larger one would arrive cut
+
+
+def _too_large(*sizes):
+    return ValueError(f"sizes {sizes}: none may be above 2^31 - 1")
+
+
+_one_device = None  # whether the process sees a single device, which then is the current one
+
+
+def _is_current(dev):
+    global _one_device
+    if _one_device is None:
+        _one_device = torch.cuda.device_count() == 1
+    return _one_device or dev == torch._C._cuda_getDevice()
 
 
 def _call(fn, dev, stream, status, *args):
@@ -374,7 +385,7 @@ def _call(fn, dev, stream, status, *args):
     or that device's current stream; raises on an error status."""
     st = None if status is None else _address("status", status, (1,), torch.int32, dev)
     handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if dev == torch._C._cuda_getDevice():
+    if _one_device or _is_current(dev):
         rc = fn(*args, st, handle)
     else:
         with torch.cuda.device(dev):
@@ -423,7 +434,8 @@ def linear(x, w, b=None, act=ACT_NONE, residual=None, y=None, pre=None, status=N
     N, K, w_ptr = _weight(w, dev)
     lead = x.shape[:-1]
     tokens, shape = lead.numel(), (*lead, N)
-    _check_sizes(tokens, K, N)
+    if tokens > _INT_MAX or K > _INT_MAX or N > _INT_MAX:
+        raise _too_large(tokens, K, N)
     if y is None:
         y = _empty(shape, _BF16, dev, stream)
     _call(load().swin_wattn_linear, dev, stream, status, _address("x", x, (*lead, K), _BF16, dev), w_ptr,
@@ -443,7 +455,8 @@ def linear_bwd_data(dy, w, pre=None, act=ACT_NONE, dx=None, status=None, stream=
     N, K, w_ptr = _weight(w, dev)
     lead = dy.shape[:-1]
     tokens, shape = lead.numel(), (*lead, K)
-    _check_sizes(tokens, K, N)
+    if tokens > _INT_MAX or K > _INT_MAX or N > _INT_MAX:
+        raise _too_large(tokens, K, N)
     if code != ACT_NONE and pre is None:
         raise ValueError("an activation needs its pre-activation: pre is None")
     if dx is None:
@@ -463,7 +476,8 @@ def linear_bwd_weight(dy, x, dw=None, db=None, accumulate=False, workspace=None,
     dev = _device_of("dy", dy)
     N, K, lead = dy.shape[-1], x.shape[-1], dy.shape[:-1]
     tokens = lead.numel()
-    _check_sizes(tokens, K, N)
+    if tokens > _INT_MAX or K > _INT_MAX or N > _INT_MAX:
+        raise _too_large(tokens, K, N)
     if dw is None:
         if accumulate:
             raise ValueError("accumulate needs the dw to add to")
@@ -490,7 +504,8 @@ def orthogonalize(g, steps=5, eps=1e-7, scale=1.0, out=None, workspace=None, sta
         raise ValueError(f"g has {len(shape)} dimensions, not 2 or 3")
     count, rows, cols = (1, *shape) if len(shape) == 2 else shape
     steps = int(steps)
-    _check_sizes(count, rows, cols, abs(steps))
+    if count > _INT_MAX or rows > _INT_MAX or cols > _INT_MAX or abs(steps) > _INT_MAX:
+        raise _too_large(count, rows, cols, steps)
     if out is None:
         out = _empty(shape, _BF16, dev, stream)
     workspace, ws_ptr, nbytes = _workspace(
