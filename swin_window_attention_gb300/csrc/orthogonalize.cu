@@ -14,18 +14,20 @@
 //
 // Operands are fp16, not bf16: the entries of X, A and B are bounded (|X| <= 1.21,
 // |A| <= 1.45, |B| < 16), so the exponent range of bf16 is not needed and its 8 significant
-// bits cost eight times the error: on random matrices the result is 1.0e-3 to 1.5e-3
-// (relative 2-norm) from the 64-bit one with fp16 and 0.8e-2 to 1.1e-2 with bf16, where the
-// final rounding to bf16 alone is 1.7e-3. Everything is kept times 2^8, so an entry of X a
+// bits cost eight times the error: on random matrices the result is 0.7e-3 to 1.4e-3
+// (relative 2-norm) from the 64-bit one, where the final rounding to bf16 alone is 1.7e-3.
+// (The diagonals of A and B: orthogonalize.cuh.) Everything is kept times 2^8, so an entry of X a
 // hundredth of the smallest typical one (1 / sqrt(rows cols) = 3e-4 at 1536 x 6144) is
 // still a normal number, and the largest B stays a tenth of the largest fp16. Products are
 // accumulated in fp32. Singular values far below the largest come out with the error of
 // rounding the large ones' entries (the same is true, eight times worse, in bf16).
 //
-// Measured on one GB300: two 1536 x 6144 455 us (Gram 36, square 16, update 41 us a step: 83, 51
-// and 71 % of the tensor pipe; norm and scaling 33 us at 61 % of DRAM), eight 2048 x 512 154 us,
+// Measured on one GB300: two 1536 x 6144 451 us (Gram 36, square 16, update 41 us a step: 83, 51
+// and 71 % of the tensor pipe; norm and scaling 33 us at 61 % of DRAM), eight 2048 x 512 151 us,
 // bound by the chain of fifteen dependent launches. A and A^2 are symmetric, and half of each would
 // do; the tiles on and above the diagonal (42 of 72 on 76 pairs) take one round all the same.
+// (One epilogue for all three products, which tells them apart as it runs, took 169 us for the
+// stack, adding e X from a second read of X instead of the factors of its rows 160 us.)
 #include "orthogonalize.cuh"
 #include "product.cuh"
 
@@ -151,10 +153,10 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(const T* __rest
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 int round8(int n) { return (n + 7) & ~7; }
 
-// Workspace: two copies of X, A, B, the partial sums of squares.
+// Workspace: two copies of X, A, B, the factors of B's diagonal, the partial sums of squares.
 struct Layout {
-  int m, ldx, lda;
-  size_t x_bytes, a_bytes, total;
+  int m, ldx, lda, ld_gain;
+  size_t x_bytes, a_bytes, gain_bytes, total;
 };
 Layout layout(int count, int rows, int cols) {
   Layout l;
@@ -163,7 +165,9 @@ Layout layout(int count, int rows, int cols) {
   l.lda = round8(l.m);
   l.x_bytes = align256((size_t)count * rows * l.ldx * 2);
   l.a_bytes = align256((size_t)count * l.m * l.lda * 2);
-  l.total = 2 * l.x_bytes + 2 * l.a_bytes + align256((size_t)count * kNormBlocks * sizeof(Squares));
+  l.ld_gain = (l.m + 31) & ~31;
+  l.gain_bytes = align256((size_t)count * l.ld_gain * sizeof(float));
+  l.total = 2 * l.x_bytes + 2 * l.a_bytes + l.gain_bytes + align256((size_t)count * kNormBlocks * sizeof(Squares));
   return l;
 }
 
@@ -195,7 +199,8 @@ cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, 
   __half* x[2] = {reinterpret_cast<__half*>(ws), reinterpret_cast<__half*>(ws + l.x_bytes)};
   __half* gram = reinterpret_cast<__half*>(ws + 2 * l.x_bytes);
   __half* poly = reinterpret_cast<__half*>(ws + 2 * l.x_bytes + l.a_bytes);
-  Squares* partial = reinterpret_cast<Squares*>(ws + 2 * l.x_bytes + 2 * l.a_bytes);
+  float* gain = reinterpret_cast<float*>(ws + 2 * l.x_bytes + 2 * l.a_bytes);
+  Squares* partial = reinterpret_cast<Squares*>(ws + 2 * l.x_bytes + 2 * l.a_bytes + l.gain_bytes);
   cudaError_t e = dtype == SWIN_WATTN_FP32
                       ? normalize(static_cast<const float*>(g), count, rows, cols, eps, partial, x[0], l.ldx, st)
                       : normalize(static_cast<const __nv_bfloat16*>(g), count, rows, cols, eps, partial, x[0], l.ldx, st);
@@ -206,29 +211,37 @@ cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, 
   const Tiling t_step = prod::choose_tiling(rows, cols, m, count, !tall, 1, false);
   const Matrix A{gram, m, m, l.lda, (int64_t)m * l.lda}, B{poly, m, m, l.lda, (int64_t)m * l.lda};
   const bool direct = cols % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
-  for (int s = 0; s < steps && e == cudaSuccess; ++s) {
+  float mu = first_shift(m);
+  for (int s = 0; s < steps && e == cudaSuccess; ++s, mu = next_shift(mu)) {
+    const NsStep k = ns_step(mu);
     const Matrix X{x[s & 1], rows, cols, l.ldx, (int64_t)rows * l.ldx};
     Matrix Y{x[(s + 1) & 1], rows, cols, l.ldx, (int64_t)rows * l.ldx};
     Params p{};
     p.status = status;
     p.M = p.N = m;
-    p.alpha = 1.0f / kScale;  // (2^8 X)(2^8 X)^T = 2^16 A -> 2^8 A
+    p.alpha = 1.0f / kScale;  // (2^8 X)(2^8 X)^T = 2^16 A -> 2^8 (A - mu I)
+    p.diag = -k.mu * (kScale * kScale);
     prod::Extra none;
-    e = tall ? prod::launch_product<true, true, prod::kEpiStep>(t_gram, p, X, X, A, count, kF16, kF16, none, st)
-             : prod::launch_product<false, false, prod::kEpiStep>(t_gram, p, X, X, A, count, kF16, kF16, none, st);
+    e = tall ? prod::launch_product<true, true, prod::kEpiGram>(t_gram, p, X, X, A, count, kF16, kF16, none, st)
+             : prod::launch_product<false, false, prod::kEpiGram>(t_gram, p, X, X, A, count, kF16, kF16, none, st);
     if (e != cudaSuccess) return e;
     p.alpha = kNsC / kScale;
-    p.beta = kNsB;
-    p.diag = kNsA * kScale;
+    p.beta = k.b;
+    p.diag = k.e * (kScale * kScale / kNsC);
+    p.gain = gain;
+    p.gain_ld = l.ld_gain;
     prod::Extra with_a;
     with_a.aux = &A;
-    e = prod::launch_product<false, false, prod::kEpiStep>(t_poly, p, A, A, B, count, kF16, kF16, with_a, st);
+    e = prod::launch_product<false, false, prod::kEpiPoly>(t_poly, p, A, A, B, count, kF16, kF16, with_a, st);
     if (e != cudaSuccess) return e;
     Params q{};
     q.status = status;
     q.M = rows;
     q.N = cols;
     q.alpha = 1.0f / kScale;
+    q.gain = gain;
+    q.gain_ld = l.ld_gain;
+    q.gain_rows = !tall;
     CUtensorMapDataType out_type = kF16;
     if (s == steps - 1) {
       q.alpha = scale / (kScale * kScale);
@@ -237,8 +250,8 @@ cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, 
       Y = Matrix{out, rows, cols, cols, (int64_t)rows * cols};
       if (!direct) q.raw_out = static_cast<__nv_bfloat16*>(out);
     }
-    e = tall ? prod::launch_product<false, false, prod::kEpiStep>(t_step, q, X, B, Y, count, kF16, out_type, none, st)
-             : prod::launch_product<false, true, prod::kEpiStep>(t_step, q, B, X, Y, count, kF16, out_type, none, st);
+    e = tall ? prod::launch_product<false, false, prod::kEpiUpdate>(t_step, q, X, B, Y, count, kF16, out_type, none, st)
+             : prod::launch_product<false, true, prod::kEpiUpdate>(t_step, q, B, X, Y, count, kF16, out_type, none, st);
   }
   return e;
 }

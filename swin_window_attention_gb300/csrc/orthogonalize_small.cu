@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
   __shared__ __align__(8) uint64_t s_bar[6];
   __shared__ float s_plain[kSmWarps];
   __shared__ Squares s_part[kSmWarps], s_norm;
+  __shared__ __align__(16) float s_gain[kSide];  // the update's factors, a row or column of X each
   pdl_launch_dependents();
   const uint32_t smem0 = smem_u32(smem), bar = smem_u32(s_bar);  // A and A^2; the update's two halves; the cluster's exchanges
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -314,8 +315,12 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
     commit_products(0);
   });
 
+  float mu = first_shift(m);
   for (int step = 0; step < p.steps; ++step) {
     const bool last = step == p.steps - 1;
+    const float alpha = last ? p.scale / (kScale * kScale) : 1.0f / kScale;
+    const NsStep ns = ns_step(mu);
+    mu = next_shift(mu);
     wait_products(0, phase);
     phase ^= 1;
     const int c0 = part * 32;
@@ -331,6 +336,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
             o[q] = pack_f16(__uint_as_float(a[8 * c + 2 * q]) * (1.0f / kScale), __uint_as_float(a[8 * c + 2 * q + 1]) * (1.0f / kScale));
           *reinterpret_cast<uint4*>(sA + mat_at(row, c0 + 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
+        if (part == quad)
+          *reinterpret_cast<__half*>(sA + mat_at(row, row)) = __float2half_rn(fmaf(of_lane(a, lane), 1.0f / kScale, -ns.mu * kScale));
       }
     } else {
       // fp32 parts [128][128] over A and B, of which nothing is needed any more; 16-byte pieces
@@ -360,6 +367,11 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
           for (int s = 0; s < S; ++s) {
             const float4 x = load_cluster4(map_to_rank(a0, s) + f_at(r, c) * 4);
             u = make_float4(u.x + x.x, u.y + x.y, u.z + x.z, u.w + x.w);
+          }
+          if (c == r >> 2) {
+            const float v = -ns.mu * (kScale * kScale);
+            u = make_float4(u.x + ((r & 3) == 0 ? v : 0.0f), u.y + ((r & 3) == 1 ? v : 0.0f),
+                            u.z + ((r & 3) == 2 ? v : 0.0f), u.w + ((r & 3) == 3 ? v : 0.0f));
           }
           constexpr float k = 1.0f / kScale;
           mine[i] = make_uint2(pack_f16(u.x * k, u.y * k), pack_f16(u.z * k, u.w * k));
@@ -402,11 +414,17 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
         for (int q = 0; q < 4; ++q) {
           const int e = 8 * c + 2 * q;
           const float2 x = unpack_f16(in[q]);
-          const float d0 = row == c0 + e ? kNsA * kScale : 0.0f, d1 = row == c0 + e + 1 ? kNsA * kScale : 0.0f;
-          o[q] = pack_f16(fmaf(__uint_as_float(a[e]), kNsC / kScale, fmaf(x.x, kNsB, d0)),
-                          fmaf(__uint_as_float(a[e + 1]), kNsC / kScale, fmaf(x.y, kNsB, d1)));
+          o[q] = pack_f16(fmaf(__uint_as_float(a[e]), kNsC / kScale, x.x * ns.b),
+                          fmaf(__uint_as_float(a[e + 1]), kNsC / kScale, x.y * ns.b));
         }
         *reinterpret_cast<uint4*>(sB + mat_at(row, c0 + 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      if (part == quad) {
+        const float x = __half2float(*reinterpret_cast<const __half*>(sA + mat_at(row, row)));
+        const float exact = fmaf(of_lane(a, lane), kNsC / kScale, fmaf(x, ns.b, ns.e * kScale));
+        const __half held = __float2half_rn(exact);
+        *reinterpret_cast<__half*>(sB + mat_at(row, row)) = held;
+        s_gain[row] = alpha * __fdividef(exact, __half2float(held));
       }
     }
     tc::fence_proxy_async();
@@ -440,7 +458,6 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
         commit_products(1 + h);
       }
     });
-    const float alpha = last ? p.scale / (kScale * kScale) : 1.0f / kScale;
     // The accumulator's 32-column pieces, four quadrants' rows each: wide, piece = columns; tall,
     // tile of 128 rows and columns. After each round of four pieces the next step's Gram product
     // takes the 128 columns (rows) that are complete; its accumulator is the first piece's place,
@@ -463,8 +480,9 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
           uint32_t o[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float x = __uint_as_float(a[8 * k + 2 * q]) * alpha, y = __uint_as_float(a[8 * k + 2 * q + 1]) * alpha;
-            o[q] = last ? pack_bf16(x, y) : pack_f16(x, y);
+            const float2 f = TALL ? *reinterpret_cast<const float2*>(&s_gain[c + 8 * k + 2 * q]) : splat(s_gain[row]);
+            const float2 x = __fmul2_rn(make_float2(__uint_as_float(a[8 * k + 2 * q]), __uint_as_float(a[8 * k + 2 * q + 1])), f);
+            o[q] = last ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
           }
           *reinterpret_cast<uint4*>(smem + at(r, c + 8 * k)) = make_uint4(o[0], o[1], o[2], o[3]);
         }

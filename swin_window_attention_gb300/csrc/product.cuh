@@ -74,7 +74,10 @@ enum Epi {
   kEpiSlope = 1,   // bf16: acc * act'(aux)
   kEpiGrad32 = 2,  // fp32: [old +] acc, optionally the column sums of A^T (sum over K of A)
   kEpiGrad16 = 3,  // bf16: [aux +] acc, optionally the same sums
-  kEpiStep = 4     // fp16 or bf16: alpha * acc + beta * aux + diag on the diagonal
+  // of the weight update (orthogonalize.cu), on fp16 operands:
+  kEpiGram = 4,    // fp16: alpha * acc, after diag was added to the diagonal of acc
+  kEpiPoly = 5,    // fp16: alpha * acc + beta * aux, likewise; and the gains of its diagonal
+  kEpiUpdate = 6   // fp16 or bf16: alpha * gain * acc
 };
 
 // Warps: the epilogue's, MMA, copy. The fp32 gradient has eight epilogue warps, which hold 128
@@ -107,13 +110,18 @@ struct Params {
   uint32_t idesc, idesc_ones;
   int act;
   bool has_aux, has_pre;
-  bool to_bf16;           // kEpiStep: bf16 instead of fp16
+  bool to_bf16;           // kEpiUpdate: bf16 instead of fp16
   const float* bias;      // kEpiAct: [N] or null
   const float* old;       // kEpiGrad32: [M, N] added to the product, or null
   float* k_sums;          // kEpiGrad*: [splits, M], or null
   bool add_k_sums;        // the sums are added to what k_sums holds
   float alpha, beta, diag;
-  __nv_bfloat16* raw_out;  // kEpiStep: plain stores (a row length the copy engine cannot address), or null
+  // fp32 [batch, gain_ld], gain_ld a multiple of 32: each diagonal entry of kEpiPoly's result over
+  // its rounding, which is kEpiUpdate's factor of a row (gain_rows) or column
+  float* gain;
+  int gain_ld;
+  bool gain_rows;
+  __nv_bfloat16* raw_out;  // kEpiUpdate: plain stores (a row length the copy engine cannot address), or null
   int* status;
   uint64_t wait_ns;
   int fault;
@@ -365,6 +373,18 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// a[lane]
+__device__ __forceinline__ float of_lane(const uint32_t (&a)[32], int lane) {
+  uint32_t t[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) t[i] = lane & 16 ? a[i + 16] : a[i];
+#pragma unroll
+  for (int n = 8; n > 0; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) t[i] = lane & n ? t[i + n] : t[i];
+  return __uint_as_float(t[0]);
+}
+
 // Bytes of one staging tile (32 rows x 32 columns) of an epilogue.
 __host__ __device__ constexpr int tile_bytes(int epi) { return epi == kEpiGrad32 ? 4096 : 2048; }
 // Staging tiles of an epilogue warp: with a second operand (aux) up to four, for the store of
@@ -569,7 +589,7 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
     const int quad = warp & 3, part = warp >> 2;
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
     unsigned char* wstage = smem + p.off_out + warp * p.warp_bytes;
-    constexpr bool kHasAux = EPI != kEpiGrad32;
+    constexpr bool kHasAux = EPI != kEpiGrad32 && EPI != kEpiGram && EPI != kEpiUpdate;
     const bool aux = kHasAux && p.has_aux, pre = EPI == kEpiAct && p.has_pre;
     const int NB = p.tiles;
     const uint32_t aux0 = bar0 + 8 * (kAux + kMaxAuxTiles * warp);
@@ -707,6 +727,22 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
           __syncwarp();
           request_next();
         }
+        // kEpiUpdate: the factors of the slice's columns
+        [[maybe_unused]] float4 factor[EPI == kEpiUpdate ? 8 : 1];
+        if constexpr (EPI == kEpiUpdate) {
+          const float* gain = p.gain + (int64_t)w.b * p.gain_ld;
+          if (p.gain_rows) {
+            const float f = row < p.M ? p.alpha * __ldcg(gain + row) : 0.0f;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) factor[c] = make_float4(f, f, f, f);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float4 g = __ldcg(reinterpret_cast<const float4*>(gain + w.n0 + c0) + c);
+              factor[c] = make_float4(p.alpha * g.x, p.alpha * g.y, p.alpha * g.z, p.alpha * g.w);
+            }
+          }
+        }
         uint32_t a[32];
         if constexpr (EPI != kEpiGrad32) tc::ld32_wait(trow + buf * kMaxNT + c0, a);
         if (aux && !warp_wait(aux0 + 8 * tile, aux_phase, p.wait_ns)) {
@@ -783,7 +819,17 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
               default: activate(std::integral_constant<int, SWIN_WATTN_ACT_NONE>()); break;
             }
           } else {
-            const float dg = w.n0 + c0 == row0 ? p.diag : 0.0f;  // both are multiples of 32
+            if constexpr (EPI == kEpiGram || EPI == kEpiPoly) {
+              if (w.n0 + c0 == row0) {  // the diagonal's slices: both are multiples of 32
+#pragma unroll
+                for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) + (lane == e ? p.diag : 0.0f));
+                if (EPI == kEpiPoly && row < p.M) {
+                  const float x = __half2float(reinterpret_cast<const __half*>(at(sr, lane >> 3))[lane & 7]);
+                  const float entry = fmaf(of_lane(a, lane), p.alpha, x * p.beta);
+                  p.gain[(int64_t)w.b * p.gain_ld + row] = __fdividef(entry, __half2float(__float2half_rn(entry)));
+                }
+              }
+            }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint4 r = make_uint4(0, 0, 0, 0);
@@ -795,10 +841,14 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
                 if constexpr (EPI == kEpiGrad16) {
                   const float2 y = __fadd2_rn(pair(e), unpack_bf16(rr[q]));
                   o[4 * c + q] = pack_bf16(y.x, y.y);
-                } else {
-                  const float2 d2 = make_float2(lane == e ? dg : 0.0f, lane == e + 1 ? dg : 0.0f);
-                  const float2 y = __ffma2_rn(pair(e), splat(p.alpha), __ffma2_rn(unpack_f16(rr[q]), splat(p.beta), d2));
+                } else if constexpr (EPI == kEpiUpdate) {
+                  const float4 f = factor[2 * c + q / 2];
+                  const float2 y = __fmul2_rn(pair(e), q % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
                   o[4 * c + q] = p.to_bf16 ? pack_bf16(y.x, y.y) : pack_f16(y.x, y.y);
+                } else {
+                  float2 y = __fmul2_rn(pair(e), splat(p.alpha));
+                  if constexpr (EPI == kEpiPoly) y = __ffma2_rn(pair(e), splat(p.alpha), __fmul2_rn(unpack_f16(rr[q]), splat(p.beta)));
+                  o[4 * c + q] = pack_f16(y.x, y.y);
                 }
               }
             }
@@ -815,13 +865,14 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
             }
           }
         }
-        if (EPI == kEpiStep && p.raw_out != nullptr) {
+        if (EPI == kEpiUpdate && p.raw_out != nullptr) {
           __syncwarp();
           const int col = w.n0 + c0 + lane;
           if (col < p.N)
             for (int r = 0; r < 32 && row0 + r < p.M; ++r)
               p.raw_out[((int64_t)w.b * p.M + row0 + r) * p.N + col] = *reinterpret_cast<const __nv_bfloat16*>(
                   so + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+          tc::fence_proxy_async();  // before a load writes the tile
           __syncwarp();
         } else {
           tc::fence_proxy_async();  // the staging tile to the copy engine
@@ -1038,7 +1089,7 @@ cudaError_t launch_tiles(const Tiling& t, Params p, const Matrix& a, const Matri
   p.has_aux = ex.aux != nullptr;
   p.has_pre = ex.pre != nullptr;
   if (p.has_aux) {
-    const CUtensorMapDataType aux_type = EPI == kEpiStep ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapDataType aux_type = EPI == kEpiPoly ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     e = encode_3d(&aux_map, *ex.aux, batch, aux_type, 2, kSC, 32, kOutSwz, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
     if (e != cudaSuccess) return e;
   }

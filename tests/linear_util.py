@@ -105,8 +105,10 @@ NS = (3.4445, -4.7750, 2.0315)
 
 
 def orthogonalize64(g, steps, eps=1e-7, scale=1.0, half=False):
-    """One matrix in fp64; with half, every held matrix rounded to fp16 (times 2^8) where the
-    kernels hold it, and the result to bf16."""
+    """One matrix in fp64; with half, with every matrix that the kernels hold rounded where and as
+    they round it (times 2^8, fp16): X, A about a shift of the diagonal, and the polynomial B, of
+    whose diagonal the rounding is taken back from the rows of X. The result then is rounded to
+    bf16."""
     a, b, c = NS
 
     def hold(t):
@@ -117,10 +119,14 @@ def orthogonalize64(g, steps, eps=1e-7, scale=1.0, half=False):
     if g.shape[0] > g.shape[1]:
         x = x.T
     eye = torch.eye(x.shape[0], dtype=torch.float64)
+    mu = 0.36 / x.shape[0]
     for s in range(steps):
-        A = hold(x @ x.T)
-        x = hold(a * eye + b * A + c * (A @ A)) @ x
+        A = hold(x @ x.T - mu * eye)
+        e = a + b * mu + c * mu * mu
+        B = e * eye + (b + 2 * c * mu) * A + c * A @ A
+        x = (hold(B) @ x) * (B.diagonal() / hold(B).diagonal())[:, None]
         if s < steps - 1:
             x = hold(x)
+        mu = 0.75 if mu > 0.12 else mu * e ** 2
     x = scale * (x.T if g.shape[0] > g.shape[1] else x)
     return x.to(torch.bfloat16).double() if half else x

@@ -58,6 +58,21 @@ def test_against_fp64(n, r, c, dtype):
     _check(_run(g), g)
 
 
+@pytest.mark.parametrize("r,c,steps", [(540, 126, 6), (96, 384, 5), (62, 588, 6), (300, 310, 6), (1400, 100, 7),
+                                       (100, 500, 12), (520, 140, 6), (1, 40, 5), (24, 64, 1), (24, 64, 20)])
+def test_error_beside_the_rounding_of_the_result(r, c, steps):
+    """Against the iteration in fp64 with the same matrices rounded (the quarter as above), and, up
+    to seven steps, no further off than half as far again as rounding the exact result to bf16."""
+    g = _g(3 * r + c, 2, r, c)
+    out = _run(g, steps=steps)
+    for o, m in zip(out, g):
+        exact, held = orthogonalize64(m, steps), orthogonalize64(m, steps, half=True)
+        err, size = float((o - exact).norm()), float(exact.norm())
+        assert err <= 1.25 * float((held - exact).norm()) + 1e-4 * size
+        if steps <= 7:
+            assert err <= 1.5 * float((exact.to(torch.bfloat16).double() - exact).norm()) + 1e-4 * size
+
+
 @pytest.mark.parametrize("steps,scale", [(1, 1.0), (2, 0.25), (3, -2.0), (8, 1.7)])
 def test_steps_and_scale(steps, scale):
     g = _g(steps, 2, 96, 160)
