@@ -27,7 +27,7 @@
 // What bounds it, measured on one GB300 (of the measured 6797 GB/s and 1865 TFLOP/s): wide products
 // the tensor cores (12561 x 6144 x 1536 with residual: 127.5 us, 1.00; 8192^3: 599 us, 0.98);
 // narrow K the memory (50176 x 192 x 768, two results: 31.5 us, 0.81); short K with a slope
-// epilogue the epilogue warps' issue (12544 x 512 -> 2048: 35.3 us, 0.49, of which the last of six
+// epilogue the epilogue warps' issue (12544 x 512 -> 2048: 34.9 us, 0.50, of which the last of six
 // rounds of tiles is a sixth full); the smallest launches latency, some 3.5 us from one launch to
 // the next (0.9 until the last grid's writes are seen, 0.9 to the first chunk, 0.6 for its
 // product, 0.7 for the epilogue, 0.4 to leave).
