@@ -22,10 +22,12 @@
 // accumulated in fp32. Singular values far below the largest come out with the error of
 // rounding the large ones' entries (the same is true, eight times worse, in bf16).
 //
-// Measured on one GB300: two 1536 x 6144 451 us (Gram 36, square 16, update 41 us a step: 83, 51
-// and 71 % of the tensor pipe; norm and scaling 33 us at 61 % of DRAM), eight 2048 x 512 151 us,
-// bound by the chain of fifteen dependent launches. A and A^2 are symmetric, and half of each would
-// do; the tiles on and above the diagonal (42 of 72 on 76 pairs) take one round all the same.
+// A and B are symmetric. Where it is estimated to pay, only the tiles on and below their
+// diagonals are computed, and stored twice (product.cuh): two 1536 x 6144 take 72 tiles of 256 x 160
+// in one round of the pairs instead of 72 of 256 x 256, and less power.
+//
+// Measured on one GB300: two 1536 x 6144 418 us (451 with all tiles), eight 2048 x 512 151 us, bound
+// by the chain of fifteen dependent launches.
 // (One epilogue for all three products, which tells them apart as it runs, took 169 us for the
 // stack, adding e X from a second read of X instead of the factors of its rows 160 us.)
 #include "orthogonalize.cuh"
@@ -206,8 +208,8 @@ cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, 
                       : normalize(static_cast<const __nv_bfloat16*>(g), count, rows, cols, eps, partial, x[0], l.ldx, st);
   const bool tall = rows > cols;
   const int m = l.m, n = std::max(rows, cols);
-  const Tiling t_gram = prod::choose_tiling(m, m, n, count, tall, 1, false);
-  const Tiling t_poly = prod::choose_tiling(m, m, m, count, false, 1, false);
+  const Tiling t_gram = prod::choose_tiling(m, m, n, count, tall, 1, false, true);
+  const Tiling t_poly = prod::choose_tiling(m, m, m, count, false, 1, false, true);
   const Tiling t_step = prod::choose_tiling(rows, cols, m, count, !tall, 1, false);
   const Matrix A{gram, m, m, l.lda, (int64_t)m * l.lda}, B{poly, m, m, l.lda, (int64_t)m * l.lda};
   const bool direct = cols % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;

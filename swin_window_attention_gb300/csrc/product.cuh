@@ -79,6 +79,9 @@ enum Epi {
   kEpiPoly = 5,    // fp16: alpha * acc + beta * aux, likewise; and the gains of its diagonal
   kEpiUpdate = 6   // fp16 or bf16: alpha * gain * acc
 };
+// Symmetric results, of which only the tiles and slices on and below the diagonal may be computed;
+// those below are then stored a second time, transposed. The tiling says whether (tiling_cost).
+__host__ __device__ constexpr bool symmetric(int epi) { return epi == kEpiGram || epi == kEpiPoly; }
 
 // Warps: the epilogue's, MMA, copy. The fp32 gradient has eight epilogue warps, which hold 128
 // running sums a thread, more than an even share of the registers: two idle warps complete a
@@ -103,7 +106,9 @@ struct FastDiv {
 struct Params {
   int M, N, NT;
   FastDiv n_mt, n_nt, n_splits;
-  int n_items;  // batch * splits * n_mt * n_nt, n fastest
+  bool half;                // of a symmetric result
+  FastDiv n_lower, per_nt;  // with half: tiles of a matrix that are computed; NT
+  int n_items;  // batch * splits * n_mt * n_nt (or batch * n_lower), n fastest
   int chunks, chunks_per_split;
   int stages, stage_bytes;
   int off_out, warp_bytes, tiles, off_small, off_bar;  // tiles: a warp's staging tiles before that of pre
@@ -385,6 +390,16 @@ __device__ __forceinline__ float of_lane(const uint32_t (&a)[32], int lane) {
   return __uint_as_float(t[0]);
 }
 
+// Tiles of `rows` x NT on or below the diagonal in row mt of tiles.
+__host__ __device__ __forceinline__ int lower_tiles(int mt, int rows, int NT, int n_nt, const FastDiv& per_nt) {
+#ifdef __CUDA_ARCH__
+  const int n = per_nt.quotient((mt + 1) * rows + NT - 1);
+#else
+  const int n = ((mt + 1) * rows + NT - 1) / NT;
+#endif
+  return n < n_nt ? n : n_nt;
+}
+
 // Bytes of one staging tile (32 rows x 32 columns) of an epilogue.
 __host__ __device__ constexpr int tile_bytes(int epi) { return epi == kEpiGrad32 ? 4096 : 2048; }
 // Staging tiles of an epilogue warp: with a second operand (aux) up to four, for the store of
@@ -426,6 +441,17 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
   };
   auto decode = [&](int it) {
     Item w;
+    if (symmetric(EPI) && p.half) {
+      w.b = p.n_lower.quotient(it);
+      w.nt = it - w.b * p.n_lower.d;
+      int mt = 0;
+      for (int n; w.nt >= (n = lower_tiles(mt, CG * kBM, p.NT, p.n_nt.d, p.per_nt)); ++mt) w.nt -= n;
+      w.m0 = (mt * CG + rank) * kBM;
+      w.n0 = w.nt * p.NT;
+      w.split = w.c0 = 0;
+      w.c1 = p.chunks;
+      return w;
+    }
     const uint32_t r1 = p.n_nt.quotient(it), r2 = p.n_mt.quotient(r1);
     w.nt = it - r1 * p.n_nt.d;
     const int mt = r1 - r2 * p.n_mt.d;
@@ -604,6 +630,7 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
         nx_n0 = w.n0;
         nx_b = w.b;
         nx_end = nx_row < p.M ? min(p.NT, p.N - w.n0) : 0;
+        if (symmetric(EPI) && p.half) nx_end = min(nx_end, nx_row + kSC - w.n0);  // none above the diagonal
       }
     };
     auto request_next = [&]() {
@@ -713,6 +740,8 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
       for (int si = 0; si < kSlices; ++si) {
         const int c0 = (part + kPerQuad * si) * kSC;
         if (!(row0 < p.M && c0 < p.NT && w.n0 + c0 < p.N)) continue;
+        if (symmetric(EPI) && p.half && w.n0 + c0 > row0) continue;
+        const bool mirror = symmetric(EPI) && p.half && w.n0 + c0 < row0;
         unsigned char* so = wstage + tile * kTile;
         unsigned char* sz = wstage + NB * kTile;
         if (aux) {
@@ -864,6 +893,12 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
               *at(sz + lane * 64, c) = make_uint4(z16[0], z16[1], z16[2], z16[3]);
             }
           }
+          if (symmetric(EPI) && mirror) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)  // column e becomes row e
+              *reinterpret_cast<uint16_t*>(sz + e * 64 + (((lane >> 3) ^ ((e >> 1) & 3)) << 4) + (lane & 7) * 2) =
+                  (uint16_t)(e & 1 ? o[e / 2] >> 16 : o[e / 2]);
+          }
         }
         if (EPI == kEpiUpdate && p.raw_out != nullptr) {
           __syncwarp();
@@ -880,6 +915,7 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
           if (lane == 0) {
             store_3d(&out_map, w.n0 + c0, row0, EPI == kEpiGrad32 ? w.split : w.b, smem_u32(so));
             if (EPI == kEpiAct && pre) store_3d(&pre_map, w.n0 + c0, row0, w.b, smem_u32(sz));
+            if (symmetric(EPI) && mirror) store_3d(&out_map, row0, w.n0 + c0, w.b, smem_u32(sz));
             tc::bulk_commit();
           }
         }
@@ -983,6 +1019,8 @@ inline cudaError_t encode_3d(CUtensorMap* map, const Matrix& x, int batch, CUten
 
 struct Tiling {
   int cg, NT, splits, chunks, chunks_per_split, n_mt, n_nt;
+  bool half;       // only the tiles on and below the diagonal
+  int per_matrix;  // tiles that are computed
 };
 
 // Estimated time, in SM clocks, of a tiling: rounds of tiles over the SMs (or pairs), each
@@ -999,18 +1037,21 @@ inline double chunk_clocks(int NT, int cg, bool bmn) {
 // `extra` columns beside a tile's hold the sums over K; where they lie in the other accumulator
 // every segment of an fp32 result waits for the last one's epilogue, some 2000 clocks.
 inline double tiling_cost(const Tiling& t, int64_t M, int64_t N, int batch, bool bmn, bool sums) {
-  const int64_t items = (int64_t)t.n_mt * t.n_nt * t.splits * batch;
+  const int64_t items = (int64_t)t.per_matrix * t.splits * batch;
   const int64_t groups = kSms / t.cg;
   const double rounds = (double)((items + groups - 1) / groups);
   const double epi = 500.0 + 14.0 * t.NT;
   double cost = 5000.0 + rounds * std::max(t.chunks_per_split * chunk_clocks(t.NT, t.cg, bmn), epi) + epi;
   if (sums && t.n_nt == 1 && t.NT + 16 * t.cg > kMaxNT) cost += rounds * 2000.0 * (t.chunks_per_split / kSegChunks);
+  // the second, transposed stores and their staging (eight 2048 x 512, all tiles 151 us, half 157
+  // us; two 1536 x 6144, 451 and 419 us)
+  if (t.half) cost += 2500.0;
   if (t.splits > 1) cost += 4000.0 + (double)(t.splits + 1) * M * N * 4.0 / 3000.0;
   return cost;
 }
 
 // The cheapest tiling. `max_splits` > 1 allows K to be split into partial results.
-inline Tiling search_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn, int max_splits, bool sums) {
+inline Tiling search_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn, int max_splits, bool sums, bool sym) {
   Tiling best{};
   double best_cost = -1.0;
   const int chunks = (int)((K + kKC - 1) / kKC);
@@ -1022,16 +1063,24 @@ inline Tiling search_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn
       t.chunks = chunks;
       t.n_mt = (int)((M + cg * kBM - 1) / (cg * kBM));
       t.n_nt = (int)((N + nt - 1) / nt);
-      for (int s = 1; s <= max_splits; ++s) {
-        const int per = (chunks + s - 1) / s;
-        if (s > 1 && per < 4) break;
-        if ((chunks + per - 1) / per != s) continue;  // every split has chunks
-        t.splits = s;
-        t.chunks_per_split = per;
-        const double c = tiling_cost(t, M, N, batch, bmn, sums);
-        if (best_cost < 0.0 || c < best_cost) {
-          best_cost = c;
-          best = t;
+      for (int half = 0; half <= (sym ? 1 : 0); ++half) {
+        t.half = half != 0;
+        t.per_matrix = t.n_mt * t.n_nt;
+        if (t.half) {
+          t.per_matrix = 0;
+          for (int mt = 0; mt < t.n_mt; ++mt) t.per_matrix += lower_tiles(mt, cg * kBM, nt, t.n_nt, FastDiv());
+        }
+        for (int s = 1; s <= max_splits; ++s) {
+          const int per = (chunks + s - 1) / s;
+          if (s > 1 && per < 4) break;
+          if ((chunks + per - 1) / per != s) continue;  // every split has chunks
+          t.splits = s;
+          t.chunks_per_split = per;
+          const double c = tiling_cost(t, M, N, batch, bmn, sums);
+          if (best_cost < 0.0 || c < best_cost) {
+            best_cost = c;
+            best = t;
+          }
         }
       }
     }
@@ -1041,20 +1090,21 @@ inline Tiling search_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn
 
 // The same, with the calling thread's last choices remembered by their sizes (a search
 // compares some hundred tilings, which is more than a small launch takes).
-inline Tiling choose_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn, int max_splits, bool sums) {
+inline Tiling choose_tiling(int64_t M, int64_t N, int64_t K, int batch, bool bmn, int max_splits, bool sums,
+                            bool sym = false) {
   struct Entry {
-    int64_t key[7];
+    int64_t key[8];
     Tiling t;
   };
   constexpr int kEntries = 64;
   thread_local Entry cache[kEntries] = {};
-  const int64_t key[7] = {M, N, K, batch, bmn, max_splits, sums};
+  const int64_t key[8] = {M, N, K, batch, bmn, max_splits, sums, sym};
   uint64_t h = 0;
   for (const int64_t k : key) h = (h ^ (uint64_t)k) * 0x9E3779B97F4A7C15ull;
   Entry& c = cache[h >> 58];
-  if (!std::equal(key, key + 7, c.key)) {
-    c.t = search_tiling(M, N, K, batch, bmn, max_splits, sums);
-    std::copy(key, key + 7, c.key);
+  if (!std::equal(key, key + 8, c.key)) {
+    c.t = search_tiling(M, N, K, batch, bmn, max_splits, sums, sym);
+    std::copy(key, key + 8, c.key);
   }
   return c.t;
 }
@@ -1103,8 +1153,13 @@ cudaError_t launch_tiles(const Tiling& t, Params p, const Matrix& a, const Matri
   p.n_splits = FastDiv(t.splits);
   p.chunks = t.chunks;
   p.chunks_per_split = t.chunks_per_split;
-  const int64_t items = (int64_t)t.n_mt * t.n_nt * t.splits * batch;
+  const int64_t items = (int64_t)t.per_matrix * t.splits * batch;
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
+  p.half = t.half;
+  if (t.half) {
+    p.n_lower = FastDiv(t.per_matrix);
+    p.per_nt = FastDiv(t.NT);
+  }
   p.n_items = (int)items;
   p.wait_ns = wait_limit_ns();
   p.fault = fault_site();
@@ -1122,9 +1177,10 @@ cudaError_t launch_tiles(const Tiling& t, Params p, const Matrix& a, const Matri
   constexpr int kSmall = EPI == kEpiAct ? 2 * kMaxNT * 4 : EPI == kEpiGrad32 || EPI == kEpiGrad16 ? 512 : 0;
   const bool long_k = t.chunks_per_split >= kLongK;
   int fixed = 0;
-  p.tiles = p.has_aux ? (p.has_pre || long_k ? 2 : kMaxAuxTiles) : (p.has_pre || long_k ? 1 : 2);
+  const bool second = p.has_pre || t.half;  // a second result's tile, or the transposed one
+  p.tiles = p.has_aux ? (second || long_k ? 2 : kMaxAuxTiles) : (second || long_k ? 1 : 2);
   for (;; --p.tiles) {  // fewer aux tiles where the ring would not have three stages
-    p.warp_bytes = (p.tiles + (p.has_pre ? 1 : 0)) * kTile;
+    p.warp_bytes = (p.tiles + (second ? 1 : 0)) * kTile;
     fixed = kEW * p.warp_bytes + kSmall + 8 * kNBar + 16;
     p.stages = std::min(kMaxStages, (smem_max - fixed) / p.stage_bytes);
     if (p.stages >= 3 || p.tiles <= 2) break;

@@ -58,6 +58,19 @@ def test_against_fp64(n, r, c, dtype):
     _check(_run(g), g)
 
 
+@pytest.mark.parametrize("n,r,c", [(40, 333, 340), (40, 390, 384), (30, 264, 530), (4, 777, 800), (4, 810, 777),
+                                   (2, 1100, 1101)])
+def test_only_half_of_the_symmetric_products(n, r, c):
+    """Stacks large enough that only the tiles on and below the diagonal of A and B are computed."""
+    g = _g(n + r, n, r, c)
+    out = _run(g)
+    pick = [0, n // 2, n - 1]
+    _check(out[pick], g[pick])
+    # the same matrices one at a time, where all tiles may be computed (each within 2^-9 of the exact)
+    one = torch.cat([_run(g[k:k + 1]) for k in pick])
+    assert float((one - out[pick]).norm() / one.norm()) < 2.0 ** -8
+
+
 @pytest.mark.parametrize("r,c,steps", [(540, 126, 6), (96, 384, 5), (62, 588, 6), (300, 310, 6), (1400, 100, 7),
                                        (100, 500, 12), (520, 140, 6), (1, 40, 5), (24, 64, 1), (24, 64, 20)])
 def test_error_beside_the_rounding_of_the_result(r, c, steps):
