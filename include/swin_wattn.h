@@ -359,7 +359,8 @@ int swin_wattn_linear_bwd_weight(const void* dy, const void* x, void* dw, float*
  *   out    bf16 [count, rows, cols], 2-byte aligned, written (16-byte aligned with cols a
  *          multiple of 8 is the fast case); must not overlap g;
  *   count  in [0, 65535] (0: nothing is done); rows, cols in [1, 16384];
- *   steps  in [1, 20]; eps finite and > 0, not subnormal; scale finite;
+ *   steps  in [1, 20]; eps finite and > 0, not subnormal; scale finite, zero or
+ *          at least 2^-100 in size;
  *   workspace  caller-owned device memory of at least
  *          swin_wattn_orthogonalize_workspace_bytes(count, rows, cols) bytes, 256-byte
  *          aligned, overwritten; one call at a time per workspace.

@@ -724,6 +724,8 @@ int swin_wattn_orthogonalize(const void* g, void* out, int count, int rows, int 
   if (count < 0 || (dtype != SWIN_WATTN_FP32 && dtype != SWIN_WATTN_BF16)) return SWIN_WATTN_ERR_INVALID_ARG;
   if (!(eps >= FLT_MIN) || !std::isfinite(eps) || !std::isfinite(scale) || steps < 1 || steps > 20)
     return SWIN_WATTN_ERR_INVALID_ARG;
+  // (the last product's factor, scale / 2^16 times a gain, stays a normal number)
+  if (scale != 0.0f && std::fabs(scale) < 0x1p-100f) return SWIN_WATTN_ERR_INVALID_ARG;
   if (!orthogonalize_sizes(count, rows, cols)) return SWIN_WATTN_ERR_UNSUPPORTED;
   if (count == 0) return SWIN_WATTN_OK;
   if (g == nullptr || out == nullptr || workspace == nullptr) return SWIN_WATTN_ERR_INVALID_ARG;

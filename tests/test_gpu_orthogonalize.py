@@ -92,6 +92,13 @@ def test_steps_and_scale(steps, scale):
     _check(_run(g, steps=steps, scale=scale), g, steps, scale)
 
 
+@pytest.mark.parametrize("r,c", [(40, 96), (140, 150)])
+def test_smallest_and_largest_scales(r, c):
+    g = _g(r, 1, r, c)
+    for scale in (2.0 ** -100, -(2.0 ** 100), 0.0):
+        _check(_run(g, scale=scale), g, scale=scale)
+
+
 @pytest.mark.parametrize("r,c", [(1, 1), (1, 7), (9, 1), (1, 1000), (8, 8), (2, 3)])
 def test_smallest_sizes(r, c):
     g = _g(r + c, 3, r, c)

@@ -58,6 +58,12 @@ def test_update_rejects_a_subnormal_eps(lib):
     assert f(1e-40) == lib.ERR_INVALID_ARG and f(2.0 ** -149) == lib.ERR_INVALID_ARG and f(2.0 ** -126) == lib.OK
 
 
+def test_update_rejects_a_tiny_scale(lib):
+    f = lambda scale: lib.swin_wattn_orthogonalize(None, None, 0, 8, 8, 1, 5, 1e-7, scale, None, 0, None, None)
+    assert f(1e-38) == lib.ERR_INVALID_ARG and f(-(2.0 ** -101)) == lib.ERR_INVALID_ARG
+    assert f(0.0) == lib.OK and f(-(2.0 ** -100)) == lib.OK and f(1e38) == lib.OK
+
+
 def test_wrappers_refuse_host_tensors(lib):
     x, w = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(8, 8, dtype=torch.bfloat16)
     for call in (lambda: lib.linear(x, w), lambda: lib.linear_bwd_data(x, w), lambda: lib.linear_bwd_weight(x, x),
