@@ -331,6 +331,7 @@ def swin_wattn_orthogonalize(g_ptr, out_ptr, count, rows, cols, dtype, steps, ep
 
 _BF16 = torch.bfloat16
 _F32 = torch.float32
+_U8 = torch.uint8
 
 
 def _address(name, t, shape, dtype, dev):
@@ -345,6 +346,21 @@ def _address(name, t, shape, dtype, dev):
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     raise ValueError(f"{name} is not contiguous")
+
+
+def _plain(name, t, dtype, dev):
+    """The same of an operand whose shape its caller has looked at."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _address(name, t, t.shape, dtype, dev)
+
+
+def _leading(shape, width):
+    """The axes before the last of an operand, as sizes of a result that ends in `width`, and how
+    many rows they make."""
+    if len(shape) == 2:
+        return shape[0], (shape[0], width)
+    return shape[:-1].numel(), (*shape[:-1], width)
 
 
 def _device_of(name, t):
@@ -403,14 +419,6 @@ def _empty(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _workspace(workspace, need, dev, stream):
-    """The workspace given, or one of `need` bytes: the tensor, its address and its size."""
-    if workspace is None:
-        workspace = _empty((max(need(), 1),), torch.uint8, dev, stream)
-    nbytes = workspace.numel()
-    return workspace, _address("workspace", workspace, (nbytes,), torch.uint8, dev), nbytes
-
-
 def _act_code(act):
     code = ACTIVATIONS.get(act) if type(act) is str else act
     if code is None or not ACT_NONE <= code <= ACT_SILU:
@@ -418,11 +426,14 @@ def _act_code(act):
     return code
 
 
-def _weight(w, dev):
-    shape = w.shape
-    if len(shape) != 2:
-        raise ValueError(f"w has {len(shape)} dimensions, not 2")
-    return (*shape, _address("w", w, shape, _BF16, dev))
+def _widths(name, shape, w, axis):
+    """N and K of the weight [N, K], `axis` of which is the last of the operand `name`."""
+    ws = w.shape
+    if len(ws) != 2:
+        raise ValueError(f"w has {len(ws)} dimensions, not 2")
+    if not shape or shape[-1] != ws[axis]:
+        raise ValueError(f"{name} has shape {tuple(shape)}, whose last axis does not fit w's {tuple(ws)}")
+    return ws
 
 
 def linear(x, w, b=None, act=ACT_NONE, residual=None, y=None, pre=None, status=None, stream=None):
@@ -430,15 +441,14 @@ def linear(x, w, b=None, act=ACT_NONE, residual=None, y=None, pre=None, status=N
     W [N, K] bf16 and b [N] fp32 (or None), into a bf16 [..., N] tensor (allocated here when
     not given; it may be the residual itself). act: "none", "relu", "gelu", "gelu_tanh",
     "silu" or an ACT_ code. pre, a bf16 [..., N] tensor, receives x W^T + b for the backward."""
-    dev = _device_of("x", x)
-    N, K, w_ptr = _weight(w, dev)
-    lead = x.shape[:-1]
-    tokens, shape = lead.numel(), (*lead, N)
+    dev, xs = _device_of("x", x), x.shape
+    N, K = _widths("x", xs, w, 1)
+    tokens, shape = _leading(xs, N)
     if tokens > _INT_MAX or K > _INT_MAX or N > _INT_MAX:
         raise _too_large(tokens, K, N)
     if y is None:
         y = _empty(shape, _BF16, dev, stream)
-    _call(load().swin_wattn_linear, dev, stream, status, _address("x", x, (*lead, K), _BF16, dev), w_ptr,
+    _call((_lib or load()).swin_wattn_linear, dev, stream, status, _plain("x", x, _BF16, dev), _plain("w", w, _BF16, dev),
           None if b is None else _address("b", b, (N,), _F32, dev),
           None if residual is None else _address("residual", residual, shape, _BF16, dev),
           _address("y", y, shape, _BF16, dev), None if pre is None else _address("pre", pre, shape, _BF16, dev),
@@ -450,20 +460,19 @@ def linear_bwd_data(dy, w, pre=None, act=ACT_NONE, dx=None, status=None, stream=
     """(dy W) * act'(pre) for dy [..., N] and W [N, K], into a bf16 [..., K] tensor (allocated
     here when not given; it may be pre itself): with act "none" the gradient of the product's
     input, else of the pre-activation [..., K] whose activation that input was."""
-    dev = _device_of("dy", dy)
+    dev, ds = _device_of("dy", dy), dy.shape
     code = _act_code(act)
-    N, K, w_ptr = _weight(w, dev)
-    lead = dy.shape[:-1]
-    tokens, shape = lead.numel(), (*lead, K)
+    N, K = _widths("dy", ds, w, 0)
+    tokens, shape = _leading(ds, K)
     if tokens > _INT_MAX or K > _INT_MAX or N > _INT_MAX:
         raise _too_large(tokens, K, N)
     if code != ACT_NONE and pre is None:
         raise ValueError("an activation needs its pre-activation: pre is None")
     if dx is None:
         dx = _empty(shape, _BF16, dev, stream)
-    _call(load().swin_wattn_linear_bwd_data, dev, stream, status, _address("dy", dy, (*lead, N), _BF16, dev), w_ptr,
-          None if pre is None else _address("pre", pre, shape, _BF16, dev), _address("dx", dx, shape, _BF16, dev),
-          tokens, K, N, code)
+    _call((_lib or load()).swin_wattn_linear_bwd_data, dev, stream, status, _plain("dy", dy, _BF16, dev),
+          _plain("w", w, _BF16, dev), None if pre is None else _address("pre", pre, shape, _BF16, dev),
+          _address("dx", dx, shape, _BF16, dev), tokens, K, N, code)
     return dx
 
 
@@ -473,9 +482,11 @@ def linear_bwd_weight(dy, x, dw=None, db=None, accumulate=False, workspace=None,
     to add to; without dw both are allocated here, in fp32; with dw alone there is no db.
     workspace: a uint8 tensor of swin_wattn_linear_bwd_weight_workspace_bytes (allocated here
     when not given). Returns (dw, db)."""
-    dev = _device_of("dy", dy)
-    N, K, lead = dy.shape[-1], x.shape[-1], dy.shape[:-1]
-    tokens = lead.numel()
+    dev, ds, xs = _device_of("dy", dy), dy.shape, x.shape
+    if not ds or not xs or ds[:-1] != xs[:-1]:
+        raise ValueError(f"dy and x have shapes {tuple(ds)} and {tuple(xs)}: they differ before the last axis")
+    N, K = ds[-1], xs[-1]
+    tokens = ds[0] if len(ds) == 2 else ds[:-1].numel()
     if tokens > _INT_MAX or K > _INT_MAX or N > _INT_MAX:
         raise _too_large(tokens, K, N)
     if dw is None:
@@ -484,12 +495,12 @@ def linear_bwd_weight(dy, x, dw=None, db=None, accumulate=False, workspace=None,
         dw = _empty((N, K), _F32, dev, stream)
         db = _empty((N,), _F32, dev, stream) if db is None else db
     code = _float_code("dw", dw)
-    workspace, ws_ptr, nbytes = _workspace(
-        workspace, lambda: swin_wattn_linear_bwd_weight_workspace_bytes(tokens, K, N), dev, stream)
-    _call(load().swin_wattn_linear_bwd_weight, dev, stream, status, _address("dy", dy, (*lead, N), _BF16, dev),
-          _address("x", x, (*lead, K), _BF16, dev), _address("dw", dw, (N, K), dw.dtype, dev),
+    if workspace is None:
+        workspace = _empty((max(swin_wattn_linear_bwd_weight_workspace_bytes(tokens, K, N), 1),), _U8, dev, stream)
+    _call((_lib or load()).swin_wattn_linear_bwd_weight, dev, stream, status, _plain("dy", dy, _BF16, dev),
+          _plain("x", x, _BF16, dev), _address("dw", dw, (N, K), dw.dtype, dev),
           None if db is None else _address("db", db, (N,), _F32, dev), tokens, K, N, code, 1 if accumulate else 0,
-          ws_ptr, nbytes)
+          _plain("workspace", workspace, _U8, dev), workspace.numel())
     return dw, db
 
 
@@ -508,11 +519,11 @@ def orthogonalize(g, steps=5, eps=1e-7, scale=1.0, out=None, workspace=None, sta
         raise _too_large(count, rows, cols, steps)
     if out is None:
         out = _empty(shape, _BF16, dev, stream)
-    workspace, ws_ptr, nbytes = _workspace(
-        workspace, lambda: swin_wattn_orthogonalize_workspace_bytes(count, rows, cols), dev, stream)
-    _call(load().swin_wattn_orthogonalize, dev, stream, status, _address("g", g, shape, g.dtype, dev),
+    if workspace is None:
+        workspace = _empty((max(swin_wattn_orthogonalize_workspace_bytes(count, rows, cols), 1),), _U8, dev, stream)
+    _call((_lib or load()).swin_wattn_orthogonalize, dev, stream, status, _plain("g", g, g.dtype, dev),
           _address("out", out, shape, _BF16, dev), count, rows, cols, code, steps, float(eps), float(scale),
-          ws_ptr, nbytes)
+          _plain("workspace", workspace, _U8, dev), workspace.numel())
     return out
 
 
