@@ -373,7 +373,7 @@ int swin_wattn_linear_bwd_weight(const void* dy, const void* x, void* dw, float*
  * count as zero, and a norm beyond the largest fp32 gives zeros. A matrix with a
  * NaN or an infinity gives NaN and leaves the others of the stack alone; a zero matrix gives zeros.
  * One launch where the smaller side is at most 128 and the larger at most 4096, else
- * 2 + 3 * steps; nothing is allocated. Deterministic. Errors: INVALID_ARG for the
+ * 2 + 3 * steps, or 2 + 4 * steps where the longer side is split; nothing is allocated. Deterministic. Errors: INVALID_ARG for the
  * scalars, overlaps, a small workspace or a pointer that is not memory of the current
  * device; MISALIGNED; UNSUPPORTED for sizes out of range. The size query returns 0 for
  * unsupported arguments.

@@ -57,7 +57,7 @@ int linear_bwd_weight_launches(int64_t T, int K, int N);
 cudaError_t linear_bwd_weight_launch(const void* dy, const void* x, void* dw, float* db, int T, int K, int N,
                                      int dtype, int accumulate, void* workspace, int* status, cudaStream_t st);
 size_t orthogonalize_workspace_bytes(int count, int rows, int cols);
-int orthogonalize_launches(int rows, int cols, int steps);
+int orthogonalize_launches(int count, int rows, int cols, int steps);
 cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, int cols, int dtype, int steps,
                                  float eps, float scale, void* workspace, int* status, cudaStream_t st);
 }  // namespace swin
@@ -743,7 +743,7 @@ int swin_wattn_orthogonalize(const void* g, void* out, int count, int rows, int 
   cudaError_t e = swin::orthogonalize_launch(g, out, count, rows, cols, dtype, steps, eps, scale, workspace, status,
                                              reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_orthogonalize");
-  g_launches += swin::orthogonalize_launches(rows, cols, steps);
+  g_launches += swin::orthogonalize_launches(count, rows, cols, steps);
   return SWIN_WATTN_OK;
 }
 

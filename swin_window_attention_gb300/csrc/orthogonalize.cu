@@ -46,6 +46,7 @@ using prod::Params;
 using prod::Tiling;
 
 constexpr CUtensorMapDataType kF16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+constexpr CUtensorMapDataType kF32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
 constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 
 constexpr int kNormThreads = 256;
@@ -152,13 +153,54 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(const T* __rest
   }
 }
 
+// A' = sum over the splits of the Gram product's parts, less mu on the diagonal: four columns a
+// thread, all parts' reads in flight (they are in L2). Rows have ld elements, of parts and result.
+constexpr int kSumThreads = 128;
+__global__ void __launch_bounds__(kSumThreads) gram_sum_kernel(const float* __restrict__ part, int splits, int m, int ld,
+                                                               float mu, __half* __restrict__ out) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int i = blockIdx.x * kSumThreads + threadIdx.x;  // four columns of the matrix
+  if (i >= m * (ld / 4)) return;
+  const int64_t size = (int64_t)m * ld;
+  const float4* p = reinterpret_cast<const float4*>(part + blockIdx.y * splits * size) + i;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const float4 a = __ldcg(p + s * (size / 4));
+    v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
+  }
+  const int r = i / (ld / 4), c = i % (ld / 4) * 4;
+  constexpr float k = 1.0f / kScale;
+  const float d = -mu * kScale;
+  reinterpret_cast<uint2*>(out + blockIdx.y * size)[i] =
+      make_uint2(prod::pack_f16(fmaf(v.x, k, r == c ? d : 0.0f), fmaf(v.y, k, r == c + 1 ? d : 0.0f)),
+                 prod::pack_f16(fmaf(v.z, k, r == c + 2 ? d : 0.0f), fmaf(v.w, k, r == c + 3 ? d : 0.0f)));
+}
+
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 int round8(int n) { return (n + 7) & ~7; }
 
-// Workspace: two copies of X, A, B, the factors of B's diagonal, the partial sums of squares.
+// The Gram product, over the longer side. Where that is long and its tiles are few, it is split
+// into parts and their sum is a launch of its own, of some 3000 clocks beyond what tiling_cost counts
+// for it (two 70 x 5497, three steps: 109 us whole, 65 us in parts).
+constexpr int kMaxGramSplits = 16;
+Tiling gram_tiling(int count, int rows, int cols) {
+  const int m = std::min(rows, cols), n = std::max(rows, cols);
+  const bool tall = rows > cols;
+  const Tiling whole = prod::choose_tiling(m, m, n, count, tall, 1, false, true);
+  const Tiling parts = prod::choose_tiling(m, m, n, count, tall, kMaxGramSplits, false);
+  return parts.splits > 1 && prod::tiling_cost(parts, m, m, count, tall, false) + 3000.0 <
+                                 prod::tiling_cost(whole, m, m, count, tall, false)
+             ? parts
+             : whole;
+}
+
+// Workspace: two copies of X, A, B, the factors of B's diagonal, the partial sums of squares, the
+// parts of the Gram product.
 struct Layout {
   int m, ldx, lda, ld_gain;
-  size_t x_bytes, a_bytes, gain_bytes, total;
+  size_t x_bytes, a_bytes, gain_bytes, partial_bytes, total;
 };
 Layout layout(int count, int rows, int cols) {
   Layout l;
@@ -169,7 +211,10 @@ Layout layout(int count, int rows, int cols) {
   l.a_bytes = align256((size_t)count * l.m * l.lda * 2);
   l.ld_gain = (l.m + 31) & ~31;
   l.gain_bytes = align256((size_t)count * l.ld_gain * sizeof(float));
-  l.total = 2 * l.x_bytes + 2 * l.a_bytes + l.gain_bytes + align256((size_t)count * kNormBlocks * sizeof(Squares));
+  l.partial_bytes = align256((size_t)count * kNormBlocks * sizeof(Squares));
+  const int splits = gram_tiling(count, rows, cols).splits;
+  l.total = 2 * l.x_bytes + 2 * l.a_bytes + l.gain_bytes + l.partial_bytes +
+            (splits > 1 ? align256((size_t)count * splits * l.m * l.lda * 4) : 0);
   return l;
 }
 
@@ -190,7 +235,9 @@ cudaError_t normalize(const T* g, int count, int rows, int cols, float eps, Squa
 size_t orthogonalize_workspace_bytes(int count, int rows, int cols) {
   return orthogonalize_small_applies(rows, cols) ? 256 : layout(count, rows, cols).total;
 }
-int orthogonalize_launches(int rows, int cols, int steps) { return orthogonalize_small_applies(rows, cols) ? 1 : 2 + 3 * steps; }
+int orthogonalize_launches(int count, int rows, int cols, int steps) {
+  return orthogonalize_small_applies(rows, cols) ? 1 : 2 + (gram_tiling(count, rows, cols).splits > 1 ? 4 : 3) * steps;
+}
 
 cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, int cols, int dtype, int steps,
                                  float eps, float scale, void* workspace, int* status, cudaStream_t st) {
@@ -203,12 +250,13 @@ cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, 
   __half* poly = reinterpret_cast<__half*>(ws + 2 * l.x_bytes + l.a_bytes);
   float* gain = reinterpret_cast<float*>(ws + 2 * l.x_bytes + 2 * l.a_bytes);
   Squares* partial = reinterpret_cast<Squares*>(ws + 2 * l.x_bytes + 2 * l.a_bytes + l.gain_bytes);
+  float* parts = reinterpret_cast<float*>(ws + 2 * l.x_bytes + 2 * l.a_bytes + l.gain_bytes + l.partial_bytes);
   cudaError_t e = dtype == SWIN_WATTN_FP32
                       ? normalize(static_cast<const float*>(g), count, rows, cols, eps, partial, x[0], l.ldx, st)
                       : normalize(static_cast<const __nv_bfloat16*>(g), count, rows, cols, eps, partial, x[0], l.ldx, st);
   const bool tall = rows > cols;
   const int m = l.m, n = std::max(rows, cols);
-  const Tiling t_gram = prod::choose_tiling(m, m, n, count, tall, 1, false, true);
+  const Tiling t_gram = gram_tiling(count, rows, cols);
   const Tiling t_poly = prod::choose_tiling(m, m, m, count, false, 1, false, true);
   const Tiling t_step = prod::choose_tiling(rows, cols, m, count, !tall, 1, false);
   const Matrix A{gram, m, m, l.lda, (int64_t)m * l.lda}, B{poly, m, m, l.lda, (int64_t)m * l.lda};
@@ -224,8 +272,17 @@ cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, 
     p.alpha = 1.0f / kScale;  // (2^8 X)(2^8 X)^T = 2^16 A -> 2^8 (A - mu I)
     p.diag = -k.mu * (kScale * kScale);
     prod::Extra none;
-    e = tall ? prod::launch_product<true, true, prod::kEpiGram>(t_gram, p, X, X, A, count, kF16, kF16, none, st)
-             : prod::launch_product<false, false, prod::kEpiGram>(t_gram, p, X, X, A, count, kF16, kF16, none, st);
+    if (t_gram.splits > 1) {
+      const Matrix P{parts, m, m, l.lda, (int64_t)m * l.lda};
+      e = tall ? prod::launch_product<true, true, prod::kEpiGrad32>(t_gram, p, X, X, P, count, kF16, kF32, none, st)
+               : prod::launch_product<false, false, prod::kEpiGrad32>(t_gram, p, X, X, P, count, kF16, kF32, none, st);
+      if (e == cudaSuccess)
+        e = launch_pdl(gram_sum_kernel, dim3((m * (l.lda / 4) + kSumThreads - 1) / kSumThreads, count), dim3(kSumThreads), 0,
+                       st, (const float*)parts, t_gram.splits, m, l.lda, k.mu, gram);
+    } else {
+      e = tall ? prod::launch_product<true, true, prod::kEpiGram>(t_gram, p, X, X, A, count, kF16, kF16, none, st)
+               : prod::launch_product<false, false, prod::kEpiGram>(t_gram, p, X, X, A, count, kF16, kF16, none, st);
+    }
     if (e != cudaSuccess) return e;
     p.alpha = kNsC / kScale;
     p.beta = k.b;

@@ -72,7 +72,8 @@ constexpr int kNBar = kAux + kMaxAuxTiles * 16;
 enum Epi {
   kEpiAct = 0,     // bf16: aux + act(acc + bias), optionally acc + bias into a second result
   kEpiSlope = 1,   // bf16: acc * act'(aux)
-  kEpiGrad32 = 2,  // fp32: [old +] acc, optionally the column sums of A^T (sum over K of A)
+  kEpiGrad32 = 2,  // fp32: [old +] acc, optionally the column sums of A^T (sum over K of A);
+                   // where K is split, a result per split (of each matrix)
   kEpiGrad16 = 3,  // bf16: [aux +] acc, optionally the same sums
   // of the weight update (orthogonalize.cu), on fp16 operands:
   kEpiGram = 4,    // fp16: alpha * acc, after diag was added to the diagonal of acc
@@ -913,7 +914,7 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
           tc::fence_proxy_async();  // the staging tile to the copy engine
           __syncwarp();
           if (lane == 0) {
-            store_3d(&out_map, w.n0 + c0, row0, EPI == kEpiGrad32 ? w.split : w.b, smem_u32(so));
+            store_3d(&out_map, w.n0 + c0, row0, EPI == kEpiGrad32 ? w.b * p.n_splits.d + w.split : w.b, smem_u32(so));
             if (EPI == kEpiAct && pre) store_3d(&pre_map, w.n0 + c0, row0, w.b, smem_u32(sz));
             if (symmetric(EPI) && mirror) store_3d(&out_map, row0, w.n0 + c0, w.b, smem_u32(sz));
             tc::bulk_commit();
@@ -1046,7 +1047,7 @@ inline double tiling_cost(const Tiling& t, int64_t M, int64_t N, int batch, bool
   // the second, transposed stores and their staging (eight 2048 x 512, all tiles 151 us, half 157
   // us; two 1536 x 6144, 451 and 419 us)
   if (t.half) cost += 2500.0;
-  if (t.splits > 1) cost += 4000.0 + (double)(t.splits + 1) * M * N * 4.0 / 3000.0;
+  if (t.splits > 1) cost += 4000.0 + (double)(t.splits + 1) * M * N * batch * 4.0 / 3000.0;
   return cost;
 }
 
@@ -1129,7 +1130,7 @@ cudaError_t launch_tiles(const Tiling& t, Params p, const Matrix& a, const Matri
     e = encode_3d(&b_map, b, batch, in_type, 2, kKC, BMN ? 64 : t.NT / CG, CU_TENSOR_MAP_SWIZZLE_128B, kL2);
   if (e != cudaSuccess) return e;
   if (p.raw_out == nullptr) {
-    e = encode_3d(&out_map, out, EPI == kEpiGrad32 ? t.splits : batch, out_type, EPI == kEpiGrad32 ? 4 : 2, kSC, 32,
+    e = encode_3d(&out_map, out, EPI == kEpiGrad32 ? t.splits * batch : batch, out_type, EPI == kEpiGrad32 ? 4 : 2, kSC, 32,
                   kOutSwz, CU_TENSOR_MAP_L2_PROMOTION_NONE);
     if (e != cudaSuccess) return e;
   } else {

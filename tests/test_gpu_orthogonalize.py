@@ -71,6 +71,14 @@ def test_only_half_of_the_symmetric_products(n, r, c):
     assert float((one - out[pick]).norm() / one.norm()) < 2.0 ** -8
 
 
+@pytest.mark.parametrize("n,r,c", [(2, 70, 5497), (2, 5496, 71), (1, 135, 3341), (1, 300, 6000), (3, 2500, 131),
+                                   (1, 16384, 40), (1, 1, 16384), (1, 4097, 1)])
+def test_gram_product_in_parts(n, r, c):
+    """Few tiles of a long product: its parts are summed in a launch of their own."""
+    g = _g(n + r, n, r, c)
+    _check(_run(g), g)
+
+
 @pytest.mark.parametrize("r,c,steps", [(540, 126, 6), (96, 384, 5), (62, 588, 6), (300, 310, 6), (1400, 100, 7),
                                        (100, 500, 12), (520, 140, 6), (1, 40, 5), (24, 64, 1), (24, 64, 20)])
 def test_error_beside_the_rounding_of_the_result(r, c, steps):
