@@ -182,15 +182,15 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 int round8(int n) { return (n + 7) & ~7; }
 
 // The Gram product, over the longer side. Where that is long and its tiles are few, it is split
-// into parts and their sum is a launch of its own, of some 3000 clocks beyond what tiling_cost counts
-// for it (two 70 x 5497, three steps: 109 us whole, 65 us in parts).
+// into parts and their sum is a launch of its own (two 70 x 5497, three steps: 109 us whole, 65 us in
+// parts; 512 x 2048, five steps: 100 and 90 us; 300 x 900: 72 and 76 us). The 500 clocks keep ties whole.
 constexpr int kMaxGramSplits = 16;
 Tiling gram_tiling(int count, int rows, int cols) {
   const int m = std::min(rows, cols), n = std::max(rows, cols);
   const bool tall = rows > cols;
   const Tiling whole = prod::choose_tiling(m, m, n, count, tall, 1, false, true);
   const Tiling parts = prod::choose_tiling(m, m, n, count, tall, kMaxGramSplits, false);
-  return parts.splits > 1 && prod::tiling_cost(parts, m, m, count, tall, false) + 3000.0 <
+  return parts.splits > 1 && prod::tiling_cost(parts, m, m, count, tall, false) + 500.0 <
                                  prod::tiling_cost(whole, m, m, count, tall, false)
              ? parts
              : whole;
