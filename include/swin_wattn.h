@@ -364,15 +364,20 @@ int swin_wattn_linear_bwd_weight(const void* dy, const void* x, void* dw, float*
  *   workspace  caller-owned device memory of at least
  *          swin_wattn_orthogonalize_workspace_bytes(count, rows, cols) bytes, 256-byte
  *          aligned, overwritten; one call at a time per workspace.
- * Operands of the products are held in fp16 (scaled; the values are bounded), products are
- * accumulated in fp32; the result is within about 1.5e-3 (relative 2-norm, before its
- * rounding to bf16) of the exact iteration for matrices whose singular values span a
- * factor of about a hundred, and loses accuracy in the directions of smaller ones. Where |G|
- * is far below eps, X is small from the start; its entries are held to 2^-33. The norm is summed
- * in fp32, in three ranges of size so that no square overflows or is lost; subnormal values
- * count as zero, and a norm beyond the largest fp32 gives zeros. A matrix with a
- * NaN or an infinity gives NaN and leaves the others of the stack alone; a zero matrix gives zeros.
- * One launch where the smaller side is at most 128 and the larger at most 4096, else
+ * A and the polynomial are held in fp16 (scaled; the values are bounded), X in two fp16 parts of
+ * 22 bits together, products are accumulated in fp32. Five steps end within 2e-3 (relative
+ * 2-norm, before the rounding of the result to bf16) of the exact iteration where the smaller
+ * side is at least 64, whatever G's rank and singular values: directions that G does not have
+ * stay empty. Fewer rows average their roundings less: within 4e-3 from 32, 6e-3 from 2. Each
+ * further step multiplies what the earlier ones left in directions still rising by up to 3.44, as
+ * it does to G's own rounding: 4e-3 after seven steps, 1.1e-2 after ten (smaller side at least 64).
+ * (The largest found over ranks from 1, singular values from flat to k^-2, and two groups of them up to
+ * 1e4 apart.) Where |G| is far below eps, X is small from the start; its entries are held to
+ * 2^-39. The norm is summed in fp32, in three ranges of size so that no square overflows or is
+ * lost; subnormal values count as zero, and a norm beyond the largest fp32 gives zeros. A matrix
+ * with a NaN or an infinity gives NaN and leaves the others of the stack alone; a zero matrix
+ * gives zeros.
+ * One launch where the smaller side is at most 128 and the larger at most 2048, else
  * 2 + 3 * steps, or 2 + 4 * steps where the longer side is split; nothing is allocated. Deterministic. Errors: INVALID_ARG for the
  * scalars, overlaps, a small workspace or a pointer that is not memory of the current
  * device; MISALIGNED; UNSUPPORTED for sizes out of range. The size query returns 0 for

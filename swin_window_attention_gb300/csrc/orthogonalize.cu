@@ -14,22 +14,24 @@
 //
 // Operands are fp16, not bf16: the entries of X, A and B are bounded (|X| <= 1.21,
 // |A| <= 1.45, |B| < 16), so the exponent range of bf16 is not needed and its 8 significant
-// bits cost eight times the error: on random matrices the result is 0.7e-3 to 1.4e-3
-// (relative 2-norm) from the 64-bit one, where the final rounding to bf16 alone is 1.7e-3.
-// (The diagonals of A and B: orthogonalize.cuh.) Everything is kept times 2^8, so an entry of X a
-// hundredth of the smallest typical one (1 / sqrt(rows cols) = 3e-4 at 1536 x 6144) is
-// still a normal number, and the largest B stays a tenth of the largest fp16. Products are
-// accumulated in fp32. Singular values far below the largest come out with the error of
-// rounding the large ones' entries (the same is true, eight times worse, in bf16).
+// bits cost eight times the error. X is held in two parts, its rounding and what that leaves, and
+// the update's product walks K once for each (why: orthogonalize.cuh, with the diagonals of A
+// and B); A is made of the larger part, whose rounding there does what A's own does. Before the
+// rounding to bf16 (1.7e-3 by itself, relative 2-norm) five steps end 0.5e-3 to 1.7e-3 from the
+// 64-bit result, over spectra from flat to 1 / k^2, halves a thousandfold apart and ranks from
+// 1. A and B are kept times 2^8, which leaves the largest B a tenth of the largest fp16, X times
+// 2^14, which leaves the smaller part of a typical entry (1 / sqrt(rows cols) = 3e-4 at
+// 1536 x 6144) some ten bits. Products are accumulated in fp32.
 //
 // A and B are symmetric. Where it is estimated to pay, only the tiles on and below their
 // diagonals are computed, and stored twice (product.cuh): two 1536 x 6144 take 72 tiles of 256 x 160
 // in one round of the pairs instead of 72 of 256 x 256, and less power.
 //
-// Measured on one GB300: two 1536 x 6144 418 us (451 with all tiles), eight 2048 x 512 151 us, bound
-// by the chain of fifteen dependent launches.
-// (One epilogue for all three products, which tells them apart as it runs, took 169 us for the
-// stack, adding e X from a second read of X instead of the factors of its rows 160 us.)
+// Measured on one GB300, graph of calls: two 1536 x 6144 650 us, of which the second part of X takes
+// some 43 us a step (441 us on the same card with X in one part), bound by the tensor cores; eight
+// 2048 x 512 192 us (154), bound by the chain of seventeen dependent launches.
+// (With X in one part: all tiles of A and B 451 us where half of them took 418; one epilogue for
+// all three products, which tells them apart as it runs, 169 us for the stack where three took 151.)
 #include "orthogonalize.cuh"
 #include "product.cuh"
 
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_partial_kernel(const T* __r
   if (threadIdx.x == 0) partial[blockIdx.y * gridDim.x + blockIdx.x] = sum;
 }
 
-// X = G / (|G| + eps), times 2^8, in fp16 rows of ld elements.
+// X = G / (|G| + eps), times 2^14, in two fp16 parts, of `rows` rows of ld elements each.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) normalize_kernel(const T* __restrict__ g, int rows, int cols, int ld,
                                                                  bool vec, const Squares* __restrict__ partial,
@@ -133,23 +135,29 @@ __global__ void __launch_bounds__(kNormThreads) normalize_kernel(const T* __rest
   const Inverse k = inverse_of(block_sum(sum), eps);
   const int64_t elements = (int64_t)rows * cols;
   const T* gm = g + (int64_t)blockIdx.y * elements;
-  __half* xm = x + (int64_t)blockIdx.y * rows * ld;
+  __half* xm = x + (int64_t)blockIdx.y * 2 * rows * ld;
+  __half* low = xm + (int64_t)rows * ld;
   if (vec && ld == cols) {
     const int64_t n8 = elements / 8, stride = (int64_t)gridDim.x * kNormThreads;
 #pragma unroll 4
     for (int64_t i = (int64_t)blockIdx.x * kNormThreads + threadIdx.x; i < n8; i += stride) {
       float v[8];
       load8(gm + i * 8, v);
-      uint32_t o[4];
+      uint32_t o[4], r[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = prod::pack_f16(v[2 * e] * k.pre * k.inv, v[2 * e + 1] * k.pre * k.inv);
+      for (int e = 0; e < 4; ++e) two_parts(make_float2(v[2 * e] * k.pre * k.inv, v[2 * e + 1] * k.pre * k.inv), o[e], r[e]);
       reinterpret_cast<uint4*>(xm)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<uint4*>(low)[i] = make_uint4(r[0], r[1], r[2], r[3]);
     }
   } else {
     const int wpb = kNormThreads / 32, lane = threadIdx.x & 31;
     for (int r = blockIdx.x * wpb + (threadIdx.x >> 5); r < rows; r += gridDim.x * wpb)
-      for (int c = lane; c < cols; c += 32)
-        xm[(int64_t)r * ld + c] = __float2half_rn(load_f32(gm + (int64_t)r * cols + c) * k.pre * k.inv);
+      for (int c = lane; c < cols; c += 32) {
+        const float v = load_f32(gm + (int64_t)r * cols + c) * k.pre * k.inv;
+        const __half h = __float2half_rn(v);
+        xm[(int64_t)r * ld + c] = h;
+        low[(int64_t)r * ld + c] = __float2half_rn(v - __half2float(h));
+      }
   }
 }
 
@@ -171,7 +179,7 @@ __global__ void __launch_bounds__(kSumThreads) gram_sum_kernel(const float* __re
     v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
   }
   const int r = i / (ld / 4), c = i % (ld / 4) * 4;
-  constexpr float k = 1.0f / kScale;
+  constexpr float k = kScale / (kScaleX * kScaleX);
   const float d = -mu * kScale;
   reinterpret_cast<uint2*>(out + blockIdx.y * size)[i] =
       make_uint2(prod::pack_f16(fmaf(v.x, k, r == c ? d : 0.0f), fmaf(v.y, k, r == c + 1 ? d : 0.0f)),
@@ -196,7 +204,7 @@ Tiling gram_tiling(int count, int rows, int cols) {
              : whole;
 }
 
-// Workspace: two copies of X, A, B, the factors of B's diagonal, the partial sums of squares, the
+// Workspace: two copies of X in two parts, A, B, the factors of B's diagonal, the partial sums of squares, the
 // parts of the Gram product.
 struct Layout {
   int m, ldx, lda, ld_gain;
@@ -207,7 +215,7 @@ Layout layout(int count, int rows, int cols) {
   l.m = std::min(rows, cols);
   l.ldx = round8(cols);
   l.lda = round8(l.m);
-  l.x_bytes = align256((size_t)count * rows * l.ldx * 2);
+  l.x_bytes = align256((size_t)count * 2 * rows * l.ldx * 2);
   l.a_bytes = align256((size_t)count * l.m * l.lda * 2);
   l.ld_gain = (l.m + 31) & ~31;
   l.gain_bytes = align256((size_t)count * l.ld_gain * sizeof(float));
@@ -258,30 +266,32 @@ cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, 
   const int m = l.m, n = std::max(rows, cols);
   const Tiling t_gram = gram_tiling(count, rows, cols);
   const Tiling t_poly = prod::choose_tiling(m, m, m, count, false, 1, false, true);
-  const Tiling t_step = prod::choose_tiling(rows, cols, m, count, !tall, 1, false);
+  const int part_chunks = (m + prod::kKC - 1) / prod::kKC;
+  const Tiling t_step = prod::choose_tiling(rows, cols, 2 * part_chunks * prod::kKC, count, !tall, 1, false);
   const Matrix A{gram, m, m, l.lda, (int64_t)m * l.lda}, B{poly, m, m, l.lda, (int64_t)m * l.lda};
   const bool direct = cols % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
   float mu = first_shift(m);
   for (int s = 0; s < steps && e == cudaSuccess; ++s, mu = next_shift(mu)) {
     const NsStep k = ns_step(mu);
-    const Matrix X{x[s & 1], rows, cols, l.ldx, (int64_t)rows * l.ldx};
-    Matrix Y{x[(s + 1) & 1], rows, cols, l.ldx, (int64_t)rows * l.ldx};
+    // X in both parts, and its larger part alone, of which A is made
+    const Matrix X{x[s & 1], rows, cols, l.ldx, (int64_t)rows * l.ldx, 2}, H{x[s & 1], rows, cols, l.ldx, (int64_t)2 * rows * l.ldx};
+    Matrix Y{x[(s + 1) & 1], rows, cols, l.ldx, (int64_t)rows * l.ldx, 2};
     Params p{};
     p.status = status;
     p.M = p.N = m;
-    p.alpha = 1.0f / kScale;  // (2^8 X)(2^8 X)^T = 2^16 A -> 2^8 (A - mu I)
-    p.diag = -k.mu * (kScale * kScale);
+    p.alpha = kScale / (kScaleX * kScaleX);  // (2^14 X)(2^14 X)^T = 2^28 A -> 2^8 (A - mu I)
+    p.diag = -k.mu * (kScaleX * kScaleX);
     prod::Extra none;
     if (t_gram.splits > 1) {
       const Matrix P{parts, m, m, l.lda, (int64_t)m * l.lda};
-      e = tall ? prod::launch_product<true, true, prod::kEpiGrad32>(t_gram, p, X, X, P, count, kF16, kF32, none, st)
-               : prod::launch_product<false, false, prod::kEpiGrad32>(t_gram, p, X, X, P, count, kF16, kF32, none, st);
+      e = tall ? prod::launch_product<true, true, prod::kEpiGrad32>(t_gram, p, H, H, P, count, kF16, kF32, none, st)
+               : prod::launch_product<false, false, prod::kEpiGrad32>(t_gram, p, H, H, P, count, kF16, kF32, none, st);
       if (e == cudaSuccess)
         e = launch_pdl(gram_sum_kernel, dim3((m * (l.lda / 4) + kSumThreads - 1) / kSumThreads, count), dim3(kSumThreads), 0,
                        st, (const float*)parts, t_gram.splits, m, l.lda, k.mu, gram);
     } else {
-      e = tall ? prod::launch_product<true, true, prod::kEpiGram>(t_gram, p, X, X, A, count, kF16, kF16, none, st)
-               : prod::launch_product<false, false, prod::kEpiGram>(t_gram, p, X, X, A, count, kF16, kF16, none, st);
+      e = tall ? prod::launch_product<true, true, prod::kEpiGram>(t_gram, p, H, H, A, count, kF16, kF16, none, st)
+               : prod::launch_product<false, false, prod::kEpiGram>(t_gram, p, H, H, A, count, kF16, kF16, none, st);
     }
     if (e != cudaSuccess) return e;
     p.alpha = kNsC / kScale;
@@ -301,9 +311,10 @@ cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, 
     q.gain = gain;
     q.gain_ld = l.ld_gain;
     q.gain_rows = !tall;
+    q.part_chunks = part_chunks;
     CUtensorMapDataType out_type = kF16;
     if (s == steps - 1) {
-      q.alpha = scale / (kScale * kScale);
+      q.alpha = scale / (kScale * kScaleX);
       q.to_bf16 = true;
       out_type = kBf16;
       Y = Matrix{out, rows, cols, cols, (int64_t)rows * cols};

@@ -1,16 +1,17 @@
 // The Newton-Schulz update (orthogonalize.cu) of matrices whose smaller side is at most 128, in
 // one launch. A cluster of CTAs keeps a matrix in shared memory for all its steps: each CTA a
-// slab of up to 512 of the longer side (fp16, times 2^8), and all of A and B = a I + b A + c A^2.
+// slab of the longer side (X in two fp16 parts, times 2^14), and all of A and B = a I + b A + c A^2.
 // Per step
 //   1. A's part from the slab on the tensor cores; the cluster's parts are summed in order
 //      through distributed shared memory, each CTA adding up its share of the rows and handing
 //      the rounded rows to the others;
 //   2. A^2, and B from it;
-//   3. the slab times B, written over the slab.
+//   3. the slab's two parts times B, written over the slab.
 // Nothing but the matrix itself crosses memory, once in (twice, from L2, for its norm) and once
-// out. What bounds it is latency: the steps' products depend on each other, and take a few
-// hundred to two thousand clocks each. As separate launches of product.cuh's tiles the same
-// products take about 3.5 us each (96 x 384, five steps: 52 us; here 24.2 us).
+// out. What bounds it is latency: the steps' products depend on each other, and with the
+// rounding, exchange and barriers between them take some 2 us each (96 x 384, five steps: 29.9 us;
+// with X in one part 23.8 us). As separate launches of product.cuh's tiles they would take about
+// 3.5 us each.
 //
 // The slab lies in blocks of 64 columns of 128-byte rows, 128-byte swizzled, so that one
 // placement serves both products: for wide matrices (slab: all rows, a range of columns) the
@@ -27,7 +28,10 @@ using namespace prod;
 
 constexpr int kSmThreads = 512, kSmWarps = kSmThreads / 32;
 constexpr int kSide = 128;        // the smaller side at most
-constexpr int kSlab = 512;        // of the longer side, per CTA
+// Of the longer side, per CTA, at most: alone, or in a cluster, whose exchange of A's parts needs the
+// room of two matrices.
+constexpr int kSlabAlone = 384, kSlabShared = 256;
+constexpr int kReadSide = 512;     // that the reads of G are laid out for
 constexpr int kSmCluster = 8;
 constexpr int kMatBytes = kSide * kSide * 2;
 constexpr uint32_t kF16Format = (1u << 7) | (1u << 10);  // bits that make an operand bf16
@@ -118,10 +122,13 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
   const int mp = (m + 15) & ~15;
   int bad = (smem0 & 1023u) != 0;
 
-  // slab at 0; A and B behind it
-  unsigned char* sA = smem + p.slab_bytes;
-  unsigned char* sB = sA + kMatBytes;
-  const uint32_t slab0 = smem0, a0 = smem0 + p.slab_bytes, b0 = a0 + kMatBytes;
+  // the slab's larger parts at 0, the smaller ones, A and B behind them. Alone, B is written over A:
+  // each thread over the entries that it makes it from.
+  unsigned char* sLow = smem + p.slab_bytes;
+  unsigned char* sA = sLow + p.slab_bytes;
+  const int b_off = S > 1 ? kMatBytes : 0;
+  unsigned char* sB = sA + b_off;
+  const uint32_t slab0 = smem0, low0 = slab0 + p.slab_bytes, a0 = low0 + p.slab_bytes, b0 = a0 + b_off;
   const int block = p.slab_rows * 128;  // bytes of 64 columns of the slab
   // element (r, c) of the slab; of A or B (blocks of 128 rows)
   auto at = [&](int r, int c) { return (c >> 6) * block + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) + (c & 7) * 2; };
@@ -132,7 +139,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
     for (int i = 0; i < 6; ++i) tc::mbar_init(bar + 8 * i, i < 3 ? 1 : S);
     tc::mbar_init_fence();
   }
-  for (int i = tid; i < p.slab_bytes / 16; i += kSmThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < p.slab_bytes / 8; i += kSmThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -161,8 +168,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
   };
   // else kRows rows (16 apart) of kGroups groups of 32 columns, a lane each. (Element by element
   // as the pieces, the addresses alone took 12 us of one 97 x 385.)
-  constexpr int kGroups = TALL ? kSide / 32 : kSlab / 32, kRows = 32 / kGroups;
-  constexpr int kBatches = kSide * kSlab / 32 / kSmThreads;
+  constexpr int kGroups = TALL ? kSide / 32 : kReadSide / 32, kRows = 32 / kGroups;
+  constexpr int kBatches = kSide * kReadSide / 32 / kSmThreads;
   // place in the slab's row r of the lane's column of group j
   auto at_group = [&](int r, int j) {
     return (j >> 1) * block + r * 128 + (((lane >> 3) + 4 * (j & 1) ^ (r & 7)) << 4) + (lane & 7) * 2;
@@ -247,18 +254,26 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
         const int i = 4 * batch * kSmThreads + tid;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          uint32_t o[4];
+          uint32_t o[4], l[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = pack_f16(v[8 * u + 2 * e], v[8 * u + 2 * e + 1]);
-          if (i + u * kSmThreads < n8) *reinterpret_cast<uint4*>(smem + at(r, 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int e = 0; e < 4; ++e) two_parts(make_float2(v[8 * u + 2 * e], v[8 * u + 2 * e + 1]), o[e], l[e]);
+          if (i + u * kSmThreads < n8) {
+            const int to = at(r, 8 * c);
+            *reinterpret_cast<uint4*>(smem + to) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(sLow + to) = make_uint4(l[0], l[1], l[2], l[3]);
+          }
           advance(r, c);
         }
       } else {
 #pragma unroll
         for (int u = 0; u < 32; ++u) {
           const int row = warp + kSmWarps * (batch * kRows + u / kGroups), col = lane + u % kGroups * 32;
-          if (row < srows && col < scols)
-            *reinterpret_cast<__half*>(smem + at_group(row, u % kGroups)) = __float2half_rn(v[u]);
+          if (row < srows && col < scols) {
+            const int to = at_group(row, u % kGroups);
+            const __half h = __float2half_rn(v[u]);
+            *reinterpret_cast<__half*>(smem + to) = h;
+            *reinterpret_cast<__half*>(sLow + to) = __float2half_rn(v[u] - __half2float(h));
+          }
         }
       }
     }
@@ -318,7 +333,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
   float mu = first_shift(m);
   for (int step = 0; step < p.steps; ++step) {
     const bool last = step == p.steps - 1;
-    const float alpha = last ? p.scale / (kScale * kScale) : 1.0f / kScale;
+    const float alpha = last ? p.scale / (kScale * kScaleX) : 1.0f / kScale;
+    constexpr float kToA = kScale / (kScaleX * kScaleX);  // (2^14 X)(2^14 X)^T = 2^28 A -> 2^8 A
     const NsStep ns = ns_step(mu);
     mu = next_shift(mu);
     wait_products(0, phase);
@@ -333,11 +349,11 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
           uint32_t o[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            o[q] = pack_f16(__uint_as_float(a[8 * c + 2 * q]) * (1.0f / kScale), __uint_as_float(a[8 * c + 2 * q + 1]) * (1.0f / kScale));
+            o[q] = pack_f16(__uint_as_float(a[8 * c + 2 * q]) * kToA, __uint_as_float(a[8 * c + 2 * q + 1]) * kToA);
           *reinterpret_cast<uint4*>(sA + mat_at(row, c0 + 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         if (part == quad)
-          *reinterpret_cast<__half*>(sA + mat_at(row, row)) = __float2half_rn(fmaf(of_lane(a, lane), 1.0f / kScale, -ns.mu * kScale));
+          *reinterpret_cast<__half*>(sA + mat_at(row, row)) = __float2half_rn(fmaf(of_lane(a, lane), kToA, -ns.mu * kScale));
       }
     } else {
       // fp32 parts [128][128] over A and B, of which nothing is needed any more; 16-byte pieces
@@ -355,7 +371,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
       exchange(0, step & 1);
       // Rows rank, rank + S, ...: a thread sums four columns of a row over the cluster, a warp
       // whole rows, so that what it reads of another CTA at once is contiguous (2048 x 128, read
-      // by scattered pieces 67 us, by rows 51 us).
+      // by scattered pieces it took 16 us more).
       constexpr int kMine = kSide / 2 * (kSide / 4) / kSmThreads;  // at S = 2, pieces per thread
       uint2 mine[kMine];
       const int my_rows = (mp - rank + S - 1) / S, pieces = mp / 4;
@@ -369,12 +385,11 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
             u = make_float4(u.x + x.x, u.y + x.y, u.z + x.z, u.w + x.w);
           }
           if (c == r >> 2) {
-            const float v = -ns.mu * (kScale * kScale);
+            const float v = -ns.mu * (kScaleX * kScaleX);
             u = make_float4(u.x + ((r & 3) == 0 ? v : 0.0f), u.y + ((r & 3) == 1 ? v : 0.0f),
                             u.z + ((r & 3) == 2 ? v : 0.0f), u.w + ((r & 3) == 3 ? v : 0.0f));
           }
-          constexpr float k = 1.0f / kScale;
-          mine[i] = make_uint2(pack_f16(u.x * k, u.y * k), pack_f16(u.z * k, u.w * k));
+          mine[i] = make_uint2(pack_f16(u.x * kToA, u.y * kToA), pack_f16(u.z * kToA, u.w * kToA));
         }
       }
       exchange(1, step & 1);  // every part has been read
@@ -405,6 +420,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
     if (c0 < mp) {
       uint32_t a[32];
       tc::ld32_wait(trow + kSide + c0, a);
+      const float x_diag = part == quad ? __half2float(*reinterpret_cast<const __half*>(sA + mat_at(row, row))) : 0.0f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const uint4 w = *reinterpret_cast<const uint4*>(sA + mat_at(row, c0 + 8 * c));
@@ -420,8 +436,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
         *reinterpret_cast<uint4*>(sB + mat_at(row, c0 + 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
       if (part == quad) {
-        const float x = __half2float(*reinterpret_cast<const __half*>(sA + mat_at(row, row)));
-        const float exact = fmaf(of_lane(a, lane), kNsC / kScale, fmaf(x, ns.b, ns.e * kScale));
+        const float exact = fmaf(of_lane(a, lane), kNsC / kScale, fmaf(x_diag, ns.b, ns.e * kScale));
         const __half held = __float2half_rn(exact);
         *reinterpret_cast<__half*>(sB + mat_at(row, row)) = held;
         s_gain[row] = alpha * __fdividef(exact, __half2float(held));
@@ -438,21 +453,25 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
       for (int h = 0; h < halves; ++h) {
         if constexpr (TALL) {
           for (int tile = 2 * h; tile < min(2 * h + 2, p.slab_rows / kSide); ++tile) {
-            uint32_t x = desc_lo(slab0 + tile * (kSide * 128), 16), y = desc_lo(b0, 16);
-            for (int t = 0; t < m_steps; ++t) {
-              mma<1>(tmem + tile * kSide, x, kHi, y, kHi, id_mat, t > 0);
-              x += (t & 3) == 3 ? block_d - 6 : 2;
-              y += (t & 3) == 3 ? (kSide * 128 >> 4) - 6 : 2;
+            for (int high = 0; high < 2; ++high) {  // the smaller part first
+              uint32_t x = desc_lo((high ? slab0 : low0) + tile * (kSide * 128), 16), y = desc_lo(b0, 16);
+              for (int t = 0; t < m_steps; ++t) {
+                mma<1>(tmem + tile * kSide, x, kHi, y, kHi, id_mat, t + high > 0);
+                x += (t & 3) == 3 ? block_d - 6 : 2;
+                y += (t & 3) == 3 ? (kSide * 128 >> 4) - 6 : 2;
+              }
             }
           }
         } else {
           const int c = 256 * h, nn = min(256, (len - c + 15) & ~15);
           const uint32_t id = (tc::idesc_bf16(kSide, 16, true, false) ^ kF16Format) + ((uint32_t)(nn - 16) >> 3 << 17);
-          uint32_t x = desc_lo(b0, 16), y = desc_lo(slab0 + 4 * h * block, block);
-          for (int t = 0; t < m_steps; ++t) {
-            mma<1>(tmem + c, x, kHi, y, kHi, id, t > 0);
-            x += (t & 3) == 3 ? (kSide * 128 >> 4) - 6 : 2;
-            y += 128;
+          for (int high = 0; high < 2; ++high) {  // the smaller part first
+            uint32_t x = desc_lo(b0, 16), y = desc_lo((high ? slab0 : low0) + 4 * h * block, block);
+            for (int t = 0; t < m_steps; ++t) {
+              mma<1>(tmem + c, x, kHi, y, kHi, id, t + high > 0);
+              x += (t & 3) == 3 ? (kSide * 128 >> 4) - 6 : 2;
+              y += 128;
+            }
           }
         }
         commit_products(1 + h);
@@ -477,14 +496,19 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
         tc::ld32_wait(trow + col, a);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint32_t o[4];
+          uint32_t o[4], l[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float2 f = TALL ? *reinterpret_cast<const float2*>(&s_gain[c + 8 * k + 2 * q]) : splat(s_gain[row]);
             const float2 x = __fmul2_rn(make_float2(__uint_as_float(a[8 * k + 2 * q]), __uint_as_float(a[8 * k + 2 * q + 1])), f);
-            o[q] = last ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
+            if (last)
+              o[q] = pack_bf16(x.x, x.y);
+            else
+              two_parts(x, o[q], l[q]);
           }
-          *reinterpret_cast<uint4*>(smem + at(r, c + 8 * k)) = make_uint4(o[0], o[1], o[2], o[3]);
+          const int to = at(r, c + 8 * k);
+          *reinterpret_cast<uint4*>(smem + to) = make_uint4(o[0], o[1], o[2], o[3]);
+          if (!last) *reinterpret_cast<uint4*>(sLow + to) = make_uint4(l[0], l[1], l[2], l[3]);
         }
       }
       tc::fence_proxy_async();
@@ -530,11 +554,11 @@ __global__ void __launch_bounds__(kSmThreads, 1) orthogonalize_small_kernel(cons
 template <bool TALL, typename T>
 cudaError_t launch_small(SmallParams p, int count, cudaStream_t st) {
   const int n = TALL ? p.rows : p.cols;
-  // One CTA where the matrix fits it (no exchange: 128 x 512 32 us, in four CTAs 41 us); else the
-  // largest cluster that leaves every matrix of the stack resident at once (128 x 2048: in
-  // clusters of eight 48 us, of four 52 us; sixteen 100 x 1500: of six 54 us, of three 59 us,
-  // of eight in two rounds 97 us). Slabs are multiples of 64, none empty.
-  p.cluster = (n + kSlab - 1) / kSlab;
+  // One CTA where the matrix fits it (no exchange); else the largest cluster that leaves every
+  // matrix of the stack resident at once (128 x 512: in clusters of eight 41 us, of two 46 us;
+  // sixteen 100 x 1500: of six 60 us, of eight in two rounds 105 us). Slabs are multiples of 64,
+  // none empty.
+  p.cluster = n <= kSlabAlone ? 1 : (n + kSlabShared - 1) / kSlabShared;
   if (p.cluster > 1)
     for (int s = p.cluster + 1; s <= kSmCluster; ++s)
       if (count <= kResidentClusters[s]) p.cluster = s;
@@ -547,7 +571,7 @@ cudaError_t launch_small(SmallParams p, int count, cudaStream_t st) {
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
-  const int smem = std::max(120 * 1024, p.slab_bytes + 2 * kMatBytes);
+  const int smem = std::max(120 * 1024, 2 * p.slab_bytes + (p.cluster > 1 ? 2 : 1) * kMatBytes);
   const bool vec = p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(p.g) % 16 == 0;
   auto kern = vec ? orthogonalize_small_kernel<TALL, true, T> : orthogonalize_small_kernel<TALL, false, T>;
   static std::atomic<uint64_t> allowed[2];
@@ -572,7 +596,7 @@ cudaError_t launch_small(SmallParams p, int count, cudaStream_t st) {
 }  // namespace
 
 bool orthogonalize_small_applies(int rows, int cols) {
-  return std::min(rows, cols) <= kSide && std::max(rows, cols) <= kSlab * kSmCluster;
+  return std::min(rows, cols) <= kSide && std::max(rows, cols) <= kSlabShared * kSmCluster;
 }
 
 cudaError_t orthogonalize_small_launch(const void* g, void* out, int count, int rows, int cols, int dtype, int steps,

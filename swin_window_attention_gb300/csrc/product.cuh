@@ -78,7 +78,9 @@ enum Epi {
   // of the weight update (orthogonalize.cu), on fp16 operands:
   kEpiGram = 4,    // fp16: alpha * acc, after diag was added to the diagonal of acc
   kEpiPoly = 5,    // fp16: alpha * acc + beta * aux, likewise; and the gains of its diagonal
-  kEpiUpdate = 6   // fp16 or bf16: alpha * gain * acc
+  // alpha * gain * acc, in bf16, or in two fp16 parts: its rounding, and what that leaves. One operand
+  // is X in such parts, and K is walked once for each
+  kEpiUpdate = 6
 };
 // Symmetric results, of which only the tiles and slices on and below the diagonal may be computed;
 // those below are then stored a second time, transposed. The tiling says whether (tiling_cost).
@@ -116,7 +118,8 @@ struct Params {
   uint32_t idesc, idesc_ones;
   int act;
   bool has_aux, has_pre;
-  bool to_bf16;           // kEpiUpdate: bf16 instead of fp16
+  bool to_bf16;           // kEpiUpdate: bf16 instead of fp16 parts
+  int part_chunks;        // kEpiUpdate: chunks of K of one part of X; B where gain_rows, else A
   const float* bias;      // kEpiAct: [N] or null
   const float* old;       // kEpiGrad32: [M, N] added to the product, or null
   float* k_sums;          // kEpiGrad*: [splits, M], or null
@@ -505,6 +508,13 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
           const Item w = decode(it);
           const int nb0 = w.n0 + rank * (p.NT / CG);
           for (int c = w.c0; c < w.c1; ++c) {
+            int kc = c * kKC, ba = w.b, bb = w.b;
+            if constexpr (EPI == kEpiUpdate) {
+              // the smaller part first: added to the larger one's sum it would lose its low bits
+              const bool low = c < p.part_chunks;
+              if (!low) kc -= p.part_chunks * kKC;
+              (p.gain_rows ? bb : ba) = 2 * w.b + (low ? 1 : 0);
+            }
             if (!first && !wait(empty_bar(st), ph ^ 1, p.wait_ns)) {
               bad = 1;
               break;
@@ -515,16 +525,16 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
             if constexpr (AMN) {
 #pragma unroll
               for (int j = 0; j < kBM / 64; ++j)
-                load_3d<CG>(base + j * 8192, &a_map, w.m0 + 64 * j, c * kKC, w.b, fb);
+                load_3d<CG>(base + j * 8192, &a_map, w.m0 + 64 * j, kc, ba, fb);
             } else {
-              load_3d<CG>(base, &a_map, c * kKC, w.m0, w.b, fb);
+              load_3d<CG>(base, &a_map, kc, w.m0, ba, fb);
             }
             if constexpr (BMN) {
               // whole boxes of 64 columns: the last one may bring some that belong to the next part
               for (int j = 0; j * 64 < p.NT / CG; ++j)
-                load_3d<CG>(base + kABytes + j * 8192, &b_map, nb0 + 64 * j, c * kKC, w.b, fb);
+                load_3d<CG>(base + kABytes + j * 8192, &b_map, nb0 + 64 * j, kc, bb, fb);
             } else {
-              load_3d<CG>(base + kABytes, &b_map, c * kKC, nb0, w.b, fb);
+              load_3d<CG>(base + kABytes, &b_map, kc, nb0, bb, fb);
             }
             if (++st == stages) {
               st = 0;
@@ -618,6 +628,7 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
     unsigned char* wstage = smem + p.off_out + warp * p.warp_bytes;
     constexpr bool kHasAux = EPI != kEpiGrad32 && EPI != kEpiGram && EPI != kEpiUpdate;
     const bool aux = kHasAux && p.has_aux, pre = EPI == kEpiAct && p.has_pre;
+    const bool parts = EPI == kEpiUpdate && !p.to_bf16;
     const int NB = p.tiles;
     const uint32_t aux0 = bar0 + 8 * (kAux + kMaxAuxTiles * warp);
     // the next slice whose second operand is to be requested: its item, decoded, and its columns,
@@ -809,6 +820,7 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
           auto at = [&](unsigned char* base, int c) { return reinterpret_cast<uint4*>(base + ((c ^ sw) << 4)); };
           auto pair = [&](int e) { return make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])); };
           uint32_t o[16];  // the result, packed
+          [[maybe_unused]] uint32_t low[EPI == kEpiUpdate ? 16 : 1];
           auto activate = [&](auto act) {
             constexpr int ACT = decltype(act)::value;
 #pragma unroll
@@ -874,7 +886,13 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
                 } else if constexpr (EPI == kEpiUpdate) {
                   const float4 f = factor[2 * c + q / 2];
                   const float2 y = __fmul2_rn(pair(e), q % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
-                  o[4 * c + q] = p.to_bf16 ? pack_bf16(y.x, y.y) : pack_f16(y.x, y.y);
+                  if (parts) {
+                    o[4 * c + q] = pack_f16(y.x, y.y);
+                    const float2 rest = fsub2(y, unpack_f16(o[4 * c + q]));
+                    low[4 * c + q] = pack_f16(rest.x, rest.y);
+                  } else {
+                    o[4 * c + q] = pack_bf16(y.x, y.y);
+                  }
                 } else {
                   float2 y = __fmul2_rn(pair(e), splat(p.alpha));
                   if constexpr (EPI == kEpiPoly) y = __ffma2_rn(pair(e), splat(p.alpha), __fmul2_rn(unpack_f16(rr[q]), splat(p.beta)));
@@ -893,6 +911,8 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
               for (int q = 0; q < 4; ++q) z16[q] = pack_bf16(pair(8 * c + 2 * q).x, pair(8 * c + 2 * q).y);
               *at(sz + lane * 64, c) = make_uint4(z16[0], z16[1], z16[2], z16[3]);
             }
+            if constexpr (EPI == kEpiUpdate)
+              if (parts) *at(sz + lane * 64, c) = make_uint4(low[4 * c], low[4 * c + 1], low[4 * c + 2], low[4 * c + 3]);
           }
           if (symmetric(EPI) && mirror) {
 #pragma unroll
@@ -914,7 +934,9 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
           tc::fence_proxy_async();  // the staging tile to the copy engine
           __syncwarp();
           if (lane == 0) {
-            store_3d(&out_map, w.n0 + c0, row0, EPI == kEpiGrad32 ? w.b * p.n_splits.d + w.split : w.b, smem_u32(so));
+            const int batch = EPI == kEpiGrad32 ? w.b * p.n_splits.d + w.split : parts ? 2 * w.b : w.b;
+            store_3d(&out_map, w.n0 + c0, row0, batch, smem_u32(so));
+            if (parts) store_3d(&out_map, w.n0 + c0, row0, batch + 1, smem_u32(sz));
             if (EPI == kEpiAct && pre) store_3d(&pre_map, w.n0 + c0, row0, w.b, smem_u32(sz));
             if (symmetric(EPI) && mirror) store_3d(&out_map, row0, w.n0 + c0, w.b, smem_u32(sz));
             tc::bulk_commit();
@@ -1002,14 +1024,16 @@ inline cudaError_t allow_smem(const void* kern, int bytes, int device, std::atom
 struct Matrix {
   const void* ptr;
   int64_t rows, cols, ld, batch_stride;
+  int parts = 1;  // matrices of the stack to one of the product's batch
 };
 
 inline cudaError_t encode_3d(CUtensorMap* map, const Matrix& x, int batch, CUtensorMapDataType type, int elem,
                              int box_cols, int box_rows, CUtensorMapSwizzle swz, CUtensorMapL2promotion l2) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder_fn();
   if (encode == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows, (cuuint64_t)batch};
-  const cuuint64_t strides[2] = {(cuuint64_t)x.ld * elem, (cuuint64_t)(batch > 1 ? x.batch_stride : x.ld) * elem};
+  const int count = batch * x.parts;
+  const cuuint64_t dims[3] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows, (cuuint64_t)count};
+  const cuuint64_t strides[2] = {(cuuint64_t)x.ld * elem, (cuuint64_t)(count > 1 ? x.batch_stride : x.ld) * elem};
   const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
   const cuuint32_t es[3] = {1, 1, 1};
   return encode(map, type, 3, const_cast<void*>(x.ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, l2,
@@ -1178,7 +1202,8 @@ cudaError_t launch_tiles(const Tiling& t, Params p, const Matrix& a, const Matri
   constexpr int kSmall = EPI == kEpiAct ? 2 * kMaxNT * 4 : EPI == kEpiGrad32 || EPI == kEpiGrad16 ? 512 : 0;
   const bool long_k = t.chunks_per_split >= kLongK;
   int fixed = 0;
-  const bool second = p.has_pre || t.half;  // a second result's tile, or the transposed one
+  // a second result's tile, the transposed one, or the smaller part
+  const bool second = p.has_pre || t.half || (EPI == kEpiUpdate && !p.to_bf16);
   p.tiles = p.has_aux ? (second || long_k ? 2 : kMaxAuxTiles) : (second || long_k ? 1 : 2);
   for (;; --p.tiles) {  // fewer aux tiles where the ring would not have three stages
     p.warp_bytes = (p.tiles + (second ? 1 : 0)) * kTile;
