@@ -60,14 +60,17 @@ constexpr int kTmemCols = 512;  // two accumulators of up to 256 columns
 // (32 MMAs) in tensor memory, whose additions truncate; the epilogue warps add such segments
 // up in registers, rounding to nearest. On 50176 tokens the error against 64 bits is 4.8e-7
 // (relative 2-norm), where one accumulation per tile of 33 chunks left 2.1e-6; an 8192^3 product
-// takes 777 us instead of the 709 us of a bf16 result without segments.
+// takes 777 us instead of the 709 us of a bf16 result without segments. The sums over K, which are
+// fp32 beside a bf16 result too, are taken out of tensor memory in the same segments (12544 tokens of
+// sizes spread over six decades: 0.6e-6, or 1.2e-6 of terms of one sign, where one accumulation lost
+// 1.5e-5 and 4.0e-5).
 constexpr int kSegChunks = 8;
 
 // Barriers: full and empty per stage, full and free per accumulator, the last commit, aux
-// loads (up to four per epilogue warp).
+// loads (up to four per epilogue warp), full and free per segment of kEpiGrad16's sums.
 constexpr int kMaxAuxTiles = 4;
 constexpr int kDFull = 2 * kMaxStages, kDFree = kDFull + 2, kDrain = kDFree + 2, kAux = kDrain + 1;
-constexpr int kNBar = kAux + kMaxAuxTiles * 16;
+constexpr int kSumFull = kAux + kMaxAuxTiles * 16, kSumFree = kSumFull + 2, kNBar = kSumFree + 2;
 
 enum Epi {
   kEpiAct = 0,     // bf16: aux + act(acc + bias), optionally acc + bias into a second result
@@ -429,12 +432,19 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
   auto empty_bar = [&](int st) { return bar0 + 8 * (kMaxStages + st); };
   auto dfull_bar = [&](int b) { return bar0 + 8 * (kDFull + b); };
   auto dfree_bar = [&](int b) { return bar0 + 8 * (kDFree + b); };
+  auto sum_full_bar = [&](int s) { return bar0 + 8 * (kSumFull + (s & 1)); };
+  auto sum_free_bar = [&](int s) { return bar0 + 8 * (kSumFree + (s & 1)); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + p.off_bar + 8 * kNBar);
   const int stages = p.stages;
   constexpr int kEW = epi_warps(EPI), kMMA = kEW, kCOPY = kEW + 1;
   constexpr int kPerQuad = kEW / 4, kSlices = kMaxNT / kSC / kPerQuad;  // warps per quadrant, slices per warp
   constexpr bool kSums = EPI == kEpiGrad32 || EPI == kEpiGrad16;
   constexpr int kSeg = EPI == kEpiGrad32 ? kSegChunks : 1 << 30;
+  // The sums of a first-column tile take columns of their own: one set a segment of an fp32 result,
+  // two in turn beside a bf16 one, whose sums alone are in segments. They lie behind the tile's
+  // columns where there is room, else in the other accumulator's first columns.
+  constexpr int kSumCols = 16 * CG;
+  const bool sums_aside = p.NT + (EPI == kEpiGrad16 ? 2 : 1) * kSumCols > kMaxNT;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rank = CG == 2 ? (int)cluster_rank() : 0;
   const int group = blockIdx.x / CG, n_groups = gridDim.x / CG;
@@ -480,6 +490,10 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
     }
     for (int b = 0; b < kMaxAuxTiles * kEW; ++b) tc::mbar_init(bar0 + 8 * (kAux + b), 1);
     tc::mbar_init(bar0 + 8 * kDrain, 1);
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(sum_full_bar(b), 1);
+      tc::mbar_init(sum_free_bar(b), 4 * CG);  // the warps of an epilogue's first part
+    }
     tc::mbar_init_fence();
   }
   if constexpr (kSums) {
@@ -561,18 +575,18 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
         const uint32_t stage_step = p.stage_bytes >> 4, idesc = p.idesc;
         [[maybe_unused]] const uint32_t idesc_ones = p.idesc_ones;
         int st = 0, g = 0;  // ring stage; accumulations begun
+        [[maybe_unused]] int q = 0;  // segments of kEpiGrad16's sums begun
         uint32_t ph = 0;
         bool prev_ones = false;
         for (int it = group; it < p.n_items && !bad; it += n_groups) {
           const Item w = decode(it);
           const bool ones = kSums && p.k_sums != nullptr && w.nt == 0;
-          // the sums of a first-column tile: behind the tile's columns where there is room, else
-          // in the other accumulator's first columns
-          const bool ones_aside = ones && p.NT + 16 * CG > kMaxNT;
+          const bool ones_aside = ones && sums_aside;
           for (int s0 = w.c0; s0 < w.c1 && !bad; s0 += kSeg, ++g) {
             const int s1 = min(s0 + kSeg, w.c1), buf = g & 1;
             const uint32_t acc = tmem + buf * kMaxNT;
-            const uint32_t sums = ones_aside ? tmem + (buf ^ 1) * kMaxNT : acc + p.NT;
+            const uint32_t sums0 = ones_aside ? tmem + (buf ^ 1) * kMaxNT : acc + p.NT;
+            [[maybe_unused]] uint32_t sums = sums0;
             if (g >= 2 && !warp_wait(dfree_bar(buf), ((g >> 1) - 1) & 1, p.wait_ns)) {
               bad = 1;
               break;
@@ -589,6 +603,15 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
                 bad = 1;
                 break;
               }
+              const int of_sums = EPI == kEpiGrad16 ? (c - s0) % kSegChunks : c - s0;  // chunk of its segment
+              if (EPI == kEpiGrad16 && ones && of_sums == 0) {
+                if (q >= 2 && !warp_wait(sum_free_bar(q), ((q >> 1) - 1) & 1, p.wait_ns)) {
+                  bad = 1;
+                  break;
+                }
+                sums = sums0 + (q & 1) * kSumCols;
+                ++q;
+              }
               tc::fence_after_sync();
               const uint32_t a = a0 + st * stage_step, b = b0 + st * stage_step;
               if (elect_one()) {
@@ -596,9 +619,10 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
                 for (int kk = 0; kk < 4; ++kk) {
                   mma<CG>(acc, a + kk * kAStep, kHi, b + kk * kBStep, kHi, idesc, c > s0 || kk > 0);
                   if (kSums && ones)
-                    mma<CG>(sums, a + kk * kAStep, kHi, ones_lo, kOnesHi, idesc_ones, c > s0 || kk > 0);
+                    mma<CG>(sums, a + kk * kAStep, kHi, ones_lo, kOnesHi, idesc_ones, of_sums > 0 || kk > 0);
                 }
                 commit<CG>(empty_bar(st));
+                if (EPI == kEpiGrad16 && ones && (of_sums == kSegChunks - 1 || c == s1 - 1)) commit<CG>(sum_full_bar(q - 1));
 #ifdef SWIN_WATTN_FAULT_INJECTION
                 if (!(p.fault == kFaultGemm && g == 0))
 #endif
@@ -667,6 +691,7 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
     if (aux)
       for (int i = 0; i < max(NB - 2, 1); ++i) request_next();
     int g = 0, m = 0;                   // accumulations, slices of this warp
+    [[maybe_unused]] int q = 0;         // segments of kEpiGrad16's sums
     int tile = 0;                       // the slice's staging tile
     uint32_t aux_phase = 0;             // of that tile's barrier
     for (int it = group; it < p.n_items && !bad; it += n_groups) {
@@ -692,8 +717,35 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
           for (int e = 0; e < 32; ++e) seg_sum[i][e] = 0.0f;
       }
       float ones_sum = 0.0f;
-      const bool ones = kSums && p.k_sums != nullptr && w.nt == 0 && part == 0 && row0 < p.M;
+      const bool adds_ones = kSums && p.k_sums != nullptr && w.nt == 0 && part == 0, ones = adds_ones && row0 < p.M;
       int buf = g & 1;
+      const uint32_t sums = trow + (sums_aside ? (buf ^ 1) * kMaxNT : buf * kMaxNT + p.NT);  // of a single segment's tile
+      if constexpr (EPI == kEpiGrad16) {
+        // ahead of the product, which does not wait for more than two of them
+        if (adds_ones) {
+          for (int c = w.c0; c < w.c1; c += kSegChunks, ++q) {
+            if (!warp_wait(sum_full_bar(q), (q >> 1) & 1, p.wait_ns)) {
+              bad = 1;
+              break;
+            }
+            tc::fence_after_sync();
+            uint32_t s;
+            tc::ld1_nowait(sums + (q & 1) * kSumCols, s);
+            tc::wait_ld_then();
+            tc::dep1(s);
+            ones_sum += __uint_as_float(s);
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (CG == 2)
+                arrive_cluster(map_to_rank(sum_free_bar(q), 0));
+              else
+                tc::mbar_arrive(sum_free_bar(q));
+            }
+          }
+          if (bad) break;
+        }
+      }
       auto release = [&]() {
         tc::fence_before_sync();
         __syncwarp();
@@ -717,9 +769,9 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
           for (int i = 0; i < kSlices; ++i) sbias[kPerQuad * kSC * i + lane] = bt[i];
           __syncwarp();
         }
-        if (ones) {
+        if (EPI == kEpiGrad32 && ones) {
           uint32_t s;
-          tc::ld1_nowait(trow + (p.NT + 16 * CG > kMaxNT ? (buf ^ 1) * kMaxNT : buf * kMaxNT + p.NT), s);
+          tc::ld1_nowait(trow + (sums_aside ? (buf ^ 1) * kMaxNT : buf * kMaxNT + p.NT), s);
           tc::wait_ld_then();
           tc::dep1(s);
           ones_sum += __uint_as_float(s);
