@@ -284,8 +284,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t mbar, uint32_t parity, uint64
 //   parabola, so h = 2^Q(t) with Q of degree 6, fitted (minimax, iteratively reweighted
 //   least squares) on [0, 6]: |h / Phi(-t) - 1| < 5e-5 there, |t h - t Phi(-t)| < 7e-6
 //   everywhere, a fortieth of a bf16 rounding; six multiply-adds and one exponential where
-//   erff takes some twenty instructions. Q falls monotonically up to t = 12, where
-//   t is cut (t h < 1e-30), which also keeps infinities out of the polynomial.
+//   erff takes some twenty instructions. Q falls monotonically up to t = 15, where
+//   t is cut, which also keeps infinities out of the polynomial; 2^Q is below the smallest normal
+//   fp32, and so 0, from t = 13.9 on.
 // * tanh-GELU: 0.5 (1 + tanh u) = 1 / (1 + exp(-2u)), so h = 1 / (1 + exp(2 u(t))).
 // * SiLU: h = 1 / (1 + exp(t)).
 // t is cut at 100 there: exp overflows to infinity and h is 0 long before.
@@ -314,7 +315,7 @@ __device__ __forceinline__ float fast_rcp(float x) {
 }
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 
-constexpr float kGeluCut = 12.0f, kSigmoidCut = 100.0f;
+constexpr float kGeluCut = 15.0f, kSigmoidCut = 100.0f;
 constexpr float kTanhA = 0.7978845608028654f, kTanhB = 0.044715f;  // u(z) = A (z + B z^3)
 
 // t = min(|z|, cut), NaN kept, and h(t), for two values.
