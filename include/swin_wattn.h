@@ -301,7 +301,9 @@ int swin_wattn_proj_residual(const void* o, const void* w_proj, const float* b_p
  *   status   optional device int (may be NULL): bit 0 is OR-ed in if a bounded device wait
  *            ran out (then the results are not valid).
  * The product is accumulated in fp32 on the bf16 operands; bias, activation and residual are
- * applied in fp32 and each result is rounded once. One kernel launch on `stream`; nothing is
+ * applied in fp32 and each result is rounded once. Activations are a fit or hardware exponentials
+ * in fp32: GELU is off by at most 7e-6, and by 5e-5 of itself for z < 0 down to -6, the others by
+ * 2e-6; NaN gives NaN, +inf gives +inf, -inf gives 0. One kernel launch on `stream`; nothing is
  * allocated. Deterministic. Errors: INVALID_ARG for negative tokens, an unknown act, overlapping
  * buffers, or a pointer that is not memory of the current device; MISALIGNED for a pointer
  * off its alignment; UNSUPPORTED for K, N or tokens out of range.
@@ -318,7 +320,9 @@ int swin_wattn_linear(const void* x, const void* w, const float* b, const void* 
  *   dx   bf16 [tokens, K], written. dx may be the pre buffer itself but must not overlap dy
  *        or w.
  * With act NONE, dx = dy W is the gradient of x; with an activation, of the pre-activation
- * that x = act(pre) came from. Sizes, status, arithmetic and errors as for swin_wattn_linear.
+ * that x = act(pre) came from. act' is off by at most 3e-5 for GELU, which shows beside the rounding
+ * to bf16 only where act' is near zero (z = -0.75), and by 4e-6 for the others; ReLU's is 0 at 0 and
+ * at NaN. Sizes, status, arithmetic and errors as for swin_wattn_linear.
  * One launch.
  */
 int swin_wattn_linear_bwd_data(const void* dy, const void* w, const void* pre, void* dx, int tokens, int K, int N,
