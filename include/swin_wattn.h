@@ -277,6 +277,10 @@ int swin_wattn_qkv_proj_prepared_fp8(const void* x, const void* prepared, void* 
  * launch on `stream`; nothing is allocated. Errors: INVALID_ARG for negative tokens,
  * overlapping o and y, or a pointer that is not device memory; MISALIGNED for a pointer
  * off its alignment; UNSUPPORTED for C.
+ * swin_wattn_linear(o, w_proj, b_proj, residual, y, NULL, tokens, C, C, SWIN_WATTN_ACT_NONE, ...)
+ * computes the same, for any C that is a multiple of 8, and is the one to call in new code: it takes
+ * as long or less (49 x 768 6.2 against 9.3 us, 3136 x 768 8.6 against 10.3, 50176 x 192 14.5
+ * against 14.4). This one stays for its callers.
  */
 int swin_wattn_proj_residual(const void* o, const void* w_proj, const float* b_proj, const void* residual,
                              void* y, int tokens, int C, int* status, struct CUstream_st* stream);
@@ -305,8 +309,9 @@ int swin_wattn_proj_residual(const void* o, const void* w_proj, const float* b_p
  * in fp32: GELU is off by at most 7e-6, and by 5e-5 of itself for z < 0 down to -6, the others by
  * 2e-6; NaN gives NaN, +inf gives +inf, -inf gives 0. One kernel launch on `stream`; nothing is
  * allocated. Deterministic. Errors: INVALID_ARG for negative tokens, an unknown act, overlapping
- * buffers, or a pointer that is not memory of the current device; MISALIGNED for a pointer
- * off its alignment; UNSUPPORTED for K, N or tokens out of range.
+ * buffers, or a pointer that the current device cannot address as its own (another device's
+ * memory, host memory that is not mapped); MISALIGNED for a pointer off its alignment;
+ * UNSUPPORTED for K, N or tokens out of range.
  */
 int swin_wattn_linear(const void* x, const void* w, const float* b, const void* residual, void* y, void* pre,
                       int tokens, int K, int N, int act, int* status, struct CUstream_st* stream);
@@ -341,7 +346,9 @@ int swin_wattn_linear_bwd_data(const void* dy, const void* w, const void* pre, v
  *        swin_wattn_linear_bwd_weight_workspace_bytes(tokens, K, N) bytes, 256-byte aligned,
  *        overwritten (partial results of groups of tokens); one call at a time per workspace,
  *        and none of the other buffers.
- * Summed in fp32, in an order that depends on the sizes alone: deterministic. One or two
+ * Summed in fp32, in an order that depends on the sizes alone: deterministic. (512 tokens at a time
+ * by the tensor cores, whose additions truncate, these rounded to nearest: fp32 results are off by
+ * 5e-7 of random sums, relative 2-norm, and by up to 2e-6 where all terms have one sign.) One or two
  * launches; nothing is allocated. dw, db and workspace must not overlap the inputs or one
  * another. Sizes, status and errors as for swin_wattn_linear (INVALID_ARG also for a small
  * workspace or an unknown dtype). The size query returns 0 for unsupported arguments.
@@ -382,10 +389,10 @@ int swin_wattn_linear_bwd_weight(const void* dy, const void* x, void* dw, float*
  * with a NaN or an infinity gives NaN and leaves the others of the stack alone; a zero matrix
  * gives zeros.
  * One launch where the smaller side is at most 128 and the larger at most 2048, else
- * 2 + 3 * steps, or 2 + 4 * steps where the longer side is split; nothing is allocated. Deterministic. Errors: INVALID_ARG for the
- * scalars, overlaps, a small workspace or a pointer that is not memory of the current
- * device; MISALIGNED; UNSUPPORTED for sizes out of range. The size query returns 0 for
- * unsupported arguments.
+ * 2 + 3 * steps, or 2 + 4 * steps where the longer side is split; nothing is allocated.
+ * Deterministic. Errors: INVALID_ARG for the scalars, overlaps, a small workspace or a pointer
+ * that the current device cannot address as its own; MISALIGNED; UNSUPPORTED for sizes out of
+ * range. The size query returns 0 for unsupported arguments.
  */
 size_t swin_wattn_orthogonalize_workspace_bytes(int count, int rows, int cols);
 int swin_wattn_orthogonalize(const void* g, void* out, int count, int rows, int cols, int dtype, int steps, float eps,
