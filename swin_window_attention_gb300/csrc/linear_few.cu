@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
     cluster_sync_all();
   else
     __syncthreads();
-  // This CTA finishes the tokens rank, rank + S, ... of the tile: two warps per 32 output
+  // This CTA finishes the tokens rank, rank + S, ... of the tile: four warps per 32 output
   // channels in turn, kBatch tokens at a time with their loads in flight together.
   if (!bad) {
     constexpr int kBatch = 8;

@@ -25,7 +25,8 @@
 // at full rate at NT = 256 (shared memory is both filled and read by the chunk).
 //
 // What bounds it, measured on one GB300 (of the measured 6797 GB/s and 1865 TFLOP/s): wide products
-// the tensor cores (12561 x 6144 x 1536 with residual: 127.5 us, 1.00; 8192^3: 599 us, 0.98);
+// the tensor cores (12561 x 6144 x 1536 with residual: 127.5 us, 1.00, of calls one after the other
+// 147 us, 0.86, at the power limit; 8192^3: 599 us, 0.98);
 // narrow K the memory (50176 x 192 x 768, two results: 31.5 us, 0.81); short K with a slope
 // epilogue the epilogue warps' issue (12544 x 512 -> 2048: 34.9 us, 0.50, of which the last of six
 // rounds of tiles is a sixth full); the smallest launches latency, some 3.5 us from one launch to
@@ -981,8 +982,7 @@ __global__ void __launch_bounds__(n_threads(EPI), 1)
             for (int r = 0; r < 32 && row0 + r < p.M; ++r)
               p.raw_out[((int64_t)w.b * p.M + row0 + r) * p.N + col] = *reinterpret_cast<const __nv_bfloat16*>(
                   so + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
-          tc::fence_proxy_async();  // before a load writes the tile
-          __syncwarp();
+          __syncwarp();  // every lane has read the tile
         } else {
           tc::fence_proxy_async();  // the staging tile to the copy engine
           __syncwarp();
@@ -1113,7 +1113,9 @@ inline double chunk_clocks(int NT, int cg, bool bmn) {
   return std::max({2.0 * NT, 200.0, 2.4 * (kBM + b_rows(NT, cg, bmn))});
 }
 // `extra` columns beside a tile's hold the sums over K; where they lie in the other accumulator
-// every segment of an fp32 result waits for the last one's epilogue, some 2000 clocks.
+// every segment of an fp32 result waits for the last one's epilogue, some 2000 clocks. (Of several
+// columns of tiles only the first pays that, which is not charged: 12544 x 1536 x 6144 takes 167 us
+// with the sums, 157 us without.)
 inline double tiling_cost(const Tiling& t, int64_t M, int64_t N, int batch, bool bmn, bool sums) {
   const int64_t items = (int64_t)t.per_matrix * t.splits * batch;
   const int64_t groups = kSms / t.cg;
