@@ -5,8 +5,8 @@ import pytest
 import torch
 
 from swin_window_attention_gb300 import capi
-from tests.linear_util import orthogonalize64
-from tests.orthogonalize_util import assert_update, matrix
+from tests.linear_util import HALF_BF16, NS, orthogonalize64
+from tests.orthogonalize_util import BOUND, assert_update, matrix
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -96,3 +96,23 @@ def test_few_rows(m, n):
         g = matrix(kind, m, n, seed=m)
         assert_update(_run(g), g, orthogonalize64(g, 5), 5, bound=6e-3 if min(m, n) < 32 else 4e-3,
                       model=False)
+
+
+def test_largest_matrix():
+    """One step of the largest sides, on sampled rows: with y = x_r X^T, row r of A, the result's row is
+    a x_r + b y X + c ((y X) X^T) X."""
+    a, b, c = NS
+    n = 16384
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    g = torch.randn(n, n, generator=gen, device=DEV)
+    out = capi.orthogonalize(g, steps=1, status=(st := torch.zeros(1, dtype=torch.int32, device=DEV)))
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    rows = torch.tensor([0, 1, 255, 256, 8191, 12345, 16383], device=DEV)
+    x = g.double()
+    x /= x.norm()
+    xr = x[rows]
+    z = (xr @ x.T) @ x
+    exact = a * xr + b * z + c * ((z @ x.T) @ x)
+    err = (out[rows].double() - exact).norm(dim=1) / exact.norm(dim=1)
+    assert float(err.max()) <= BOUND + HALF_BF16 * (1.0 + BOUND)
