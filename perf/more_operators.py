@@ -4,7 +4,7 @@ What a Swin block needs beside its attention and its products, in training and i
 
 * ``block_norm``: the residual sum of a block with its gate, its stochastic depth and the norms
   before and after it; ``block_norm_bwd``: its gradients;
-* ``clip_grad_norm``: the norm over all gradients of a model, and their clipping;
+* ``GradClip``: the norm over all gradients of a model, and their clipping;
 * ``quantize_fp4``, ``dequantize_fp4``: microscaled 4-bit operands (NVFP4: blocks of 16 with an
   E4M3 scale and a scale of the tensor, a power of two where it is not given; MXFP4: blocks of 32
   with a power of two), and back;
@@ -174,6 +174,9 @@ def prepare(case, seed):
         st["out"] = [torch.empty_like(f) for f in st["flat"]]
         st["grads"] = [t for f, n in zip(st["flat"], (mats, vecs)) for t in torch.split(f, n)]
         st["clipped"] = [t for f, n in zip(st["out"], (mats, vecs)) for t in torch.split(f, n)]
+        if own:
+            from swin_window_attention_gb300 import capi
+            st["clip"] = capi.GradClip(st["grads"], out=st["clipped"])
         return st
     if case["op"] == "round_trip":
         st["x"] = normal(case["rows"], case["K"], std=case["std"], dtype=_DT[case["dtype"]])
@@ -215,7 +218,7 @@ def _run_own(st):
                                             workspace=st["workspace"])
         return _given(dx, df, *(grads.get(k) for k in ("pre_weight", "pre_bias", "post_weight", "post_bias", "gate")))
     if case["op"] == "clip":
-        norm = capi.clip_grad_norm(st["grads"], case["max_norm"], out=st["clipped"])
+        norm = st["clip"](case["max_norm"])
         return [*st["out"], norm]
     if case["op"] == "round_trip":
         q = capi.quantize_fp4(st["x"], case["format"])
