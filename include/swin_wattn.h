@@ -85,6 +85,16 @@ enum swin_wattn_activation {
   SWIN_WATTN_ACT_SILU = 4       /* z / (1 + exp(-z)) */
 };
 
+/* Norms of swin_wattn_block_norm, and formats of the 4-bit operands. */
+enum swin_wattn_norm {
+  SWIN_WATTN_NORM_LAYER = 0, /* (v - mean) / sqrt(var + eps) */
+  SWIN_WATTN_NORM_RMS = 1    /* v / sqrt(mean of v^2 + eps) */
+};
+enum swin_wattn_fp4_format {
+  SWIN_WATTN_NVFP4 = 0, /* blocks of 16 with an E4M3 scale, and one fp32 scale of the tensor */
+  SWIN_WATTN_MXFP4 = 1  /* blocks of 32 with a power of two (E8M0) */
+};
+
 /*
  * Create a plan for one layer shape and run the preprocessing on `stream`:
  * the dense bias [nH, M^2, M^2] is expanded from `bias_table` (the lookup done once, as
@@ -398,6 +408,120 @@ size_t swin_wattn_orthogonalize_workspace_bytes(int count, int rows, int cols);
 int swin_wattn_orthogonalize(const void* g, void* out, int count, int rows, int cols, int dtype, int steps, float eps,
                              float scale, void* workspace, size_t workspace_bytes, int* status,
                              struct CUstream_st* stream);
+
+/*
+ * The residual sum around a block, with its gate, its stochastic depth and the norms on both sides
+ * (NVIDIA Swin talk, section 1: a block's LayerNorm and shortcut):
+ *   u = post(f), or f without post;   y = alpha x + keep[sample] gate[channel] u;   h = pre(y)
+ * pre is the norm before the next block (its output feeds that block's products), post the norm after
+ * this one. norm(v) = vhat w + b, vhat by `kind` (SWIN_WATTN_NORM_*) over the C channels of a token.
+ *   x      [tokens, C], the residual stream, bf16 or fp32 by `dtype`;
+ *   f      bf16 [tokens, C], the block's output, or NULL: then h = pre(x), and y, post_*, gate
+ *          and keep are NULL and alpha is not used;
+ *   pre_w, pre_b, post_w, post_b  fp32 [C], 4-byte aligned; pre_w NULL: no pre norm (h is not
+ *          written); post_w NULL: no post norm; pre_b, post_b NULL: no bias;
+ *   gate   fp32 [C] or NULL (1);   keep  fp32 [samples] or NULL (1): a factor for each run of
+ *          tokens / samples tokens (stochastic depth: 0, or 1 / the probability of keeping);
+ *   y      [tokens, C] of x's dtype, written; may be x itself;
+ *   h      bf16 [tokens, C], written; overlaps nothing;
+ *   tokens in [0, 2^31 - 1024] (0: nothing is done); C a multiple of 8 in [8, 8192]; samples divides tokens;
+ *   alpha, eps finite, eps a normal number above 0.
+ * Device pointers of the current device, 16-byte aligned unless stated. Arithmetic in fp32: the mean is
+ * taken out before squares are summed; h is normalised from y before y is rounded. Squares are summed in
+ * fp32: rows are right while C times the largest square is below 3e38. NaN and infinities stay in
+ * their token (0 * NaN is NaN: a dropped sample's f counts). One launch, deterministic, nothing is allocated.
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED (C or tokens out of range).
+ */
+int swin_wattn_block_norm(const void* x, const void* f, const float* pre_w, const float* pre_b, const float* post_w,
+                          const float* post_b, const float* gate, const float* keep, void* y, void* h, int tokens, int C,
+                          int samples, int dtype, int kind, float alpha, float eps, struct CUstream_st* stream);
+
+/*
+ * Its gradients, for the gradients dh of h and dy of y (that of y's other uses):
+ *   y      the forward's y (or x, without f); f, pre_w, post_w, post_b, gate, keep, alpha, kind, eps as there;
+ *   dh     bf16 [tokens, C]; NULL exactly where pre_w is;
+ *   dy     [tokens, C] of the stream's dtype, or NULL for none;
+ *   dx     [tokens, C] of the stream's dtype, written; may be dy itself;
+ *   df     bf16 [tokens, C], written; NULL exactly where f is;
+ *   dpre_w, dpre_b, dpost_w, dpost_b, dgate  fp32 [C], written or added to (accumulate); NULL: not
+ *          computed. Only those of what is there may be given;
+ *   workspace  at least swin_wattn_block_norm_bwd_workspace_bytes(tokens, C) bytes, 256-byte aligned,
+ *          overwritten; one call at a time per workspace.
+ * With no tokens the parameter gradients are zeroed (left as they are when accumulating). The channel sums are
+ * taken in fp32 in an order that depends on the sizes alone: deterministic. Two launches (one without
+ * parameter gradients); nothing is allocated.
+ */
+size_t swin_wattn_block_norm_bwd_workspace_bytes(int tokens, int C);
+int swin_wattn_block_norm_bwd(const void* y, const void* f, const void* dh, const void* dy, const float* pre_w,
+                              const float* post_w, const float* post_b, const float* gate, const float* keep, void* dx,
+                              void* df, float* dpre_w, float* dpre_b, float* dpost_w, float* dpost_b, float* dgate,
+                              int tokens, int C, int samples, int dtype, int kind, float alpha, float eps, int accumulate,
+                              void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
+
+/*
+ * The norm over all gradients of a model and their clipping, between the gradients and the weight updates:
+ *   n = scale * sqrt(sum of g^2 over all tensors),   out = g * scale * min(1, max_norm / (n + eps))
+ * swin_wattn_clip_plan looks at the tensors once and keeps their addresses and sizes (on the host); the tensors
+ * have to stay where they are while the plan is used, their values may change.
+ *   grads, outs  `count` device pointers each, at any multiple of their element size; outs[i] may be
+ *          grads[i] itself (in place), else it overlaps nothing; no tensor may be written twice;
+ *   sizes  elements of each (0: the tensor is skipped); dtypes  SWIN_WATTN_FP32 or SWIN_WATTN_BF16 of each.
+ * swin_wattn_clip_grad_norm runs it: norm (device fp32, or NULL) receives n; max_norm >= 0, scale > 0 and
+ * eps >= 0, finite; workspace at least swin_wattn_clip_workspace_bytes(plan) bytes, 256-byte aligned,
+ * overwritten, one call at a time per workspace. The squares are summed in 64 bits (fp32 within 64 bytes),
+ * in an order that depends on the sizes alone: deterministic, without overflow. A NaN anywhere makes n and every
+ * out NaN; an infinity makes n infinite, the finite values 0 and itself NaN. Two launches for each 1024 tensors;
+ * where all are in place and their factor is 1 nothing is written. Errors: BAD_PLAN; INVALID_ARG, MISALIGNED as
+ * above; INVALID_ARG also where the plan's device is not the current one.
+ */
+typedef struct swin_wattn_clip_s* swin_wattn_clip_t;
+int swin_wattn_clip_plan(swin_wattn_clip_t* plan, const void* const* grads, void* const* outs, const int64_t* sizes,
+                         const int* dtypes, int count);
+size_t swin_wattn_clip_workspace_bytes(swin_wattn_clip_t plan);
+int swin_wattn_clip_grad_norm(swin_wattn_clip_t plan, float max_norm, float scale, float eps, float* norm, void* workspace,
+                              size_t workspace_bytes, struct CUstream_st* stream);
+int swin_wattn_clip_destroy(swin_wattn_clip_t plan);
+
+/*
+ * Microscaled 4-bit operands: E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two to a byte, the
+ * even one in the low half, rows of K / 2 bytes; and a scale for each block of a row, by `format`:
+ *   NVFP4: s = E4M3(amax / 6 / ts), q = E2M1(x / (s ts)), blocks of 16, ts the tensor's scale;
+ *   MXFP4: s = 2^(floor(log2 amax) - 2), at least 2^-127, q = E2M1(x / s), blocks of 32 (OCP MX);
+ * amax the block's largest magnitude; to nearest, ties to even, saturated. A block with a NaN or an
+ * infinity gets a NaN scale and reads back as NaN.
+ * The scales lie in tiles of 128 rows by 4 blocks, as the tensor core reads them: row r and block j of tile
+ * (R, J) at byte (R * ceil(blocks / 4) + J) * 512 + (r % 32) * 16 + (r / 32) * 4 + j; rows and blocks past the end
+ * hold zeros. swin_wattn_fp4_scale_bytes gives their size (0: unsupported sizes).
+ *   x      [rows, K], fp32 or bf16 by `dtype`; codes [rows, K / 2] bytes, written; scales, written;
+ *   tensor_scale  NVFP4: device fp32. scale_given: read, between 2^-100 and 2^100; else written: the
+ *          smallest power of two with max |x| <= 2688 ts (finite x; at least 2^-90), with which every rounding is
+ *          that of the exact quotient and every value read back is exact in bf16. MXFP4: NULL;
+ *   rows   in [0, 2^31 - 1024]; K a multiple of 32 in [32, 32768];
+ *   workspace  needed for a scale that is not given: swin_wattn_fp4_workspace_bytes() bytes, 256-byte
+ *          aligned, overwritten, one call at a time per workspace.
+ * swin_wattn_fp4_dequantize reads them back: out [rows, K], fp32 or bf16 by `dtype`, one rounding each.
+ * Device pointers of the current device, 16-byte aligned (tensor_scale 4). One launch, or two for a scale that is
+ * not given; deterministic; nothing is allocated.
+ */
+size_t swin_wattn_fp4_scale_bytes(int rows, int K, int format);
+size_t swin_wattn_fp4_workspace_bytes(void);
+int swin_wattn_fp4_quantize(const void* x, void* codes, void* scales, float* tensor_scale, int rows, int K, int format,
+                            int dtype, int scale_given, void* workspace, size_t workspace_bytes,
+                            struct CUstream_st* stream);
+int swin_wattn_fp4_dequantize(const void* codes, const void* scales, const float* tensor_scale, void* out, int rows, int K,
+                              int format, int dtype, struct CUstream_st* stream);
+
+/*
+ * A dense layer on such operands (swin_wattn_linear's, for serving):
+ *   y = residual + act(ts_x ts_w sum over k of (q_x s_x)(q_w s_w) + b)
+ * x [tokens, K] and w [N, K] as codes, scales and tensor scales of one format (tensor scales NULL for MXFP4); b,
+ * residual, y, act and status as for swin_wattn_linear; y must not overlap the operands.
+ * K a multiple of 32, N a multiple of 8, up to 32768. The tensor cores multiply the 4-bit values with their block
+ * scales and accumulate in fp32; the rest is fp32, y is rounded once. One launch; deterministic.
+ */
+int swin_wattn_linear_fp4(const void* x_codes, const void* x_scales, const float* x_tensor_scale, const void* w_codes,
+                          const void* w_scales, const float* w_tensor_scale, const float* b, const void* residual, void* y,
+                          int tokens, int K, int N, int format, int act, int* status, struct CUstream_st* stream);
 
 /*
  * Forward on 8-bit operands (7x7 windows, a SWIN_WATTN_BF16 plan): the attention of

@@ -34,6 +34,12 @@ ACT_RELU = 1
 ACT_GELU = 2
 ACT_GELU_TANH = 3
 ACT_SILU = 4
+NORM_LAYER = 0
+NORM_RMS = 1
+NORMS = {"layer": NORM_LAYER, "rms": NORM_RMS}
+NVFP4 = 0
+MXFP4 = 1
+FP4_FORMATS = {"nvfp4": NVFP4, "mxfp4": MXFP4}
 ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
 
 # Every symbol include/swin_wattn.h declares, with (argtypes, restype).
@@ -61,6 +67,18 @@ SIGNATURES = {
     "swin_wattn_linear_bwd_weight": ([_vp] * 4 + [_i] * 5 + [_vp, ctypes.c_size_t, _vp, _vp], _i),
     "swin_wattn_orthogonalize_workspace_bytes": ([_i] * 3, ctypes.c_size_t),
     "swin_wattn_orthogonalize": ([_vp, _vp] + [_i] * 5 + [ctypes.c_float] * 2 + [_vp, ctypes.c_size_t, _vp, _vp], _i),
+    "swin_wattn_block_norm": ([_vp] * 10 + [_i] * 5 + [ctypes.c_float] * 2 + [_vp], _i),
+    "swin_wattn_block_norm_bwd_workspace_bytes": ([_i] * 2, ctypes.c_size_t),
+    "swin_wattn_block_norm_bwd": ([_vp] * 16 + [_i] * 5 + [ctypes.c_float] * 2 + [_i, _vp, ctypes.c_size_t, _vp], _i),
+    "swin_wattn_clip_plan": ([ctypes.POINTER(_vp)] + [_vp] * 4 + [_i], _i),
+    "swin_wattn_clip_workspace_bytes": ([_vp], ctypes.c_size_t),
+    "swin_wattn_clip_grad_norm": ([_vp] + [ctypes.c_float] * 3 + [_vp, _vp, ctypes.c_size_t, _vp], _i),
+    "swin_wattn_clip_destroy": ([_vp], _i),
+    "swin_wattn_fp4_scale_bytes": ([_i] * 3, ctypes.c_size_t),
+    "swin_wattn_fp4_workspace_bytes": ([], ctypes.c_size_t),
+    "swin_wattn_fp4_quantize": ([_vp] * 4 + [_i] * 5 + [_vp, ctypes.c_size_t, _vp], _i),
+    "swin_wattn_fp4_dequantize": ([_vp] * 4 + [_i] * 4 + [_vp], _i),
+    "swin_wattn_linear_fp4": ([_vp] * 9 + [_i] * 5 + [_vp, _vp], _i),
     "swin_wattn_fwd_fp8": ([_vp, _vp, ctypes.c_float, ctypes.c_float, ctypes.c_float, _vp, _vp], _i),
     "swin_wattn_set_fwd_kernel": ([_vp, _i], _i),
     "swin_wattn_fwd_kernel": ([_vp], _i),
@@ -325,6 +343,70 @@ def swin_wattn_orthogonalize(g_ptr, out_ptr, count, rows, cols, dtype, steps, ep
                                            workspace_bytes, status_ptr, stream)
 
 
+def swin_wattn_block_norm(x_ptr, f_ptr, pre_w_ptr, pre_b_ptr, post_w_ptr, post_b_ptr, gate_ptr, keep_ptr, y_ptr, h_ptr,
+                          tokens, C, samples, dtype, kind, alpha, eps, stream):
+    return load().swin_wattn_block_norm(x_ptr, f_ptr, pre_w_ptr, pre_b_ptr, post_w_ptr, post_b_ptr, gate_ptr, keep_ptr,
+                                        y_ptr, h_ptr, tokens, C, samples, dtype, kind, alpha, eps, stream)
+
+
+def swin_wattn_block_norm_bwd_workspace_bytes(tokens, C):
+    return int(load().swin_wattn_block_norm_bwd_workspace_bytes(tokens, C))
+
+
+def swin_wattn_block_norm_bwd(y_ptr, f_ptr, dh_ptr, dy_ptr, pre_w_ptr, post_w_ptr, post_b_ptr, gate_ptr, keep_ptr, dx_ptr,
+                              df_ptr, dpre_w_ptr, dpre_b_ptr, dpost_w_ptr, dpost_b_ptr, dgate_ptr, tokens, C, samples,
+                              dtype, kind, alpha, eps, accumulate, workspace_ptr, workspace_bytes, stream):
+    return load().swin_wattn_block_norm_bwd(y_ptr, f_ptr, dh_ptr, dy_ptr, pre_w_ptr, post_w_ptr, post_b_ptr, gate_ptr,
+                                            keep_ptr, dx_ptr, df_ptr, dpre_w_ptr, dpre_b_ptr, dpost_w_ptr, dpost_b_ptr,
+                                            dgate_ptr, tokens, C, samples, dtype, kind, alpha, eps, accumulate,
+                                            workspace_ptr, workspace_bytes, stream)
+
+
+def swin_wattn_clip_plan(grad_ptrs, out_ptrs, sizes, dtypes):
+    """Returns (status, plan handle or None) for lists of device pointers, sizes and dtype codes."""
+    n, h = len(grad_ptrs), _vp()
+    rc = load().swin_wattn_clip_plan(ctypes.byref(h), (_vp * n)(*grad_ptrs), (_vp * n)(*out_ptrs),
+                                     (ctypes.c_int64 * n)(*sizes), (_i * n)(*dtypes), n)
+    return rc, (h.value if rc == OK else None)
+
+
+def swin_wattn_clip_workspace_bytes(plan):
+    return int(load().swin_wattn_clip_workspace_bytes(plan))
+
+
+def swin_wattn_clip_grad_norm(plan, max_norm, scale, eps, norm_ptr, workspace_ptr, workspace_bytes, stream):
+    return load().swin_wattn_clip_grad_norm(plan, max_norm, scale, eps, norm_ptr, workspace_ptr, workspace_bytes, stream)
+
+
+def swin_wattn_clip_destroy(plan):
+    return load().swin_wattn_clip_destroy(plan)
+
+
+def swin_wattn_fp4_scale_bytes(rows, K, format):
+    return int(load().swin_wattn_fp4_scale_bytes(rows, K, format))
+
+
+def swin_wattn_fp4_workspace_bytes():
+    return int(load().swin_wattn_fp4_workspace_bytes())
+
+
+def swin_wattn_fp4_quantize(x_ptr, codes_ptr, scales_ptr, tensor_scale_ptr, rows, K, format, dtype, scale_given,
+                            workspace_ptr, workspace_bytes, stream):
+    return load().swin_wattn_fp4_quantize(x_ptr, codes_ptr, scales_ptr, tensor_scale_ptr, rows, K, format, dtype,
+                                          scale_given, workspace_ptr, workspace_bytes, stream)
+
+
+def swin_wattn_fp4_dequantize(codes_ptr, scales_ptr, tensor_scale_ptr, out_ptr, rows, K, format, dtype, stream):
+    return load().swin_wattn_fp4_dequantize(codes_ptr, scales_ptr, tensor_scale_ptr, out_ptr, rows, K, format, dtype, stream)
+
+
+def swin_wattn_linear_fp4(x_codes_ptr, x_scales_ptr, x_tensor_scale_ptr, w_codes_ptr, w_scales_ptr, w_tensor_scale_ptr,
+                          b_ptr, residual_ptr, y_ptr, tokens, K, N, format, act, status_ptr, stream):
+    return load().swin_wattn_linear_fp4(x_codes_ptr, x_scales_ptr, x_tensor_scale_ptr, w_codes_ptr, w_scales_ptr,
+                                        w_tensor_scale_ptr, b_ptr, residual_ptr, y_ptr, tokens, K, N, format, act,
+                                        status_ptr, stream)
+
+
 # The wrappers of the MLP's products and the weight update check their tensors: a small product
 # is over in a few microseconds, so the checks compare attributes first and look for the
 # reason only when one differs.
@@ -525,6 +607,292 @@ def orthogonalize(g, steps=5, eps=1e-7, scale=1.0, out=None, workspace=None, sta
           _address("out", out, shape, _BF16, dev), count, rows, cols, code, steps, float(eps), float(scale),
           _plain("workspace", workspace, _U8, dev), workspace.numel())
     return out
+
+
+def _launch(fn, dev, stream, *args):
+    """The C function fn(*args, stream) as _call runs it, for those that take no status word."""
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if _one_device or _is_current(dev):
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
+    if rc != OK:
+        raise SwinWAttnError(fn.__name__, rc)
+
+
+def _kind_code(kind):
+    code = NORMS.get(kind) if type(kind) is str else kind
+    if code is None or not NORM_LAYER <= code <= NORM_RMS:
+        raise ValueError(f"unknown norm {kind!r}: one of {sorted(NORMS)} or a NORM_ code")
+    return code
+
+
+def _norm_params(name, wb, C, dev):
+    """The addresses of a norm's weight and bias, or of neither."""
+    if wb is None:
+        return None, None
+    w, b = wb
+    return (_address(name + " weight", w, (C,), _F32, dev),
+            None if b is None else _address(name + " bias", b, (C,), _F32, dev))
+
+
+def _block_shape(x, f, post, gate, keep, alpha):
+    """Sizes of a block_norm call, checked: device, shape, tokens, C, samples."""
+    dev, shape = _device_of("x", x), x.shape
+    if not shape:
+        raise ValueError("x has no dimensions")
+    C = shape[-1]
+    tokens = shape[0] if len(shape) == 2 else shape[:-1].numel()
+    if tokens > _INT_MAX or C > _INT_MAX:
+        raise _too_large(tokens, C)
+    if f is None and not (post is None and gate is None and keep is None and alpha == 1.0):
+        raise ValueError("post, gate, keep and alpha belong to a block: f is None")
+    samples = 0
+    if keep is not None:
+        samples = keep.numel()
+        if samples < 1 or tokens % samples:
+            raise ValueError(f"keep has {samples} samples, which do not divide {tokens} tokens")
+    return dev, shape, tokens, C, samples
+
+
+def block_norm(x, f=None, pre=None, post=None, gate=None, keep=None, alpha=1.0, kind="layer", eps=1e-5, y=None, h=None,
+               stream=None):
+    """The residual sum around a block and the norms on both sides: with u = post(f) (f without
+    post), y = alpha x + keep[sample] gate[channel] u and h = pre(y). x [..., C] is the residual
+    stream, a bf16 or fp32 CUDA tensor, f the block's output in bf16. pre and post: (weight, bias)
+    of the norm before the next block and after this one, fp32 [C], the bias may be None; gate fp32
+    [C]; keep fp32 [samples], for equal runs of tokens (stochastic depth). kind: "layer" or "rms".
+    Returns (y, h), y of x's dtype (into y, which may be x itself) or None without f, h in bf16 or
+    None without pre."""
+    dev, shape, tokens, C, samples = _block_shape(x, f, post, gate, keep, alpha)
+    code = _float_code("x", x)
+    if f is None and pre is None:
+        raise ValueError("neither f nor pre is given: there is nothing to do")
+    if (f is None and y is not None) or (pre is None and h is not None):
+        raise ValueError("y needs f, and h needs pre")
+    if f is not None and y is None:
+        y = _empty(shape, x.dtype, dev, stream)
+    if pre is not None and h is None:
+        h = _empty(shape, _BF16, dev, stream)
+    pre_w, pre_b = _norm_params("pre", pre, C, dev)
+    post_w, post_b = _norm_params("post", post, C, dev)
+    _launch((_lib or load()).swin_wattn_block_norm, dev, stream, _plain("x", x, x.dtype, dev),
+            None if f is None else _address("f", f, shape, _BF16, dev), pre_w, pre_b, post_w, post_b,
+            None if gate is None else _address("gate", gate, (C,), _F32, dev),
+            None if keep is None else _address("keep", keep, (samples,), _F32, dev),
+            None if y is None else _address("y", y, shape, x.dtype, dev),
+            None if h is None else _address("h", h, shape, _BF16, dev), tokens, C, samples, code, _kind_code(kind),
+            float(alpha), float(eps))
+    return y, h
+
+
+_NORM_GRADS = ("pre_weight", "pre_bias", "post_weight", "post_bias", "gate")
+
+
+def block_norm_bwd(y, f=None, dh=None, dy=None, pre=None, post=None, gate=None, keep=None, alpha=1.0, kind="layer",
+                   eps=1e-5, dx=None, df=None, grads=None, accumulate=False, workspace=None, stream=None):
+    """The gradients of block_norm, for dh (of h, bf16; exactly with pre) and dy (of y's other uses, of
+    y's dtype, or None). y is the forward's y (its x, without f); f, pre, post, gate, keep, alpha, kind and
+    eps are the forward's. Returns (dx, df, grads): dx of y's dtype (into dx, which may be dy itself),
+    df in bf16 or None without f, and a dict of the fp32 gradients of the parameters that are there:
+    "pre_weight", "pre_bias", "post_weight", "post_bias", "gate". grads, such a dict: only these are
+    computed, written there, or with accumulate added to. workspace: a uint8 tensor of
+    swin_wattn_block_norm_bwd_workspace_bytes (allocated here when not given)."""
+    dev, shape, tokens, C, samples = _block_shape(y, f, post, gate, keep, alpha)
+    code = _float_code("y", y)
+    if (dh is None) != (pre is None):
+        raise ValueError("dh and pre belong together: one of them is None")
+    if dh is None and dy is None:
+        raise ValueError("neither dh nor dy is given: there is no gradient")
+    if f is None and df is not None:
+        raise ValueError("df needs f")
+    there = {"pre_weight": pre is not None, "pre_bias": pre is not None and pre[1] is not None,
+             "post_weight": post is not None, "post_bias": post is not None and post[1] is not None,
+             "gate": gate is not None}
+    if grads is None:
+        if accumulate:
+            raise ValueError("accumulate needs the grads to add to")
+        made = iter(_empty((sum(there.values()), C), _F32, dev, stream).unbind(0)) if any(there.values()) else None
+        grads = {k: next(made) for k in _NORM_GRADS if there[k]}
+    for k in grads:
+        if not there.get(k):
+            raise ValueError(f"grads has {k!r}, which the call has no parameter for")
+    if dx is None:
+        dx = _empty(shape, y.dtype, dev, stream)
+    if f is not None and df is None:
+        df = _empty(shape, _BF16, dev, stream)
+    if workspace is None:
+        workspace = _empty((max(swin_wattn_block_norm_bwd_workspace_bytes(tokens, C), 1),), _U8, dev, stream)
+    pre_w, _ = _norm_params("pre", pre, C, dev)
+    post_w, post_b = _norm_params("post", post, C, dev)
+    _launch((_lib or load()).swin_wattn_block_norm_bwd, dev, stream, _plain("y", y, y.dtype, dev),
+            None if f is None else _address("f", f, shape, _BF16, dev),
+            None if dh is None else _address("dh", dh, shape, _BF16, dev),
+            None if dy is None else _address("dy", dy, shape, y.dtype, dev), pre_w, post_w, post_b,
+            None if gate is None else _address("gate", gate, (C,), _F32, dev),
+            None if keep is None else _address("keep", keep, (samples,), _F32, dev),
+            _address("dx", dx, shape, y.dtype, dev), None if df is None else _address("df", df, shape, _BF16, dev),
+            *(None if k not in grads else _address(k, grads[k], (C,), _F32, dev) for k in _NORM_GRADS), tokens, C, samples,
+            code, _kind_code(kind), float(alpha), float(eps), 1 if accumulate else 0,
+            _plain("workspace", workspace, _U8, dev), workspace.numel())
+    return dx, df, grads
+
+
+class GradClip:
+    """Clipping by the norm over all gradients of a model: a plan over the fp32 and bf16 CUDA tensors
+    `grads` (of any sizes, contiguous), which are checked once and kept. Each call computes
+    n = scale |grads| and writes grads * scale * min(1, max_norm / (n + eps)) to `out`, tensors of the
+    same shapes and dtypes (the gradients themselves when not given). The plan's workspace serves one
+    stream at a time; a call may bring its own."""
+
+    handle = None
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if not self.grads:
+            raise ValueError("grads is empty")
+        if len(self.out) != len(self.grads):
+            raise ValueError(f"out has {len(self.out)} tensors, grads {len(self.grads)}")
+        self.dev = dev = _device_of("grads[0]", self.grads[0])
+        codes = [_float_code(f"grads[{i}]", g) for i, g in enumerate(self.grads)]
+        ins = [_plain(f"grads[{i}]", g, g.dtype, dev) for i, g in enumerate(self.grads)]
+        outs = [_address(f"out[{i}]", o, g.shape, g.dtype, dev) for i, (g, o) in enumerate(zip(self.grads, self.out))]
+        sizes = [g.numel() for g in self.grads]
+        with torch.cuda.device(dev):
+            rc, self.handle = swin_wattn_clip_plan(ins, outs, sizes, codes)
+        if rc != OK:
+            raise SwinWAttnError("swin_wattn_clip_plan", rc)
+        self.workspace = torch.empty(swin_wattn_clip_workspace_bytes(self.handle), dtype=_U8, device=dev)
+
+    def __call__(self, max_norm, scale=1.0, eps=1e-6, norm=None, workspace=None, stream=None):
+        """Clips; returns the norm n, an fp32 tensor [1] (into norm when given)."""
+        dev = self.dev
+        if norm is None:
+            norm = _empty((1,), _F32, dev, stream)
+        if workspace is None:
+            workspace = self.workspace
+        _launch((_lib or load()).swin_wattn_clip_grad_norm, dev, stream, self.handle, float(max_norm), float(scale), float(eps),
+                _address("norm", norm, (1,), _F32, dev), _plain("workspace", workspace, _U8, dev), workspace.numel())
+        return norm
+
+    def close(self):
+        if self.handle:
+            swin_wattn_clip_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Fp4Tensor:
+    """A matrix [..., K] in microscaled 4-bit floating point: `codes`, a uint8 tensor [..., K / 2]; `scales`,
+    a flat uint8 tensor in the tensor core's tiles; `tensor_scale`, fp32 [1], of NVFP4 (else None);
+    `format`, NVFP4 or MXFP4; `shape`, of the matrix."""
+
+    __slots__ = ("codes", "scales", "tensor_scale", "format", "shape")
+
+    def __init__(self, codes, scales, tensor_scale, format, shape):
+        self.codes, self.scales, self.tensor_scale, self.format, self.shape = codes, scales, tensor_scale, format, shape
+
+    def _addresses(self, name, dev):
+        """Addresses of codes, scales and tensor scale, checked; rows and K."""
+        shape = self.shape
+        K = shape[-1]
+        rows, packed = _leading(shape, K // 2)
+        if rows > _INT_MAX or K > _INT_MAX:
+            raise _too_large(rows, K)
+        size = _scale_bytes(rows, K, self.format)
+        return (_address(name + ".codes", self.codes, packed, _U8, dev), _address(name + ".scales", self.scales, (size,), _U8, dev),
+                None if self.tensor_scale is None else _address(name + ".tensor_scale", self.tensor_scale, (1,), _F32, dev)
+                ), rows, K
+
+
+def _format_code(format):
+    code = FP4_FORMATS.get(format) if type(format) is str else format
+    if code is None or not NVFP4 <= code <= MXFP4:
+        raise ValueError(f"unknown format {format!r}: one of {sorted(FP4_FORMATS)} or NVFP4, MXFP4")
+    return code
+
+
+def _scale_bytes(rows, K, format):
+    """swin_wattn_fp4_scale_bytes without a call."""
+    block = 32 if format else 16
+    return (rows + 127) // 128 * ((K // block + 3) // 4) * 512
+
+
+def quantize_fp4(x, format="nvfp4", scale=None, out=None, workspace=None, stream=None):
+    """The bf16 or fp32 CUDA tensor x [..., K] in microscaled 4-bit floating point, an Fp4Tensor (`out` when given):
+    "nvfp4", blocks of 16 with E4M3 scales and a scale of the tensor, or "mxfp4", blocks of 32 with powers
+    of two. scale, fp32 [1], is the tensor's scale of NVFP4, calibrated ahead of time; without it it is taken
+    from x. workspace: a uint8 tensor of swin_wattn_fp4_workspace_bytes (allocated here when it is needed)."""
+    dev, shape, fmt, code = _device_of("x", x), x.shape, _format_code(format), _float_code("x", x)
+    if not shape:
+        raise ValueError("x has no dimensions")
+    K = shape[-1]
+    rows, packed = _leading(shape, K // 2)
+    if rows > _INT_MAX or K > _INT_MAX:
+        raise _too_large(rows, K)
+    if fmt == MXFP4 and scale is not None:
+        raise ValueError("MXFP4 has no scale of the tensor")
+    own = fmt == NVFP4 and scale is None
+    if out is None:
+        ts = _empty((1,), _F32, dev, stream) if own else scale
+        out = Fp4Tensor(_empty(packed, _U8, dev, stream), _empty((_scale_bytes(rows, K, fmt),), _U8, dev, stream), ts, fmt, shape)
+    else:
+        if out.format != fmt or out.shape != shape:
+            raise ValueError(f"out is of format {out.format} and shape {tuple(out.shape)}, not {fmt} and {tuple(shape)}")
+        if scale is not None and out.tensor_scale is not scale:
+            raise ValueError("out.tensor_scale is not the given scale")
+    if own and workspace is None:
+        workspace = _empty((swin_wattn_fp4_workspace_bytes(),), _U8, dev, stream)
+    (codes, scales, ts), _, _ = out._addresses("out", dev)
+    _launch((_lib or load()).swin_wattn_fp4_quantize, dev, stream, _plain("x", x, x.dtype, dev), codes, scales, ts, rows, K,
+            fmt, code, 0 if own else 1, None if workspace is None else _plain("workspace", workspace, _U8, dev),
+            0 if workspace is None else workspace.numel())
+    return out
+
+
+def dequantize_fp4(q, dtype=torch.bfloat16, out=None, stream=None):
+    """The values that an Fp4Tensor stands for, in bf16 or fp32 (into `out` when given)."""
+    dev = _device_of("q.codes", q.codes)
+    if out is None:
+        out = _empty(q.shape, dtype, dev, stream)
+    code = _float_code("out", out)
+    (codes, scales, ts), rows, K = q._addresses("q", dev)
+    _launch((_lib or load()).swin_wattn_fp4_dequantize, dev, stream, codes, scales, ts,
+            _address("out", out, q.shape, out.dtype, dev), rows, K, q.format, code)
+    return out
+
+
+def linear_fp4(x, w, b=None, act=ACT_NONE, residual=None, x_scale=None, y=None, status=None, stream=None):
+    """residual + act(x W^T + b) on 4-bit operands: w [N, K] an Fp4Tensor (a weight quantised once), x [..., K] an
+    Fp4Tensor of the same format, or a bf16 or fp32 CUDA tensor, which is quantised here (x_scale: its tensor's
+    scale for NVFP4, fp32 [1], else taken from x). The rest as for linear; y is bf16 [..., N]."""
+    if not isinstance(x, Fp4Tensor):
+        x = quantize_fp4(x, w.format, scale=x_scale, stream=stream)
+    elif x_scale is not None:
+        raise ValueError("x is quantised: it has its own scale")
+    if x.format != w.format:
+        raise ValueError(f"x and w have the formats {x.format} and {w.format}")
+    dev = _device_of("x.codes", x.codes)
+    xs, ws = x.shape, w.shape
+    if len(ws) != 2 or xs[-1] != ws[1]:
+        raise ValueError(f"x and w have shapes {tuple(xs)} and {tuple(ws)}: not [..., K] and [N, K]")
+    (xc, xsc, xts), tokens, K = x._addresses("x", dev)
+    (wc, wsc, wts), N, _ = w._addresses("w", dev)
+    _, shape = _leading(xs, N)
+    if y is None:
+        y = _empty(shape, _BF16, dev, stream)
+    _call((_lib or load()).swin_wattn_linear_fp4, dev, stream, status, xc, xsc, xts, wc, wsc, wts,
+          None if b is None else _address("b", b, (N,), _F32, dev),
+          None if residual is None else _address("residual", residual, shape, _BF16, dev),
+          _address("y", y, shape, _BF16, dev), tokens, K, N, x.format, _act_code(act))
+    return y
 
 
 def swin_wattn_fwd_fp8(plan, qkv8_ptr, scale_q, scale_k, scale_v, out_ptr, stream):

@@ -1,5 +1,6 @@
 // C ABI of the swin_wattn library: argument validation, plan ownership, launches and
 // error surfacing. No exception, abort or trap crosses this boundary.
+#include <algorithm>
 #include <atomic>
 #include <cfloat>
 #include <cmath>
@@ -8,10 +9,13 @@
 #include <mutex>
 #include <new>
 #include <unordered_set>
+#include <vector>
 
 #include "common.cuh"
+#include "fp4.cuh"
 
 namespace swin {
+struct ClipTables;
 cudaError_t launch_bias_tables(const Plan& p, const float* table, bool with_mask, cudaStream_t st);
 bool fwd_fp8_applies(const Plan& pl);
 cudaError_t fwd_fp8_launch(const Plan& pl, const void* qkv8, float sq, float sk, float sv, void* out,
@@ -60,6 +64,28 @@ size_t orthogonalize_workspace_bytes(int count, int rows, int cols);
 int orthogonalize_launches(int count, int rows, int cols, int steps);
 cudaError_t orthogonalize_launch(const void* g, void* out, int count, int rows, int cols, int dtype, int steps,
                                  float eps, float scale, void* workspace, int* status, cudaStream_t st);
+cudaError_t block_norm_launch(const void* x, const void* f, const float* pre_w, const float* pre_b, const float* post_w,
+                              const float* post_b, const float* gate, const float* keep, void* y, void* h, int tokens,
+                              int C, int samples, int dtype, int kind, float alpha, float eps, cudaStream_t st);
+size_t block_norm_bwd_workspace_bytes(int tokens, int C);
+cudaError_t block_norm_bwd_launch(const void* y, const void* f, const void* dh, const void* dy, const float* pre_w,
+                                  const float* post_w, const float* post_b, const float* gate, const float* keep,
+                                  void* dx, void* df, float* dpre_w, float* dpre_b, float* dpost_w, float* dpost_b,
+                                  float* dgate, int tokens, int C, int samples, int dtype, int kind, float alpha,
+                                  float eps, int accumulate, void* workspace, cudaStream_t st);
+ClipTables* clip_tables_make(const void* const* in, void* const* out, const int64_t* sizes, const int* dtypes, int count);
+void clip_tables_free(ClipTables* c);
+size_t clip_workspace_bytes(const ClipTables* c);
+int clip_launches(const ClipTables* c);
+cudaError_t clip_launch(const ClipTables* c, float max_norm, float scale, float eps, float* norm, void* workspace,
+                        cudaStream_t st);
+size_t fp4_workspace_bytes();
+cudaError_t fp4_quantize_launch(const void* x, void* codes, void* scales, float* tensor_scale, int rows, int K, int format,
+                                int dtype, bool scale_given, void* workspace, cudaStream_t st);
+cudaError_t fp4_dequantize_launch(const void* codes, const void* scales, const float* tensor_scale, void* out, int rows,
+                                  int K, int format, int dtype, cudaStream_t st);
+cudaError_t linear_fp4_launch(const Fp4Operand& x, const Fp4Operand& w, const float* b, const void* residual, void* y, int T,
+                              int K, int N, int format, int act, int* status, cudaStream_t st);
 }  // namespace swin
 
 // Streams and events of the host-buffer forward's copy/compute pipeline, created on
@@ -77,6 +103,13 @@ struct swin_wattn_plan_s {
   swin::FwdLaunch fwd;
   swin::BwdLaunch bwd;
   HostPipe pipe;
+};
+
+// A plan of swin_wattn_clip_plan.
+struct swin_wattn_clip_s {
+  swin::ClipTables* tables;
+  std::vector<std::pair<uint64_t, uint64_t>> spans;  // of all its bytes, joined and in order
+  int device;
 };
 
 namespace {
@@ -176,6 +209,19 @@ int check_plan(const swin_wattn_plan_s* pl) {
   if (pl->p.magic != swin::kPlanMagic) return SWIN_WATTN_ERR_BAD_PLAN;
   return SWIN_WATTN_OK;
 }
+
+std::unordered_set<const swin_wattn_clip_s*> g_clips;  // under g_plans_mu
+
+int check_clip(const swin_wattn_clip_s* pl) {
+  std::lock_guard<std::mutex> lk(g_plans_mu);
+  return pl != nullptr && g_clips.find(pl) != g_clips.end() ? SWIN_WATTN_OK : SWIN_WATTN_ERR_BAD_PLAN;
+}
+
+bool normal_eps(float eps) { return eps >= FLT_MIN && std::isfinite(eps); }
+bool float_dtype(int dtype) { return dtype == SWIN_WATTN_FP32 || dtype == SWIN_WATTN_BF16; }
+bool norm_width(int C) { return C >= 8 && C <= 8192 && C % 8 == 0; }
+bool fp4_width(int K) { return K >= 32 && K <= 32768 && K % 32 == 0; }
+bool fp4_format(int f) { return f == SWIN_WATTN_NVFP4 || f == SWIN_WATTN_MXFP4; }
 
 void free_pipe(HostPipe& hp) {
   if (!hp.ready) return;
@@ -744,6 +790,274 @@ int swin_wattn_orthogonalize(const void* g, void* out, int count, int rows, int 
                                              reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_orthogonalize");
   g_launches += swin::orthogonalize_launches(count, rows, cols, steps);
+  return SWIN_WATTN_OK;
+}
+
+int swin_wattn_block_norm(const void* x, const void* f, const float* pre_w, const float* pre_b, const float* post_w,
+                          const float* post_b, const float* gate, const float* keep, void* y, void* h, int tokens, int C,
+                          int samples, int dtype, int kind, float alpha, float eps, struct CUstream_st* stream) {
+  if (tokens < 0 || !float_dtype(dtype) || (kind != SWIN_WATTN_NORM_LAYER && kind != SWIN_WATTN_NORM_RMS) ||
+      !normal_eps(eps) || !std::isfinite(alpha))
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  if (!norm_width(C) || tokens > kMaxLinearTokens) return SWIN_WATTN_ERR_UNSUPPORTED;
+  if (keep != nullptr && (samples < 1 || tokens % samples != 0)) return SWIN_WATTN_ERR_INVALID_ARG;
+  if (tokens == 0) return SWIN_WATTN_OK;  // (tensors of no elements have no address to tell them by)
+  if (f == nullptr ? post_w != nullptr || gate != nullptr || keep != nullptr || y != nullptr || pre_w == nullptr : y == nullptr)
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  if ((pre_w == nullptr && (pre_b != nullptr || h != nullptr)) || (post_w == nullptr && post_b != nullptr))
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  if (x == nullptr || (pre_w != nullptr && h == nullptr)) return SWIN_WATTN_ERR_INVALID_ARG;
+  const uint64_t n = (uint64_t)tokens * C, stream_bytes = n * (dtype == SWIN_WATTN_FP32 ? 4 : 2), c4 = (uint64_t)C * 4;
+  const Buffer bufs[] = {{x, stream_bytes, 16, false}, {y, stream_bytes, 16, true}, {f, n * 2, 16, false},
+                         {h, n * 2, 16, true}, {pre_w, c4, 4, false}, {pre_b, c4, 4, false}, {post_w, c4, 4, false},
+                         {post_b, c4, 4, false}, {gate, c4, 4, false}, {keep, (uint64_t)(keep ? samples : 0) * 4, 4, false}};
+  const int rc = check_buffers("swin_wattn_block_norm", bufs, 10, 0, 1);
+  if (rc != SWIN_WATTN_OK) return rc;
+  const cudaError_t e = swin::block_norm_launch(x, f, pre_w, pre_b, post_w, post_b, gate, keep, y, h, tokens, C, samples,
+                                                dtype, kind, alpha, eps, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_block_norm");
+  ++g_launches;
+  return SWIN_WATTN_OK;
+}
+
+size_t swin_wattn_block_norm_bwd_workspace_bytes(int tokens, int C) {
+  return tokens < 0 || tokens > kMaxLinearTokens || !norm_width(C) ? 0 : swin::block_norm_bwd_workspace_bytes(tokens, C);
+}
+
+int swin_wattn_block_norm_bwd(const void* y, const void* f, const void* dh, const void* dy, const float* pre_w,
+                              const float* post_w, const float* post_b, const float* gate, const float* keep, void* dx,
+                              void* df, float* dpre_w, float* dpre_b, float* dpost_w, float* dpost_b, float* dgate,
+                              int tokens, int C, int samples, int dtype, int kind, float alpha, float eps, int accumulate,
+                              void* workspace, size_t workspace_bytes, struct CUstream_st* stream) {
+  if (tokens < 0 || !float_dtype(dtype) || (kind != SWIN_WATTN_NORM_LAYER && kind != SWIN_WATTN_NORM_RMS) ||
+      !normal_eps(eps) || !std::isfinite(alpha))
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  if (!norm_width(C) || tokens > kMaxLinearTokens) return SWIN_WATTN_ERR_UNSUPPORTED;
+  if (keep != nullptr && (samples < 1 || tokens % samples != 0)) return SWIN_WATTN_ERR_INVALID_ARG;
+  if (tokens > 0 && f == nullptr && (post_w != nullptr || gate != nullptr || keep != nullptr))
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  if ((pre_w == nullptr && (dpre_w != nullptr || dpre_b != nullptr)) ||
+      (post_w == nullptr && (post_b != nullptr || dpost_w != nullptr || dpost_b != nullptr)) ||
+      (gate == nullptr && dgate != nullptr))
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  if (tokens > 0) {
+    if ((dh == nullptr) != (pre_w == nullptr) || (df == nullptr) != (f == nullptr) || dx == nullptr ||
+        (pre_w != nullptr && y == nullptr) || (dh == nullptr && dy == nullptr) || workspace == nullptr)
+      return SWIN_WATTN_ERR_INVALID_ARG;
+    if (workspace_bytes < swin::block_norm_bwd_workspace_bytes(tokens, C)) {
+      swin::set_last_error("swin_wattn_block_norm_bwd: workspace smaller than "
+                           "swin_wattn_block_norm_bwd_workspace_bytes(tokens, C)");
+      return SWIN_WATTN_ERR_INVALID_ARG;
+    }
+  }
+  float* const sums[] = {dpre_w, dpre_b, dpost_w, dpost_b, dgate};
+  const bool wanted = std::any_of(sums, sums + 5, [](float* g) { return g != nullptr; });
+  if (tokens == 0 && !wanted) return SWIN_WATTN_OK;
+  auto live = [&](const void* ptr) { return tokens > 0 ? ptr : nullptr; };
+  const uint64_t n = (uint64_t)tokens * C, stream_bytes = n * (dtype == SWIN_WATTN_FP32 ? 4 : 2), c4 = (uint64_t)C * 4;
+  const Buffer bufs[] = {{live(dy), stream_bytes, 16, false}, {live(dx), stream_bytes, 16, true},
+                         {live(y), stream_bytes, 16, false}, {live(f), n * 2, 16, false}, {live(dh), n * 2, 16, false},
+                         {live(df), n * 2, 16, true}, {pre_w, c4, 4, false}, {post_w, c4, 4, false}, {post_b, c4, 4, false},
+                         {gate, c4, 4, false}, {live(keep), (uint64_t)(keep ? samples : 0) * 4, 4, false},
+                         {dpre_w, c4, 4, true}, {dpre_b, c4, 4, true}, {dpost_w, c4, 4, true}, {dpost_b, c4, 4, true},
+                         {dgate, c4, 4, true}, {live(workspace), workspace_bytes, 256, true}};
+  const int rc = check_buffers("swin_wattn_block_norm_bwd", bufs, 17, 0, 1);
+  if (rc != SWIN_WATTN_OK) return rc;
+  const cudaError_t e = swin::block_norm_bwd_launch(y, f, dh, dy, pre_w, post_w, post_b, gate, keep, dx, df, dpre_w, dpre_b,
+                                                    dpost_w, dpost_b, dgate, tokens, C, samples, dtype, kind, alpha, eps,
+                                                    accumulate, workspace, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_block_norm_bwd");
+  g_launches += (tokens > 0) + wanted;
+  return SWIN_WATTN_OK;
+}
+
+int swin_wattn_clip_plan(swin_wattn_clip_t* plan, const void* const* grads, void* const* outs, const int64_t* sizes,
+                         const int* dtypes, int count) {
+  if (plan == nullptr) return SWIN_WATTN_ERR_INVALID_ARG;
+  *plan = nullptr;
+  if (count < 0 || count > 1 << 20 || (count > 0 && (grads == nullptr || outs == nullptr || sizes == nullptr || dtypes == nullptr)))
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  int dev = 0;
+  for (int i = 0; i < count; ++i)
+    if (sizes[i] < 0 || sizes[i] > (int64_t)1 << 40 || !float_dtype(dtypes[i]) ||
+        (sizes[i] > 0 && (grads[i] == nullptr || outs[i] == nullptr)))
+      return SWIN_WATTN_ERR_INVALID_ARG;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  }
+  try {
+    struct Span {
+      uint64_t begin, end;
+      bool written;
+    };
+    std::vector<Span> spans;
+    for (int i = 0; i < count; ++i) {
+      if (sizes[i] == 0) continue;
+      const uint64_t elem = dtypes[i] == SWIN_WATTN_FP32 ? 4 : 2, bytes = (uint64_t)sizes[i] * elem;
+      for (const void* ptr : {grads[i], (const void*)outs[i]}) {
+        const int rc = check_on_device(ptr, elem, dev);
+        if (rc != SWIN_WATTN_OK) return rc;
+      }
+      const uint64_t in = reinterpret_cast<uintptr_t>(grads[i]), out = reinterpret_cast<uintptr_t>(outs[i]);
+      spans.push_back({out, out + bytes, true});
+      if (in != out) spans.push_back({in, in + bytes, false});
+    }
+    std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+    uint64_t end_any = 0, end_written = 0;
+    for (const Span& s : spans) {
+      if (s.begin < (s.written ? end_any : end_written)) {
+        swin::set_last_error("swin_wattn_clip_plan: overlapping tensors");
+        return SWIN_WATTN_ERR_INVALID_ARG;
+      }
+      end_any = std::max(end_any, s.end);
+      if (s.written) end_written = std::max(end_written, s.end);
+    }
+    swin_wattn_clip_s* pl = new swin_wattn_clip_s{nullptr, {}, dev};
+    try {
+      for (const Span& s : spans) {
+        if (pl->spans.empty() || s.begin > pl->spans.back().second)
+          pl->spans.push_back({s.begin, s.end});
+        else
+          pl->spans.back().second = std::max(pl->spans.back().second, s.end);
+      }
+      pl->tables = swin::clip_tables_make(grads, outs, sizes, dtypes, count);
+      if (pl->tables == nullptr) throw std::bad_alloc();
+      std::lock_guard<std::mutex> lk(g_plans_mu);
+      g_clips.insert(pl);
+    } catch (...) {
+      swin::clip_tables_free(pl->tables);
+      delete pl;
+      throw;
+    }
+    *plan = pl;
+  } catch (...) {
+    swin::set_last_error("swin_wattn_clip_plan: out of host memory");
+    return SWIN_WATTN_ERR_CUDA;
+  }
+  return SWIN_WATTN_OK;
+}
+
+size_t swin_wattn_clip_workspace_bytes(swin_wattn_clip_t plan) {
+  return check_clip(plan) == SWIN_WATTN_OK ? swin::clip_workspace_bytes(plan->tables) : 0;
+}
+
+int swin_wattn_clip_grad_norm(swin_wattn_clip_t plan, float max_norm, float scale, float eps, float* norm, void* workspace,
+                              size_t workspace_bytes, struct CUstream_st* stream) {
+  int rc = check_clip(plan);
+  if (rc != SWIN_WATTN_OK) return rc;
+  if (!(max_norm >= 0.0f) || !std::isfinite(max_norm) || !(scale >= FLT_MIN) || !std::isfinite(scale) || !(eps >= 0.0f) ||
+      !std::isfinite(eps) || workspace == nullptr)
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < swin::clip_workspace_bytes(plan->tables)) {
+    swin::set_last_error("swin_wattn_clip_grad_norm: workspace smaller than swin_wattn_clip_workspace_bytes(plan)");
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != plan->device) {
+    cudaGetLastError();
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  }
+  const Buffer bufs[] = {{norm, 4, 4, true}, {workspace, workspace_bytes, 256, true}};
+  if ((rc = check_buffers("swin_wattn_clip_grad_norm", bufs, 2)) != SWIN_WATTN_OK) return rc;
+  for (const Buffer& b : bufs) {  // against the plan's tensors: the last one that begins before the buffer ends
+    if (b.ptr == nullptr) continue;
+    const uint64_t p = reinterpret_cast<uintptr_t>(b.ptr);
+    auto it = std::lower_bound(plan->spans.begin(), plan->spans.end(), std::make_pair(p + b.bytes, (uint64_t)0));
+    if (it != plan->spans.begin() && std::prev(it)->second > p) {
+      swin::set_last_error("swin_wattn_clip_grad_norm: norm or workspace overlaps a tensor of the plan");
+      return SWIN_WATTN_ERR_INVALID_ARG;
+    }
+  }
+  const cudaError_t e = swin::clip_launch(plan->tables, max_norm, scale, eps, norm, workspace,
+                                          reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_clip_grad_norm");
+  g_launches += swin::clip_launches(plan->tables);
+  return SWIN_WATTN_OK;
+}
+
+int swin_wattn_clip_destroy(swin_wattn_clip_t plan) {
+  if (plan == nullptr) return SWIN_WATTN_OK;
+  {
+    std::lock_guard<std::mutex> lk(g_plans_mu);
+    if (g_clips.erase(plan) == 0) return SWIN_WATTN_ERR_BAD_PLAN;
+  }
+  swin::clip_tables_free(plan->tables);
+  delete plan;
+  return SWIN_WATTN_OK;
+}
+
+size_t swin_wattn_fp4_scale_bytes(int rows, int K, int format) {
+  return rows < 0 || rows > kMaxLinearTokens || !fp4_width(K) || !fp4_format(format) ? 0 : swin::fp4::scale_bytes(rows, K, format);
+}
+size_t swin_wattn_fp4_workspace_bytes(void) { return swin::fp4_workspace_bytes(); }
+
+int swin_wattn_fp4_quantize(const void* x, void* codes, void* scales, float* tensor_scale, int rows, int K, int format,
+                            int dtype, int scale_given, void* workspace, size_t workspace_bytes,
+                            struct CUstream_st* stream) {
+  if (rows < 0 || !fp4_format(format) || !float_dtype(dtype)) return SWIN_WATTN_ERR_INVALID_ARG;
+  if (!fp4_width(K) || rows > kMaxLinearTokens) return SWIN_WATTN_ERR_UNSUPPORTED;
+  const bool nv = format == SWIN_WATTN_NVFP4, own = nv && !scale_given;
+  if (nv != (tensor_scale != nullptr) || (own && (workspace == nullptr || workspace_bytes < swin::fp4_workspace_bytes())))
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  if (rows > 0 && (x == nullptr || codes == nullptr || scales == nullptr)) return SWIN_WATTN_ERR_INVALID_ARG;
+  if (rows == 0 && !own) return SWIN_WATTN_OK;
+  auto live = [&](const void* ptr) { return rows > 0 ? ptr : nullptr; };
+  const uint64_t n = (uint64_t)rows * K;
+  const Buffer bufs[] = {{live(x), n * (dtype == SWIN_WATTN_FP32 ? 4 : 2), 16, false}, {live(codes), n / 2, 16, true},
+                         {live(scales), swin::fp4::scale_bytes(rows, K, format), 16, true}, {tensor_scale, 4, 4, own},
+                         {own ? workspace : nullptr, workspace_bytes, 256, true}};
+  const int rc = check_buffers("swin_wattn_fp4_quantize", bufs, 5);
+  if (rc != SWIN_WATTN_OK) return rc;
+  const cudaError_t e = swin::fp4_quantize_launch(x, codes, scales, tensor_scale, rows, K, format, dtype, scale_given != 0,
+                                                  workspace, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_fp4_quantize");
+  g_launches += rows == 0 ? 1 : own ? 2 : 1;
+  return SWIN_WATTN_OK;
+}
+
+int swin_wattn_fp4_dequantize(const void* codes, const void* scales, const float* tensor_scale, void* out, int rows, int K,
+                              int format, int dtype, struct CUstream_st* stream) {
+  if (rows < 0 || !fp4_format(format) || !float_dtype(dtype) || (format == SWIN_WATTN_NVFP4) != (tensor_scale != nullptr))
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  if (!fp4_width(K) || rows > kMaxLinearTokens) return SWIN_WATTN_ERR_UNSUPPORTED;
+  if (rows == 0) return SWIN_WATTN_OK;
+  if (codes == nullptr || scales == nullptr || out == nullptr) return SWIN_WATTN_ERR_INVALID_ARG;
+  const uint64_t n = (uint64_t)rows * K;
+  const Buffer bufs[] = {{codes, n / 2, 16, false}, {scales, swin::fp4::scale_bytes(rows, K, format), 16, false},
+                         {tensor_scale, 4, 4, false}, {out, n * (dtype == SWIN_WATTN_FP32 ? 4 : 2), 16, true}};
+  const int rc = check_buffers("swin_wattn_fp4_dequantize", bufs, 4);
+  if (rc != SWIN_WATTN_OK) return rc;
+  const cudaError_t e = swin::fp4_dequantize_launch(codes, scales, tensor_scale, out, rows, K, format, dtype,
+                                                    reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_fp4_dequantize");
+  ++g_launches;
+  return SWIN_WATTN_OK;
+}
+
+int swin_wattn_linear_fp4(const void* x_codes, const void* x_scales, const float* x_tensor_scale, const void* w_codes,
+                          const void* w_scales, const float* w_tensor_scale, const float* b, const void* residual, void* y,
+                          int tokens, int K, int N, int format, int act, int* status, struct CUstream_st* stream) {
+  const bool nv = format == SWIN_WATTN_NVFP4;
+  if (tokens < 0 || !known_act(act) || !fp4_format(format) || nv != (x_tensor_scale != nullptr) ||
+      nv != (w_tensor_scale != nullptr))
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  if (!fp4_width(K) || !linear_width(N) || tokens > kMaxLinearTokens) return SWIN_WATTN_ERR_UNSUPPORTED;
+  if (tokens == 0) return SWIN_WATTN_OK;
+  if (x_codes == nullptr || x_scales == nullptr || w_codes == nullptr || w_scales == nullptr || y == nullptr)
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  const uint64_t T = (uint64_t)tokens;
+  const Buffer bufs[] = {{residual, T * N * 2, 16, false}, {y, T * N * 2, 16, true}, {x_codes, T * K / 2, 16, false},
+                         {x_scales, swin::fp4::scale_bytes(tokens, K, format), 16, false}, {x_tensor_scale, 4, 4, false},
+                         {w_codes, (uint64_t)N * K / 2, 16, false}, {w_scales, swin::fp4::scale_bytes(N, K, format), 16, false},
+                         {w_tensor_scale, 4, 4, false}, {b, (uint64_t)N * 4, 4, false}, {status, 4, 4, true}};
+  const int rc = check_buffers("swin_wattn_linear_fp4", bufs, 10, 0, 1);
+  if (rc != SWIN_WATTN_OK) return rc;
+  const cudaError_t e = swin::linear_fp4_launch({x_codes, x_scales, x_tensor_scale}, {w_codes, w_scales, w_tensor_scale}, b,
+                                                residual, y, tokens, K, N, format, act, status,
+                                                reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_linear_fp4");
+  ++g_launches;
   return SWIN_WATTN_OK;
 }
 
