@@ -1,0 +1,11 @@
+// The gradients of block_norm for a residual stream in bf16 (block_norm_bwd.cuh).
+#include "block_norm_bwd.cuh"
+
+namespace swin {
+
+cudaError_t block_norm_bwd_bf16(const NormBwdParams& p, cudaStream_t st) {
+  const Shape s = shape_of(p.C);
+  return launch<__nv_bfloat16>(p, s, blocks_of(p.rows, s), st);
+}
+
+}  // namespace swin
