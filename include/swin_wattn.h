@@ -499,7 +499,8 @@ int swin_wattn_clip_destroy(swin_wattn_clip_t plan);
  *   rows   in [0, 2^31 - 1024]; K a multiple of 32 in [32, 32768];
  *   workspace  needed for a scale that is not given: swin_wattn_fp4_workspace_bytes() bytes, 256-byte
  *          aligned, overwritten, one call at a time per workspace.
- * swin_wattn_fp4_dequantize reads them back: out [rows, K], fp32 or bf16 by `dtype`, one rounding each.
+ * swin_wattn_fp4_dequantize reads them back, q (s ts) or q s: out [rows, K], fp32 or bf16 by `dtype`; fp32 is rounded as the
+ * two products are, bf16 once more.
  * Device pointers of the current device, 16-byte aligned (tensor_scale 4). One launch, or two for a scale that is
  * not given; deterministic; nothing is allocated.
  */
