@@ -5,8 +5,8 @@
 //
 // One persistent CTA per SM (CG = 1) or pair of CTAs on two SMs (CG = 2) walks output tiles of CG * 128 tokens by
 // NT <= 192 channels, as the 16-bit products do (product.cuh):
-// * copy warp: per chunk of 256 along K, 128 rows of x and NT / CG of w (128 bytes each) and their scale
-//   tiles into a ring of stages;
+// * copy warp: per chunk of 256 along K, 128 rows of x and NT / CG of w (128 bytes each) into a ring of stages;
+// * scale warp: their scale tiles into the same stages;
 // * MMA warp: the chunk's scales from shared to tensor memory (two sets of columns in turn), and four MMAs
 //   of K = 64 into one of two accumulators;
 // * sixteen epilogue warps: 32-column slices, arithmetic in fp32, one rounding, TMA stores; a residual arrives by
@@ -21,9 +21,8 @@ namespace {
 
 using namespace prod;
 
-constexpr int kEpiWarps = 16, kMMA = kEpiWarps, kCOPY = kEpiWarps + 1, kNThreads = (kEpiWarps + 2) * 32;
-constexpr int kPerQuad = kEpiWarps / 4;
-constexpr int kMaxNT4 = 192, kSlices4 = (kMaxNT4 / kSC + kPerQuad - 1) / kPerQuad;
+constexpr int kEpiWarps = 16, kMMA = kEpiWarps, kCOPY = kEpiWarps + 1, kSCALES = kEpiWarps + 2, kNThreads = (kEpiWarps + 3) * 32;
+constexpr int kMaxNT4 = 192, kSlices4 = 3;  // slices of a warp: six of a tile between at least two warps
 // Tensor memory: two accumulators, then two sets of scales: A's four tiles, B's four times two.
 constexpr int kScaleCols = 2 * kMaxNT4, kSetCols = 48, kScaleB = 16;
 constexpr int kMaxTiles = 4;  // staging tiles of an epilogue warp
@@ -36,8 +35,11 @@ struct Fp4Params {
   FastDiv n_nt;
   int n_items;  // tiles, along N fastest
   int chunks, steps;  // of K, in 256 and in 64
+  const unsigned char *scales_a, *scales_b;
+  int k_tiles;  // scale tiles along K
   int stages, stage_bytes, off_sa, off_sb, b_tiles;  // b_tiles: scale row tiles of B a stage holds
   int off_out, warp_bytes, tiles, off_bias, off_bar;
+  int per_quad;  // epilogue warps of a quadrant of lanes that have slices
   uint32_t idesc;
   int act;
   bool has_aux;
@@ -50,8 +52,7 @@ struct Fp4Params {
 
 template <int CG, int FORMAT>
 __global__ void __launch_bounds__(kNThreads, 1)
-    linear_fp4_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap sa_map,
-                      const __grid_constant__ CUtensorMap b_map, const __grid_constant__ CUtensorMap sb_map,
+    linear_fp4_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
                       const __grid_constant__ CUtensorMap out_map, const __grid_constant__ CUtensorMap aux_map,
                       const Fp4Params p) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
   if (warp == kMMA) tmem_alloc<CG>(smem_u32(tmem_slot));
   if (tid == 0) {
     for (int st = 0; st < stages; ++st) {
-      tc::mbar_init(full_bar(st), 1);
+      tc::mbar_init(full_bar(st), 1 + CG);  // the codes of both CTAs and the scales of each
       tc::mbar_init(empty_bar(st), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -116,13 +117,9 @@ __global__ void __launch_bounds__(kNThreads, 1)
             break;
           }
           const uint32_t base = smem0 + st * p.stage_bytes, fb = full0 + 8 * st;
-          const uint32_t bytes = kABytes + (p.NT / CG) * 128 + (1 + p.b_tiles) * kSetBytes;
-          if (rank == 0) tc::mbar_expect_tx(full_bar(st), CG * bytes);
+          if (rank == 0) tc::mbar_expect_tx(full_bar(st), CG * (kABytes + (p.NT / CG) * 128));
           load_3d<CG>(base, &a_map, c * 128, m0, 0, fb);
           load_3d<CG>(base + kABytes, &b_map, c * 128, n0 + rank * (p.NT / CG), 0, fb);
-          load_3d<CG>(base + p.off_sa, &sa_map, 0, c * kTPC, m0 >> 7, fb);
-          for (int j = 0; j < p.b_tiles; ++j)
-            load_3d<CG>(base + p.off_sb + j * kSetBytes, &sb_map, 0, c * kTPC, (n0 >> 7) + j, fb);
           if (++st == stages) {
             st = 0;
             ph ^= 1;
@@ -137,10 +134,76 @@ __global__ void __launch_bounds__(kNThreads, 1)
           tc::mbar_wait(full_bar(s2), s2 < st ? ph : ph ^ 1, p.wait_ns);
     }
     __syncwarp();
+  } else if (warp == kSCALES) {
+    // The chunk's scale tiles, 16 bytes a lane: an own path beside the copy engine, whose copies cost some 100 clocks
+    // each whatever their size. Chunk c is handed over once it has landed, while the next ones are on their way.
+    int st = 0, done_st = 0, behind = 0;  // stages of the next chunk and of the next to hand over; chunks between them
+    uint32_t ph = 0, first = 1;
+    const uint32_t full0 = CG == 2 ? map_to_rank(full_bar(0), 0) : full_bar(0);
+    auto hand_over = [&]() {
+      tc::fence_proxy_async();  // these copies are the tensor core's to read
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2)
+          arrive_cluster(full0 + 8 * done_st);
+        else
+          tc::mbar_arrive(full0 + 8 * done_st);
+      }
+      if (++done_st == stages) done_st = 0;
+      --behind;
+    };
+    const int row_tiles_b = (p.N + 127) >> 7, row_tiles_a = (int)(((int64_t)p.M + 127) >> 7);
+    const int64_t row_bytes = (int64_t)p.k_tiles * fp4::kTileBytes;
+    for (int it = group; it < p.n_items && !bad; it += n_groups) {
+      int m0, n0;
+      rows_of_item(it, m0, n0);
+      // row tiles past the end are left as they are: their rows and columns are not stored
+      const bool has_a = (m0 >> 7) < row_tiles_a, has_b1 = p.b_tiles == 2 && (n0 >> 7) + 1 < row_tiles_b;
+      const unsigned char* from_a = p.scales_a + (m0 >> 7) * row_bytes + lane * 16;
+      const unsigned char* from_b = p.scales_b + (n0 >> 7) * row_bytes + lane * 16;
+      for (int c = 0; c < p.chunks; ++c) {
+        if (!first && !warp_wait(empty_bar(st), ph ^ 1, p.wait_ns)) {
+          bad = 1;
+          break;
+        }
+        const uint32_t to = smem0 + st * p.stage_bytes + lane * 16;
+#pragma unroll
+        for (int k = 0; k < kTPC; ++k) {
+          if (c * kTPC + k < p.k_tiles) {  // (tiles past the end have no step)
+            if (has_a) cp_async_16(to + p.off_sa + k * fp4::kTileBytes, from_a + k * fp4::kTileBytes);
+            cp_async_16(to + p.off_sb + k * fp4::kTileBytes, from_b + k * fp4::kTileBytes);
+            if (has_b1) cp_async_16(to + p.off_sb + kSetBytes + k * fp4::kTileBytes, from_b + row_bytes + k * fp4::kTileBytes);
+          }
+        }
+        cp_async_commit();
+        from_a += kSetBytes;
+        from_b += kSetBytes;
+        if (++st == stages) {
+          st = 0;
+          ph ^= 1;
+          first = 0;
+        }
+        // chunks on their way behind the newest: fewer than there are stages
+        if (stages >= 4) {
+          if (++behind > 2) {
+            cp_async_wait<2>();
+            hand_over();
+          }
+        } else if (++behind > 1) {
+          cp_async_wait<1>();
+          hand_over();
+        }
+      }
+    }
+    cp_async_wait_all();
+    while (behind > 0) hand_over();
   } else if (warp == kMMA) {
     if (rank == 0) {
       constexpr uint32_t kHi = desc_hi(1024, kSW128);
       const uint32_t a0 = desc_lo(smem0, 16), b0 = desc_lo(smem0 + kABytes, 16), stage_step = p.stage_bytes >> 4;
+      const uint32_t sa0 = fp4::scale_lo(smem0 + p.off_sa), sb0 = fp4::scale_lo(smem0 + p.off_sb);
+      const uint32_t id0 = p.idesc, id1 = p.idesc | fp4::idesc_second_half();
+      const int b_tiles = p.b_tiles;
       int st = 0, g = 0, set = 0;  // ring stage; accumulations begun; set of scales
       uint32_t ph = 0;
       for (int it = group; it < p.n_items && !bad; it += n_groups, ++g) {
@@ -158,27 +221,31 @@ __global__ void __launch_bounds__(kNThreads, 1)
             break;
           }
           tc::fence_after_sync();
-          const uint32_t a = a0 + st * stage_step, b = b0 + st * stage_step, base = smem0 + st * p.stage_bytes;
+          const uint32_t at = st * stage_step, a = a0 + at, b = b0 + at, la = sa0 + at, lb = sb0 + at;
           const uint32_t sa = tmem + kScaleCols + set * kSetCols, sb = sa + kScaleB;
           const uint32_t sb_n = sb + ((n0 & 127) >> 5);  // the tile's first column may lie inside a scale tile
           const int steps = min(4, p.steps - 4 * c);
           if (elect_one()) {
+            constexpr uint32_t kTileStep = fp4::kTileBytes >> 4;
             // B's tiles of one step lie side by side, four columns for 128 rows
+            auto copy = [&](int k) {
+              fp4::copy_scales<CG>(sa + 4 * k, la + k * kTileStep);
+              fp4::copy_scales<CG>(sb + 8 * k, lb + k * kTileStep);
+              if (b_tiles == 2) fp4::copy_scales<CG>(sb + 8 * k + 4, lb + (kTPC + k) * kTileStep);
+            };
+            auto step = [&](int kk) {
+              const int k = kk / (4 / kTPC);
+              fp4::mma<CG, FORMAT>(acc, a + kk * 2, b + kk * 2, kHi, FORMAT == 1 && (kk & 1) ? id1 : id0, sa + 4 * k, sb_n + 8 * k,
+                                   c > 0 || kk > 0);
+            };
+            if (steps == 4) {
 #pragma unroll
-            for (int k = 0; k < kTPC; ++k) {
-              if (k * (4 / kTPC) < steps) {
-                fp4::copy_scales<CG>(sa + 4 * k, base + p.off_sa + k * fp4::kTileBytes);
-                fp4::copy_scales<CG>(sb + 8 * k, base + p.off_sb + k * fp4::kTileBytes);
-                if (p.b_tiles == 2) fp4::copy_scales<CG>(sb + 8 * k + 4, base + p.off_sb + kSetBytes + k * fp4::kTileBytes);
-              }
-            }
+              for (int k = 0; k < kTPC; ++k) copy(k);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (kk < steps) {
-                const int k = kk / (4 / kTPC);
-                const uint32_t id = p.idesc | (FORMAT == 1 && (kk & 1) ? fp4::idesc_second_half() : 0u);
-                fp4::mma<CG, FORMAT>(acc, a + kk * 2, b + kk * 2, kHi, id, sa + 4 * k, sb_n + 8 * k, c > 0 || kk > 0);
-              }
+              for (int kk = 0; kk < 4; ++kk) step(kk);
+            } else {
+              for (int k = 0; k * (4 / kTPC) < steps; ++k) copy(k);
+              for (int kk = 0; kk < steps; ++kk) step(kk);
             }
             commit<CG>(empty_bar(st));
 #ifdef SWIN_WATTN_FAULT_INJECTION
@@ -202,7 +269,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
     __syncwarp();
   } else {
     // ==== epilogue warps ================================================================
-    const int quad = warp & 3, part = warp >> 2;
+    const int quad = warp & 3, part = warp >> 2, per_quad = p.per_quad;
     const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
     unsigned char* wstage = smem + p.off_out + warp * p.warp_bytes;
     const bool aux = p.has_aux;
@@ -217,7 +284,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
         int m0;
         rows_of_item(nx_it, m0, nx_n0);
         nx_row = m0 + quad * 32;
-        nx_end = nx_row < p.M ? min(p.NT, p.N - nx_n0) : 0;
+        nx_end = part < per_quad && nx_row < p.M ? min(p.NT, p.N - nx_n0) : 0;
       }
     };
     auto request_next = [&]() {
@@ -230,7 +297,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
           }
           ++issued;
           if (++nx_tile == NB) nx_tile = 0;
-          nx_c0 += kPerQuad * kSC;
+          nx_c0 += per_quad * kSC;
           return;
         }
         nx_it += n_groups;
@@ -251,12 +318,12 @@ __global__ void __launch_bounds__(kNThreads, 1)
       // the bias of the tile's columns in shared memory, for broadcast reads. Every warp of a part
       // writes the same values; two buffers, and the write waits for this tile's accumulator, which is
       // given out when every warp has left the tile before last.
-      float* sbias = reinterpret_cast<float*>(smem + p.off_bias) + buf * kMaxNT + part * kSC;
+      float* sbias = reinterpret_cast<float*>(smem + p.off_bias) + buf * kMaxNT4 + lane;
       float bt[kSlices4];
 #pragma unroll
       for (int i = 0; i < kSlices4; ++i) {
-        const int c = n0 + (part + kPerQuad * i) * kSC + lane;
-        bt[i] = p.bias != nullptr && c < p.N ? p.bias[c] : 0.0f;
+        const int c0 = (part + per_quad * i) * kSC, c = n0 + c0 + lane;
+        bt[i] = p.bias != nullptr && part < per_quad && c0 < p.NT && c < p.N ? p.bias[c] : 0.0f;
       }
       if (!warp_wait(dfull_bar(buf), (g >> 1) & 1, p.wait_ns)) {
         bad = 1;
@@ -264,12 +331,13 @@ __global__ void __launch_bounds__(kNThreads, 1)
       }
       tc::fence_after_sync();
 #pragma unroll
-      for (int i = 0; i < kSlices4; ++i) sbias[kPerQuad * kSC * i + lane] = bt[i];
+      for (int i = 0; i < kSlices4; ++i)
+        if (part < per_quad && (part + per_quad * i) * kSC < p.NT) sbias[(part + per_quad * i) * kSC] = bt[i];
       __syncwarp();
 #pragma unroll 1
       for (int si = 0; si < kSlices4; ++si) {
-        const int c0 = (part + kPerQuad * si) * kSC;
-        if (!(row0 < p.M && c0 < p.NT && n0 + c0 < p.N)) continue;
+        const int c0 = (part + per_quad * si) * kSC;
+        if (!(part < per_quad && row0 < p.M && c0 < p.NT && n0 + c0 < p.N)) continue;
         unsigned char* so = wstage + tile * kTile;
         if (aux) {
           // all stores but the last slice's (of two tiles, all) have read their tiles: load
@@ -300,8 +368,8 @@ __global__ void __launch_bounds__(kNThreads, 1)
             uint4 r = make_uint4(0, 0, 0, 0);
             if (aux) r = *at(c);
             const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
-            const float4 b0 = reinterpret_cast<const float4*>(sbias + kPerQuad * kSC * si)[2 * c];
-            const float4 b1 = reinterpret_cast<const float4*>(sbias + kPerQuad * kSC * si)[2 * c + 1];
+            const float4 b0 = reinterpret_cast<const float4*>(sbias - lane + c0)[2 * c];
+            const float4 b1 = reinterpret_cast<const float4*>(sbias - lane + c0)[2 * c + 1];
             const float2 bb[4] = {make_float2(b0.x, b0.y), make_float2(b0.z, b0.w), make_float2(b1.x, b1.y),
                                   make_float2(b1.z, b1.w)};
 #pragma unroll
@@ -321,7 +389,12 @@ __global__ void __launch_bounds__(kNThreads, 1)
           default: activate(std::integral_constant<int, SWIN_WATTN_ACT_NONE>()); break;
         }
         if (!aux) {  // the store that held the tile has read it
-          if (lane == 0) tc::bulk_wait_read<1>();
+          if (lane == 0) {
+            if (NB == 1)
+              tc::bulk_wait_read<0>();
+            else
+              tc::bulk_wait_read<1>();
+          }
           __syncwarp();
         }
 #pragma unroll
@@ -376,16 +449,18 @@ struct Fp4Tiling {
 };
 
 // The cheapest tile by estimated clocks: rounds of tiles, each the longer of its chunks and its epilogue, plus
-// one epilogue that nothing overlaps. A chunk of CG * 128 x NT x 256 arrives at some 53 bytes a clock (product.cuh).
-Fp4Tiling choose(int64_t T, int64_t N, int K) {
+// one epilogue that nothing overlaps. A chunk takes 100 and a clock for each 88 of its bytes (8192^3, clocks a chunk of
+// NVFP4: pairs with 192 columns 510, 128 columns 461; single SMs 609, 503).
+Fp4Tiling choose(int64_t T, int64_t N, int K, int format) {
   Fp4Tiling best{1, 64, -1.0};
   const int chunks = (K + fp4::kChunk - 1) / fp4::kChunk;
-  for (int cg = 1; cg <= 1; ++cg)
+  for (int cg = 1; cg <= 2; ++cg)
     for (int nt = 64; nt <= kMaxNT4; nt += 64) {
       const int64_t items = (T + cg * kBM - 1) / (cg * kBM) * ((N + nt - 1) / nt), groups = kSms / cg;
       const double rounds = (double)((items + groups - 1) / groups);
-      const double chunk = std::max(1.5 * nt, 2.4 * (kBM + nt / cg + 32)), epi = 500.0 + 14.0 * nt;
-      const double cost = 5000.0 + rounds * std::max(chunks * chunk, epi) + epi;
+      const int sets = fp4::chunk_tiles(format) * fp4::kTileBytes * (1 + (128 % nt != 0 ? 2 : 1));
+      const double chunk = 100.0 + ((kBM + nt / cg) * 128 + sets) / 88.0, epi = 500.0 + 14.0 * nt;
+      const double cost = 5000.0 + rounds * std::max(chunks * chunk, epi) + epi + (cg - 1) * 500.0;
       if (best.cost < 0.0 || cost < best.cost) best = {cg, nt, cost};
     }
   return best;
@@ -396,9 +471,9 @@ cudaError_t launch_tiles4(int NT, const Fp4Operand& x, const Fp4Operand& w, cons
                           cudaStream_t st) {
   constexpr int kTPC = fp4::chunk_tiles(FORMAT), kSetBytes = kTPC * fp4::kTileBytes;
   constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  CUtensorMap a_map, sa_map, b_map, sb_map, out_map, aux_map;
-  cudaError_t e = fp4::encode_operand(&a_map, &sa_map, x, p.M, K, FORMAT, kBM);
-  if (e == cudaSuccess) e = fp4::encode_operand(&b_map, &sb_map, w, p.N, K, FORMAT, NT / CG);
+  CUtensorMap a_map, b_map, out_map, aux_map;
+  cudaError_t e = fp4::encode_codes(&a_map, x, p.M, K, kBM);
+  if (e == cudaSuccess) e = fp4::encode_codes(&b_map, w, p.N, K, NT / CG);
   const Matrix out{y, p.M, p.N, p.N, 0};
   if (e == cudaSuccess)
     e = encode_3d(&out_map, out, 1, kBf16, 2, kSC, 32, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
@@ -416,6 +491,9 @@ cudaError_t launch_tiles4(int NT, const Fp4Operand& x, const Fp4Operand& w, cons
   p.n_nt = FastDiv((p.N + NT - 1) / NT);
   p.n_items = (int)items;
   p.steps = (K + fp4::kStep - 1) / fp4::kStep;
+  p.scales_a = static_cast<const unsigned char*>(x.scales);
+  p.scales_b = static_cast<const unsigned char*>(w.scales);
+  p.k_tiles = fp4::k_tiles(K, FORMAT);
   p.chunks = (K + fp4::kChunk - 1) / fp4::kChunk;
   p.idesc = fp4::idesc(CG * kBM, NT, FORMAT);
   p.wait_ns = wait_limit_ns();
@@ -425,18 +503,24 @@ cudaError_t launch_tiles4(int NT, const Fp4Operand& x, const Fp4Operand& w, cons
   p.off_sa = kABytes + NT / CG * 128;
   p.off_sb = p.off_sa + kSetBytes;
   p.stage_bytes = (p.off_sb + p.b_tiles * kSetBytes + 1023) / 1024 * 1024;
-  constexpr int kBiasBytes = 2 * kMaxNT * 4;
-  p.tiles = p.has_aux ? kMaxTiles : 2;
+  constexpr int kBiasBytes = 2 * kMaxNT4 * 4;
+  // Where K is long, a tile's product takes longer than its epilogue, and shared memory is worth more in the ring: a
+  // staging tile a warp, or two of half the warps where a residual comes through them. (8192^3 at five stages instead of
+  // four: 192 -> 163 us NVFP4, 168 -> 158 us MXFP4; half the warps with a residual, 12561 x 6144 x 1536 54 -> 47 us, but
+  // 12544 x 1536 x 6144 64 -> 70 us.)
+  const bool long_k = p.chunks >= 6, longer_k = p.chunks >= 10;
+  p.per_quad = p.has_aux && longer_k ? 2 : 4;
+  p.tiles = p.has_aux ? (long_k ? 2 : kMaxTiles) : (long_k ? 1 : 2);
   int fixed = 0;
   for (;; --p.tiles) {  // fewer staging tiles where the ring would not have three stages
     p.warp_bytes = p.tiles * kTile;
-    fixed = kEpiWarps * p.warp_bytes + kBiasBytes + 8 * kBars + 16;
+    fixed = 4 * p.per_quad * p.warp_bytes + kBiasBytes + 8 * kBars + 16;
     p.stages = std::min(kMaxStages, (di.smem_max - fixed) / p.stage_bytes);
-    if (p.stages >= 3 || p.tiles <= 2) break;
+    if (p.stages >= 3 || p.tiles <= (p.has_aux ? 2 : 1)) break;
   }
   if (p.stages < 2) return cudaErrorInvalidConfiguration;
   p.off_out = p.stages * p.stage_bytes;
-  p.off_bias = p.off_out + kEpiWarps * p.warp_bytes;
+  p.off_bias = p.off_out + 4 * p.per_quad * p.warp_bytes;
   p.off_bar = p.off_bias + kBiasBytes;
   // more than half of an SM's shared memory: one CTA per SM, so the tensor memory is free
   const int smem = std::max(120 * 1024, p.off_out + fixed);
@@ -457,7 +541,7 @@ cudaError_t launch_tiles4(int NT, const Fp4Operand& x, const Fp4Operand& w, cons
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, a_map, sa_map, b_map, sb_map, out_map, aux_map, p);
+  return cudaLaunchKernelEx(&cfg, kern, a_map, b_map, out_map, aux_map, p);
 }
 
 }  // namespace
@@ -472,7 +556,10 @@ cudaError_t linear_fp4_launch(const Fp4Operand& x, const Fp4Operand& w, const fl
   p.scale_x = x.tensor_scale;
   p.scale_w = w.tensor_scale;
   p.status = status;
-  const Fp4Tiling t = choose(T, N, K);
+  const Fp4Tiling t = choose(T, N, K, format);
+  if (t.cg == 2)
+    return format == 0 ? launch_tiles4<2, 0>(t.NT, x, w, residual, y, p, K, st)
+                       : launch_tiles4<2, 1>(t.NT, x, w, residual, y, p, K, st);
   return format == 0 ? launch_tiles4<1, 0>(t.NT, x, w, residual, y, p, K, st)
                      : launch_tiles4<1, 1>(t.NT, x, w, residual, y, p, K, st);
 }

@@ -41,29 +41,29 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t
 }
 // A scale tile (32 rows of 16 bytes, each the four words of rows r, r + 32, r + 64, r + 96) from shared memory
 // to four columns of tensor memory, the same in each quadrant of lanes (of both CTAs of a pair).
+// `lo` is the low word of the tile's descriptor.
+constexpr uint32_t kScaleHi = 128 >> 4 | 1u << 14;  // groups of eight rows 128 bytes apart, no swizzle
+__device__ __forceinline__ uint32_t scale_lo(uint32_t smem) { return ((smem >> 4) & 0x3FFFu) | 1u << 16; }
 template <int CG>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem) {
-  const uint64_t desc = tc::sdesc(smem, 16, 128);
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo) {
   if constexpr (CG == 2)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
+    asm volatile("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n}\n" ::"r"(taddr),
+                 "r"(lo), "r"(kScaleHi)
+                 : "memory");
   else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
+    asm volatile("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n}\n" ::"r"(taddr),
+                 "r"(lo), "r"(kScaleHi)
+                 : "memory");
 }
 #endif
 
 namespace {
 
-// Tensor maps of an operand: 128-byte rows of codes, and its scale tiles.
-inline cudaError_t encode_operand(CUtensorMap* codes, CUtensorMap* scales, const Fp4Operand& x, int64_t rows, int K,
-                                  int format, int box_rows) {
+// Tensor map of an operand's codes, in 128-byte rows.
+inline cudaError_t encode_codes(CUtensorMap* codes, const Fp4Operand& x, int64_t rows, int K, int box_rows) {
   const prod::Matrix m{x.codes, rows, K / 2, K / 2, 0};
-  const int tiles = k_tiles(K, format);
-  const prod::Matrix s{x.scales, tiles, kTileBytes / 4, kTileBytes / 4, (int64_t)tiles * (kTileBytes / 4)};
-  const cudaError_t e = prod::encode_3d(codes, m, 1, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128, box_rows,
-                                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-  if (e != cudaSuccess) return e;
-  return prod::encode_3d(scales, s, (int)((rows + 127) / 128), CU_TENSOR_MAP_DATA_TYPE_INT32, 4, kTileBytes / 4,
-                         chunk_tiles(format), CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  return prod::encode_3d(codes, m, 1, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 }  // namespace
