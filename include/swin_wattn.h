@@ -461,8 +461,10 @@ int swin_wattn_block_norm_bwd(const void* y, const void* f, const void* dh, cons
 /*
  * The norm over all gradients of a model and their clipping, between the gradients and the weight updates:
  *   n = scale * sqrt(sum of g^2 over all tensors),   out = g * scale * min(1, max_norm / (n + eps))
- * swin_wattn_clip_plan looks at the tensors once and keeps their addresses and sizes (on the host); the tensors
- * have to stay where they are while the plan is used, their values may change.
+ * swin_wattn_clip_plan looks at the tensors once and keeps their addresses and sizes (a list in device memory, which
+ * the plan owns; 32 bytes for some 2048 to 16384 elements, at most 2 MB and 32 bytes a tensor); the tensors
+ * have to stay where they are while the plan is used, their values may change. Not to be called during a stream's
+ * capture; swin_wattn_clip_destroy waits for the device.
  *   grads, outs  `count` device pointers each, at any multiple of their element size; outs[i] may be
  *          grads[i] itself (in place), else it overlaps nothing; no tensor may be written twice;
  *   sizes  elements of each (0: the tensor is skipped); dtypes  SWIN_WATTN_FP32 or SWIN_WATTN_BF16 of each.
@@ -470,7 +472,7 @@ int swin_wattn_block_norm_bwd(const void* y, const void* f, const void* dh, cons
  * eps >= 0, finite; workspace at least swin_wattn_clip_workspace_bytes(plan) bytes, 256-byte aligned,
  * overwritten, one call at a time per workspace. The squares are summed in 64 bits (fp32 within 64 bytes),
  * in an order that depends on the sizes alone: deterministic, without overflow. A NaN anywhere makes n and every
- * out NaN; an infinity makes n infinite, the finite values 0 and itself NaN. Two launches for each 1024 tensors;
+ * out NaN; an infinity makes n infinite, the finite values 0 and itself NaN. Two launches;
  * where all are in place and their factor is 1 nothing is written. Errors: BAD_PLAN; INVALID_ARG, MISALIGNED as
  * above; INVALID_ARG also where the plan's device is not the current one.
  */

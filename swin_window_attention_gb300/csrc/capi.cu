@@ -6,16 +6,17 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <unordered_set>
 #include <vector>
 
+#include "clip_grad.cuh"
 #include "common.cuh"
 #include "fp4.cuh"
 
 namespace swin {
-struct ClipTables;
 cudaError_t launch_bias_tables(const Plan& p, const float* table, bool with_mask, cudaStream_t st);
 bool fwd_fp8_applies(const Plan& pl);
 cudaError_t fwd_fp8_launch(const Plan& pl, const void* qkv8, float sq, float sk, float sv, void* out,
@@ -73,12 +74,6 @@ cudaError_t block_norm_bwd_launch(const void* y, const void* f, const void* dh, 
                                   void* dx, void* df, float* dpre_w, float* dpre_b, float* dpost_w, float* dpost_b,
                                   float* dgate, int tokens, int C, int samples, int dtype, int kind, float alpha,
                                   float eps, int accumulate, void* workspace, cudaStream_t st);
-ClipTables* clip_tables_make(const void* const* in, void* const* out, const int64_t* sizes, const int* dtypes, int count);
-void clip_tables_free(ClipTables* c);
-size_t clip_workspace_bytes(const ClipTables* c);
-int clip_launches(const ClipTables* c);
-cudaError_t clip_launch(const ClipTables* c, float max_norm, float scale, float eps, float* norm, void* workspace,
-                        cudaStream_t st);
 size_t fp4_workspace_bytes();
 cudaError_t fp4_quantize_launch(const void* x, void* codes, void* scales, float* tensor_scale, int rows, int K, int format,
                                 int dtype, bool scale_given, void* workspace, cudaStream_t st);
@@ -107,7 +102,8 @@ struct swin_wattn_plan_s {
 
 // A plan of swin_wattn_clip_plan.
 struct swin_wattn_clip_s {
-  swin::ClipTables* tables;
+  swin::ClipShape shape;
+  swin::ClipPiece* list;  // device memory, owned
   std::vector<std::pair<uint64_t, uint64_t>> spans;  // of all its bytes, joined and in order
   int device;
 };
@@ -913,24 +909,35 @@ int swin_wattn_clip_plan(swin_wattn_clip_t* plan, const void* const* grads, void
       end_any = std::max(end_any, s.end);
       if (s.written) end_written = std::max(end_written, s.end);
     }
-    swin_wattn_clip_s* pl = new swin_wattn_clip_s{nullptr, {}, dev};
-    try {
-      for (const Span& s : spans) {
-        if (pl->spans.empty() || s.begin > pl->spans.back().second)
-          pl->spans.push_back({s.begin, s.end});
-        else
-          pl->spans.back().second = std::max(pl->spans.back().second, s.end);
+    std::vector<swin::ClipPiece> list;
+    std::unique_ptr<swin_wattn_clip_s> pl(new swin_wattn_clip_s{{}, nullptr, {}, dev});
+    for (const Span& s : spans) {
+      if (pl->spans.empty() || s.begin > pl->spans.back().second)
+        pl->spans.push_back({s.begin, s.end});
+      else
+        pl->spans.back().second = std::max(pl->spans.back().second, s.end);
+    }
+    swin::clip_pieces(grads, outs, sizes, dtypes, count, &list, &pl->shape);
+    if (!list.empty()) {
+      const size_t bytes = list.size() * sizeof(swin::ClipPiece);
+      cudaError_t e = cudaMalloc(&pl->list, bytes);
+      if (e == cudaSuccess) {
+        e = cudaMemcpy(pl->list, list.data(), bytes, cudaMemcpyHostToDevice);
+        if (e != cudaSuccess) cudaFree(pl->list);
       }
-      pl->tables = swin::clip_tables_make(grads, outs, sizes, dtypes, count);
-      if (pl->tables == nullptr) throw std::bad_alloc();
+      if (e != cudaSuccess) {
+        cudaGetLastError();
+        return cuda_fail(e, "swin_wattn_clip_plan");
+      }
+    }
+    try {
       std::lock_guard<std::mutex> lk(g_plans_mu);
-      g_clips.insert(pl);
+      g_clips.insert(pl.get());
     } catch (...) {
-      swin::clip_tables_free(pl->tables);
-      delete pl;
+      cudaFree(pl->list);
       throw;
     }
-    *plan = pl;
+    *plan = pl.release();
   } catch (...) {
     swin::set_last_error("swin_wattn_clip_plan: out of host memory");
     return SWIN_WATTN_ERR_CUDA;
@@ -939,7 +946,7 @@ int swin_wattn_clip_plan(swin_wattn_clip_t* plan, const void* const* grads, void
 }
 
 size_t swin_wattn_clip_workspace_bytes(swin_wattn_clip_t plan) {
-  return check_clip(plan) == SWIN_WATTN_OK ? swin::clip_workspace_bytes(plan->tables) : 0;
+  return check_clip(plan) == SWIN_WATTN_OK ? swin::clip_workspace_bytes() : 0;
 }
 
 int swin_wattn_clip_grad_norm(swin_wattn_clip_t plan, float max_norm, float scale, float eps, float* norm, void* workspace,
@@ -949,7 +956,7 @@ int swin_wattn_clip_grad_norm(swin_wattn_clip_t plan, float max_norm, float scal
   if (!(max_norm >= 0.0f) || !std::isfinite(max_norm) || !(scale >= FLT_MIN) || !std::isfinite(scale) || !(eps >= 0.0f) ||
       !std::isfinite(eps) || workspace == nullptr)
     return SWIN_WATTN_ERR_INVALID_ARG;
-  if (workspace_bytes < swin::clip_workspace_bytes(plan->tables)) {
+  if (workspace_bytes < swin::clip_workspace_bytes()) {
     swin::set_last_error("swin_wattn_clip_grad_norm: workspace smaller than swin_wattn_clip_workspace_bytes(plan)");
     return SWIN_WATTN_ERR_INVALID_ARG;
   }
@@ -969,10 +976,10 @@ int swin_wattn_clip_grad_norm(swin_wattn_clip_t plan, float max_norm, float scal
       return SWIN_WATTN_ERR_INVALID_ARG;
     }
   }
-  const cudaError_t e = swin::clip_launch(plan->tables, max_norm, scale, eps, norm, workspace,
+  const cudaError_t e = swin::clip_launch(plan->list, plan->shape, max_norm, scale, eps, norm, workspace,
                                           reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_clip_grad_norm");
-  g_launches += swin::clip_launches(plan->tables);
+  g_launches += swin::clip_launches(plan->shape);
   return SWIN_WATTN_OK;
 }
 
@@ -982,7 +989,7 @@ int swin_wattn_clip_destroy(swin_wattn_clip_t plan) {
     std::lock_guard<std::mutex> lk(g_plans_mu);
     if (g_clips.erase(plan) == 0) return SWIN_WATTN_ERR_BAD_PLAN;
   }
-  swin::clip_tables_free(plan->tables);
+  if (plan->list != nullptr) cudaFree(plan->list);  // waits for what still reads it
   delete plan;
   return SWIN_WATTN_OK;
 }

@@ -1,16 +1,19 @@
 // The norm over all gradients of a model, and their clipping:
 //   n = scale |g|,   out = g * scale * min(1, max_norm / (n + eps))
-// over any number of fp32 and bf16 tensors of any size and alignment. The tensors are cut into
-// pieces, which blocks take in turn, so that one launch covers hundreds of tensors of all sizes;
-// their addresses and lengths travel as kernel parameters, a table of up to 1024 tensors a launch.
-// * squares_kernel: a block's sum of squares in 64 bits, one for each block, in the workspace.
+// over any number of fp32 and bf16 tensors of any size and alignment. A plan cuts the tensors into pieces, of which it
+// keeps a list in device memory, and blocks take pieces in turn, so that one launch covers hundreds of tensors of
+// all sizes. (With the tensors' addresses as kernel parameters and a search for each piece, whose steps miss the
+// constant cache one after the other, 196 M gradients took 225 us.)
+// * squares_kernel: a block's sum of squares, one for each block, in the workspace.
 // * scale_kernel: every block adds those up in the same order (the same bits on every run),
 //   forms the factor, and scales its pieces, from the last one back: what the first launch read
 //   last is still in L2.
 // Where the factor is 1 and the tensors are scaled in place there is nothing to write.
 #include <algorithm>
 #include <new>
+#include <vector>
 
+#include "clip_grad.cuh"
 #include "common.cuh"
 
 namespace swin {
@@ -20,43 +23,16 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxBlocks = 4 * 152;
 
-template <int N>
-struct Table {
-  const void* in[N];
-  void* out[N];
-  int64_t n_bf16[N];  // 2 * elements + (1 for bf16)
-  uint32_t first[N];  // the number of pieces before this tensor's
-  int count;
-  uint32_t pieces, piece;  // all pieces; elements of one
-};
-
-struct Piece {
-  const void* in;
-  void* out;
-  int64_t begin;
-  int len;
-  bool bf16;
-};
-
-// Piece number i: the last tensor whose first piece is at most i.
-template <int N>
-__device__ __forceinline__ Piece piece_of(const Table<N>& t, uint32_t i) {
-  int lo = 0, hi = t.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (t.first[mid] <= i)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  Piece p;
-  const int64_t n = t.n_bf16[lo] >> 1;
-  p.bf16 = t.n_bf16[lo] & 1;
-  p.in = t.in[lo];
-  p.out = t.out[lo];
-  p.begin = (int64_t)(i - t.first[lo]) * t.piece;
-  p.len = (int)min((int64_t)t.piece, n - p.begin);
-  return p;
+using Piece = ClipPiece;
+// One of the list, as two 16-byte reads.
+__device__ __forceinline__ Piece piece_at(const Piece* list, uint32_t i) {
+  union {
+    uint4 w[2];
+    Piece p;
+  } u;
+  u.w[0] = __ldg(reinterpret_cast<const uint4*>(list + i));
+  u.w[1] = __ldg(reinterpret_cast<const uint4*>(list + i) + 1);
+  return u.p;
 }
 
 __device__ __forceinline__ float value(const float* p) { return *p; }
@@ -84,30 +60,51 @@ __device__ __forceinline__ int head_of(const T* p, int len) {
 }
 
 constexpr int kLoads = 4;  // 16-byte loads of a thread in flight
+// A 16-byte read that L2 may drop at once, or keep.
+__device__ __forceinline__ uint4 read16(const uint4* p, bool keep) { return keep ? *p : __ldcs(p); }
 
-// The squares of up to 64 bytes a thread are summed in fp32 and joined to the block's sum in 64 bits.
-// That holds where the fp32 sum comes out between these bounds: no square has overflowed, and those
-// lost are nothing beside it. Else (tiny, huge or no values, NaN) they are summed again in 64 bits.
-__device__ __forceinline__ bool holds(float s) { return s >= 0x1p-60f && s <= 0x1p96f; }
+// A sum of squares: hi + lo in two fp32 parts (48 bits), and beside it `wide`, of those that fp32 does not hold. The GPU
+// adds two 64-bit numbers in the time of 64 fp32 additions: with 64-bit sums throughout, 1.2 M gradients took 21 us
+// and 393 MB of them were read at 5.8 TB/s.
+struct Sum {
+  float hi, lo;
+  double wide;
+};
+// hi + lo + v in two parts (Knuth's two-sum, then the parts brought in order).
+__device__ __forceinline__ void add(Sum& s, float v) {
+  const float t = __fadd_rn(s.hi, v), b = __fsub_rn(t, s.hi);
+  const float e = __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, b)), __fsub_rn(v, b));
+  s.lo = __fadd_rn(s.lo, e);
+  s.hi = t;
+}
+__device__ __forceinline__ void add(Sum& s, const Sum& o) {
+  add(s, o.hi);
+  s.lo = __fadd_rn(s.lo, o.lo);
+}
+
+// The squares of up to 64 bytes a thread are summed in fp32. That holds where the sum comes out between these bounds: no
+// square has overflowed, and those lost (below 2^-126 each) are below its rounding. Else (tiny, huge or no values,
+// NaN) they are summed again in 64 bits.
+__device__ __forceinline__ bool holds(float s) { return s >= 0x1p-94f && s <= 0x1p96f; }
 
 template <typename T>
-__device__ double squares(const T* p, int len) {
+__device__ void squares(const T* p, int len, bool keep, Sum& sum) {
   constexpr int kPer = 16 / sizeof(T);
   const int head = head_of(p, len), vecs = (len - head) / kPer, tail = head + vecs * kPer;
-  double sum = 0.0;
-  if ((int)threadIdx.x < head) {
-    const double v = value(p + threadIdx.x);
-    sum += v * v;
-  }
-  if (tail + (int)threadIdx.x < len) {
-    const double v = value(p + tail + threadIdx.x);
-    sum += v * v;
-  }
+  auto one = [&](const T* q) {
+    const float v = value(q), s = v * v;
+    if (holds(s))
+      add(sum, s);
+    else
+      sum.wide += (double)v * (double)v;
+  };
+  if ((int)threadIdx.x < head) one(p + threadIdx.x);
+  if (tail + (int)threadIdx.x < len) one(p + tail + threadIdx.x);
   const uint4* body = reinterpret_cast<const uint4*>(p + head);
   for (int i0 = threadIdx.x; i0 < vecs; i0 += kThreads * kLoads) {
     uint4 w[kLoads];
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) w[k] = i0 + k * kThreads < vecs ? body[i0 + k * kThreads] : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < kLoads; ++k) w[k] = i0 + k * kThreads < vecs ? read16(body + i0 + k * kThreads, keep) : make_uint4(0, 0, 0, 0);
     float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
@@ -118,46 +115,62 @@ __device__ double squares(const T* p, int len) {
     }
     const float all = s.x + s.y;
     if (holds(all)) {
-      sum += (double)all;
+      add(sum, all);
     } else {
       uint32_t bits = 0;
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) bits |= w[k].x | w[k].y | w[k].z | w[k].w;
-      if ((bits & 0x7fff7fffu) == 0) continue;  // zeros
-#pragma unroll 1
+      if ((bits & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu)) == 0) continue;  // zeros
+#pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         float v[kPer];
         unpack<T>(w[k], v);
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) sum = fma((double)v[e], (double)v[e], sum);
+#pragma unroll 1
+        for (int e = 0; e < kPer; ++e) sum.wide = fma((double)v[e], (double)v[e], sum.wide);
       }
     }
   }
-  return sum;
 }
 
 // The sum over the block, in every thread.
-__device__ __forceinline__ double block_sum(double v) {
-  __shared__ double warps[kThreads / 32];
+__device__ __forceinline__ Sum block_sum(Sum v) {
+  __shared__ Sum warps[kThreads / 32];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    Sum u;
+    u.hi = __shfl_xor_sync(0xffffffffu, v.hi, o);
+    u.lo = __shfl_xor_sync(0xffffffffu, v.lo, o);
+    add(v, u);
+  }
+  if (__any_sync(0xffffffffu, v.wide != 0.0)) {  // (NaN is not 0)
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) v.wide += __shfl_xor_sync(0xffffffffu, v.wide, o);
+  }
   if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0.0;
+  v = warps[0];
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) v += warps[w];
+  for (int w = 1; w < kThreads / 32; ++w) {
+    add(v, warps[w]);
+    if (warps[w].wide != 0.0) v.wide += warps[w].wide;
+  }
   return v;
 }
 
-template <int N>
-__global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ Table<N> t, double* partial) {
+__global__ void __launch_bounds__(kThreads)
+    squares_kernel(const Piece* __restrict__ list, uint32_t pieces, uint32_t keep_from, Sum* partial) {
   pdl_launch_dependents();
+  Piece next = piece_at(list, blockIdx.x);  // (the list was written when the plan was made)
   pdl_wait();
-  double sum = 0.0;
-  for (uint32_t i = blockIdx.x; i < t.pieces; i += gridDim.x) {
-    const Piece p = piece_of(t, i);
-    sum += p.bf16 ? squares(static_cast<const __nv_bfloat16*>(p.in) + p.begin, p.len)
-                  : squares(static_cast<const float*>(p.in) + p.begin, p.len);
+  Sum sum{0.0f, 0.0f, 0.0};
+  for (uint32_t i = blockIdx.x; i < pieces; i += gridDim.x) {
+    const Piece p = next;
+    if (i + gridDim.x < pieces) next = piece_at(list, i + gridDim.x);
+    const bool keep = i >= keep_from;
+    if (p.bf16)
+      squares(static_cast<const __nv_bfloat16*>(p.in), p.len, keep, sum);
+    else
+      squares(static_cast<const float*>(p.in), p.len, keep, sum);
   }
   sum = block_sum(sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
@@ -188,7 +201,7 @@ __device__ void scale_piece(const T* in, T* out, int len, float factor) {
     uint4 w[kLoads];
 #pragma unroll
     for (int k = 0; k < kLoads; ++k)
-      if (i0 + k * kThreads < vecs) w[k] = from[i0 + k * kThreads];
+      if (i0 + k * kThreads < vecs) w[k] = __ldcs(from + i0 + k * kThreads);
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
       if (i0 + k * kThreads >= vecs) break;
@@ -201,134 +214,97 @@ __device__ void scale_piece(const T* in, T* out, int len, float factor) {
         o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
       else
         o = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-      to[i0 + k * kThreads] = o;
+      __stcs(to + i0 + k * kThreads, o);
     }
   }
 }
 
-template <int N>
 __global__ void __launch_bounds__(kThreads)
-    scale_kernel(const __grid_constant__ Table<N> t, const double* partial, int n_partial, float max_norm, float scale,
-                 float eps, bool in_place, float* norm) {
+    scale_kernel(const Piece* __restrict__ list, uint32_t pieces, const Sum* partial, int n_partial, float max_norm,
+                 float scale, float eps, bool in_place, float* norm) {
   pdl_launch_dependents();
+  Piece next{};
+  if (blockIdx.x < pieces) next = piece_at(list, pieces - 1 - blockIdx.x);
   pdl_wait();
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < n_partial; i += kThreads) sum += __ldcg(partial + i);
-  const float n = (float)((double)scale * sqrt(block_sum(sum)));
+  Sum sum{0.0f, 0.0f, 0.0};
+  for (int i = threadIdx.x; i < n_partial; i += kThreads) {
+    const float4 raw = __ldcg(reinterpret_cast<const float4*>(partial) + i);
+    const Sum o = *reinterpret_cast<const Sum*>(&raw);
+    add(sum, o);
+    if (o.wide != 0.0) sum.wide += o.wide;
+  }
+  sum = block_sum(sum);
+  // the root of the fp32 sum, or where there is more, or it would be scaled out of fp32, that in 64 bits
+  float n = scale * __fsqrt_rn(sum.hi + sum.lo);
+  if (sum.wide != 0.0) n = (float)((double)scale * sqrt((double)sum.hi + (double)sum.lo + sum.wide));
   if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
   const float c = __fdiv_rn(max_norm, n + eps);
   const float factor = scale * (c > 1.0f ? 1.0f : c);  // NaN stays NaN
   if (in_place && factor == 1.0f) return;
-  for (uint32_t i = blockIdx.x; i < t.pieces; i += gridDim.x) {
-    const Piece p = piece_of(t, t.pieces - 1 - i);
+  for (uint32_t i = blockIdx.x; i < pieces; i += gridDim.x) {
+    const Piece p = next;
+    if (i + gridDim.x < pieces) next = piece_at(list, pieces - 1 - i - gridDim.x);
     if (p.bf16)
-      scale_piece(static_cast<const __nv_bfloat16*>(p.in) + p.begin, static_cast<__nv_bfloat16*>(p.out) + p.begin, p.len, factor);
+      scale_piece(static_cast<const __nv_bfloat16*>(p.in), static_cast<__nv_bfloat16*>(p.out), p.len, factor);
     else
-      scale_piece(static_cast<const float*>(p.in) + p.begin, static_cast<float*>(p.out) + p.begin, p.len, factor);
+      scale_piece(static_cast<const float*>(p.in), static_cast<float*>(p.out), p.len, factor);
   }
 }
 
-// Elements of a piece: some four pieces for each block that fits, of 2048 to 16384 elements (a thread's
-// loads are then 16 bytes times kLoads and a few times that).
-uint32_t piece_of_total(int64_t total) {
+// Elements of a piece: some four pieces for each block that fits, of 2048 to 16384 elements (a thread's loads are then 16
+// bytes times kLoads and a few times that), and more where the list would be longer than 2 MB.
+int64_t piece_of_total(int64_t total) {
   int64_t piece = 2048;
   while (piece < 16384 && total / piece > 4 * kMaxBlocks) piece *= 2;
-  return (uint32_t)piece;
+  while (total / piece > 65536) piece *= 2;
+  return piece;
 }
 
-constexpr int kFewEntries = 64, kManyEntries = 1024;
-
-template <int N>
-cudaError_t run(const Table<N>* tables, int n_tables, bool in_place, float max_norm, float scale, float eps, float* norm,
-                double* partial, cudaStream_t st) {
-  int n_partial = 0;
-  for (int i = 0; i < n_tables; ++i) {
-    const int blocks = (int)std::min<uint32_t>(tables[i].pieces, kMaxBlocks);
-    if (blocks == 0) continue;  // no elements at all: the norm is zero
-    const cudaError_t e = launch_pdl(squares_kernel<N>, dim3(blocks), dim3(kThreads), 0, st, tables[i], partial + n_partial);
-    if (e != cudaSuccess) return e;
-    n_partial += blocks;
-  }
-  for (int i = 0; i < n_tables; ++i) {
-    const int blocks = std::max(1, (int)std::min<uint32_t>(tables[i].pieces, kMaxBlocks));
-    const cudaError_t e = launch_pdl(scale_kernel<N>, dim3(blocks), dim3(kThreads), 0, st, tables[i], (const double*)partial,
-                                     n_partial, max_norm, scale, eps, in_place, i == 0 ? norm : (float*)nullptr);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
-}
-
-template <int N>
-Table<N>* make_tables(const void* const* in, void* const* out, const int64_t* sizes, const int* dtypes, int count,
-                      int n_tables, uint32_t piece) {
-  Table<N>* t = new (std::nothrow) Table<N>[n_tables]();
-  if (t == nullptr) return nullptr;
-  int k = 0;
-  for (int i = 0; i < n_tables; ++i) t[i].piece = piece;
-  for (int i = 0; i < count; ++i) {
-    if (sizes[i] == 0) continue;
-    if (t[k].count == N) ++k;
-    Table<N>& to = t[k];
-    to.in[to.count] = in[i];
-    to.out[to.count] = out[i];
-    to.n_bf16[to.count] = sizes[i] * 2 + (dtypes[i] == SWIN_WATTN_BF16 ? 1 : 0);
-    to.first[to.count++] = to.pieces;
-    to.pieces += (uint32_t)((sizes[i] + piece - 1) / piece);
-  }
-  return t;
-}
+// What the first launch leaves in L2 for the second: half of it. All other reads and the writes of the second may be dropped
+// at once. (392 MB in, as much out: 192 us without these hints, 182 with the reads' of the first launch, 179 with all.)
+constexpr int64_t kKeepBytes = 64 << 20;
 
 }  // namespace
 
-// A plan's tables. `few` or `many` by the number of tensors that have elements.
-struct ClipTables {
-  int n_tables;
-  bool in_place;
-  Table<kFewEntries>* few;
-  Table<kManyEntries>* many;
-};
-
-ClipTables* clip_tables_make(const void* const* in, void* const* out, const int64_t* sizes, const int* dtypes, int count) {
-  int64_t total = 0;
-  int used = 0;
-  bool in_place = true;
+// The list of a plan's pieces (may throw bad_alloc).
+void clip_pieces(const void* const* in, void* const* out, const int64_t* sizes, const int* dtypes, int count,
+                 std::vector<ClipPiece>* list, ClipShape* shape) {
+  int64_t total = 0, kept = 0;
+  shape->in_place = true;
   for (int i = 0; i < count; ++i) {
     total += sizes[i];
-    used += sizes[i] > 0;
-    in_place = in_place && (sizes[i] == 0 || in[i] == out[i]);
+    if (sizes[i] > 0 && in[i] != out[i]) shape->in_place = false;
   }
-  ClipTables* c = new (std::nothrow) ClipTables{};
-  if (c == nullptr) return nullptr;
-  const uint32_t piece = piece_of_total(total);
-  const int per = used <= kFewEntries ? kFewEntries : kManyEntries;
-  c->n_tables = std::max(1, (used + per - 1) / per);
-  c->in_place = in_place;
-  if (per == kFewEntries)
-    c->few = make_tables<kFewEntries>(in, out, sizes, dtypes, count, c->n_tables, piece);
-  else
-    c->many = make_tables<kManyEntries>(in, out, sizes, dtypes, count, c->n_tables, piece);
-  if (c->few == nullptr && c->many == nullptr) {
-    delete c;
-    return nullptr;
+  const int64_t piece = piece_of_total(total);
+  for (int i = 0; i < count; ++i) {
+    const bool bf16 = dtypes[i] == SWIN_WATTN_BF16;
+    for (int64_t at = 0; at < sizes[i]; at += piece) {
+      const int64_t bytes = at * (bf16 ? 2 : 4);
+      list->push_back({static_cast<const char*>(in[i]) + bytes, static_cast<char*>(out[i]) + bytes,
+                       (int)std::min(piece, sizes[i] - at), bf16 ? 1 : 0, 0, 0});
+    }
   }
-  return c;
+  shape->pieces = (uint32_t)list->size();
+  shape->keep_from = shape->pieces;
+  while (shape->keep_from > 0 && kept < kKeepBytes) {
+    const ClipPiece& p = (*list)[--shape->keep_from];
+    kept += (int64_t)p.len * (p.bf16 ? 2 : 4);
+  }
 }
-void clip_tables_free(ClipTables* c) {
-  if (c == nullptr) return;
-  delete[] c->few;
-  delete[] c->many;
-  delete c;
-}
-size_t clip_workspace_bytes(const ClipTables* c) { return (size_t)c->n_tables * kMaxBlocks * sizeof(double); }
-int clip_launches(const ClipTables* c) {
-  const uint32_t pieces = c->few != nullptr ? c->few->pieces : c->many->pieces;  // only a single table can be empty
-  return c->n_tables * 2 - (pieces == 0 ? 1 : 0);
-}
-cudaError_t clip_launch(const ClipTables* c, float max_norm, float scale, float eps, float* norm, void* workspace,
-                        cudaStream_t st) {
-  double* partial = static_cast<double*>(workspace);
-  return c->few != nullptr ? run(c->few, c->n_tables, c->in_place, max_norm, scale, eps, norm, partial, st)
-                           : run(c->many, c->n_tables, c->in_place, max_norm, scale, eps, norm, partial, st);
+
+size_t clip_workspace_bytes() { return kMaxBlocks * sizeof(Sum); }
+int clip_launches(const ClipShape& s) { return s.pieces == 0 ? 1 : 2; }
+
+cudaError_t clip_launch(const ClipPiece* list, const ClipShape& s, float max_norm, float scale, float eps, float* norm,
+                        void* workspace, cudaStream_t st) {
+  Sum* partial = static_cast<Sum*>(workspace);
+  const int blocks = (int)std::min<uint32_t>(s.pieces, kMaxBlocks);
+  if (blocks > 0) {
+    const cudaError_t e = launch_pdl(squares_kernel, dim3(blocks), dim3(kThreads), 0, st, list, s.pieces, s.keep_from, partial);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(scale_kernel, dim3(std::max(1, blocks)), dim3(kThreads), 0, st, list, s.pieces, (const Sum*)partial, blocks,
+                    max_norm, scale, eps, s.in_place, norm);
 }
 
 }  // namespace swin
