@@ -527,6 +527,19 @@ int swin_wattn_linear_fp4(const void* x_codes, const void* x_scales, const float
                           int tokens, int K, int N, int format, int act, int* status, struct CUstream_st* stream);
 
 /*
+ * The same for an x [tokens, K] that is not quantised, fp32 or bf16 by `dtype`: it is quantised into the workspace, as
+ * swin_wattn_fp4_quantize would (x_tensor_scale: the given scale of NVFP4, or NULL: taken from x; NULL for MXFP4).
+ *   workspace  at least swin_wattn_linear_fp4_workspace_bytes(tokens, K, format) bytes, 256-byte aligned, overwritten,
+ *          one call at a time per workspace (the query returns 0 for unsupported arguments).
+ * Two launches, or three for a scale that is taken from x.
+ */
+size_t swin_wattn_linear_fp4_workspace_bytes(int tokens, int K, int format);
+int swin_wattn_linear_fp4_of(const void* x, const float* x_tensor_scale, const void* w_codes, const void* w_scales,
+                             const float* w_tensor_scale, const float* b, const void* residual, void* y, int tokens, int K,
+                             int N, int format, int dtype, int act, void* workspace, size_t workspace_bytes, int* status,
+                             struct CUstream_st* stream);
+
+/*
  * Forward on 8-bit operands (7x7 windows, a SWIN_WATTN_BF16 plan): the attention of
  * q = scale_q * q8, k = scale_k * k8, v = scale_v * v8 for
  *   qkv8   device, 16-byte aligned: [B,H,W,3C] OCP FP8 E4M3 values, one byte each, in the

@@ -79,6 +79,8 @@ SIGNATURES = {
     "swin_wattn_fp4_quantize": ([_vp] * 4 + [_i] * 5 + [_vp, ctypes.c_size_t, _vp], _i),
     "swin_wattn_fp4_dequantize": ([_vp] * 4 + [_i] * 4 + [_vp], _i),
     "swin_wattn_linear_fp4": ([_vp] * 9 + [_i] * 5 + [_vp, _vp], _i),
+    "swin_wattn_linear_fp4_workspace_bytes": ([_i] * 3, ctypes.c_size_t),
+    "swin_wattn_linear_fp4_of": ([_vp] * 8 + [_i] * 6 + [_vp, ctypes.c_size_t, _vp, _vp], _i),
     "swin_wattn_fwd_fp8": ([_vp, _vp, ctypes.c_float, ctypes.c_float, ctypes.c_float, _vp, _vp], _i),
     "swin_wattn_set_fwd_kernel": ([_vp, _i], _i),
     "swin_wattn_fwd_kernel": ([_vp], _i),
@@ -407,6 +409,17 @@ def swin_wattn_linear_fp4(x_codes_ptr, x_scales_ptr, x_tensor_scale_ptr, w_codes
                                         status_ptr, stream)
 
 
+def swin_wattn_linear_fp4_workspace_bytes(tokens, K, format):
+    return int(load().swin_wattn_linear_fp4_workspace_bytes(tokens, K, format))
+
+
+def swin_wattn_linear_fp4_of(x_ptr, x_tensor_scale_ptr, w_codes_ptr, w_scales_ptr, w_tensor_scale_ptr, b_ptr, residual_ptr,
+                             y_ptr, tokens, K, N, format, dtype, act, workspace_ptr, workspace_bytes, status_ptr, stream):
+    return load().swin_wattn_linear_fp4_of(x_ptr, x_tensor_scale_ptr, w_codes_ptr, w_scales_ptr, w_tensor_scale_ptr, b_ptr,
+                                           residual_ptr, y_ptr, tokens, K, N, format, dtype, act, workspace_ptr,
+                                           workspace_bytes, status_ptr, stream)
+
+
 # The wrappers of the MLP's products and the weight update check their tensors: a small product
 # is over in a few microseconds, so the checks compare attributes first and look for the
 # reason only when one differs.
@@ -495,10 +508,17 @@ def _call(fn, dev, stream, status, *args):
 def _empty(shape, dtype, dev, stream):
     """A tensor of `stream`'s own memory pool (of the device's current stream without one),
     so that it may be used and freed in that stream's order."""
+    try:
+        device = _devices[dev]  # (torch takes two microseconds longer for a number)
+    except KeyError:
+        device = _devices.setdefault(dev, torch.device("cuda", dev))
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+_devices = {}
 
 
 def _act_code(act):
@@ -628,18 +648,15 @@ def _kind_code(kind):
     return code
 
 
-def _norm_params(name, wb, C, dev):
-    """The addresses of a norm's weight and bias, or of neither."""
-    if wb is None:
-        return None, None
-    w, b = wb
-    return (_address(name + " weight", w, (C,), _F32, dev),
-            None if b is None else _address(name + " bias", b, (C,), _F32, dev))
+def _vector(name, t, n, dev):
+    """The address of an fp32 vector of n values."""
+    if t.dtype is _F32 and t.get_device() == dev and t.numel() == n and t.dim() == 1 and t.is_contiguous():
+        return t.data_ptr()
+    return _address(name, t, (n,), _F32, dev)
 
 
-def _block_shape(x, f, post, gate, keep, alpha):
-    """Sizes of a block_norm call, checked: device, shape, tokens, C, samples."""
-    dev, shape = _device_of("x", x), x.shape
+def _block_shape(shape, f, post, gate, keep, alpha):
+    """Sizes of a block_norm call, checked: tokens, C, samples."""
     if not shape:
         raise ValueError("x has no dimensions")
     C = shape[-1]
@@ -648,12 +665,12 @@ def _block_shape(x, f, post, gate, keep, alpha):
         raise _too_large(tokens, C)
     if f is None and not (post is None and gate is None and keep is None and alpha == 1.0):
         raise ValueError("post, gate, keep and alpha belong to a block: f is None")
-    samples = 0
-    if keep is not None:
-        samples = keep.numel()
-        if samples < 1 or tokens % samples:
-            raise ValueError(f"keep has {samples} samples, which do not divide {tokens} tokens")
-    return dev, shape, tokens, C, samples
+    if keep is None:
+        return tokens, C, 0
+    samples = keep.numel()
+    if samples < 1 or tokens % samples:
+        raise ValueError(f"keep has {samples} samples, which do not divide {tokens} tokens")
+    return tokens, C, samples
 
 
 def block_norm(x, f=None, pre=None, post=None, gate=None, keep=None, alpha=1.0, kind="layer", eps=1e-5, y=None, h=None,
@@ -665,25 +682,38 @@ def block_norm(x, f=None, pre=None, post=None, gate=None, keep=None, alpha=1.0, 
     [C]; keep fp32 [samples], for equal runs of tokens (stochastic depth). kind: "layer" or "rms".
     Returns (y, h), y of x's dtype (into y, which may be x itself) or None without f, h in bf16 or
     None without pre."""
-    dev, shape, tokens, C, samples = _block_shape(x, f, post, gate, keep, alpha)
+    dev, shape, dtype = _device_of("x", x), x.shape, x.dtype
+    tokens, C, samples = _block_shape(shape, f, post, gate, keep, alpha)
     code = _float_code("x", x)
-    if f is None and pre is None:
+    pf = py = ph = pre_w = pre_b = post_w = post_b = None
+    if f is not None:
+        pf = _address("f", f, shape, _BF16, dev)
+        if y is None:
+            y = _empty(shape, dtype, dev, stream)
+        py = _address("y", y, shape, dtype, dev)
+    elif pre is None:
         raise ValueError("neither f nor pre is given: there is nothing to do")
-    if (f is None and y is not None) or (pre is None and h is not None):
-        raise ValueError("y needs f, and h needs pre")
-    if f is not None and y is None:
-        y = _empty(shape, x.dtype, dev, stream)
-    if pre is not None and h is None:
-        h = _empty(shape, _BF16, dev, stream)
-    pre_w, pre_b = _norm_params("pre", pre, C, dev)
-    post_w, post_b = _norm_params("post", post, C, dev)
-    _launch((_lib or load()).swin_wattn_block_norm, dev, stream, _plain("x", x, x.dtype, dev),
-            None if f is None else _address("f", f, shape, _BF16, dev), pre_w, pre_b, post_w, post_b,
-            None if gate is None else _address("gate", gate, (C,), _F32, dev),
-            None if keep is None else _address("keep", keep, (samples,), _F32, dev),
-            None if y is None else _address("y", y, shape, x.dtype, dev),
-            None if h is None else _address("h", h, shape, _BF16, dev), tokens, C, samples, code, _kind_code(kind),
-            float(alpha), float(eps))
+    elif y is not None:
+        raise ValueError("y needs f")
+    if pre is not None:
+        w, b = pre
+        pre_w = _vector("pre weight", w, C, dev)
+        if b is not None:
+            pre_b = _vector("pre bias", b, C, dev)
+        if h is None:
+            h = _empty(shape, _BF16, dev, stream)
+        ph = _address("h", h, shape, _BF16, dev)
+    elif h is not None:
+        raise ValueError("h needs pre")
+    if post is not None:
+        w, b = post
+        post_w = _vector("post weight", w, C, dev)
+        if b is not None:
+            post_b = _vector("post bias", b, C, dev)
+    _launch((_lib or load()).swin_wattn_block_norm, dev, stream, _plain("x", x, dtype, dev), pf, pre_w, pre_b, post_w, post_b,
+            None if gate is None else _vector("gate", gate, C, dev),
+            None if keep is None else _vector("keep", keep, samples, dev), py, ph, tokens, C, samples, code,
+            _kind_code(kind), alpha, eps)
     return y, h
 
 
@@ -699,7 +729,8 @@ def block_norm_bwd(y, f=None, dh=None, dy=None, pre=None, post=None, gate=None, 
     "pre_weight", "pre_bias", "post_weight", "post_bias", "gate". grads, such a dict: only these are
     computed, written there, or with accumulate added to. workspace: a uint8 tensor of
     swin_wattn_block_norm_bwd_workspace_bytes (allocated here when not given)."""
-    dev, shape, tokens, C, samples = _block_shape(y, f, post, gate, keep, alpha)
+    dev, shape, dtype = _device_of("y", y), y.shape, y.dtype
+    tokens, C, samples = _block_shape(shape, f, post, gate, keep, alpha)
     code = _float_code("y", y)
     if (dh is None) != (pre is None):
         raise ValueError("dh and pre belong together: one of them is None")
@@ -707,35 +738,49 @@ def block_norm_bwd(y, f=None, dh=None, dy=None, pre=None, post=None, gate=None, 
         raise ValueError("neither dh nor dy is given: there is no gradient")
     if f is None and df is not None:
         raise ValueError("df needs f")
-    there = {"pre_weight": pre is not None, "pre_bias": pre is not None and pre[1] is not None,
-             "post_weight": post is not None, "post_bias": post is not None and post[1] is not None,
-             "gate": gate is not None}
+    pf = pdh = pdf = pre_w = post_w = post_b = None
+    there = []
+    if pre is not None:
+        w, b = pre
+        pre_w, pdh = _vector("pre weight", w, C, dev), _address("dh", dh, shape, _BF16, dev)
+        there.append("pre_weight")
+        if b is not None:
+            there.append("pre_bias")
+    if post is not None:
+        w, b = post
+        post_w = _vector("post weight", w, C, dev)
+        there.append("post_weight")
+        if b is not None:
+            post_b = _vector("post bias", b, C, dev)
+            there.append("post_bias")
+    if gate is not None:
+        there.append("gate")
     if grads is None:
         if accumulate:
             raise ValueError("accumulate needs the grads to add to")
-        made = iter(_empty((sum(there.values()), C), _F32, dev, stream).unbind(0)) if any(there.values()) else None
-        grads = {k: next(made) for k in _NORM_GRADS if there[k]}
-    for k in grads:
-        if not there.get(k):
-            raise ValueError(f"grads has {k!r}, which the call has no parameter for")
+        if len(there) > 2:  # one allocation, cut, is cheaper than three
+            grads = dict(zip(there, _empty((len(there), C), _F32, dev, stream).unbind(0)))
+        else:
+            grads = {k: _empty((C,), _F32, dev, stream) for k in there}
+    else:
+        for k in grads:
+            if k not in there:
+                raise ValueError(f"grads has {k!r}, which the call has no parameter for")
     if dx is None:
-        dx = _empty(shape, y.dtype, dev, stream)
-    if f is not None and df is None:
-        df = _empty(shape, _BF16, dev, stream)
+        dx = _empty(shape, dtype, dev, stream)
+    if f is not None:
+        pf = _address("f", f, shape, _BF16, dev)
+        if df is None:
+            df = _empty(shape, _BF16, dev, stream)
+        pdf = _address("df", df, shape, _BF16, dev)
     if workspace is None:
         workspace = _empty((max(swin_wattn_block_norm_bwd_workspace_bytes(tokens, C), 1),), _U8, dev, stream)
-    pre_w, _ = _norm_params("pre", pre, C, dev)
-    post_w, post_b = _norm_params("post", post, C, dev)
-    _launch((_lib or load()).swin_wattn_block_norm_bwd, dev, stream, _plain("y", y, y.dtype, dev),
-            None if f is None else _address("f", f, shape, _BF16, dev),
-            None if dh is None else _address("dh", dh, shape, _BF16, dev),
-            None if dy is None else _address("dy", dy, shape, y.dtype, dev), pre_w, post_w, post_b,
-            None if gate is None else _address("gate", gate, (C,), _F32, dev),
-            None if keep is None else _address("keep", keep, (samples,), _F32, dev),
-            _address("dx", dx, shape, y.dtype, dev), None if df is None else _address("df", df, shape, _BF16, dev),
-            *(None if k not in grads else _address(k, grads[k], (C,), _F32, dev) for k in _NORM_GRADS), tokens, C, samples,
-            code, _kind_code(kind), float(alpha), float(eps), 1 if accumulate else 0,
-            _plain("workspace", workspace, _U8, dev), workspace.numel())
+    _launch((_lib or load()).swin_wattn_block_norm_bwd, dev, stream, _plain("y", y, dtype, dev), pf, pdh,
+            None if dy is None else _address("dy", dy, shape, dtype, dev), pre_w, post_w, post_b,
+            None if gate is None else _vector("gate", gate, C, dev),
+            None if keep is None else _vector("keep", keep, samples, dev), _address("dx", dx, shape, dtype, dev), pdf,
+            *[_vector(k, grads[k], C, dev) if k in grads else None for k in _NORM_GRADS], tokens, C, samples, code,
+            _kind_code(kind), alpha, eps, 1 if accumulate else 0, _plain("workspace", workspace, _U8, dev), workspace.numel())
     return dx, df, grads
 
 
@@ -789,29 +834,6 @@ class GradClip:
             pass
 
 
-class Fp4Tensor:
-    """A matrix [..., K] in microscaled 4-bit floating point: `codes`, a uint8 tensor [..., K / 2]; `scales`,
-    a flat uint8 tensor in the tensor core's tiles; `tensor_scale`, fp32 [1], of NVFP4 (else None);
-    `format`, NVFP4 or MXFP4; `shape`, of the matrix."""
-
-    __slots__ = ("codes", "scales", "tensor_scale", "format", "shape")
-
-    def __init__(self, codes, scales, tensor_scale, format, shape):
-        self.codes, self.scales, self.tensor_scale, self.format, self.shape = codes, scales, tensor_scale, format, shape
-
-    def _addresses(self, name, dev):
-        """Addresses of codes, scales and tensor scale, checked; rows and K."""
-        shape = self.shape
-        K = shape[-1]
-        rows, packed = _leading(shape, K // 2)
-        if rows > _INT_MAX or K > _INT_MAX:
-            raise _too_large(rows, K)
-        size = _scale_bytes(rows, K, self.format)
-        return (_address(name + ".codes", self.codes, packed, _U8, dev), _address(name + ".scales", self.scales, (size,), _U8, dev),
-                None if self.tensor_scale is None else _address(name + ".tensor_scale", self.tensor_scale, (1,), _F32, dev)
-                ), rows, K
-
-
 def _format_code(format):
     code = FP4_FORMATS.get(format) if type(format) is str else format
     if code is None or not NVFP4 <= code <= MXFP4:
@@ -819,79 +841,158 @@ def _format_code(format):
     return code
 
 
-def _scale_bytes(rows, K, format):
-    """swin_wattn_fp4_scale_bytes without a call."""
-    block = 32 if format else 16
-    return (rows + 127) // 128 * ((K // block + 3) // 4) * 512
+def _fp4_sizes(shape, fmt):
+    """Rows, K and the bytes of the scales of a matrix [..., K]."""
+    if not shape:
+        raise ValueError("the matrix has no dimensions")
+    K = shape[-1]
+    rows = shape[0] if len(shape) == 2 else shape[:-1].numel()
+    if rows > _INT_MAX or K > _INT_MAX:
+        raise _too_large(rows, K)
+    return rows, K, (rows + 127) // 128 * ((K // (32 if fmt else 16) + 3) // 4) * 512
+
+
+class Fp4Tensor:
+    """A matrix [..., K] in microscaled 4-bit floating point: `codes`, a uint8 tensor [..., K / 2]; `scales`,
+    a flat uint8 tensor in the tensor core's tiles; `tensor_scale`, fp32 [1], of NVFP4 (else None);
+    `format`, NVFP4 or MXFP4; `shape`, of the matrix. The tensors are checked here, once."""
+
+    __slots__ = ("_data", "_parts", "_at", "_dev", "_rows", "_K", "format", "shape")
+
+    def __init__(self, codes, scales, tensor_scale, format, shape):
+        self.format, self.shape = fmt, shape = _format_code(format), torch.Size(shape)
+        self._rows, self._K, size = _fp4_sizes(shape, fmt)
+        self._dev = dev = _device_of("codes", codes)
+        if (tensor_scale is None) != (fmt == MXFP4):
+            raise ValueError("NVFP4 has a scale of the tensor, MXFP4 has none")
+        self._data, self._parts = None, (codes, scales, tensor_scale)
+        self._at = (_address("codes", codes, (*shape[:-1], self._K // 2), _U8, dev), _address("scales", scales, (size,), _U8, dev),
+                    None if tensor_scale is None else _address("tensor_scale", tensor_scale, (1,), _F32, dev))
+
+    @classmethod
+    def _empty(cls, shape, fmt, scale, dev, stream):
+        """Room for a matrix, in one allocation: codes, scales, the tensor's scale (unless `scale` is it) and what
+        finding it takes, each from a multiple of 256 bytes on."""
+        self = cls.__new__(cls)
+        self.format, self.shape, self._dev = fmt, shape, dev
+        self._rows, self._K, size = _fp4_sizes(shape, fmt)
+        codes = (self._rows * (self._K // 2) + 255) & -256
+        own = fmt == NVFP4 and scale is None
+        self._data = data = _empty((codes + size + (256 + _fp4_scratch() if own else 0),), _U8, dev, stream)
+        p = data.data_ptr()
+        self._parts = scale
+        self._at = (p, p + codes, p + codes + size if own else None if scale is None else
+                    _address("scale", scale, (1,), _F32, dev))
+        return self
+
+    @property
+    def codes(self):
+        if self._data is None:
+            return self._parts[0]
+        return self._data[:self._rows * (self._K // 2)].view(*self.shape[:-1], self._K // 2)
+
+    @property
+    def scales(self):
+        if self._data is None:
+            return self._parts[1]
+        at = self._at[1] - self._at[0]
+        return self._data[at:at + _fp4_sizes(self.shape, self.format)[2]]
+
+    @property
+    def tensor_scale(self):
+        if self._data is None:
+            return self._parts[2]
+        if self._parts is not None or self.format == MXFP4:
+            return self._parts  # the given scale, or none
+        at = self._at[2] - self._at[0]
+        return self._data[at:at + 4].view(_F32)
+
+
+_scratch_bytes = None
+
+
+def _fp4_scratch():
+    global _scratch_bytes
+    if _scratch_bytes is None:
+        _scratch_bytes = swin_wattn_fp4_workspace_bytes()
+    return _scratch_bytes
 
 
 def quantize_fp4(x, format="nvfp4", scale=None, out=None, workspace=None, stream=None):
     """The bf16 or fp32 CUDA tensor x [..., K] in microscaled 4-bit floating point, an Fp4Tensor (`out` when given):
     "nvfp4", blocks of 16 with E4M3 scales and a scale of the tensor, or "mxfp4", blocks of 32 with powers
     of two. scale, fp32 [1], is the tensor's scale of NVFP4, calibrated ahead of time; without it it is taken
-    from x. workspace: a uint8 tensor of swin_wattn_fp4_workspace_bytes (allocated here when it is needed)."""
+    from x. workspace: a uint8 tensor of swin_wattn_fp4_workspace_bytes (part of the result when not given)."""
     dev, shape, fmt, code = _device_of("x", x), x.shape, _format_code(format), _float_code("x", x)
-    if not shape:
-        raise ValueError("x has no dimensions")
-    K = shape[-1]
-    rows, packed = _leading(shape, K // 2)
-    if rows > _INT_MAX or K > _INT_MAX:
-        raise _too_large(rows, K)
     if fmt == MXFP4 and scale is not None:
         raise ValueError("MXFP4 has no scale of the tensor")
     own = fmt == NVFP4 and scale is None
     if out is None:
-        ts = _empty((1,), _F32, dev, stream) if own else scale
-        out = Fp4Tensor(_empty(packed, _U8, dev, stream), _empty((_scale_bytes(rows, K, fmt),), _U8, dev, stream), ts, fmt, shape)
-    else:
-        if out.format != fmt or out.shape != shape:
-            raise ValueError(f"out is of format {out.format} and shape {tuple(out.shape)}, not {fmt} and {tuple(shape)}")
-        if scale is not None and out.tensor_scale is not scale:
-            raise ValueError("out.tensor_scale is not the given scale")
-    if own and workspace is None:
-        workspace = _empty((swin_wattn_fp4_workspace_bytes(),), _U8, dev, stream)
-    (codes, scales, ts), _, _ = out._addresses("out", dev)
-    _launch((_lib or load()).swin_wattn_fp4_quantize, dev, stream, _plain("x", x, x.dtype, dev), codes, scales, ts, rows, K,
-            fmt, code, 0 if own else 1, None if workspace is None else _plain("workspace", workspace, _U8, dev),
-            0 if workspace is None else workspace.numel())
+        out = Fp4Tensor._empty(shape, fmt, scale, dev, stream)
+    elif out.format != fmt or out.shape != shape:
+        raise ValueError(f"out is of format {out.format} and shape {tuple(out.shape)}, not {fmt} and {tuple(shape)}")
+    elif out._dev != dev:
+        raise ValueError(f"out is on cuda:{out._dev}, not on cuda:{dev}")
+    elif scale is not None and out.tensor_scale.data_ptr() != scale.data_ptr():
+        raise ValueError("out.tensor_scale is not the given scale")
+    ws, size = None, 0
+    if own:
+        if workspace is None and out._data is not None and out._parts is None:
+            ws, size = out._at[2] + 256, _fp4_scratch()
+        else:
+            if workspace is None:
+                workspace = _empty((_fp4_scratch(),), _U8, dev, stream)
+            ws, size = _plain("workspace", workspace, _U8, dev), workspace.numel()
+    _launch((_lib or load()).swin_wattn_fp4_quantize, dev, stream, _plain("x", x, x.dtype, dev), *out._at, out._rows, out._K,
+            fmt, code, 0 if own else 1, ws, size)
     return out
 
 
 def dequantize_fp4(q, dtype=torch.bfloat16, out=None, stream=None):
     """The values that an Fp4Tensor stands for, in bf16 or fp32 (into `out` when given)."""
-    dev = _device_of("q.codes", q.codes)
+    dev = q._dev
     if out is None:
         out = _empty(q.shape, dtype, dev, stream)
     code = _float_code("out", out)
-    (codes, scales, ts), rows, K = q._addresses("q", dev)
-    _launch((_lib or load()).swin_wattn_fp4_dequantize, dev, stream, codes, scales, ts,
-            _address("out", out, q.shape, out.dtype, dev), rows, K, q.format, code)
+    _launch((_lib or load()).swin_wattn_fp4_dequantize, dev, stream, *q._at, _address("out", out, q.shape, out.dtype, dev),
+            q._rows, q._K, q.format, code)
     return out
 
 
-def linear_fp4(x, w, b=None, act=ACT_NONE, residual=None, x_scale=None, y=None, status=None, stream=None):
+def linear_fp4(x, w, b=None, act=ACT_NONE, residual=None, x_scale=None, y=None, workspace=None, status=None, stream=None):
     """residual + act(x W^T + b) on 4-bit operands: w [N, K] an Fp4Tensor (a weight quantised once), x [..., K] an
-    Fp4Tensor of the same format, or a bf16 or fp32 CUDA tensor, which is quantised here (x_scale: its tensor's
-    scale for NVFP4, fp32 [1], else taken from x). The rest as for linear; y is bf16 [..., N]."""
-    if not isinstance(x, Fp4Tensor):
-        x = quantize_fp4(x, w.format, scale=x_scale, stream=stream)
-    elif x_scale is not None:
-        raise ValueError("x is quantised: it has its own scale")
-    if x.format != w.format:
-        raise ValueError(f"x and w have the formats {x.format} and {w.format}")
-    dev = _device_of("x.codes", x.codes)
-    xs, ws = x.shape, w.shape
-    if len(ws) != 2 or xs[-1] != ws[1]:
+    Fp4Tensor of the same format, or a bf16 or fp32 CUDA tensor, which is quantised on the way (x_scale: its tensor's
+    scale for NVFP4, fp32 [1], else taken from x; workspace: a uint8 tensor of swin_wattn_linear_fp4_workspace_bytes,
+    allocated here when not given). The rest as for linear; y is bf16 [..., N]."""
+    dev, ws, xs, fmt = w._dev, w.shape, x.shape, w.format
+    if len(ws) != 2 or not xs or xs[-1] != ws[1]:
         raise ValueError(f"x and w have shapes {tuple(xs)} and {tuple(ws)}: not [..., K] and [N, K]")
-    (xc, xsc, xts), tokens, K = x._addresses("x", dev)
-    (wc, wsc, wts), N, _ = w._addresses("w", dev)
-    _, shape = _leading(xs, N)
+    N, K = ws
+    tokens, shape = _leading(xs, N)
     if y is None:
         y = _empty(shape, _BF16, dev, stream)
-    _call((_lib or load()).swin_wattn_linear_fp4, dev, stream, status, xc, xsc, xts, wc, wsc, wts,
-          None if b is None else _address("b", b, (N,), _F32, dev),
-          None if residual is None else _address("residual", residual, shape, _BF16, dev),
-          _address("y", y, shape, _BF16, dev), tokens, K, N, x.format, _act_code(act))
+    rest = (None if b is None else _vector("b", b, N, dev),
+            None if residual is None else _address("residual", residual, shape, _BF16, dev),
+            _address("y", y, shape, _BF16, dev), tokens, K, N, fmt)
+    if isinstance(x, Fp4Tensor):
+        if x_scale is not None:
+            raise ValueError("x is quantised: it has its own scale")
+        if x.format != fmt:
+            raise ValueError(f"x and w have the formats {x.format} and {fmt}")
+        if x._dev != dev:
+            raise ValueError(f"x is on cuda:{x._dev}, not on cuda:{dev}")
+        _call((_lib or load()).swin_wattn_linear_fp4, dev, stream, status, *x._at, *w._at, *rest, _act_code(act))
+        return y
+    code = _float_code("x", x)
+    if tokens > _INT_MAX:
+        raise _too_large(tokens)
+    if x_scale is not None and fmt == MXFP4:
+        raise ValueError("MXFP4 has no scale of the tensor")
+    if workspace is None:
+        workspace = _empty((max((_lib or load()).swin_wattn_linear_fp4_workspace_bytes(tokens, K, fmt), 1),), _U8, dev, stream)
+    _call((_lib or load()).swin_wattn_linear_fp4_of, dev, stream, status, _plain("x", x, x.dtype, dev),
+          None if x_scale is None else _vector("x_scale", x_scale, 1, dev), *w._at, *rest, code, _act_code(act),
+          _plain("workspace", workspace, _U8, dev), workspace.numel())
     return y
 
 

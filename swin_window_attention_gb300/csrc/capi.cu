@@ -1068,6 +1068,62 @@ int swin_wattn_linear_fp4(const void* x_codes, const void* x_scales, const float
   return SWIN_WATTN_OK;
 }
 
+// The workspace of swin_wattn_linear_fp4_of: codes, scales, the tensor's scale, and what finding it takes.
+struct Fp4Workspace {
+  size_t scales, tensor_scale, scratch, bytes;
+};
+static Fp4Workspace fp4_workspace(int tokens, int K, int format) {
+  Fp4Workspace w;
+  w.scales = ((uint64_t)tokens * K / 2 + 255) / 256 * 256;
+  w.tensor_scale = w.scales + swin::fp4::scale_bytes(tokens, K, format);
+  w.scratch = w.tensor_scale + 256;
+  w.bytes = w.scratch + swin::fp4_workspace_bytes();
+  return w;
+}
+
+size_t swin_wattn_linear_fp4_workspace_bytes(int tokens, int K, int format) {
+  return tokens < 0 || tokens > kMaxLinearTokens || !fp4_width(K) || !fp4_format(format) ? 0 : fp4_workspace(tokens, K, format).bytes;
+}
+
+int swin_wattn_linear_fp4_of(const void* x, const float* x_tensor_scale, const void* w_codes, const void* w_scales,
+                             const float* w_tensor_scale, const float* b, const void* residual, void* y, int tokens, int K,
+                             int N, int format, int dtype, int act, void* workspace, size_t workspace_bytes, int* status,
+                             struct CUstream_st* stream) {
+  const bool nv = format == SWIN_WATTN_NVFP4, given = x_tensor_scale != nullptr;
+  if (tokens < 0 || !known_act(act) || !fp4_format(format) || !float_dtype(dtype) || (given && !nv) ||
+      nv != (w_tensor_scale != nullptr))
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  if (!fp4_width(K) || !linear_width(N) || tokens > kMaxLinearTokens) return SWIN_WATTN_ERR_UNSUPPORTED;
+  if (tokens == 0) return SWIN_WATTN_OK;
+  if (x == nullptr || w_codes == nullptr || w_scales == nullptr || y == nullptr || workspace == nullptr)
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  const Fp4Workspace ws = fp4_workspace(tokens, K, format);
+  if (workspace_bytes < ws.bytes) {
+    swin::set_last_error("swin_wattn_linear_fp4_of: workspace smaller than "
+                         "swin_wattn_linear_fp4_workspace_bytes(tokens, K, format)");
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  }
+  const uint64_t T = (uint64_t)tokens;
+  const Buffer bufs[] = {{residual, T * N * 2, 16, false}, {y, T * N * 2, 16, true},
+                         {x, T * K * (dtype == SWIN_WATTN_FP32 ? 4 : 2), 16, false}, {x_tensor_scale, 4, 4, false},
+                         {w_codes, (uint64_t)N * K / 2, 16, false}, {w_scales, swin::fp4::scale_bytes(N, K, format), 16, false},
+                         {w_tensor_scale, 4, 4, false}, {b, (uint64_t)N * 4, 4, false}, {status, 4, 4, true},
+                         {workspace, workspace_bytes, 256, true}};
+  const int rc = check_buffers("swin_wattn_linear_fp4_of", bufs, 10, 0, 1);
+  if (rc != SWIN_WATTN_OK) return rc;
+  unsigned char* at = static_cast<unsigned char*>(workspace);
+  float* scale = !nv ? nullptr : given ? const_cast<float*>(x_tensor_scale) : reinterpret_cast<float*>(at + ws.tensor_scale);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = swin::fp4_quantize_launch(x, at, at + ws.scales, scale, tokens, K, format, dtype, given, at + ws.scratch, st);
+  if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_linear_fp4_of");
+  g_launches += nv && !given ? 2 : 1;
+  e = swin::linear_fp4_launch({at, at + ws.scales, scale}, {w_codes, w_scales, w_tensor_scale}, b, residual, y, tokens, K, N,
+                              format, act, status, st);
+  if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_linear_fp4_of");
+  ++g_launches;
+  return SWIN_WATTN_OK;
+}
+
 int swin_wattn_set_fwd_kernel(swin_wattn_plan_t plan, int kernel) {
   int rc = check_plan(plan);
   if (rc != SWIN_WATTN_OK) return rc;

@@ -90,7 +90,7 @@ def test_quantize_with_a_given_scale():
     for ts in (2.0 ** -9, 0.5, 2.0 ** -14):  # with the last one every block saturates
         scale = torch.full((1,), ts, device=DEV)
         q = capi.quantize_fp4(x.to(DEV), "nvfp4", scale=scale)
-        assert q.tensor_scale is scale
+        assert q.tensor_scale.data_ptr() == scale.data_ptr()
         values = check_quantized(x, "nvfp4", q, ts)
         assert torch.equal(capi.dequantize_fp4(q, torch.float32).double().cpu(), values)
     # any positive scale: two roundings more at most
@@ -285,6 +285,7 @@ def test_bounded_waits(T, K, N):
 
     def call():
         ptrs = [t.data_ptr() for o in q for t in (o.codes, o.scales, o.tensor_scale)]
+        assert ptrs == [a for o in q for a in o._at]
         assert dbg.swin_wattn_linear_fp4(*ptrs, None, None, y.data_ptr(), T, K, N, capi.NVFP4, capi.ACT_NONE, status.data_ptr(),
                                          torch.cuda.current_stream().cuda_stream) == capi.OK
         torch.cuda.synchronize()
@@ -323,13 +324,12 @@ def test_refusals():
     with pytest.raises(capi.SwinWAttnError) as e:
         capi.linear_fp4(x, capi.quantize_fp4(_rand(2, 12, 64).to(DEV), "nvfp4"))
     assert e.value.status == capi.ERR_UNSUPPORTED
-    short = capi.Fp4Tensor(wq.codes, wq.scales[:-512], wq.tensor_scale, wq.format, wq.shape)
+    for parts in ((wq.codes, wq.scales[:-512], wq.tensor_scale), (wq.codes, wq.scales, None), (wq.codes[:, ::2], wq.scales,
+                  wq.tensor_scale), (wq.codes[:-1], wq.scales, wq.tensor_scale)):
+        with pytest.raises(ValueError):
+            capi.Fp4Tensor(*parts, "nvfp4", wq.shape)
     with pytest.raises(ValueError):
-        capi.linear_fp4(x, short)
-    other = capi.Fp4Tensor(wq.codes, wq.scales, None, wq.format, wq.shape)
-    with pytest.raises(capi.SwinWAttnError) as e:
-        capi.linear_fp4(x, other)
-    assert e.value.status == capi.ERR_INVALID_ARG
+        capi.Fp4Tensor(wq.codes, wq.scales, wq.tensor_scale, "mxfp4", wq.shape)
     odd = torch.empty(wq.codes.numel() + 1, dtype=torch.uint8, device=DEV)[1:].view_as(wq.codes)
     with pytest.raises(capi.SwinWAttnError) as e:
         capi.linear_fp4(x, capi.Fp4Tensor(odd, wq.scales, wq.tensor_scale, wq.format, wq.shape))
