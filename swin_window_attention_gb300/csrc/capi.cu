@@ -79,6 +79,10 @@ cudaError_t fp4_quantize_launch(const void* x, void* codes, void* scales, float*
                                 int dtype, bool scale_given, void* workspace, cudaStream_t st);
 cudaError_t fp4_dequantize_launch(const void* codes, const void* scales, const float* tensor_scale, void* out, int rows,
                                   int K, int format, int dtype, cudaStream_t st);
+bool linear_fp4_quantizes(int T, int K, int N, int format);
+cudaError_t linear_fp4_of_few(const void* x, int dtype, const float* x_scale, const Fp4Operand& w, const float* b,
+                              const void* residual, void* y, int T, int K, int N, int format, int act, int* status,
+                              cudaStream_t st);
 cudaError_t linear_fp4_launch(const Fp4Operand& x, const Fp4Operand& w, const float* b, const void* residual, void* y, int T,
                               int K, int N, int format, int act, int* status, cudaStream_t st);
 }  // namespace swin
@@ -1114,6 +1118,13 @@ int swin_wattn_linear_fp4_of(const void* x, const float* x_tensor_scale, const v
   unsigned char* at = static_cast<unsigned char*>(workspace);
   float* scale = !nv ? nullptr : given ? const_cast<float*>(x_tensor_scale) : reinterpret_cast<float*>(at + ws.tensor_scale);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if ((!nv || given) && swin::linear_fp4_quantizes(tokens, K, N, format)) {
+    const cudaError_t e = swin::linear_fp4_of_few(x, dtype, x_tensor_scale, {w_codes, w_scales, w_tensor_scale}, b, residual, y,
+                                                  tokens, K, N, format, act, status, st);
+    if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_linear_fp4_of");
+    ++g_launches;
+    return SWIN_WATTN_OK;
+  }
   cudaError_t e = swin::fp4_quantize_launch(x, at, at + ws.scales, scale, tokens, K, format, dtype, given, at + ws.scratch, st);
   if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_linear_fp4_of");
   g_launches += nv && !given ? 2 : 1;

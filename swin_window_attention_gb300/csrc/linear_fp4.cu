@@ -450,7 +450,8 @@ struct Fp4Tiling {
 
 // The cheapest tile by estimated clocks: rounds of tiles, each the longer of its chunks and its epilogue, plus
 // one epilogue that nothing overlaps. A chunk takes 100 and a clock for each 88 of its bytes (8192^3, clocks a chunk of
-// NVFP4: pairs with 192 columns 510, 128 columns 461; single SMs 609, 503).
+// NVFP4: pairs with 192 columns 510, 128 columns 461; single SMs 609, 503); of fewer than 32 tokens, whose missing rows
+// the copy engine fills in, 500 more (one token of 8192 x 8192: 18.9 us, 32 tokens: 10.4).
 Fp4Tiling choose(int64_t T, int64_t N, int K, int format) {
   Fp4Tiling best{1, 64, -1.0};
   const int chunks = (K + fp4::kChunk - 1) / fp4::kChunk;
@@ -459,8 +460,8 @@ Fp4Tiling choose(int64_t T, int64_t N, int K, int format) {
       const int64_t items = (T + cg * kBM - 1) / (cg * kBM) * ((N + nt - 1) / nt), groups = kSms / cg;
       const double rounds = (double)((items + groups - 1) / groups);
       const int sets = fp4::chunk_tiles(format) * fp4::kTileBytes * (1 + (128 % nt != 0 ? 2 : 1));
-      const double chunk = 100.0 + ((kBM + nt / cg) * 128 + sets) / 88.0, epi = 500.0 + 14.0 * nt;
-      const double cost = 5000.0 + rounds * std::max(chunks * chunk, epi) + epi + (cg - 1) * 500.0;
+      const double chunk = 100.0 + ((kBM + nt / cg) * 128 + sets) / 88.0 + (T < 32 ? 500.0 : 0.0), epi = 500.0 + 14.0 * nt;
+      const double cost = 4000.0 + rounds * std::max(chunks * chunk, epi) + epi + (cg - 1) * 500.0;
       if (best.cost < 0.0 || cost < best.cost) best = {cg, nt, cost};
     }
   return best;
@@ -544,7 +545,26 @@ cudaError_t launch_tiles4(int NT, const Fp4Operand& x, const Fp4Operand& w, cons
   return cudaLaunchKernelEx(&cfg, kern, a_map, b_map, out_map, aux_map, p);
 }
 
+// Above these, clusters never came out shorter.
+constexpr int kFewTokens4 = 128, kFewQuantized = 64;
+
 }  // namespace
+
+// Whether the product itself quantises an x that is not: few tokens, of which every CTA quantises its part of K, some 400
+// clocks for each 32 tokens of a chunk, against a launch of its own, some 4000. (One token 1536 -> 6144 5.3 us instead of
+// 7.2, 6144 -> 1536 6.4 and 9.9; 49 tokens 7.4 and 7.0, 8.8 and 10.4.)
+bool linear_fp4_quantizes(int T, int K, int N, int format) {
+  if (T > kFewQuantized) return false;
+  const FewFp4Tiling few = few_fp4_tiling(T, N, K);
+  return few.cost + few.chunk_rounds * ((T + 31) / 32) * 400.0 < choose(T, N, K, format).cost + 4000.0;
+}
+
+cudaError_t linear_fp4_of_few(const void* x, int dtype, const float* x_scale, const Fp4Operand& w, const float* b,
+                              const void* residual, void* y, int T, int K, int N, int format, int act, int* status,
+                              cudaStream_t st) {
+  return linear_fp4_few_launch(few_fp4_tiling(T, N, K), x, nullptr, dtype == SWIN_WATTN_FP32 ? 4 : 2, x_scale, w, b, residual, y,
+                               T, K, N, format, act, status, st);
+}
 
 cudaError_t linear_fp4_launch(const Fp4Operand& x, const Fp4Operand& w, const float* b, const void* residual, void* y, int T,
                               int K, int N, int format, int act, int* status, cudaStream_t st) {
@@ -557,6 +577,13 @@ cudaError_t linear_fp4_launch(const Fp4Operand& x, const Fp4Operand& w, const fl
   p.scale_w = w.tensor_scale;
   p.status = status;
   const Fp4Tiling t = choose(T, N, K, format);
+  // Few tokens as clusters where that is estimated shorter (clusters against tiles, codes of NVFP4: one token 6144 x 1536
+  // 6.8 and 8.0 us, 8192 x 8192 10.6 and 18.9, 384 x 1152 4.4 and 3.2).
+  if (T <= kFewTokens4) {
+    const FewFp4Tiling few = few_fp4_tiling(T, N, K);
+    if (few.cost < t.cost)
+      return linear_fp4_few_launch(few, x.codes, x.scales, 1, x.tensor_scale, w, b, residual, y, T, K, N, format, act, status, st);
+  }
   if (t.cg == 2)
     return format == 0 ? launch_tiles4<2, 0>(t.NT, x, w, residual, y, p, K, st)
                        : launch_tiles4<2, 1>(t.NT, x, w, residual, y, p, K, st);

@@ -7,6 +7,20 @@
 
 namespace swin {
 
+// The cluster-per-tile form for few tokens (linear_fp4_few.cu): TN tokens and 128 output channels per tile, `cluster` CTAs to
+// a tile, each over its part of K, the largest cluster with which every tile is resident at once. `cost` estimates the
+// time in SM clocks, on codes; chunk_rounds: the chunks that a CTA takes one after the other.
+struct FewFp4Tiling {
+  int TN, n_tiles, t_tiles, chunks, cluster;
+  double chunk_rounds, cost;
+};
+FewFp4Tiling few_fp4_tiling(int64_t T, int N, int K);
+// x: codes (x_bytes 1, with their scales), or bf16 or fp32 values (2, 4), which are quantised on the way; x_scale: the
+// tensor's scale of NVFP4.
+cudaError_t linear_fp4_few_launch(const FewFp4Tiling& t, const void* x, const void* x_scales, int x_bytes, const float* x_scale,
+                                  const Fp4Operand& w, const float* b, const void* residual, void* y, int T, int K, int N,
+                                  int format, int act, int* status, cudaStream_t st);
+
 namespace fp4 {
 
 // A chunk of K is 256 elements, a 128-byte row of codes, and takes four MMAs of 64; their scales are four
