@@ -650,8 +650,6 @@ def _kind_code(kind):
 
 def _vector(name, t, n, dev):
     """The address of an fp32 vector of n values."""
-    if t.dtype is _F32 and t.get_device() == dev and t.numel() == n and t.dim() == 1 and t.is_contiguous():
-        return t.data_ptr()
     return _address(name, t, (n,), _F32, dev)
 
 
@@ -690,7 +688,9 @@ def block_norm(x, f=None, pre=None, post=None, gate=None, keep=None, alpha=1.0, 
         pf = _address("f", f, shape, _BF16, dev)
         if y is None:
             y = _empty(shape, dtype, dev, stream)
-        py = _address("y", y, shape, dtype, dev)
+            py = y.data_ptr()
+        else:
+            py = _address("y", y, shape, dtype, dev)
     elif pre is None:
         raise ValueError("neither f nor pre is given: there is nothing to do")
     elif y is not None:
@@ -702,7 +702,9 @@ def block_norm(x, f=None, pre=None, post=None, gate=None, keep=None, alpha=1.0, 
             pre_b = _vector("pre bias", b, C, dev)
         if h is None:
             h = _empty(shape, _BF16, dev, stream)
-        ph = _address("h", h, shape, _BF16, dev)
+            ph = h.data_ptr()
+        else:
+            ph = _address("h", h, shape, _BF16, dev)
     elif h is not None:
         raise ValueError("h needs pre")
     if post is not None:
@@ -759,27 +761,35 @@ def block_norm_bwd(y, f=None, dh=None, dy=None, pre=None, post=None, gate=None, 
         if accumulate:
             raise ValueError("accumulate needs the grads to add to")
         if len(there) > 2:  # one allocation, cut, is cheaper than three
-            grads = dict(zip(there, _empty((len(there), C), _F32, dev, stream).unbind(0)))
+            room = _empty((len(there), C), _F32, dev, stream)
+            grads, at = dict(zip(there, room.unbind(0))), room.data_ptr()
+            pg = [at + 4 * C * there.index(k) if k in there else None for k in _NORM_GRADS]
         else:
             grads = {k: _empty((C,), _F32, dev, stream) for k in there}
+            pg = [grads[k].data_ptr() if k in grads else None for k in _NORM_GRADS]
     else:
         for k in grads:
             if k not in there:
                 raise ValueError(f"grads has {k!r}, which the call has no parameter for")
+        pg = [_vector(k, grads[k], C, dev) if k in grads else None for k in _NORM_GRADS]
     if dx is None:
         dx = _empty(shape, dtype, dev, stream)
+        pdx = dx.data_ptr()
+    else:
+        pdx = _address("dx", dx, shape, dtype, dev)
     if f is not None:
         pf = _address("f", f, shape, _BF16, dev)
         if df is None:
             df = _empty(shape, _BF16, dev, stream)
-        pdf = _address("df", df, shape, _BF16, dev)
+            pdf = df.data_ptr()
+        else:
+            pdf = _address("df", df, shape, _BF16, dev)
     if workspace is None:
         workspace = _empty((max(swin_wattn_block_norm_bwd_workspace_bytes(tokens, C), 1),), _U8, dev, stream)
     _launch((_lib or load()).swin_wattn_block_norm_bwd, dev, stream, _plain("y", y, dtype, dev), pf, pdh,
             None if dy is None else _address("dy", dy, shape, dtype, dev), pre_w, post_w, post_b,
             None if gate is None else _vector("gate", gate, C, dev),
-            None if keep is None else _vector("keep", keep, samples, dev), _address("dx", dx, shape, dtype, dev), pdf,
-            *[_vector(k, grads[k], C, dev) if k in grads else None for k in _NORM_GRADS], tokens, C, samples, code,
+            None if keep is None else _vector("keep", keep, samples, dev), pdx, pdf, *pg, tokens, C, samples, code,
             _kind_code(kind), alpha, eps, 1 if accumulate else 0, _plain("workspace", workspace, _U8, dev), workspace.numel())
     return dx, df, grads
 
@@ -816,10 +826,13 @@ class GradClip:
         dev = self.dev
         if norm is None:
             norm = _empty((1,), _F32, dev, stream)
+            pn = norm.data_ptr()
+        else:
+            pn = _address("norm", norm, (1,), _F32, dev)
         if workspace is None:
             workspace = self.workspace
-        _launch((_lib or load()).swin_wattn_clip_grad_norm, dev, stream, self.handle, float(max_norm), float(scale), float(eps),
-                _address("norm", norm, (1,), _F32, dev), _plain("workspace", workspace, _U8, dev), workspace.numel())
+        _launch((_lib or load()).swin_wattn_clip_grad_norm, dev, stream, self.handle, max_norm, scale, eps, pn,
+                _plain("workspace", workspace, _U8, dev), workspace.numel())
         return norm
 
     def close(self):
@@ -953,9 +966,11 @@ def dequantize_fp4(q, dtype=torch.bfloat16, out=None, stream=None):
     dev = q._dev
     if out is None:
         out = _empty(q.shape, dtype, dev, stream)
-    code = _float_code("out", out)
-    _launch((_lib or load()).swin_wattn_fp4_dequantize, dev, stream, *q._at, _address("out", out, q.shape, out.dtype, dev),
-            q._rows, q._K, q.format, code)
+        po = out.data_ptr()
+    else:
+        po = _address("out", out, q.shape, out.dtype, dev)
+    _launch((_lib or load()).swin_wattn_fp4_dequantize, dev, stream, *q._at, po, q._rows, q._K, q.format,
+            _float_code("out", out))
     return out
 
 
@@ -971,9 +986,11 @@ def linear_fp4(x, w, b=None, act=ACT_NONE, residual=None, x_scale=None, y=None, 
     tokens, shape = _leading(xs, N)
     if y is None:
         y = _empty(shape, _BF16, dev, stream)
+        py = y.data_ptr()
+    else:
+        py = _address("y", y, shape, _BF16, dev)
     rest = (None if b is None else _vector("b", b, N, dev),
-            None if residual is None else _address("residual", residual, shape, _BF16, dev),
-            _address("y", y, shape, _BF16, dev), tokens, K, N, fmt)
+            None if residual is None else _address("residual", residual, shape, _BF16, dev), py, tokens, K, N, fmt)
     if isinstance(x, Fp4Tensor):
         if x_scale is not None:
             raise ValueError("x is quantised: it has its own scale")
@@ -990,9 +1007,12 @@ def linear_fp4(x, w, b=None, act=ACT_NONE, residual=None, x_scale=None, y=None, 
         raise ValueError("MXFP4 has no scale of the tensor")
     if workspace is None:
         workspace = _empty((max((_lib or load()).swin_wattn_linear_fp4_workspace_bytes(tokens, K, fmt), 1),), _U8, dev, stream)
+        pw = workspace.data_ptr()
+    else:
+        pw = _plain("workspace", workspace, _U8, dev)
     _call((_lib or load()).swin_wattn_linear_fp4_of, dev, stream, status, _plain("x", x, x.dtype, dev),
-          None if x_scale is None else _vector("x_scale", x_scale, 1, dev), *w._at, *rest, code, _act_code(act),
-          _plain("workspace", workspace, _U8, dev), workspace.numel())
+          None if x_scale is None else _vector("x_scale", x_scale, 1, dev), *w._at, *rest, code, _act_code(act), pw,
+          workspace.numel())
     return y
 
 
