@@ -461,15 +461,16 @@ int swin_wattn_block_norm_bwd(const void* y, const void* f, const void* dh, cons
 /*
  * The norm over all gradients of a model and their clipping, between the gradients and the weight updates:
  *   n = scale * sqrt(sum of g^2 over all tensors),   out = g * scale * min(1, max_norm / (n + eps))
- * swin_wattn_clip_plan looks at the tensors once and keeps their addresses and sizes (a list in device memory, which
- * the plan owns; 32 bytes for some 2048 to 16384 elements, at most 2 MB and 32 bytes a tensor); the tensors
- * have to stay where they are while the plan is used, their values may change. Not to be called during a stream's
- * capture; swin_wattn_clip_destroy waits for the device.
+ * swin_wattn_clip_plan looks at the tensors once and writes a list of them, cut into pieces, into `list`, the caller's
+ * device memory of at least swin_wattn_clip_list_bytes(sizes, dtypes, count) bytes, 256-byte aligned (32 bytes for some 2048
+ * to 16384 elements); it copies to the device and waits for `stream`, so not during a capture. The tensors and the
+ * list have to stay where they are while the plan or a graph made with it is used, the tensors' values may change.
+ * The plan itself is host memory: swin_wattn_clip_destroy touches no device.
  *   grads, outs  `count` device pointers each, at any multiple of their element size; outs[i] may be
  *          grads[i] itself (in place), else it overlaps nothing; no tensor may be written twice;
  *   sizes  elements of each (0: the tensor is skipped); dtypes  SWIN_WATTN_FP32 or SWIN_WATTN_BF16 of each.
  * swin_wattn_clip_grad_norm runs it: norm (device fp32, or NULL) receives n; max_norm >= 0, scale > 0 and
- * eps >= 0, finite; workspace at least swin_wattn_clip_workspace_bytes(plan) bytes, 256-byte aligned,
+ * eps >= 0, finite; workspace at least swin_wattn_clip_workspace_bytes() bytes, 256-byte aligned,
  * overwritten, one call at a time per workspace. The squares are summed in 64 bits (fp32 within 64 bytes),
  * in an order that depends on the sizes alone: deterministic, without overflow. A NaN anywhere makes n and every
  * out NaN; an infinity makes n infinite, the finite values 0 and itself NaN. Two launches;
@@ -477,9 +478,10 @@ int swin_wattn_block_norm_bwd(const void* y, const void* f, const void* dh, cons
  * above; INVALID_ARG also where the plan's device is not the current one.
  */
 typedef struct swin_wattn_clip_s* swin_wattn_clip_t;
+size_t swin_wattn_clip_list_bytes(const int64_t* sizes, const int* dtypes, int count);
 int swin_wattn_clip_plan(swin_wattn_clip_t* plan, const void* const* grads, void* const* outs, const int64_t* sizes,
-                         const int* dtypes, int count);
-size_t swin_wattn_clip_workspace_bytes(swin_wattn_clip_t plan);
+                         const int* dtypes, int count, void* list, size_t list_bytes, struct CUstream_st* stream);
+size_t swin_wattn_clip_workspace_bytes(void);
 int swin_wattn_clip_grad_norm(swin_wattn_clip_t plan, float max_norm, float scale, float eps, float* norm, void* workspace,
                               size_t workspace_bytes, struct CUstream_st* stream);
 int swin_wattn_clip_destroy(swin_wattn_clip_t plan);

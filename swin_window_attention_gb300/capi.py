@@ -70,8 +70,9 @@ SIGNATURES = {
     "swin_wattn_block_norm": ([_vp] * 10 + [_i] * 5 + [ctypes.c_float] * 2 + [_vp], _i),
     "swin_wattn_block_norm_bwd_workspace_bytes": ([_i] * 2, ctypes.c_size_t),
     "swin_wattn_block_norm_bwd": ([_vp] * 16 + [_i] * 5 + [ctypes.c_float] * 2 + [_i, _vp, ctypes.c_size_t, _vp], _i),
-    "swin_wattn_clip_plan": ([ctypes.POINTER(_vp)] + [_vp] * 4 + [_i], _i),
-    "swin_wattn_clip_workspace_bytes": ([_vp], ctypes.c_size_t),
+    "swin_wattn_clip_list_bytes": ([_vp, _vp, _i], ctypes.c_size_t),
+    "swin_wattn_clip_plan": ([ctypes.POINTER(_vp)] + [_vp] * 4 + [_i, _vp, ctypes.c_size_t, _vp], _i),
+    "swin_wattn_clip_workspace_bytes": ([], ctypes.c_size_t),
     "swin_wattn_clip_grad_norm": ([_vp] + [ctypes.c_float] * 3 + [_vp, _vp, ctypes.c_size_t, _vp], _i),
     "swin_wattn_clip_destroy": ([_vp], _i),
     "swin_wattn_fp4_scale_bytes": ([_i] * 3, ctypes.c_size_t),
@@ -364,16 +365,21 @@ def swin_wattn_block_norm_bwd(y_ptr, f_ptr, dh_ptr, dy_ptr, pre_w_ptr, post_w_pt
                                             workspace_ptr, workspace_bytes, stream)
 
 
-def swin_wattn_clip_plan(grad_ptrs, out_ptrs, sizes, dtypes):
+def swin_wattn_clip_list_bytes(sizes, dtypes):
+    n = len(sizes)
+    return int(load().swin_wattn_clip_list_bytes((ctypes.c_int64 * n)(*sizes), (_i * n)(*dtypes), n))
+
+
+def swin_wattn_clip_plan(grad_ptrs, out_ptrs, sizes, dtypes, list_ptr, list_bytes, stream):
     """Returns (status, plan handle or None) for lists of device pointers, sizes and dtype codes."""
     n, h = len(grad_ptrs), _vp()
     rc = load().swin_wattn_clip_plan(ctypes.byref(h), (_vp * n)(*grad_ptrs), (_vp * n)(*out_ptrs),
-                                     (ctypes.c_int64 * n)(*sizes), (_i * n)(*dtypes), n)
+                                     (ctypes.c_int64 * n)(*sizes), (_i * n)(*dtypes), n, list_ptr, list_bytes, stream)
     return rc, (h.value if rc == OK else None)
 
 
-def swin_wattn_clip_workspace_bytes(plan):
-    return int(load().swin_wattn_clip_workspace_bytes(plan))
+def swin_wattn_clip_workspace_bytes():
+    return int(load().swin_wattn_clip_workspace_bytes())
 
 
 def swin_wattn_clip_grad_norm(plan, max_norm, scale, eps, norm_ptr, workspace_ptr, workspace_bytes, stream):
@@ -815,11 +821,16 @@ class GradClip:
         ins = [_plain(f"grads[{i}]", g, g.dtype, dev) for i, g in enumerate(self.grads)]
         outs = [_address(f"out[{i}]", o, g.shape, g.dtype, dev) for i, (g, o) in enumerate(zip(self.grads, self.out))]
         sizes = [g.numel() for g in self.grads]
+        size = swin_wattn_clip_list_bytes(sizes, codes)
+        # the list of the tensors' pieces, then the workspace, of the current stream's memory
+        room = _empty((size + swin_wattn_clip_workspace_bytes() + 256,), _U8, dev, None)
+        self._home = torch._C._cuda_getCurrentRawStream(dev)
         with torch.cuda.device(dev):
-            rc, self.handle = swin_wattn_clip_plan(ins, outs, sizes, codes)
+            rc, self.handle = swin_wattn_clip_plan(ins, outs, sizes, codes, room.data_ptr(), size, self._home)
         if rc != OK:
             raise SwinWAttnError("swin_wattn_clip_plan", rc)
-        self.workspace = torch.empty(swin_wattn_clip_workspace_bytes(self.handle), dtype=_U8, device=dev)
+        at = (size + 255) & -256
+        self._room, self.workspace = room, room[at:at + swin_wattn_clip_workspace_bytes()]
 
     def __call__(self, max_norm, scale=1.0, eps=1e-6, norm=None, workspace=None, stream=None):
         """Clips; returns the norm n, an fp32 tensor [1] (into norm when given)."""
@@ -831,6 +842,9 @@ class GradClip:
             pn = _address("norm", norm, (1,), _F32, dev)
         if workspace is None:
             workspace = self.workspace
+        if (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream) != self._home:
+            # the list is not given to anyone else while that stream may read it
+            self._room.record_stream(torch.cuda.current_stream(dev) if stream is None else stream)
         _launch((_lib or load()).swin_wattn_clip_grad_norm, dev, stream, self.handle, max_norm, scale, eps, pn,
                 _plain("workspace", workspace, _U8, dev), workspace.numel())
         return norm

@@ -107,7 +107,7 @@ struct swin_wattn_plan_s {
 // A plan of swin_wattn_clip_plan.
 struct swin_wattn_clip_s {
   swin::ClipShape shape;
-  swin::ClipPiece* list;  // device memory, owned
+  const swin::ClipPiece* list;  // device memory, the caller's
   std::vector<std::pair<uint64_t, uint64_t>> spans;  // of all its bytes, joined and in order
   int device;
 };
@@ -871,17 +871,30 @@ int swin_wattn_block_norm_bwd(const void* y, const void* f, const void* dh, cons
   return SWIN_WATTN_OK;
 }
 
+static bool clip_sizes(const int64_t* sizes, const int* dtypes, int count) {
+  if (count < 0 || count > 1 << 20 || (count > 0 && (sizes == nullptr || dtypes == nullptr))) return false;
+  for (int i = 0; i < count; ++i)
+    if (sizes[i] < 0 || sizes[i] > (int64_t)1 << 40 || !float_dtype(dtypes[i])) return false;
+  return true;
+}
+
+size_t swin_wattn_clip_list_bytes(const int64_t* sizes, const int* dtypes, int count) {
+  return clip_sizes(sizes, dtypes, count) ? std::max<size_t>(256, swin::clip_piece_count(sizes, count) * sizeof(swin::ClipPiece)) : 0;
+}
+
 int swin_wattn_clip_plan(swin_wattn_clip_t* plan, const void* const* grads, void* const* outs, const int64_t* sizes,
-                         const int* dtypes, int count) {
+                         const int* dtypes, int count, void* list, size_t list_bytes, struct CUstream_st* stream) {
   if (plan == nullptr) return SWIN_WATTN_ERR_INVALID_ARG;
   *plan = nullptr;
-  if (count < 0 || count > 1 << 20 || (count > 0 && (grads == nullptr || outs == nullptr || sizes == nullptr || dtypes == nullptr)))
+  if (!clip_sizes(sizes, dtypes, count) || list == nullptr || (count > 0 && (grads == nullptr || outs == nullptr)))
     return SWIN_WATTN_ERR_INVALID_ARG;
-  int dev = 0;
   for (int i = 0; i < count; ++i)
-    if (sizes[i] < 0 || sizes[i] > (int64_t)1 << 40 || !float_dtype(dtypes[i]) ||
-        (sizes[i] > 0 && (grads[i] == nullptr || outs[i] == nullptr)))
-      return SWIN_WATTN_ERR_INVALID_ARG;
+    if (sizes[i] > 0 && (grads[i] == nullptr || outs[i] == nullptr)) return SWIN_WATTN_ERR_INVALID_ARG;
+  if (list_bytes < swin_wattn_clip_list_bytes(sizes, dtypes, count)) {
+    swin::set_last_error("swin_wattn_clip_plan: list smaller than swin_wattn_clip_list_bytes(sizes, dtypes, count)");
+    return SWIN_WATTN_ERR_INVALID_ARG;
+  }
+  int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return SWIN_WATTN_ERR_INVALID_ARG;
@@ -892,12 +905,14 @@ int swin_wattn_clip_plan(swin_wattn_clip_t* plan, const void* const* grads, void
       bool written;
     };
     std::vector<Span> spans;
+    int rc = check_on_device(list, 256, dev);
+    if (rc != SWIN_WATTN_OK) return rc;
+    spans.push_back({reinterpret_cast<uintptr_t>(list), reinterpret_cast<uintptr_t>(list) + list_bytes, true});
     for (int i = 0; i < count; ++i) {
       if (sizes[i] == 0) continue;
       const uint64_t elem = dtypes[i] == SWIN_WATTN_FP32 ? 4 : 2, bytes = (uint64_t)sizes[i] * elem;
       for (const void* ptr : {grads[i], (const void*)outs[i]}) {
-        const int rc = check_on_device(ptr, elem, dev);
-        if (rc != SWIN_WATTN_OK) return rc;
+        if ((rc = check_on_device(ptr, elem, dev)) != SWIN_WATTN_OK) return rc;
       }
       const uint64_t in = reinterpret_cast<uintptr_t>(grads[i]), out = reinterpret_cast<uintptr_t>(outs[i]);
       spans.push_back({out, out + bytes, true});
@@ -913,34 +928,23 @@ int swin_wattn_clip_plan(swin_wattn_clip_t* plan, const void* const* grads, void
       end_any = std::max(end_any, s.end);
       if (s.written) end_written = std::max(end_written, s.end);
     }
-    std::vector<swin::ClipPiece> list;
-    std::unique_ptr<swin_wattn_clip_s> pl(new swin_wattn_clip_s{{}, nullptr, {}, dev});
+    std::vector<swin::ClipPiece> pieces;
+    std::unique_ptr<swin_wattn_clip_s> pl(new swin_wattn_clip_s{{}, static_cast<const swin::ClipPiece*>(list), {}, dev});
     for (const Span& s : spans) {
       if (pl->spans.empty() || s.begin > pl->spans.back().second)
         pl->spans.push_back({s.begin, s.end});
       else
         pl->spans.back().second = std::max(pl->spans.back().second, s.end);
     }
-    swin::clip_pieces(grads, outs, sizes, dtypes, count, &list, &pl->shape);
-    if (!list.empty()) {
-      const size_t bytes = list.size() * sizeof(swin::ClipPiece);
-      cudaError_t e = cudaMalloc(&pl->list, bytes);
-      if (e == cudaSuccess) {
-        e = cudaMemcpy(pl->list, list.data(), bytes, cudaMemcpyHostToDevice);
-        if (e != cudaSuccess) cudaFree(pl->list);
-      }
-      if (e != cudaSuccess) {
-        cudaGetLastError();
-        return cuda_fail(e, "swin_wattn_clip_plan");
-      }
+    swin::clip_pieces(grads, outs, sizes, dtypes, count, &pieces, &pl->shape);
+    if (!pieces.empty()) {
+      const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+      cudaError_t e = cudaMemcpyAsync(list, pieces.data(), pieces.size() * sizeof(swin::ClipPiece), cudaMemcpyHostToDevice, st);
+      if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+      if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_clip_plan");
     }
-    try {
-      std::lock_guard<std::mutex> lk(g_plans_mu);
-      g_clips.insert(pl.get());
-    } catch (...) {
-      cudaFree(pl->list);
-      throw;
-    }
+    std::lock_guard<std::mutex> lk(g_plans_mu);
+    g_clips.insert(pl.get());
     *plan = pl.release();
   } catch (...) {
     swin::set_last_error("swin_wattn_clip_plan: out of host memory");
@@ -949,8 +953,8 @@ int swin_wattn_clip_plan(swin_wattn_clip_t* plan, const void* const* grads, void
   return SWIN_WATTN_OK;
 }
 
-size_t swin_wattn_clip_workspace_bytes(swin_wattn_clip_t plan) {
-  return check_clip(plan) == SWIN_WATTN_OK ? swin::clip_workspace_bytes() : 0;
+size_t swin_wattn_clip_workspace_bytes(void) {
+  return swin::clip_workspace_bytes();
 }
 
 int swin_wattn_clip_grad_norm(swin_wattn_clip_t plan, float max_norm, float scale, float eps, float* norm, void* workspace,
@@ -961,7 +965,7 @@ int swin_wattn_clip_grad_norm(swin_wattn_clip_t plan, float max_norm, float scal
       !std::isfinite(eps) || workspace == nullptr)
     return SWIN_WATTN_ERR_INVALID_ARG;
   if (workspace_bytes < swin::clip_workspace_bytes()) {
-    swin::set_last_error("swin_wattn_clip_grad_norm: workspace smaller than swin_wattn_clip_workspace_bytes(plan)");
+    swin::set_last_error("swin_wattn_clip_grad_norm: workspace smaller than swin_wattn_clip_workspace_bytes()");
     return SWIN_WATTN_ERR_INVALID_ARG;
   }
   int dev = 0;
@@ -993,7 +997,6 @@ int swin_wattn_clip_destroy(swin_wattn_clip_t plan) {
     std::lock_guard<std::mutex> lk(g_plans_mu);
     if (g_clips.erase(plan) == 0) return SWIN_WATTN_ERR_BAD_PLAN;
   }
-  if (plan->list != nullptr) cudaFree(plan->list);  // waits for what still reads it
   delete plan;
   return SWIN_WATTN_OK;
 }

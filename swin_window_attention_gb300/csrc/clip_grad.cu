@@ -1,7 +1,7 @@
 // The norm over all gradients of a model, and their clipping:
 //   n = scale |g|,   out = g * scale * min(1, max_norm / (n + eps))
-// over any number of fp32 and bf16 tensors of any size and alignment. A plan cuts the tensors into pieces, of which it
-// keeps a list in device memory, and blocks take pieces in turn, so that one launch covers hundreds of tensors of
+// over any number of fp32 and bf16 tensors of any size and alignment. A plan cuts the tensors into pieces, of which there
+// is a list in device memory, and blocks take pieces in turn, so that one launch covers hundreds of tensors of
 // all sizes. (With the tensors' addresses as kernel parameters and a search for each piece, whose steps miss the
 // constant cache one after the other, 196 M gradients took 225 us.)
 // * squares_kernel: a block's sum of squares, one for each block, in the workspace.
@@ -265,6 +265,14 @@ int64_t piece_of_total(int64_t total) {
 constexpr int64_t kKeepBytes = 64 << 20;
 
 }  // namespace
+
+size_t clip_piece_count(const int64_t* sizes, int count) {
+  int64_t total = 0, n = 0;
+  for (int i = 0; i < count; ++i) total += sizes[i];
+  const int64_t piece = piece_of_total(total);
+  for (int i = 0; i < count; ++i) n += (sizes[i] + piece - 1) / piece;
+  return (size_t)n;
+}
 
 // The list of a plan's pieces (may throw bad_alloc).
 void clip_pieces(const void* const* in, void* const* out, const int64_t* sizes, const int* dtypes, int count,

@@ -21,6 +21,7 @@ struct ClipShape {
 
 void clip_pieces(const void* const* in, void* const* out, const int64_t* sizes, const int* dtypes, int count,
                  std::vector<ClipPiece>* list, ClipShape* shape);
+size_t clip_piece_count(const int64_t* sizes, int count);
 size_t clip_workspace_bytes();
 int clip_launches(const ClipShape& s);
 cudaError_t clip_launch(const ClipPiece* list, const ClipShape& s, float max_norm, float scale, float eps, float* norm,

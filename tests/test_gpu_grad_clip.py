@@ -143,6 +143,24 @@ def test_other_stream_replay_and_same_bits():
     assert all(torch.allclose(a.float(), b.float(), rtol=2.0 ** -7, atol=0.0) for a, b in zip(first, out))
 
 
+def test_plans_are_dropped_while_another_stream_reads_them():
+    """A plan's list outlives its calls on other streams: plans made, called and dropped, while new tensors take their
+    memory."""
+    s = torch.cuda.Stream()
+    grads = make([3000000], 9)
+    want = float(grads[0].double().square().sum()) ** 0.5
+    torch.cuda.synchronize()
+    norms = []
+    for _ in range(50):
+        clip = capi.GradClip(grads, out=[torch.empty_like(grads[0])])
+        norms.append(clip(1.0, stream=s))
+        n = clip._room.numel()
+        del clip
+        torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    assert all(abs(float(n) - want) < 1e-5 * want for n in norms)
+
+
 def test_refusals():
     a, b = torch.ones(100, device=DEV), torch.ones(50, device=DEV)
     with pytest.raises(ValueError):
@@ -170,13 +188,14 @@ def test_refusals():
         assert e.value.status == capi.ERR_INVALID_ARG
     with pytest.raises(capi.SwinWAttnError):
         clip(1.0, norm=a[3:4])
+    with pytest.raises(capi.SwinWAttnError):  # the norm in the plan's own list
+        clip(1.0, norm=clip._room[:4].view(torch.float32))
     with pytest.raises(capi.SwinWAttnError):
         clip(1.0, workspace=clip.workspace[:256])
     assert (a == 1).all() and (b == 1).all()
     h = clip.handle
     clip.close()
     assert capi.swin_wattn_clip_destroy(h) == capi.ERR_BAD_PLAN
-    assert capi.swin_wattn_clip_workspace_bytes(h) == 0
     with pytest.raises(capi.SwinWAttnError) as e:
         clip(1.0)
     assert e.value.status == capi.ERR_BAD_PLAN

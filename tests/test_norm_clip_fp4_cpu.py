@@ -100,11 +100,18 @@ def test_clip_plan_rejects_bad_arguments(lib):
     plan = lib.swin_wattn_clip_plan
     for grads, outs, sizes, dtypes in (([1 << 14], [1 << 14], [-1], [1]), ([1 << 14], [1 << 14], [4], [3]), ([None], [1 << 14], [4], [1]),
                                        ([1 << 14], [None], [4], [1]), ([1 << 14], [1 << 14], [2 ** 41], [1])):
-        rc, h = plan(grads, outs, sizes, dtypes)
+        rc, h = plan(grads, outs, sizes, dtypes, 1 << 16, 1 << 20, None)
         assert rc == lib.ERR_INVALID_ARG and h is None
+    for ptr, size in ((None, 1 << 20), (1 << 16, 16)):
+        rc, h = plan([1 << 14], [1 << 14], [4], [1], ptr, size, None)
+        assert rc == lib.ERR_INVALID_ARG and h is None
+    lb = lib.swin_wattn_clip_list_bytes
+    assert lb([-1], [1]) == 0 and lb([4], [7]) == 0 and lb([], []) == 256 and lb([0, 0], [0, 1]) == 256
+    assert lb([2048 * 9], [0]) == 32 * 9 and lb([2048 * 9 + 1] * 100, [0] * 100) == 32 * 1000
+    assert lb([2 ** 38], [1]) <= 2 << 20
     assert lib.swin_wattn_clip_grad_norm(None, 1.0, 1.0, 0.0, None, 1 << 14, 1 << 20, None) == lib.ERR_BAD_PLAN
     assert lib.swin_wattn_clip_grad_norm(1 << 14, 1.0, 1.0, 0.0, None, 1 << 14, 1 << 20, None) == lib.ERR_BAD_PLAN
-    assert lib.swin_wattn_clip_workspace_bytes(None) == 0 and lib.swin_wattn_clip_destroy(None) == lib.OK
+    assert lib.swin_wattn_clip_workspace_bytes() > 0 and lib.swin_wattn_clip_destroy(None) == lib.OK
     assert lib.swin_wattn_clip_destroy(1 << 14) == lib.ERR_BAD_PLAN
 
 
