@@ -132,27 +132,34 @@ __device__ void squares(const T* p, int len, bool keep, Sum& sum) {
   }
 }
 
-// The sum over the block, in every thread.
-__device__ __forceinline__ Sum block_sum(Sum v) {
-  __shared__ Sum warps[kThreads / 32];
+// Whether there are squares that fp32 does not hold (NaN among them). Of the bits: a comparison in 64 bits takes the time
+// of 64 others.
+__device__ __forceinline__ bool has_wide(const Sum& s) { return (__double2hiint(s.wide) | __double2loint(s.wide)) != 0; }
+
+template <int N>
+__device__ __forceinline__ void warp_sum(Sum& v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = N / 2; o > 0; o >>= 1) {
     Sum u;
     u.hi = __shfl_xor_sync(0xffffffffu, v.hi, o);
     u.lo = __shfl_xor_sync(0xffffffffu, v.lo, o);
     add(v, u);
   }
-  if (__any_sync(0xffffffffu, v.wide != 0.0)) {  // (NaN is not 0)
+  if (__any_sync(0xffffffffu, has_wide(v))) {
 #pragma unroll 1
-    for (int o = 16; o > 0; o >>= 1) v.wide += __shfl_xor_sync(0xffffffffu, v.wide, o);
+    for (int o = N / 2; o > 0; o >>= 1) v.wide += __shfl_xor_sync(0xffffffffu, v.wide, o);
   }
+}
+// The sum over the block, in the first warp.
+__device__ __forceinline__ Sum block_sum(Sum v) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ Sum warps[kWarps];
+  warp_sum<32>(v);
   if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = warps[0];
-#pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) {
-    add(v, warps[w]);
-    if (warps[w].wide != 0.0) v.wide += warps[w].wide;
+  if (threadIdx.x < 32) {
+    v = warps[threadIdx.x % kWarps];
+    warp_sum<kWarps>(v);
   }
   return v;
 }
@@ -231,15 +238,20 @@ __global__ void __launch_bounds__(kThreads)
     const float4 raw = __ldcg(reinterpret_cast<const float4*>(partial) + i);
     const Sum o = *reinterpret_cast<const Sum*>(&raw);
     add(sum, o);
-    if (o.wide != 0.0) sum.wide += o.wide;
+    if (has_wide(o)) sum.wide += o.wide;
   }
   sum = block_sum(sum);
-  // the root of the fp32 sum, or where there is more, or it would be scaled out of fp32, that in 64 bits
-  float n = scale * __fsqrt_rn(sum.hi + sum.lo);
-  if (sum.wide != 0.0) n = (float)((double)scale * sqrt((double)sum.hi + (double)sum.lo + sum.wide));
-  if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
-  const float c = __fdiv_rn(max_norm, n + eps);
-  const float factor = scale * (c > 1.0f ? 1.0f : c);  // NaN stays NaN
+  __shared__ float shared_factor;
+  if (threadIdx.x == 0) {
+    // the root of the fp32 sum, or where there is more, that in 64 bits
+    float n = scale * __fsqrt_rn(sum.hi + sum.lo);
+    if (has_wide(sum)) n = (float)((double)scale * sqrt((double)sum.hi + (double)sum.lo + sum.wide));
+    if (norm != nullptr && blockIdx.x == 0) *norm = n;
+    const float c = __fdiv_rn(max_norm, n + eps);
+    shared_factor = scale * (c > 1.0f ? 1.0f : c);  // NaN stays NaN
+  }
+  __syncthreads();
+  const float factor = shared_factor;
   if (in_place && factor == 1.0f) return;
   for (uint32_t i = blockIdx.x; i < pieces; i += gridDim.x) {
     const Piece p = next;
