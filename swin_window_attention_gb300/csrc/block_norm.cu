@@ -26,8 +26,9 @@ struct FwdParams {
 
 // A group takes kRows rows at a time: the parameters, as many bytes of a row as its own in bf16, are read from the
 // caches once for both, and one round of sums serves both. (A row at a time, 100352 x 192 with both norms, gate
-// and depth took 38 us, the load and store units 72 % busy.)
-constexpr int kRows = 2;
+// and depth took 38 us, the load and store units 72 % busy; 25088 x 768 with gate 32.6 us instead of 30.3.) One row where a
+// thread has three or four chunks, whose registers for two leave one block on an SM (2400 x 8192: 51 us, 38 with one).
+__host__ __device__ constexpr int rows_of(int lanes, int chunks) { return lanes == 0 && chunks >= 3 ? 1 : 2; }
 
 constexpr int kThreads = 256;  // of a block of groups that lie in warps
 
@@ -53,6 +54,7 @@ __global__ void __launch_bounds__(LANES == 0 ? 32 * kMaxWarps : kThreads) block_
   const int width = LANES == 0 ? blockDim.x : LANES;
   const int lane = LANES == 0 ? threadIdx.x : threadIdx.x % width;
   const int groups = LANES == 0 ? 1 : kThreads / width;
+  constexpr int kRows = rows_of(LANES, CH);
   int64_t row[kRows];  // neighbouring groups' first rows, then their second rows
   bool valid[kRows];
   int col[CH];
@@ -79,7 +81,12 @@ __global__ void __launch_bounds__(LANES == 0 ? 32 * kMaxWarps : kThreads) block_
 #pragma unroll
     for (int k = 0; k < kRows; ++k)
       keep[k] = p.keep != nullptr && valid[k] ? p.keep[(unsigned)row[k] / (unsigned)p.per_sample] : 1.0f;
-    if (p.post_w != nullptr) normalise_both<LANES, CH>(u[0], u[1], in, p.rms, p.inv_c, p.eps, sum);
+    if (p.post_w != nullptr) {
+      if constexpr (kRows == 2)
+        normalise_both<LANES, CH>(u[0], u[1], in, p.rms, p.inv_c, p.eps, sum);
+      else
+        normalise<LANES, CH>(u[0], in, p.rms, p.inv_c, p.eps, sum);
+    }
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       if (!in[j]) continue;
@@ -102,7 +109,10 @@ __global__ void __launch_bounds__(LANES == 0 ? 32 * kMaxWarps : kThreads) block_
     }
   }
   if (p.pre_w == nullptr) return;
-  normalise_both<LANES, CH>(v[0], v[1], in, p.rms, p.inv_c, p.eps, sum);
+  if constexpr (kRows == 2)
+    normalise_both<LANES, CH>(v[0], v[1], in, p.rms, p.inv_c, p.eps, sum);
+  else
+    normalise<LANES, CH>(v[0], in, p.rms, p.inv_c, p.eps, sum);
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     if (!in[j]) continue;
@@ -117,7 +127,7 @@ __global__ void __launch_bounds__(LANES == 0 ? 32 * kMaxWarps : kThreads) block_
 template <typename S>
 cudaError_t launch(const FwdParams& p, cudaStream_t st) {
   const Shape s = shape_of(p.C);
-  const int per_block = s.rows_per_block * kRows;
+  const int per_block = s.rows_per_block * rows_of(s.lanes, s.chunks);
   const dim3 grid((unsigned)(((int64_t)p.rows + per_block - 1) / per_block)), block(s.threads);
   auto go = [&](auto kern) { return launch_pdl(kern, grid, block, 0, st, p); };
   switch (s.lanes * 8 + s.chunks) {
