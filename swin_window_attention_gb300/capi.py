@@ -949,7 +949,7 @@ def quantize_fp4(x, format="nvfp4", scale=None, out=None, workspace=None, stream
     """The bf16 or fp32 CUDA tensor x [..., K] in microscaled 4-bit floating point, an Fp4Tensor (`out` when given):
     "nvfp4", blocks of 16 with E4M3 scales and a scale of the tensor, or "mxfp4", blocks of 32 with powers
     of two. scale, fp32 [1], is the tensor's scale of NVFP4, calibrated ahead of time; without it it is taken
-    from x. workspace: a uint8 tensor of swin_wattn_fp4_workspace_bytes (part of the result when not given)."""
+    from x and written to out's. workspace: a uint8 tensor of swin_wattn_fp4_workspace_bytes (part of the result when not given)."""
     dev, shape, fmt, code = _device_of("x", x), x.shape, _format_code(format), _float_code("x", x)
     if fmt == MXFP4 and scale is not None:
         raise ValueError("MXFP4 has no scale of the tensor")
@@ -962,6 +962,8 @@ def quantize_fp4(x, format="nvfp4", scale=None, out=None, workspace=None, stream
         raise ValueError(f"out is on cuda:{out._dev}, not on cuda:{dev}")
     elif scale is not None and out.tensor_scale.data_ptr() != scale.data_ptr():
         raise ValueError("out.tensor_scale is not the given scale")
+    elif own and out._data is not None and out._parts is not None:
+        raise ValueError("out was made with a given scale: pass it again (it is not overwritten)")
     ws, size = None, 0
     if own:
         if workspace is None and out._data is not None and out._parts is None:

@@ -93,6 +93,11 @@ def test_quantize_with_a_given_scale():
         assert q.tensor_scale.data_ptr() == scale.data_ptr()
         values = check_quantized(x, "nvfp4", q, ts)
         assert torch.equal(capi.dequantize_fp4(q, torch.float32).double().cpu(), values)
+    # a result that holds the caller's scale is only written with that scale
+    with pytest.raises(ValueError):
+        capi.quantize_fp4(x.to(DEV), "nvfp4", out=q)
+    assert float(scale) == 2.0 ** -14
+    assert capi.quantize_fp4(x.to(DEV), "nvfp4", scale=scale, out=q) is q
     # any positive scale: two roundings more at most
     scale = torch.full((1,), 4.8871 / 2688, device=DEV)
     q = capi.quantize_fp4(x.to(DEV), "nvfp4", scale=scale)
