@@ -429,7 +429,8 @@ int swin_wattn_orthogonalize(const void* g, void* out, int count, int rows, int 
  * Device pointers of the current device, 16-byte aligned unless stated. Arithmetic in fp32: the mean is
  * taken out before squares are summed; h is normalised from y before y is rounded. Squares are summed in
  * fp32: rows are right while C times the largest square is below 3e38. NaN and infinities stay in
- * their token (0 * NaN is NaN: a dropped sample's f counts). One launch, deterministic, nothing is allocated.
+ * their token (0 * NaN is NaN: a dropped sample's f counts). One launch, nothing is allocated. Deterministic: the order of
+ * a row's sums depends on the sizes, tokens among them, alone.
  * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED (C or tokens out of range).
  */
 int swin_wattn_block_norm(const void* x, const void* f, const float* pre_w, const float* pre_b, const float* post_w,

@@ -4,7 +4,11 @@
 // has both); either may be absent, and without f the kernel is a plain norm of x.
 // One pass: a row is read once, both norms' sums are taken in registers, y and h are written.
 // h is normalised from y in fp32, before y is rounded for its store: its one rounding is the one
-// to bf16.
+// to bf16. Bound by memory, 8 bytes an element of bf16 with f; what stood against it was the instructions of a row.
+// Two forms:
+// * block_norm_kernel: two rows to a group of threads, as many blocks as there are rows: few rows, fp32 streams, wide rows;
+// * block_norm_ring_kernel: resident blocks walk rows, the rows to come on their way through shared memory, the
+//   parameters kept there: many rows of a bf16 stream.
 #include "block_norm.cuh"
 
 namespace swin {
@@ -20,6 +24,7 @@ struct FwdParams {
   void* y;
   __nv_bfloat16* h;
   int rows, C, per_sample;
+  int stages;  // of the ring: rows of a group in shared memory
   bool rms, vec;
   float alpha, eps, inv_c;
 };
@@ -124,8 +129,166 @@ __global__ void __launch_bounds__(LANES == 0 ? 32 * kMaxWarps : kThreads) block_
   }
 }
 
+// ---- many rows ------------------------------------------------------------------------
+
+// One row to a group of threads at a time, up to 1536 channels in a warp, so that no barrier stands in a row's way: of
+// three chunks a thread and fewer four blocks an SM, of four three, of six two, above one of twelve warps. A row of 768 costs
+// half the instructions of block_norm_kernel's, which reads its parameters for two rows and then begins anew.
+__host__ __device__ constexpr int ring_threads(int chunks) { return chunks >= 8 ? 384 : 256; }
+__host__ __device__ constexpr int ring_blocks(int chunks) { return chunks <= 3 ? 4 : chunks == 4 ? 3 : chunks == 6 ? 2 : 1; }
+
+// Shared bytes of a thread's part of a row: x and, with F, f in bf16.
+__host__ __device__ constexpr int ring_bytes(int chunks, bool with_f) { return chunks * kV * (with_f ? 4 : 2); }
+
+// F, POST: whether there are a block's output and a norm behind it.
+template <int LANES, int CH, bool F, bool POST>
+__global__ void __launch_bounds__(ring_threads(CH), ring_blocks(CH)) block_norm_ring_kernel(const FwdParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  pdl_launch_dependents();
+  constexpr int kOwn = ring_threads(CH), kPer = kOwn / LANES, kStride = LANES * kV;
+  const int lane = threadIdx.x % LANES, own_row = threadIdx.x / LANES;
+  const int64_t step = (int64_t)gridDim.x * kPer;
+  RowSum<LANES> sum{nullptr};
+  // first the parameters, [CH][LANES] each: the norm before the next block, and post and gate in one
+  float4* const pre_w = reinterpret_cast<float4*>(smem);
+  float4* const pre_b = pre_w + CH * LANES;
+  float4* const behind_w = pre_b + CH * LANES;
+  float4* const behind_b = behind_w + CH * LANES;
+  // then the stages: for each thread CH chunks of x, then of f
+  unsigned char* const ring = smem + (F ? 4 : 2) * CH * LANES * 16;
+  auto slot = [&](int stage, int k) {
+    return reinterpret_cast<uint2*>(ring + stage * (ring_bytes(CH, F) * kOwn)) + k * kOwn + (int)threadIdx.x;
+  };
+  bool in[CH];
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    in[j] = (j * LANES + lane) * kV < p.C;
+    if (!in[j])  // chunks outside the row stay zero
+      for (int s = 0; s < p.stages; ++s) {
+        *slot(s, j) = make_uint2(0, 0);
+        if (F) *slot(s, CH + j) = make_uint2(0, 0);
+      }
+  }
+  pdl_wait();
+  int64_t row = (int64_t)blockIdx.x * kPer + own_row, ahead = row;  // the row to fetch next
+  const int64_t at0 = row * p.C + lane * kV, advance = step * p.C;
+  const __nv_bfloat16 *x_next = static_cast<const __nv_bfloat16*>(p.x) + at0, *f_next = p.f + at0;
+  auto fetch = [&](int stage) {
+    if (ahead < p.rows) {  // (behind the last row the slots keep what they hold; it is not stored)
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        if (!in[j]) continue;
+        copy_async<8>(slot(stage, j), x_next + j * kStride);
+        if (F) copy_async<8>(slot(stage, CH + j), f_next + j * kStride);
+      }
+    }
+    cp_async_commit();
+    ahead += step;
+    x_next += advance;
+    f_next += advance;
+  };
+  for (int s = 0; s < p.stages - 1; ++s) fetch(s);
+  for (int c = threadIdx.x; c < CH * LANES * kV; c += kOwn) {
+    const bool is = c < p.C;
+    if (p.pre_w != nullptr) {
+      reinterpret_cast<float*>(pre_w)[c] = is ? p.pre_w[c] : 0.0f;
+      reinterpret_cast<float*>(pre_b)[c] = is && p.pre_b != nullptr ? p.pre_b[c] : 0.0f;
+    }
+    if constexpr (F) {
+      const float g = is && p.gate != nullptr ? p.gate[c] : 1.0f;
+      reinterpret_cast<float*>(behind_w)[c] = POST && is ? p.post_w[c] * g : g;
+      reinterpret_cast<float*>(behind_b)[c] = POST && is && p.post_b != nullptr ? p.post_b[c] * g : 0.0f;
+    }
+  }
+  __syncthreads();
+  int stage = 0;
+  __nv_bfloat16 *y = static_cast<__nv_bfloat16*>(p.y) + at0, *h = p.h + at0;
+  for (int64_t row0 = row - own_row; row0 < p.rows; row0 += step, row += step, y += advance, h += advance) {
+    fetch(stage == 0 ? p.stages - 1 : stage - 1);
+    if (p.stages == 3)
+      cp_async_wait<2>();
+    else
+      cp_async_wait<1>();
+    const bool valid = row < p.rows;  // every thread takes part in the sums over the row
+    Four v[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) v[j] = unpack4(*slot(stage, j));
+    if constexpr (F) {
+      Four u[CH];
+#pragma unroll
+      for (int j = 0; j < CH; ++j) u[j] = unpack4(*slot(stage, CH + j));
+      if constexpr (POST) normalise<LANES, CH>(u, in, p.rms, p.inv_c, p.eps, sum);
+      const float keep = p.keep != nullptr && valid ? p.keep[(unsigned)row / (unsigned)p.per_sample] : 1.0f;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        if constexpr (POST)
+          u[j] = fma(u[j], unpack4(behind_w[j * LANES + lane]), unpack4(behind_b[j * LANES + lane]));
+        else if (p.gate != nullptr)
+          u[j] = mul(u[j], unpack4(behind_w[j * LANES + lane]));
+        v[j] = fma(v[j], p.alpha, mul(u[j], keep));
+        if (valid && in[j]) store4(y + j * kStride, v[j]);
+      }
+    }
+    if (p.pre_w != nullptr) {
+      normalise<LANES, CH>(v, in, p.rms, p.inv_c, p.eps, sum);
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+        if (valid && in[j]) store4(h + j * kStride, fma(v[j], unpack4(pre_w[j * LANES + lane]), unpack4(pre_b[j * LANES + lane])));
+    }
+    stage = stage == p.stages - 1 ? 0 : stage + 1;
+  }
+  cp_async_wait_all();
+}
+
+template <int LANES, int CH>
+cudaError_t launch_ring(FwdParams p, cudaStream_t st) {
+  const bool with_f = p.f != nullptr;
+  constexpr int kOwn = ring_threads(CH), kBlocks = ring_blocks(CH);
+  const int row = ring_bytes(CH, with_f) * kOwn, params = (with_f ? 4 : 2) * CH * LANES * 16;
+  p.stages = std::min(3, (kMaxSmem / kBlocks - 1024 - params) / row);  // (two at least, of twelve chunks with f)
+  const int smem = params + p.stages * row, blocks = 152 * kBlocks;
+  if (!with_f) return launch_rows<block_norm_ring_kernel<LANES, CH, false, false>>(p, blocks, kOwn, smem, st);
+  if (p.post_w == nullptr) return launch_rows<block_norm_ring_kernel<LANES, CH, true, false>>(p, blocks, kOwn, smem, st);
+  return launch_rows<block_norm_ring_kernel<LANES, CH, true, true>>(p, blocks, kOwn, smem, st);
+}
+
+// A group's lanes and chunks in the ring, of the least capacity, or none: rows of a bf16 stream, up to 1536 channels, three
+// at least for each group that is resident. (This form and the other, of norm and sum, with gate and depth, and with post
+// besides: 100352 x 192 26.0, 26.2, 26.9 us and 29.9, 33.7, 37.9; 25088 x 768 26.9, 28.2, 28.6 and 26.7, 30.2, 36.8; 12544 x
+// 1536 29.3, 30.3, 31.8 and 27.8, 31.6, 38.4; the norm alone 25088 x 768 15.6 and 20.1. Of a row a group, 2500 x 768,
+// 4.6, 5.0, 5.5 and 3.8, 4.2, 5.4; of fp32, 200704 x 192, 74.6, 76.1, 78.8 and 68.9, 70.7, 75.5.)
+Shape ring_of(int64_t rows, int C) {
+  const int n = C / kV;
+  for (int lanes = 4; lanes <= 32; lanes *= 2)
+    for (int ch : {2, 3, 4, 6, 8, 12})
+      if (n <= lanes * ch && (ch <= 3 || lanes == 32)) {
+        const int per = ring_threads(ch) / lanes;
+        if (rows < (int64_t)3 * 152 * ring_blocks(ch) * per) return {};
+        return {lanes, ch, ring_threads(ch), per};
+      }
+  return {};
+}
+
 template <typename S>
 cudaError_t launch(const FwdParams& p, cudaStream_t st) {
+  if constexpr (sizeof(S) == 2) {
+    const Shape r = ring_of(p.rows, p.C);
+    switch (r.lanes * 16 + r.chunks) {
+      case 4 * 16 + 2: return launch_ring<4, 2>(p, st);
+      case 4 * 16 + 3: return launch_ring<4, 3>(p, st);
+      case 8 * 16 + 2: return launch_ring<8, 2>(p, st);
+      case 8 * 16 + 3: return launch_ring<8, 3>(p, st);
+      case 16 * 16 + 2: return launch_ring<16, 2>(p, st);
+      case 16 * 16 + 3: return launch_ring<16, 3>(p, st);
+      case 32 * 16 + 2: return launch_ring<32, 2>(p, st);
+      case 32 * 16 + 3: return launch_ring<32, 3>(p, st);
+      case 32 * 16 + 4: return launch_ring<32, 4>(p, st);
+      case 32 * 16 + 6: return launch_ring<32, 6>(p, st);
+      case 32 * 16 + 8: return launch_ring<32, 8>(p, st);
+      case 32 * 16 + 12: return launch_ring<32, 12>(p, st);
+      default: break;
+    }
+  }
   const Shape s = shape_of(p.C);
   const int per_block = s.rows_per_block * rows_of(s.lanes, s.chunks);
   const dim3 grid((unsigned)(((int64_t)p.rows + per_block - 1) / per_block)), block(s.threads);

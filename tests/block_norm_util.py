@@ -44,7 +44,7 @@ def of_tokens(keep, T):
 
 def forward64(x, f, pre, post, gate, keep, alpha, kind, eps, stream):
     """(y, tolerance) and (h, tolerance), either None."""
-    y, ey = x.double(), torch.zeros(x.shape, dtype=torch.float64)
+    y, ey = x.double(), torch.zeros_like(x, dtype=torch.float64)
     first = None
     if f is not None:
         u, eu = f.double(), torch.zeros_like(y)

@@ -101,6 +101,37 @@ def test_many_tokens(T, C, stream):
     c.check_backward()
 
 
+# rows enough for the form that walks rows, in every row shape of its, a few more than fill its blocks evenly
+WALKED = [(116741, 8), (120003, 24), (116735, 40), (58403, 64), (58371, 96), (60000, 104), (29185, 128), (30001, 192), (14600, 256),
+          (14599, 264), (16000, 384), (10947, 512), (7299, 520), (9121, 768), (5475, 776), (7003, 1024), (5473, 1032), (6001, 1536)]
+
+
+@pytest.mark.parametrize("T,C", WALKED)
+def test_many_rows(T, C):
+    for i, block, post, gate, pre, kind in [(0, 1, 1, 1, 1, "layer"), (1, 1, 0, 1, 1, "layer"), (2, 1, 0, 0, 1, "rms"), (3, 0, 0, 0, 1, "layer"),
+                                            (4, 1, 1, 0, 0, "rms")]:
+        c = Case(T, C, kind=kind, block=block, post=post, gate=gate, pre=pre, samples=T if i < 2 else 0, alpha=1.0 if i else -2.5,
+                 bias=i != 2)
+        c.x[T // 2, 3], c.x[T - 1, C - 1] = float("nan"), float("-inf")
+        x, f = c.x.to(DEV), None if c.f is None else c.f.to(DEV)
+        y, h = capi.block_norm(x.clone(), f, **c.parts(DEV))
+        want = forward64(x, f, stream=c.stream, **c.parts(DEV))
+        fine = torch.ones(T, dtype=torch.bool, device=DEV)
+        fine[T // 2] = fine[T - 1] = False
+        for name, got, w in (("y", y, want[0]), ("h", h, want[1])):
+            assert (got is None) == (w is None)
+            if got is not None:
+                assert_close(name, got[fine], (w[0][fine].cpu(), w[1][fine].cpu()))
+                assert torch.equal(torch.isnan(got), torch.isnan(w[0]))
+        if block:  # over x, between guards
+            room = torch.zeros(T + 2, C, dtype=torch.bfloat16, device=DEV)
+            room[1:-1] = x
+            again, h2 = capi.block_norm(room[1:-1], f, y=room[1:-1], **c.parts(DEV))
+            assert torch.equal(again.view(torch.int16), y.view(torch.int16))
+            assert h is None or torch.equal(h2.view(torch.int16), h.view(torch.int16))
+            assert (room[0] == 0).all() and (room[-1] == 0).all()
+
+
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 @pytest.mark.parametrize("pre,post,gate,samples,bias,dy", list(itertools.product([0, 1], [0, 1], [0, 1], [0, 3], [0, 1], [0, 1])))
 def test_every_combination(kind, pre, post, gate, samples, bias, dy):
