@@ -6,9 +6,10 @@
 // h is normalised from y in fp32, before y is rounded for its store: its one rounding is the one
 // to bf16. Bound by memory, 8 bytes an element of bf16 with f; what stood against it was the instructions of a row.
 // Two forms:
-// * block_norm_kernel: two rows to a group of threads, as many blocks as there are rows: few rows, fp32 streams, wide rows;
+// * block_norm_kernel: two rows to a group of threads, as many blocks as that takes: fp32 streams, wide rows, few of middling
+//   width;
 // * block_norm_ring_kernel: resident blocks walk rows, the rows to come on their way through shared memory, the
-//   parameters kept there: many rows of a bf16 stream.
+//   parameters kept there: the others of a bf16 stream.
 #include "block_norm.cuh"
 
 namespace swin {
@@ -30,9 +31,9 @@ struct FwdParams {
 };
 
 // A group takes kRows rows at a time: the parameters, as many bytes of a row as its own in bf16, are read from the
-// caches once for both, and one round of sums serves both. (A row at a time, 100352 x 192 with both norms, gate
-// and depth took 38 us, the load and store units 72 % busy; 25088 x 768 with gate 32.6 us instead of 30.3.) One row where a
-// thread has three or four chunks, whose registers for two leave one block on an SM (2400 x 8192: 51 us, 38 with one).
+// caches once for both, and one round of sums serves both. (A row at a time, 25088 x 768 with gate took 32.6 us instead of
+// 30.3.) One row where a thread has three or four chunks, whose registers for two leave one block on an SM (2400 x 8192: 51
+// us, 38 with one).
 __host__ __device__ constexpr int rows_of(int lanes, int chunks) { return lanes == 0 && chunks >= 3 ? 1 : 2; }
 
 constexpr int kThreads = 256;  // of a block of groups that lie in warps
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(LANES == 0 ? 32 * kMaxWarps : kThreads) block_
   }
 }
 
-// ---- many rows ------------------------------------------------------------------------
+// ---- rows in turn ------------------------------------------------------------------------
 
 // One row to a group of threads at a time, up to 1536 channels in a warp, so that no barrier stands in a row's way: of
 // three chunks a thread and fewer four blocks an SM, of four three, of six two, above one of twelve warps. A row of 768 costs
@@ -244,26 +245,27 @@ template <int LANES, int CH>
 cudaError_t launch_ring(FwdParams p, cudaStream_t st) {
   const bool with_f = p.f != nullptr;
   constexpr int kOwn = ring_threads(CH), kBlocks = ring_blocks(CH);
-  const int row = ring_bytes(CH, with_f) * kOwn, params = (with_f ? 4 : 2) * CH * LANES * 16;
+  const int row = ring_bytes(CH, with_f) * kOwn, params = (with_f ? 4 : 2) * CH * LANES * 16, per = kOwn / LANES;
   p.stages = std::min(3, (kMaxSmem / kBlocks - 1024 - params) / row);  // (two at least, of twelve chunks with f)
-  const int smem = params + p.stages * row, blocks = 152 * kBlocks;
+  const int smem = params + p.stages * row, blocks = (int)std::min<int64_t>(152 * kBlocks, ((int64_t)p.rows + per - 1) / per);
   if (!with_f) return launch_rows<block_norm_ring_kernel<LANES, CH, false, false>>(p, blocks, kOwn, smem, st);
   if (p.post_w == nullptr) return launch_rows<block_norm_ring_kernel<LANES, CH, true, false>>(p, blocks, kOwn, smem, st);
   return launch_rows<block_norm_ring_kernel<LANES, CH, true, true>>(p, blocks, kOwn, smem, st);
 }
 
-// A group's lanes and chunks in the ring, of the least capacity, or none: rows of a bf16 stream, up to 1536 channels, three
-// at least for each group that is resident. (This form and the other, of norm and sum, with gate and depth, and with post
-// besides: 100352 x 192 26.0, 26.2, 26.9 us and 29.9, 33.7, 37.9; 25088 x 768 26.9, 28.2, 28.6 and 26.7, 30.2, 36.8; 12544 x
-// 1536 29.3, 30.3, 31.8 and 27.8, 31.6, 38.4; the norm alone 25088 x 768 15.6 and 20.1. Of a row a group, 2500 x 768,
-// 4.6, 5.0, 5.5 and 3.8, 4.2, 5.4; of fp32, 200704 x 192, 74.6, 76.1, 78.8 and 68.9, 70.7, 75.5.)
+// A group's lanes and chunks in the ring, of the least capacity, or none: rows of a bf16 stream, up to 384 channels, or up
+// to 1536 where there are two rows at least for each group that is resident. (This form and the other, of norm and sum, with
+// gate and depth, and with post besides: 100352 x 192 26.2, 26.2, 26.6 us and 29.9, 33.7, 37.9; 1000 x 192 2.2, 2.4, 2.5 and
+// 2.6, 3.5, 4.1; 25088 x 768 26.8, 28.2, 28.5 and 26.7, 30.2, 36.8; 4800 x 768 7.0, 7.7, 8.3 and 6.7, 8.2, 10.0; 2500 x 768
+// 4.6, 5.0, 5.6 and 3.9, 4.4, 5.4; 12544 x 1536 28.8, 29.7, 31.5 and 27.8, 31.6, 38.4; the norm alone 25088 x 768 15.5 and
+// 20.1. Of fp32, 200704 x 192, 74.6, 76.1, 78.8 and 68.9, 70.7, 75.5.)
 Shape ring_of(int64_t rows, int C) {
   const int n = C / kV;
   for (int lanes = 4; lanes <= 32; lanes *= 2)
     for (int ch : {2, 3, 4, 6, 8, 12})
       if (n <= lanes * ch && (ch <= 3 || lanes == 32)) {
         const int per = ring_threads(ch) / lanes;
-        if (rows < (int64_t)3 * 152 * ring_blocks(ch) * per) return {};
+        if (ch > 3 && rows < (int64_t)2 * 152 * ring_blocks(ch) * per) return {};
         return {lanes, ch, ring_threads(ch), per};
       }
   return {};
@@ -293,17 +295,22 @@ cudaError_t launch(const FwdParams& p, cudaStream_t st) {
   const int per_block = s.rows_per_block * rows_of(s.lanes, s.chunks);
   const dim3 grid((unsigned)(((int64_t)p.rows + per_block - 1) / per_block)), block(s.threads);
   auto go = [&](auto kern) { return launch_pdl(kern, grid, block, 0, st, p); };
-  switch (s.lanes * 8 + s.chunks) {
-    case 4 * 8 + 2: return go(block_norm_kernel<S, 4, 2>);
-    case 4 * 8 + 3: return go(block_norm_kernel<S, 4, 3>);
-    case 8 * 8 + 2: return go(block_norm_kernel<S, 8, 2>);
-    case 8 * 8 + 3: return go(block_norm_kernel<S, 8, 3>);
-    case 16 * 8 + 2: return go(block_norm_kernel<S, 16, 2>);
-    case 16 * 8 + 3: return go(block_norm_kernel<S, 16, 3>);
-    case 32 * 8 + 2: return go(block_norm_kernel<S, 32, 2>);
-    case 32 * 8 + 3: return go(block_norm_kernel<S, 32, 3>);
-    case 0 * 8 + 2: return go(block_norm_kernel<S, 0, 2>);
-    case 0 * 8 + 3: return go(block_norm_kernel<S, 0, 3>);
+  if constexpr (sizeof(S) == 4) {  // (in bf16 these walk)
+    switch (s.lanes * 8 + s.chunks) {
+      case 4 * 8 + 2: return go(block_norm_kernel<S, 4, 2>);
+      case 4 * 8 + 3: return go(block_norm_kernel<S, 4, 3>);
+      case 8 * 8 + 2: return go(block_norm_kernel<S, 8, 2>);
+      case 8 * 8 + 3: return go(block_norm_kernel<S, 8, 3>);
+      case 16 * 8 + 2: return go(block_norm_kernel<S, 16, 2>);
+      case 16 * 8 + 3: return go(block_norm_kernel<S, 16, 3>);
+      case 32 * 8 + 2: return go(block_norm_kernel<S, 32, 2>);
+      case 32 * 8 + 3: return go(block_norm_kernel<S, 32, 3>);
+      default: break;
+    }
+  }
+  switch (s.chunks) {
+    case 2: return go(block_norm_kernel<S, 0, 2>);
+    case 3: return go(block_norm_kernel<S, 0, 3>);
     default: return go(block_norm_kernel<S, 0, 4>);
   }
 }
