@@ -40,22 +40,23 @@ constexpr int kThreads = 256;  // of a block of groups that lie in warps
 
 // Of the least capacity: two or three chunks in a warp, four or six in the widest one (a row costs a warp some 250
 // instructions whatever it holds, and a block's warps a barrier for each sum besides: 25088 tokens of 768 channels in a
-// block of 96 threads 82 us without a norm behind, in a warp 46); in a block two up to 4096 channels, three or four
-// above (2304 channels: 93 us with two, 152 with six, whose registers leave nine warps an SM).
+// block of 96 threads 82 us without a norm behind, in a warp 46); then blocks of 4, 8 or 16 warps with two or three chunks,
+// above 6144 channels four. With up to 128 registers a thread four warps fit each quarter of an SM, 16 in all, which
+// blocks of six or nine warps do not fill (12544 x 1536 in blocks of 192 threads 74 us, with a norm behind 95).
 Shape shape_of(int C) {
   const int n = C / kV;
   for (int lanes = 4; lanes <= 32; lanes *= 2)
     for (int ch : {2, 3, 4, 6})
       if (n <= lanes * ch && (ch <= 3 || lanes == 32)) return {lanes, ch, kThreads, kThreads / lanes};
-  const auto threads = [&](int ch) { return ((n + ch - 1) / ch + 31) / 32 * 32; };
-  int ch = 2;
-  while (threads(ch) > 32 * kMaxWarps) ++ch;
-  return {0, ch, threads(ch), 1};
+  for (int threads = 128; threads <= 32 * kMaxWarps; threads *= 2)
+    for (int ch = 2; ch <= 3; ++ch)
+      if (n <= threads * ch) return {0, ch, threads, 1};
+  return {0, 4, 32 * kMaxWarps, 1};
 }
 
 // Blocks, and so the channel sums that each leaves: as many as are resident on 152 SMs by their registers.
 int blocks_of(int64_t rows, const Shape& s) {
-  const int per_sm = s.lanes != 0 ? (s.chunks >= 4 ? 1 : 2) : std::max(1, 576 / s.threads);
+  const int per_sm = s.lanes != 0 ? (s.chunks >= 4 ? 1 : 2) : 32 * kMaxWarps / s.threads;
   return (int)std::min<int64_t>(152 * per_sm, (rows + s.rows_per_block - 1) / s.rows_per_block);
 }
 
