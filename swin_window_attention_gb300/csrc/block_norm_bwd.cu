@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(kSumCols * kSumRows)
 }  // namespace
 
 size_t block_norm_bwd_workspace_bytes(int tokens, int C) {
-  return std::max<size_t>(256, (size_t)blocks_of(tokens, shape_of(C)) * kSums * C * 4);
+  const int blocks = std::max(blocks_of(tokens, shape_of(C, false)), blocks_of(tokens, shape_of(C, true)));
+  return std::max<size_t>(256, (size_t)blocks * kSums * C * 4);
 }
 
 cudaError_t block_norm_bwd_launch(const void* y, const void* f, const void* dh, const void* dy, const float* pre_w,
@@ -66,7 +67,7 @@ cudaError_t block_norm_bwd_launch(const void* y, const void* f, const void* dh, 
                                   void* dx, void* df, float* dpre_w, float* dpre_b, float* dpost_w, float* dpost_b,
                                   float* dgate, int tokens, int C, int samples, int dtype, int kind, float alpha,
                                   float eps, int accumulate, void* workspace, cudaStream_t st) {
-  const Shape s = shape_of(C);
+  const Shape s = shape_of(C, post_w != nullptr);
   const int blocks = blocks_of(tokens, s);
   BwdParams p{};
   p.y = y;

@@ -42,15 +42,16 @@ constexpr int kThreads = 256;  // of a block of groups that lie in warps
 // instructions whatever it holds, and a block's warps a barrier for each sum besides: 25088 tokens of 768 channels in a
 // block of 96 threads 82 us without a norm behind, in a warp 46); then blocks of 4, 8 or 16 warps with two or three chunks,
 // above 6144 channels four. With up to 128 registers a thread four warps fit each quarter of an SM, 16 in all, which
-// blocks of six or nine warps do not fill (12544 x 1536 in blocks of 192 threads 74 us, with a norm behind 95).
-Shape shape_of(int C) {
+// blocks of six or nine warps do not fill (8363 x 2304 in blocks of 288 threads 73 us, with a norm behind 94; 256: 56, 70).
+// 12544 x 1536 takes 60 us in blocks of 256 threads, 69 of 128 with three chunks; with a norm behind 80 and 69.
+Shape shape_of(int C, bool post) {
   const int n = C / kV;
   for (int lanes = 4; lanes <= 32; lanes *= 2)
     for (int ch : {2, 3, 4, 6})
       if (n <= lanes * ch && (ch <= 3 || lanes == 32)) return {lanes, ch, kThreads, kThreads / lanes};
   for (int threads = 128; threads <= 32 * kMaxWarps; threads *= 2)
     for (int ch = 2; ch <= 3; ++ch)
-      if (n <= threads * ch) return {0, ch, threads, 1};
+      if (n <= threads * ch && (threads > 128 || ch == 2 || post)) return {0, ch, threads, 1};
   return {0, 4, 32 * kMaxWarps, 1};
 }
 
