@@ -532,12 +532,13 @@ int swin_wattn_linear_fp4(const void* x_codes, const void* x_scales, const float
 /*
  * The same for an x [tokens, K] that is not quantised, fp32 or bf16 by `dtype`: it is quantised into the workspace, as
  * swin_wattn_fp4_quantize would (x_tensor_scale: the given scale of NVFP4, or NULL: taken from x; NULL for MXFP4).
- *   workspace  at least swin_wattn_linear_fp4_workspace_bytes(tokens, K, format) bytes, 256-byte aligned, overwritten,
- *          one call at a time per workspace (the query returns 0 for unsupported arguments).
- * Two launches, or three for a scale that is taken from x; one where 64 tokens at most, with no scale to take, are
- * quantised by the product itself (an estimate of both forms decides).
+ *   workspace  at least swin_wattn_linear_fp4_workspace_bytes(tokens, K, N, format, scale_given) bytes, 256-byte aligned,
+ *          overwritten, one call at a time per workspace; NULL where that is 0 (scale_given: whether x_tensor_scale
+ *          is; the query also returns 0 for unsupported arguments).
+ * Two launches, or three for a scale that is taken from x; one, without a workspace, where 64 tokens at most, with no scale to
+ * take, are quantised by the product itself (an estimate of both forms decides).
  */
-size_t swin_wattn_linear_fp4_workspace_bytes(int tokens, int K, int format);
+size_t swin_wattn_linear_fp4_workspace_bytes(int tokens, int K, int N, int format, int scale_given);
 int swin_wattn_linear_fp4_of(const void* x, const float* x_tensor_scale, const void* w_codes, const void* w_scales,
                              const float* w_tensor_scale, const float* b, const void* residual, void* y, int tokens, int K,
                              int N, int format, int dtype, int act, void* workspace, size_t workspace_bytes, int* status,

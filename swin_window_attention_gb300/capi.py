@@ -80,7 +80,7 @@ SIGNATURES = {
     "swin_wattn_fp4_quantize": ([_vp] * 4 + [_i] * 5 + [_vp, ctypes.c_size_t, _vp], _i),
     "swin_wattn_fp4_dequantize": ([_vp] * 4 + [_i] * 4 + [_vp], _i),
     "swin_wattn_linear_fp4": ([_vp] * 9 + [_i] * 5 + [_vp, _vp], _i),
-    "swin_wattn_linear_fp4_workspace_bytes": ([_i] * 3, ctypes.c_size_t),
+    "swin_wattn_linear_fp4_workspace_bytes": ([_i] * 5, ctypes.c_size_t),
     "swin_wattn_linear_fp4_of": ([_vp] * 8 + [_i] * 6 + [_vp, ctypes.c_size_t, _vp, _vp], _i),
     "swin_wattn_fwd_fp8": ([_vp, _vp, ctypes.c_float, ctypes.c_float, ctypes.c_float, _vp, _vp], _i),
     "swin_wattn_set_fwd_kernel": ([_vp, _i], _i),
@@ -415,8 +415,8 @@ def swin_wattn_linear_fp4(x_codes_ptr, x_scales_ptr, x_tensor_scale_ptr, w_codes
                                         status_ptr, stream)
 
 
-def swin_wattn_linear_fp4_workspace_bytes(tokens, K, format):
-    return int(load().swin_wattn_linear_fp4_workspace_bytes(tokens, K, format))
+def swin_wattn_linear_fp4_workspace_bytes(tokens, K, N, format, scale_given):
+    return int(load().swin_wattn_linear_fp4_workspace_bytes(tokens, K, N, format, scale_given))
 
 
 def swin_wattn_linear_fp4_of(x_ptr, x_tensor_scale_ptr, w_codes_ptr, w_scales_ptr, w_tensor_scale_ptr, b_ptr, residual_ptr,
@@ -994,7 +994,7 @@ def linear_fp4(x, w, b=None, act=ACT_NONE, residual=None, x_scale=None, y=None, 
     """residual + act(x W^T + b) on 4-bit operands: w [N, K] an Fp4Tensor (a weight quantised once), x [..., K] an
     Fp4Tensor of the same format, or a bf16 or fp32 CUDA tensor, which is quantised on the way (x_scale: its tensor's
     scale for NVFP4, fp32 [1], else taken from x; workspace: a uint8 tensor of swin_wattn_linear_fp4_workspace_bytes,
-    allocated here when not given). The rest as for linear; y is bf16 [..., N]."""
+    allocated here when needed and not given). The rest as for linear; y is bf16 [..., N]."""
     dev, ws, xs, fmt = w._dev, w.shape, x.shape, w.format
     if len(ws) != 2 or not xs or xs[-1] != ws[1]:
         raise ValueError(f"x and w have shapes {tuple(xs)} and {tuple(ws)}: not [..., K] and [N, K]")
@@ -1021,14 +1021,15 @@ def linear_fp4(x, w, b=None, act=ACT_NONE, residual=None, x_scale=None, y=None, 
         raise _too_large(tokens)
     if x_scale is not None and fmt == MXFP4:
         raise ValueError("MXFP4 has no scale of the tensor")
-    if workspace is None:
-        workspace = _empty((max((_lib or load()).swin_wattn_linear_fp4_workspace_bytes(tokens, K, fmt), 1),), _U8, dev, stream)
+    if workspace is not None:
+        pw, size = _plain("workspace", workspace, _U8, dev), workspace.numel()
+    elif size := (_lib or load()).swin_wattn_linear_fp4_workspace_bytes(tokens, K, N, fmt, x_scale is not None):
+        workspace = _empty((size,), _U8, dev, stream)
         pw = workspace.data_ptr()
     else:
-        pw = _plain("workspace", workspace, _U8, dev)
+        pw = None
     _call((_lib or load()).swin_wattn_linear_fp4_of, dev, stream, status, _plain("x", x, x.dtype, dev),
-          None if x_scale is None else _vector("x_scale", x_scale, 1, dev), *w._at, *rest, code, _act_code(act), pw,
-          workspace.numel())
+          None if x_scale is None else _vector("x_scale", x_scale, 1, dev), *w._at, *rest, code, _act_code(act), pw, size)
     return y
 
 

@@ -1088,8 +1088,14 @@ static Fp4Workspace fp4_workspace(int tokens, int K, int format) {
   return w;
 }
 
-size_t swin_wattn_linear_fp4_workspace_bytes(int tokens, int K, int format) {
-  return tokens < 0 || tokens > kMaxLinearTokens || !fp4_width(K) || !fp4_format(format) ? 0 : fp4_workspace(tokens, K, format).bytes;
+// Whether the product quantises x itself: there is no scale to take from all of x first.
+static bool fp4_in_product(int tokens, int K, int N, int format, bool scale_given) {
+  return (format != SWIN_WATTN_NVFP4 || scale_given) && swin::linear_fp4_quantizes(tokens, K, N, format);
+}
+
+size_t swin_wattn_linear_fp4_workspace_bytes(int tokens, int K, int N, int format, int scale_given) {
+  if (tokens <= 0 || tokens > kMaxLinearTokens || !fp4_width(K) || !linear_width(N) || !fp4_format(format)) return 0;
+  return fp4_in_product(tokens, K, N, format, scale_given != 0) ? 0 : fp4_workspace(tokens, K, format).bytes;
 }
 
 int swin_wattn_linear_fp4_of(const void* x, const float* x_tensor_scale, const void* w_codes, const void* w_scales,
@@ -1102,12 +1108,14 @@ int swin_wattn_linear_fp4_of(const void* x, const float* x_tensor_scale, const v
     return SWIN_WATTN_ERR_INVALID_ARG;
   if (!fp4_width(K) || !linear_width(N) || tokens > kMaxLinearTokens) return SWIN_WATTN_ERR_UNSUPPORTED;
   if (tokens == 0) return SWIN_WATTN_OK;
-  if (x == nullptr || w_codes == nullptr || w_scales == nullptr || y == nullptr || workspace == nullptr)
+  const bool in_product = fp4_in_product(tokens, K, N, format, given);
+  if (in_product) workspace = nullptr;  // (not looked at)
+  if (x == nullptr || w_codes == nullptr || w_scales == nullptr || y == nullptr || (!in_product && workspace == nullptr))
     return SWIN_WATTN_ERR_INVALID_ARG;
   const Fp4Workspace ws = fp4_workspace(tokens, K, format);
-  if (workspace_bytes < ws.bytes) {
+  if (!in_product && workspace_bytes < ws.bytes) {
     swin::set_last_error("swin_wattn_linear_fp4_of: workspace smaller than "
-                         "swin_wattn_linear_fp4_workspace_bytes(tokens, K, format)");
+                         "swin_wattn_linear_fp4_workspace_bytes(tokens, K, N, format, scale_given)");
     return SWIN_WATTN_ERR_INVALID_ARG;
   }
   const uint64_t T = (uint64_t)tokens;
@@ -1121,7 +1129,7 @@ int swin_wattn_linear_fp4_of(const void* x, const float* x_tensor_scale, const v
   unsigned char* at = static_cast<unsigned char*>(workspace);
   float* scale = !nv ? nullptr : given ? const_cast<float*>(x_tensor_scale) : reinterpret_cast<float*>(at + ws.tensor_scale);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if ((!nv || given) && swin::linear_fp4_quantizes(tokens, K, N, format)) {
+  if (in_product) {
     const cudaError_t e = swin::linear_fp4_of_few(x, dtype, x_tensor_scale, {w_codes, w_scales, w_tensor_scale}, b, residual, y,
                                                   tokens, K, N, format, act, status, st);
     if (e != cudaSuccess) return cuda_fail(e, "swin_wattn_linear_fp4_of");

@@ -551,12 +551,13 @@ constexpr int kFewTokens4 = 128, kFewQuantized = 64;
 }  // namespace
 
 // Whether the product itself quantises an x that is not: few tokens, of which every CTA quantises its part of K, some 400
-// clocks for each 32 tokens of a chunk, against a launch of its own, some 4000. (One token 1536 -> 6144 5.3 us instead of
-// 7.2, 6144 -> 1536 6.4 and 9.9; 49 tokens 7.4 and 7.0, 8.8 and 10.4.)
+// clocks for each 32 tokens of a chunk, against a launch of its own, some 4000 of the GPU and, where calls follow one another,
+// twice as many of the host, with its workspace; counted as 6000. (One token 1536 -> 6144 5.3 us instead of 7.2, 6144 -> 1536
+// 6.4 and 9.9; 49 tokens in a graph 8.0 and 6.9, called from Python 19 and 24; 6144 -> 1536 in a graph 8.8 and 10.4.)
 bool linear_fp4_quantizes(int T, int K, int N, int format) {
   if (T > kFewQuantized) return false;
   const FewFp4Tiling few = few_fp4_tiling(T, N, K);
-  return few.cost + few.chunk_rounds * ((T + 31) / 32) * 400.0 < choose(T, N, K, format).cost + 4000.0;
+  return few.cost + few.chunk_rounds * ((T + 31) / 32) * 400.0 < choose(T, N, K, format).cost + 6000.0;
 }
 
 cudaError_t linear_fp4_of_few(const void* x, int dtype, const float* x_scale, const Fp4Operand& w, const float* b,

@@ -62,8 +62,10 @@ def test_sizes(lib):
         for fmt in (0, 1):
             assert _fp4_sizes(torch.Size((rows, K)), fmt) == (rows, K, s(rows, K, fmt))
     w = lib.swin_wattn_linear_fp4_workspace_bytes
-    assert w(-1, 32, 0) == 0 and w(1, 40, 0) == 0 and w(1, 32, 5) == 0
-    assert w(7, 96, 0) >= 7 * 48 + s(7, 96, 0) + 4 + lib.swin_wattn_fp4_workspace_bytes()
+    assert w(-1, 32, 8, 0, 0) == 0 and w(1, 40, 8, 0, 0) == 0 and w(1, 32, 8, 5, 0) == 0 and w(1, 32, 9, 0, 0) == 0
+    assert w(7, 96, 8, 0, 0) >= 7 * 48 + s(7, 96, 0) + 4 + lib.swin_wattn_fp4_workspace_bytes()
+    assert w(1, 6144, 1536, 0, 1) == 0 and w(1, 6144, 1536, 1, 0) == 0  # quantised by the product
+    assert w(300, 96, 8, 0, 1) > 0 and w(300, 96, 8, 1, 0) > 0
 
 
 def test_fp4_rejects_bad_arguments_before_touching_cuda(lib):
