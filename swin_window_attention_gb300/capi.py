@@ -805,7 +805,8 @@ class GradClip:
     `grads` (of any sizes, contiguous), which are checked once and kept. Each call computes
     n = scale |grads| and writes grads * scale * min(1, max_norm / (n + eps)) to `out`, tensors of the
     same shapes and dtypes (the gradients themselves when not given). The plan's workspace serves one
-    stream at a time; a call may bring its own."""
+    stream at a time; a call may bring its own. A captured call reads the plan's list and, without one of its
+    own, its workspace on every replay: keep the plan as long as the graph."""
 
     handle = None
 
