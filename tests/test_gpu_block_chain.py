@@ -131,6 +131,22 @@ def _big(n, dtype=torch.bfloat16):
     return torch.randn(n, 8192, generator=g, device=DEV, dtype=torch.bfloat16).to(dtype)
 
 
+def test_walked_rows_past_32_bits():
+    T, C = 2900000, 1536  # 4.5e9 elements, in the form that walks rows
+    x = _big(T * C // 8192 + 1).view(-1)[:T * C].view(T, C)
+    f = x.roll(1, 0)
+    wb = (_rand(2, C, std=0.2, mean=1.0, dtype=torch.float32), _rand(3, C, std=0.2, dtype=torch.float32))
+    wbd, keep = tuple(t.to(DEV) for t in wb), (torch.arange(T, device=DEV) % 5).float()
+    r = torch.tensor(sorted({q for b in (0, 2 ** 31 // C, 2 ** 32 // C, T - 1) for q in (b - 1, b, b + 1) if 0 <= q < T}), device=DEV)
+    pick = lambda t: t[r].cpu()
+    xs, fs, ks = pick(x), pick(f), pick(keep)
+    y, h = capi.block_norm(x, f, pre=wbd, post=wbd, keep=keep, y=x)
+    want_y, want_h = forward64(xs, fs, wb, wb, None, ks, 1.0, "layer", 1e-5, torch.bfloat16)
+    assert_close("y", pick(y), want_y)
+    assert_close("h", pick(h), want_h)
+
+
+
 def test_norms_past_32_bits():
     T, C = 530000, 8192  # 4.3e9 elements
     x, f = _big(T), _big(T)
