@@ -53,10 +53,10 @@ Shape shape_of(int C) {
 
 template <typename S, int LANES, int CH>
 __global__ void __launch_bounds__(LANES == 0 ? 32 * kMaxWarps : kThreads) block_norm_kernel(const FwdParams p) {
-  __shared__ float2 slots[LANES == 0 ? 2 * kMaxWarps : 1];
+  __shared__ __align__(8) float slots[LANES == 0 ? 4 * kMaxWarps : 1];
   pdl_launch_dependents();
   pdl_wait();
-  RowSum<LANES> sum{slots};
+  RowSum<LANES, kHalves> sum{slots};
   const int width = LANES == 0 ? blockDim.x : LANES;
   const int lane = LANES == 0 ? threadIdx.x : threadIdx.x % width;
   const int groups = LANES == 0 ? 1 : kThreads / width;
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(ring_threads(CH), ring_blocks(CH)) block_norm_
   constexpr int kOwn = ring_threads(CH), kPer = kOwn / LANES, kStride = LANES * kV;
   const int lane = threadIdx.x % LANES, own_row = threadIdx.x / LANES;
   const int64_t step = (int64_t)gridDim.x * kPer;
-  RowSum<LANES> sum{nullptr};
+  RowSum<LANES, kHalves> sum{nullptr};
   // first the parameters, [CH][LANES] each: the norm before the next block, and post and gate in one
   float4* const pre_w = reinterpret_cast<float4*>(smem);
   float4* const pre_b = pre_w + CH * LANES;

@@ -63,9 +63,9 @@ int blocks_of(int64_t rows, const Shape& s) {
 
 // The gradient through a norm: r (g - [mean g] - vhat mean(g vhat)) + more, into g. Chunks outside the row hold zeros and
 // are left zero.
-template <int LANES, int CH>
+template <int LANES, int CH, int FORM>
 __device__ __forceinline__ void through_norm(Four (&g)[CH], const Four (&vhat)[CH], const Four (&more)[CH],
-                                             const bool (&in)[CH], float r, bool rms, float inv_c, RowSum<LANES>& sum) {
+                                             const bool (&in)[CH], float r, bool rms, float inv_c, RowSum<LANES, FORM>& sum) {
   Four a = g[0], b = mul(g[0], vhat[0]);
 #pragma unroll
   for (int j = 1; j < CH; ++j) {
@@ -95,13 +95,13 @@ __global__ void __launch_bounds__(LANES == 0 ? 32 * kMaxWarps : kThreads, LANES 
   using RawS = typename Raw<S>::T;
   constexpr int kWidth = LANES * CH * kV;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float2 slots[LANES == 0 ? 2 * kMaxWarps : 1];
+  __shared__ __align__(8) float slots[LANES == 0 ? 4 * kMaxWarps : 1];
   pdl_launch_dependents();
   const int threads = LANES == 0 ? blockDim.x : kThreads, width = LANES == 0 ? threads : LANES;
   const int lane = LANES == 0 ? threadIdx.x : threadIdx.x % width;
   const int per_block = LANES == 0 ? 1 : kThreads / width, own_row = LANES == 0 ? 0 : threadIdx.x / width;
   const int64_t step = (int64_t)gridDim.x * per_block;
-  RowSum<LANES> sum{slots};
+  RowSum<LANES, PRE && POST ? kEven : kWhole> sum{slots};
   // first the parameters of the row's channels, zeros outside it
   float4* const pre_w = reinterpret_cast<float4*>(smem);  // [CH][width]
   float4* const behind = pre_w + CH * width;
