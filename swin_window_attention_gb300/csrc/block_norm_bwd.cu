@@ -85,7 +85,7 @@ cudaError_t block_norm_bwd_launch(const void* y, const void* f, const void* dh, 
   p.C = C;
   p.per_sample = keep != nullptr && tokens > 0 ? tokens / samples : 1;
   p.rms = kind == SWIN_WATTN_NORM_RMS;
-  p.alpha = alpha;
+  p.alpha = f != nullptr ? alpha : 1.0f;  // (without f the forward does not use it)
   p.eps = eps;
   p.inv_c = 1.0f / (float)C;
   if (tokens > 0) {

@@ -231,6 +231,25 @@ def test_nan_and_infinity_stay_in_their_token():
     assert torch.isnan(g["pre_weight"]).any()
 
 
+def test_alpha_is_not_used_without_f():
+    """Of the C entries, whose forward without f is h = pre(x) whatever alpha says."""
+    c = Case(20, 96, block=False)
+    lib, p = capi.load(), c.parts(DEV)
+    x, dh, dy = c.x.to(DEV), c.dh.to(DEV), c.dy.to(DEV)
+    h, dx = torch.empty_like(x), torch.empty_like(x)
+    w, b = p["pre"]
+    n, stream = None, torch.cuda.current_stream().cuda_stream
+    ws = torch.empty(capi.swin_wattn_block_norm_bwd_workspace_bytes(20, 96), dtype=torch.uint8, device=DEV)
+    at = lambda t: t.data_ptr()
+    assert lib.swin_wattn_block_norm(at(x), n, at(w), at(b), n, n, n, n, n, at(h), 20, 96, 0, capi.BF16, capi.NORM_LAYER, -2.5, 1e-5,
+                                     stream) == capi.OK
+    assert lib.swin_wattn_block_norm_bwd(at(x), n, at(dh), at(dy), at(w), n, n, n, n, at(dx), n, n, n, n, n, n, 20, 96, 0, capi.BF16,
+                                         capi.NORM_LAYER, -2.5, 1e-5, 0, at(ws), ws.numel(), stream) == capi.OK
+    torch.cuda.synchronize()
+    assert torch.equal(h, capi.block_norm(x, pre=p["pre"])[1])
+    assert torch.equal(dx, capi.block_norm_bwd(x, dh=dh, dy=dy, pre=p["pre"])[0])
+
+
 def test_no_tokens():
     c = Case(1, 96)
     e = torch.empty(0, 96, dtype=torch.bfloat16, device=DEV)
