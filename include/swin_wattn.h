@@ -472,8 +472,8 @@ int swin_wattn_block_norm_bwd(const void* y, const void* f, const void* dh, cons
  *   sizes  elements of each (0: the tensor is skipped); dtypes  SWIN_WATTN_FP32 or SWIN_WATTN_BF16 of each.
  * swin_wattn_clip_grad_norm runs it: norm (device fp32, or NULL) receives n; max_norm >= 0, scale > 0 and
  * eps >= 0, finite; workspace at least swin_wattn_clip_workspace_bytes() bytes, 256-byte aligned,
- * overwritten, one call at a time per workspace. The squares are summed in 64 bits (fp32 within 64 bytes),
- * in an order that depends on the sizes alone: deterministic, without overflow. A NaN anywhere makes n and every
+ * overwritten, one call at a time per workspace. The squares are summed in two fp32 parts (in fp32 within 64 bytes), those
+ * that fp32 does not hold in 64 bits, in an order that depends on the sizes alone: deterministic, without overflow. A NaN anywhere makes n and every
  * out NaN; an infinity makes n infinite, the finite values 0 and itself NaN. Two launches;
  * where all are in place and their factor is 1 nothing is written. Errors: BAD_PLAN; INVALID_ARG, MISALIGNED as
  * above; INVALID_ARG also where the plan's device is not the current one.
