@@ -133,11 +133,15 @@ __device__ __forceinline__ uint2 quantize16(const Raw16<T>& raw, float ts, float
   unpack16(raw, v);
   uint2 codes = make_uint2(0, 0);
   if constexpr (FORMAT == 0) {
-    const float ratio = quotient(quotient(__uint_as_float(bits), 6.0f, kSixth), ts, r_ts);
+    // a given scale may be too small by any factor: the corrections need finite quotients, and from 448 on the scale is the
+    // largest, so the ratio is formed of 512 ts at most (an infinite one would be corrected to NaN), and the values are cut
+    // to 8 d, whose codes are the largest
+    const float sixth = fminf(quotient(__uint_as_float(bits), 6.0f, kSixth), 512.0f * ts);
+    const float ratio = quotient(sixth, ts, r_ts);
     scale = bits < kInfinity ? to_e4m3(ratio) : 0x7f;
     const float s = of_e4m3(scale), d = s * ts;
     if (s > 0.0f) {
-      if (ratio > 448.0f) {  // a given scale that is too small: the correction needs finite quotients
+      if (ratio > 448.0f) {
         const float most = 8.0f * d;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
