@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(kNThreads, 1)
     const bool aux = p.has_aux;
     const int NB = p.tiles;
     const uint32_t aux0 = bar0 + 8 * (kAux4 + kMaxTiles * warp);
-    const float scale = (p.scale_x != nullptr ? *p.scale_x : 1.0f) * (p.scale_w != nullptr ? *p.scale_w : 1.0f);
+    const float2 scales = FORMAT == 0 ? fp4::tensor_scales(*p.scale_x, *p.scale_w) : make_float2(1.0f, 1.0f);
+    const float scale = scales.y;
     // the next slice whose residual is to be requested: its item and columns, and its staging tile
     int nx_it = group, nx_c0 = part * kSC, nx_end = 0, nx_row = 0, nx_n0 = 0, nx_tile = 0, issued = 0;
     auto next_item = [&]() {
@@ -353,6 +354,10 @@ __global__ void __launch_bounds__(kNThreads, 1)
         }
         uint32_t a[32];
         tc::ld32_wait(trow + buf * kMaxNT4 + c0, a);
+        if (scales.x != 1.0f) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * scales.x);
+        }
         if (aux && !warp_wait(aux0 + 8 * tile, aux_phase, p.wait_ns)) {
           bad = 1;
           break;

@@ -2,6 +2,8 @@
 // linear_fp4_few.cu: few tokens) share.
 #pragma once
 
+#include <cfloat>
+
 #include "fp4.cuh"
 #include "product.cuh"
 
@@ -68,6 +70,14 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo) {
     asm volatile("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n}\n" ::"r"(taddr),
                  "r"(lo), "r"(kScaleHi)
                  : "memory");
+}
+// The two tensors' scales as two factors of a sum: x the first, y the rest. The first is 1 unless fp32 does not hold their
+// product; then it is a power of two, by which a sum (2^-20 to 2^38 in size, or zero) is multiplied exactly, and the rest is
+// held. (A product of scales above 2^192 makes each sum but zero infinite, as the largest number in its place does.)
+__device__ __forceinline__ float2 tensor_scales(float sx, float sw) {
+  const float both = sx * sw, up = both > 1.0f ? 0x1p32f : 0x1p-32f, down = both > 1.0f ? 0x1p-32f : 0x1p32f;
+  const bool held = both >= FLT_MIN && both <= FLT_MAX;
+  return make_float2(held ? 1.0f : up * up, held ? both : fminf((sx * down) * (sw * down), FLT_MAX));
 }
 #endif
 

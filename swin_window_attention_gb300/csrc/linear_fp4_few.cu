@@ -285,7 +285,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
   // the MMAs have read the last stages and every load has landed: the ring is free
   __syncthreads();
+  // (the tensors' scales are used up here as far as fp32 does not hold their product: a branch in the batches below cost 49
+  // tokens half a microsecond)
+  float2 scales = make_float2(1.0f, 1.0f);
   if (warp < kEpi) {
+    if constexpr (FORMAT == 0) scales = fp4::tensor_scales(*p.scale_x, *p.scale_w);
     if (!warp_wait(bar0 + 8 * kDoneB, 0, p.wait_ns)) bad = 1;
     if (!bad) {
       tc::fence_after_sync();
@@ -293,6 +297,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       for (int t = (warp >> 2) * 16; t < p.TN; t += kEpi / 4 * 16) {
         uint32_t a[16];
         tc::ld16_wait(trow + t, a);
+        if (scales.x != 1.0f) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * scales.x);
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) part[(t + e) * kBM + (tid & (kBM - 1))] = __uint_as_float(a[e]);
       }
@@ -310,7 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int n = n0 + (tid & (kBM - 1));
     if (warp < kEpi && n < p.N) {
       const float bias = p.bias != nullptr ? p.bias[n] : 0.0f;
-      const float scale = (p.scale_x != nullptr ? *p.scale_x : 1.0f) * (p.scale_w != nullptr ? *p.scale_w : 1.0f);
+      const float scale = scales.y;
       const uint32_t mine = smem0 + (n - n0) * 4;
       uint32_t peer[kMaxCluster4];
 #pragma unroll
