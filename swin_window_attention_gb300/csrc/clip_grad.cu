@@ -10,6 +10,7 @@
 //   last is still in L2.
 // Where the factor is 1 and the tensors are scaled in place there is nothing to write.
 #include <algorithm>
+#include <cfloat>
 #include <new>
 #include <vector>
 
@@ -184,8 +185,8 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <typename T>
-__device__ __forceinline__ void scale_one(const T* in, T* out, float factor) {
-  const float v = value(in) * factor;
+__device__ __forceinline__ void scale_one(const T* in, T* out, float first, float factor) {
+  const float v = value(in) * first * factor;
   if constexpr (sizeof(T) == 4)
     *out = v;
   else
@@ -193,15 +194,15 @@ __device__ __forceinline__ void scale_one(const T* in, T* out, float factor) {
 }
 
 template <typename T>
-__device__ void scale_piece(const T* in, T* out, int len, float factor) {
+__device__ void scale_piece(const T* in, T* out, int len, float first, float factor) {
   constexpr int kPer = 16 / sizeof(T);
   if (((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
-    for (int i = threadIdx.x; i < len; i += kThreads) scale_one(in + i, out + i, factor);
+    for (int i = threadIdx.x; i < len; i += kThreads) scale_one(in + i, out + i, first, factor);
     return;
   }
   const int head = head_of(in, len), vecs = (len - head) / kPer, tail = head + vecs * kPer;
-  if ((int)threadIdx.x < head) scale_one(in + threadIdx.x, out + threadIdx.x, factor);
-  if (tail + (int)threadIdx.x < len) scale_one(in + tail + threadIdx.x, out + tail + threadIdx.x, factor);
+  if ((int)threadIdx.x < head) scale_one(in + threadIdx.x, out + threadIdx.x, first, factor);
+  if (tail + (int)threadIdx.x < len) scale_one(in + tail + threadIdx.x, out + tail + threadIdx.x, first, factor);
   const uint4* from = reinterpret_cast<const uint4*>(in + head);
   uint4* to = reinterpret_cast<uint4*>(out + head);
   for (int i0 = threadIdx.x; i0 < vecs; i0 += kThreads * kLoads) {
@@ -214,6 +215,10 @@ __device__ void scale_piece(const T* in, T* out, int len, float factor) {
       if (i0 + k * kThreads >= vecs) break;
       float v[kPer];
       unpack<T>(w[k], v);
+      if (first != 1.0f) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) v[e] *= first;
+      }
 #pragma unroll
       for (int e = 0; e < kPer; ++e) v[e] *= factor;
       uint4 o;
@@ -241,25 +246,36 @@ __global__ void __launch_bounds__(kThreads)
     if (has_wide(o)) sum.wide += o.wide;
   }
   sum = block_sum(sum);
-  __shared__ float shared_factor;
+  __shared__ float shared_first, shared_factor;
   if (threadIdx.x == 0) {
     // the root of the fp32 sum, or where there is more, that in 64 bits
     float n = scale * __fsqrt_rn(sum.hi + sum.lo);
     if (has_wide(sum)) n = (float)((double)scale * sqrt((double)sum.hi + (double)sum.lo + sum.wide));
-    if (norm != nullptr && blockIdx.x == 0) *norm = n;
     const float c = __fdiv_rn(max_norm, n + eps);
-    shared_factor = scale * (c > 1.0f ? 1.0f : c);  // NaN stays NaN
+    float first = 1.0f, factor = scale * (c > 1.0f ? 1.0f : c);  // NaN stays NaN
+    // Where the norm or the factor leaves fp32's normal range, both in 64 bits, and a factor below it in two: the values
+    // times 2^-126, exactly but for those whose results are below 2^-126, and that times the rest.
+    if (!(n >= FLT_MIN && n + eps <= FLT_MAX && factor >= FLT_MIN)) {
+      const double root = sqrt((double)sum.hi + (double)sum.lo + sum.wide), wide = (double)scale * root;
+      const double d = (double)max_norm / (wide + (double)eps), f = (double)scale * (d > 1.0 ? 1.0 : d);
+      n = (float)wide;
+      if (f < 0x1p-126 && f > 0.0) first = 0x1p-126f;
+      factor = (float)(first == 1.0f ? f : f * 0x1p126);
+    }
+    if (norm != nullptr && blockIdx.x == 0) *norm = n;
+    shared_first = first;
+    shared_factor = factor;
   }
   __syncthreads();
-  const float factor = shared_factor;
-  if (in_place && factor == 1.0f) return;
+  const float first = shared_first, factor = shared_factor;
+  if (in_place && first == 1.0f && factor == 1.0f) return;
   for (uint32_t i = blockIdx.x; i < pieces; i += gridDim.x) {
     const Piece p = next;
     if (i + gridDim.x < pieces) next = piece_at(list, pieces - 1 - i - gridDim.x);
     if (p.bf16)
-      scale_piece(static_cast<const __nv_bfloat16*>(p.in), static_cast<__nv_bfloat16*>(p.out), p.len, factor);
+      scale_piece(static_cast<const __nv_bfloat16*>(p.in), static_cast<__nv_bfloat16*>(p.out), p.len, first, factor);
     else
-      scale_piece(static_cast<const float*>(p.in), static_cast<float*>(p.out), p.len, factor);
+      scale_piece(static_cast<const float*>(p.in), static_cast<float*>(p.out), p.len, first, factor);
   }
 }
 
