@@ -10,10 +10,23 @@
 namespace swin {
 namespace fp4 {
 
-// Products that keep subnormals (the library is built to flush them).
+// Products and their sums that keep subnormals (the library is built to flush them).
 __device__ __forceinline__ float mul_exact(float a, float b) {
   float r;
   asm("mul.rn.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float fma_exact(float a, float b, float c) {
+  float r;
+  asm("fma.rn.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 fma2_exact(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
 }
 // Eight values to eight codes, the first in the lowest four bits.
@@ -105,10 +118,11 @@ __device__ __forceinline__ float reciprocal(float d) {
   return fmaf(fmaf(-d, r, 1.0f), r, r);
 }
 // x / d, rounded to nearest: the product with the reciprocal r, corrected by its remainder, which an fma gives exactly
-// (Markstein, 1990). An exact quotient comes out exact, so ties between codes are met as a division would.
+// (Markstein, 1990). An exact quotient comes out exact, so ties between codes are met as a division would. The remainder
+// is some 2^-24 of x: below a scale of the tensor of 2^-97 it is subnormal, and kept.
 __device__ __forceinline__ float quotient(float x, float d, float r) {
   const float q = x * r;
-  return fmaf(fmaf(-q, d, x), r, q);
+  return fma_exact(fma_exact(-q, d, x), r, q);
 }
 // Codes of the 16 values x of an NVFP4 block, the quotients by d.
 __device__ __forceinline__ uint2 codes_of_quotient(const float2 (&x)[8], float d, float r) {
@@ -117,7 +131,7 @@ __device__ __forceinline__ uint2 codes_of_quotient(const float2 (&x)[8], float d
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float2 q0 = __fmul2_rn(x[e], r2);
-    q[e] = __ffma2_rn(__ffma2_rn(q0, d2, x[e]), r2, q0);
+    q[e] = fma2_exact(fma2_exact(q0, d2, x[e]), r2, q0);
   }
   return make_uint2(to_e2m1x8(q), to_e2m1x8(q + 4));
 }
