@@ -475,7 +475,7 @@ int swin_wattn_block_norm_bwd(const void* y, const void* f, const void* dh, cons
  * overwritten, one call at a time per workspace. The squares are summed in two fp32 parts (in fp32 within 64 bytes), those
  * that fp32 does not hold in 64 bits, in an order that depends on the sizes alone: deterministic, without overflow. Where n
  * or the factor leaves fp32's normal range both are formed in 64 bits: a finite n above it is stored as an infinity, and the
- * values are scaled all the same (results below 2^-126 may be flushed to zero). A NaN anywhere makes n and every out NaN; an
+ * values are scaled all the same. Subnormal gradients and results are kept. A NaN anywhere makes n and every out NaN; an
  * infinity makes n infinite, the finite values 0 and itself NaN. Two launches;
  * where all are in place and their factor is 1 nothing is written. Errors: BAD_PLAN; INVALID_ARG, MISALIGNED as
  * above; INVALID_ARG also where the plan's device is not the current one.

@@ -36,6 +36,23 @@ __device__ __forceinline__ Piece piece_at(const Piece* list, uint32_t i) {
   return u.p;
 }
 
+// Conversions and products that keep subnormal numbers (the library is built to flush them).
+__device__ __forceinline__ double to_double(float v) {
+  double r;
+  asm("cvt.f64.f32 %0, %1;\n" : "=d"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float to_float(double v) {
+  float r;
+  asm("cvt.rn.f32.f64 %0, %1;\n" : "=f"(r) : "d"(v));
+  return r;
+}
+__device__ __forceinline__ float mul_exact(float a, float b) {
+  float r;
+  asm("mul.rn.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 __device__ __forceinline__ float value(const float* p) { return *p; }
 __device__ __forceinline__ float value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
@@ -97,7 +114,7 @@ __device__ void squares(const T* p, int len, bool keep, Sum& sum) {
     if (holds(s))
       add(sum, s);
     else
-      sum.wide += (double)v * (double)v;
+      sum.wide += to_double(v) * to_double(v);
   };
   if ((int)threadIdx.x < head) one(p + threadIdx.x);
   if (tail + (int)threadIdx.x < len) one(p + tail + threadIdx.x);
@@ -127,7 +144,7 @@ __device__ void squares(const T* p, int len, bool keep, Sum& sum) {
         float v[kPer];
         unpack<T>(w[k], v);
 #pragma unroll 1
-        for (int e = 0; e < kPer; ++e) sum.wide = fma((double)v[e], (double)v[e], sum.wide);
+        for (int e = 0; e < kPer; ++e) sum.wide = fma(to_double(v[e]), to_double(v[e]), sum.wide);
       }
     }
   }
@@ -186,7 +203,7 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T>
 __device__ __forceinline__ void scale_one(const T* in, T* out, float first, float factor) {
-  const float v = value(in) * first * factor;
+  const float v = mul_exact(mul_exact(value(in), first), factor);
   if constexpr (sizeof(T) == 4)
     *out = v;
   else
@@ -217,10 +234,10 @@ __device__ void scale_piece(const T* in, T* out, int len, float first, float fac
       unpack<T>(w[k], v);
       if (first != 1.0f) {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) v[e] *= first;
+        for (int e = 0; e < kPer; ++e) v[e] = mul_exact(v[e], first);
       }
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) v[e] *= factor;
+      for (int e = 0; e < kPer; ++e) v[e] = mul_exact(v[e], factor);
       uint4 o;
       if constexpr (sizeof(T) == 4)
         o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
@@ -254,13 +271,13 @@ __global__ void __launch_bounds__(kThreads)
     const float c = __fdiv_rn(max_norm, n + eps);
     float first = 1.0f, factor = scale * (c > 1.0f ? 1.0f : c);  // NaN stays NaN
     // Where the norm or the factor leaves fp32's normal range, both in 64 bits, and a factor below it in two: the values
-    // times 2^-126, exactly but for those whose results are below 2^-126, and that times the rest.
+    // times 2^-126, exactly but for those whose results are subnormal, and that times the rest.
     if (!(n >= FLT_MIN && n + eps <= FLT_MAX && factor >= FLT_MIN)) {
-      const double root = sqrt((double)sum.hi + (double)sum.lo + sum.wide), wide = (double)scale * root;
-      const double d = (double)max_norm / (wide + (double)eps), f = (double)scale * (d > 1.0 ? 1.0 : d);
-      n = (float)wide;
+      const double root = sqrt((double)sum.hi + (double)sum.lo + sum.wide), wide = to_double(scale) * root;
+      const double d = to_double(max_norm) / (wide + to_double(eps)), f = to_double(scale) * (d > 1.0 ? 1.0 : d);
+      n = to_float(wide);
       if (f < 0x1p-126 && f > 0.0) first = 0x1p-126f;
-      factor = (float)(first == 1.0f ? f : f * 0x1p126);
+      factor = to_float(first == 1.0f ? f : f * 0x1p126);
     }
     if (norm != nullptr && blockIdx.x == 0) *norm = n;
     shared_first = first;
