@@ -538,7 +538,9 @@ int swin_wattn_linear_fp4(const void* x_codes, const void* x_scales, const float
  *          overwritten, one call at a time per workspace; NULL where that is 0 (scale_given: whether x_tensor_scale
  *          is; the query also returns 0 for unsupported arguments).
  * Two launches, or three for a scale that is taken from x; one, without a workspace, where 64 tokens at most, with no scale to
- * take, are quantised by the product itself (an estimate of both forms decides).
+ * take, are quantised by the product itself (an estimate of both forms decides, which counts what a launch costs the
+ * host; in a graph 49 tokens and more of a wide N are up to 2 us shorter as swin_wattn_fp4_quantize and
+ * swin_wattn_linear_fp4).
  */
 size_t swin_wattn_linear_fp4_workspace_bytes(int tokens, int K, int N, int format, int scale_given);
 int swin_wattn_linear_fp4_of(const void* x, const float* x_tensor_scale, const void* w_codes, const void* w_scales,

@@ -809,9 +809,14 @@ class GradClip:
     """Clipping by the norm over all gradients of a model: a plan over the fp32 and bf16 CUDA tensors
     `grads` (of any sizes, contiguous), which are checked once and kept. Each call computes
     n = scale |grads| and writes grads * scale * min(1, max_norm / (n + eps)) to `out`, tensors of the
-    same shapes and dtypes (the gradients themselves when not given). The plan's workspace serves one
-    stream at a time; a call may bring its own. A captured call reads the plan's list and, without one of its
-    own, its workspace on every replay: keep the plan as long as the graph."""
+    same shapes and dtypes (the gradients themselves when not given). max_norm is finite; with 3.4e38 and a scale of 1
+    a call in place gives the norm alone and leaves finite gradients as they are.
+
+    The plan is of the tensors' memory: it copies a list of it to the device and waits for the stream. It is made once,
+    outside of captures, for gradients that stay where they are (written into given tensors, or zeroed in place);
+    gradients that are dropped and made anew at each step need a new plan at each step. Its workspace serves one stream
+    at a time; a call may bring its own. A captured call reads the plan's list and, without one of its own, its workspace
+    on every replay: keep the plan as long as the graph."""
 
     handle = None
 

@@ -23,7 +23,8 @@ struct NormBwdParams {
   __nv_bfloat16* df;
   float* partial;  // [blocks, kSums, C]
   int rows, C, per_sample;
-  int stages;  // rows of a group in shared memory: one in use, the others (two; of wide rows one, of fp32 ones above 7168 none) on their way
+  int stages;  // rows of a group in shared memory: one in use, the others (two; of wide rows one, of fp32 ones above 6144
+               // channels none) on their way
   bool rms;
   float alpha, eps, inv_c;
 };

@@ -557,8 +557,10 @@ constexpr int kFewTokens4 = 128, kFewQuantized = 64;
 
 // Whether the product itself quantises an x that is not: few tokens, of which every CTA quantises its part of K, some 400
 // clocks for each 32 tokens of a chunk, against a launch of its own, some 4000 of the GPU and, where calls follow one another,
-// twice as many of the host, with its workspace; counted as 6000. (One token 1536 -> 6144 5.3 us instead of 7.2, 6144 -> 1536
-// 6.4 and 9.9; 49 tokens in a graph 8.0 and 6.9, called from Python 19 and 24; 6144 -> 1536 in a graph 8.8 and 10.4.)
+// twice as many of the host, with its workspace; counted as 6000. (In a graph, one launch and two, NVFP4 and MXFP4: one token
+// 1536 -> 6144 5.1, 7.2 and 5.0, 6.6 us, 32 tokens 6.1, 7.0 and 6.4, 6.2, 49 tokens 7.3, 7.2 and 7.8, 6.5, 64 tokens 7.8, 6.9
+// and 8.2, 6.2; 6144 -> 1536 one token 6.2, 7.8 and 6.0, 7.3, 64 tokens 9.2, 9.7 and 9.4, 9.0. Called from Python 49 tokens
+// of MXFP4 take 19 us and 24.)
 bool linear_fp4_quantizes(int T, int K, int N, int format) {
   if (T > kFewQuantized) return false;
   const FewFp4Tiling few = few_fp4_tiling(T, N, K);

@@ -5,7 +5,8 @@ whose squares overflow or vanish, NaN and infinities, streams, replays and the r
 Bounds: the squares are summed in fp32 over at most 32 values (32 2^-24 relative, all terms of one
 sign) and in 64 bits beyond; the norm is rounded once, the factor is two fp32 operations and a
 product, and each result one product and its rounding: 2^-20 covers the norm (64 roundings, halved by
-the square root), the factor 2^-20 + 4 2^-24, a result that and its own half step."""
+the square root), the factor 2^-20 + 4 2^-24, a result that and its own half step. (Beyond 64 bytes the squares are added in
+two fp32 parts, of 48 bits together, and in 64 bits where fp32 does not hold them: the bounds cover either.)"""
 import pytest
 import torch
 
