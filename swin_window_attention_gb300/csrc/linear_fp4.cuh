@@ -76,7 +76,7 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo) {
 // held. (A product of scales above 2^192 makes each sum but zero infinite, as the largest number in its place does.)
 __device__ __forceinline__ float2 tensor_scales(float sx, float sw) {
   const float both = sx * sw, up = both > 1.0f ? 0x1p32f : 0x1p-32f, down = both > 1.0f ? 0x1p-32f : 0x1p32f;
-  const bool held = both >= FLT_MIN && both <= FLT_MAX;
+  const bool held = !(both < FLT_MIN || both > FLT_MAX);  // (NaN as it is)
   return make_float2(held ? 1.0f : up * up, held ? both : fminf((sx * down) * (sw * down), FLT_MAX));
 }
 #endif
